@@ -346,6 +346,103 @@ unsigned long long lla_launch_count(void);
 int lla_profile_enable(int on);
 int lla_profile_collect(float* stage_ms, int max_stages, int* n_calls);
 
+/*
+ * ---------------------------------------------------------------------------------------------
+ * Paged caches: keys and values of many sequences in pages that a user's allocator hands out, the
+ * append of new tokens, attention of those tokens over the cache (softmax, or Parallax with a
+ * probe), and eviction of the positions that received the least attention.
+ *
+ * A cache holds num_pages pages of page_size slots per key/value head: k_pages is [num_pages,
+ * kv_heads, page_size, d], v_pages [num_pages, kv_heads, page_size, dv], both of type `dtype`, and
+ * mass (may be NULL where it is not used) [num_pages, kv_heads, page_size] fp32, the attention
+ * weight that each slot has received so far. Position j of sequence b is slot j % page_size of page
+ * page_table[b * max_pages + j / page_size]; lens[b] (0 .. max_pages * page_size) counts the
+ * sequence's positions. Pages may come in any order and may be shared by sequences that only read
+ * them. All pointers are device memory; k_pages, v_pages 16-byte aligned.
+ *
+ * New tokens of all sequences lie one after the other, as [tokens, heads, size] rows: sequence b's
+ * are starts[b] .. starts[b+1]-1 (device memory, [num_seqs + 1], ascending, at most `tokens`), and
+ * they are the sequence's last positions: lens already counts them.
+ *
+ * Supported: d, dv in {16, 32, 64, 128}; page_size a power of two in 16 .. 1024; max_pages *
+ * page_size < 2^30; tokens < 2^30, tokens * q_heads < 2^31, num_pages * kv_heads < 2^31, num_seqs and kv_heads
+ * at most 65535 (LLA_ERR_UNSUPPORTED otherwise). What only the device can see is checked there: a
+ * page index outside 0 .. num_pages-1, a length beyond the table, or starts that descend or pass
+ * `tokens` are recorded in the status word (lla_stream_status: LLA_ERR_INVALID_ARG); nothing out of
+ * range is read or written, and the outputs of that sequence are unspecified. Slots that no row
+ * sees may hold anything, infinities and NaN included.
+ */
+typedef struct lla_paged_cache {
+  void* k_pages;
+  void* v_pages;
+  float* mass;
+  const int* page_table; /* [num_seqs, max_pages] */
+  int* lens;             /* [num_seqs] */
+  int num_seqs, kv_heads, page_size, max_pages, num_pages, d, dv;
+  int dtype;       /* lla_dtype */
+  int reserved[2]; /* must be zero */
+} lla_paged_cache;
+
+/*
+ * Writes the new tokens' keys k_new [tokens, kv_heads, d] and values v_new [tokens, kv_heads, dv]
+ * into their slots and, when the cache has a mass, sets theirs to zero. Tokens beyond a sequence's
+ * length (more new tokens than positions) are not written. Allocates nothing.
+ */
+int lla_paged_append(const lla_paged_cache* cache, const void* k_new, const void* v_new,
+                     const int* starts, int tokens, void* stream);
+
+/*
+ * The queries of one lla_paged_attention call.
+ *   q, r, out   [tokens, q_heads, d], the same (NULL: softmax attention), [tokens, q_heads, dv],
+ *               of the cache's type. q_heads is a multiple of kv_heads: query heads hk*g ..
+ *               hk*g + g-1 read key/value head hk, g = q_heads / kv_heads.
+ *   lse         [tokens, q_heads] fp32 or NULL: log of the sum of exp(q.k/h) over the visible keys.
+ *   max_new     at least the largest number of new tokens of a sequence (it sizes the launch; the
+ *               rows of a sequence with more are unspecified).
+ *   window      0, or how many last positions a token sees, its own included; sinks: the first
+ *               positions that stay visible besides. The token at position i sees positions
+ *               j <= i with window == 0, j > i - window or j < sinks.
+ *   track_mass  nonzero: cache->mass of every visible slot grows by the softmax weights that the
+ *               new tokens' rows give it, summed over the tokens and the g heads (with a probe too:
+ *               its signed correction is not counted). The sums do not depend on scheduling.
+ *   path        lla_path: AUTO, CUDA_CORE or TENSOR_CORE.
+ */
+typedef struct lla_paged_query {
+  const void* q;
+  const void* r;
+  void* out;
+  float* lse;
+  const int* starts;
+  int tokens, max_new, q_heads;
+  float h;
+  int window, sinks, track_mass, path;
+  int reserved[2]; /* must be zero */
+} lla_paged_query;
+
+/*
+ * Attention of the new tokens over the cache (append them first). Per row, over its visible keys:
+ * p = softmax(q.k / h), o = sum p v, or with a probe the Parallax output
+ * o = sum p (1 + tbar - t) v with t = r.k and tbar = sum p t, as lla_parallax_forward computes it.
+ * A row that sees nothing (a position below zero) gives o = 0, lse = -infinity. Sums are fp32.
+ * `workspace` (256-byte aligned device memory of lla_paged_workspace_size bytes; its contents need
+ * not be kept between calls) or NULL: scratch from the stream-ordered allocator.
+ */
+size_t lla_paged_workspace_size(const lla_paged_cache* cache, const lla_paged_query* query);
+int lla_paged_attention(const lla_paged_cache* cache, const lla_paged_query* query, void* workspace,
+                        size_t workspace_bytes, void* stream);
+
+/*
+ * Eviction: for every sequence of `from` and key/value head, min(lens, budget) positions are kept:
+ * the first `sinks`, the last `recent` (sinks + recent <= budget), and of the others those with the
+ * largest mass (ties: the lower position; NaN counts as the lowest), in their order. Their keys,
+ * values and mass are copied to slots 0, 1, .. of `to`, to->lens is set, and kept [num_seqs,
+ * kv_heads, budget] gets their positions in `from` (-1 past the last). `to` has the same sequences,
+ * heads, page size and types; it may use the same page arrays (another table, and pages that no
+ * sequence of `from` holds), not the same table or lens.
+ */
+int lla_paged_evict(const lla_paged_cache* from, const lla_paged_cache* to, int budget, int sinks,
+                    int recent, int* kept, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

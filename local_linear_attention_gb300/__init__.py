@@ -11,7 +11,8 @@ _BINDING = {
     "lla_stream_status", "lla_status_string", "lla_version", "LlaError", "library_path",
     "launch_count", "profile_enable", "profile_collect", "lla_forward_noalloc",
     "lla_parallax_forward", "lla_decode", "lla_parallax_decode", "lla_parallax_backward",
-    "Options",
+    "Options", "PagedCache", "lla_paged_append", "lla_paged_attention", "lla_paged_workspace_size",
+    "lla_paged_evict",
 }
 
 

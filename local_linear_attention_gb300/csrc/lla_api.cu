@@ -68,6 +68,8 @@ cudaError_t side_stream(SideStream** out) {
   return cudaSuccess;
 }
 
+}  // namespace
+
 // Address of the status word on the current device (resolved once per device).
 cudaError_t device_status(int** out) {
   int dev = 0;
@@ -105,6 +107,8 @@ cudaError_t ensure_pool() {
   }
   return cudaSuccess;
 }
+
+namespace {
 
 // Validates per-call options into `a` (forward: every field; other operations: path only).
 int apply_options(const lla_options* o, bool forward, Args* a) {

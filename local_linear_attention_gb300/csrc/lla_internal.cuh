@@ -232,6 +232,10 @@ size_t decode_workspace_bytes(const DecodeArgs& a);
 cudaError_t launch_decode(const DecodeArgs& a, void* ws, int* status, cudaStream_t s);
 
 void count_launch();
+// Address of the current device's status word, and the one-time setup of its default memory pool
+// (lla_api.cu).
+cudaError_t device_status(int** out);
+cudaError_t ensure_pool();
 
 // ---------------------------------------------------------------------------------------------
 // Device helpers.

@@ -1,0 +1,234 @@
+// The paged-cache operators (append, attention of a chunk of new tokens, eviction): problem
+// description, the mask's key ranges and the row arithmetic their kernels share.
+//
+// Sequence b's position j lives in slot j % page_size of page table[b][j / page_size]; its new
+// tokens starts[b] .. starts[b+1]-1 (rows of q, r, out: [tokens, q_heads, d]) are its last
+// positions, pos = lens[b] - n + i. Query heads u of key/value head hk are hk*g .. hk*g + g-1, so
+// the rows of a (sequence, key/value head) pair are numbered row = i*g + u: one key/value stream
+// serves all of them.
+#pragma once
+
+#include <math_constants.h>
+
+#include "lla_internal.cuh"
+
+namespace lla {
+namespace paged {
+
+constexpr int kNoWindow = 1 << 30;  // lengths stay below this (checked on the host)
+
+// Passed to kernels by value.
+struct Params {
+  const void* q;      // [tokens, Hq, d]
+  const void* r;      // [tokens, Hq, d] or nullptr: softmax attention
+  void* k;            // [num_pages, Hkv, page, d]
+  void* v;            // [num_pages, Hkv, page, dv]
+  float* mass;        // [num_pages, Hkv, page] or nullptr
+  void* out;          // [tokens, Hq, dv]
+  float* lse;         // [tokens, Hq] or nullptr
+  const int* starts;  // [B + 1]
+  const int* table;   // [B, max_pages]
+  const int* lens;    // [B]
+  int* status;
+  int B, tokens, Hq, Hkv, g;
+  int page, page_shift, max_pages, num_pages;
+  int window, sinks;  // window = kNoWindow when there is none
+  float inv_h;
+  int max_rows;       // most rows (new tokens x g) of any sequence, as the caller states
+  int lo, hi;         // this launch takes the sequences with lo < rows <= hi
+  // Split of each row's keys over blocks, and its partial results (split > 1).
+  int split;
+  float* part_o;     // [split][tokens * Hq][nbranch][dv]   unnormalised O1 (and O2)
+  float4* part_s;    // [split][tokens * Hq]   {m, d1, d2, 0} with m the maximum of q.k (raw)
+  float* logits;     // [B][Hkv][row_cap][keys_cap]  raw q.k of the few-rows kernel (weight tracking)
+  int row_cap, keys_cap;
+};
+
+struct Seq {
+  int t0, n;     // first new token's index, number of new tokens
+  int len;       // positions in the cache, the new tokens included
+  int first;     // position of the first new token (negative when n > len)
+};
+
+// Sequence b with every field brought into range; a sequence with impossible starts or length is
+// treated as having no new tokens (or the nearest possible length) and reported once per reader.
+__device__ __forceinline__ Seq load_seq(const Params& p, int b) {
+  Seq s;
+  const int t0 = p.starts[b], t1 = p.starts[b + 1];
+  const int len = p.lens[b], cap = p.max_pages << p.page_shift;
+  const bool bad = t0 < 0 || t1 < t0 || t1 > p.tokens;
+  s.t0 = bad ? 0 : t0;
+  s.n = bad ? 0 : t1 - t0;
+  s.len = min(max(len, 0), cap);
+  s.first = s.len - s.n;
+  if (bad || s.len != len) atomicOr(p.status, kStatusBadIndex);
+  return s;
+}
+
+// Page index of a position's page, or -1 (reported) when the table's entry is out of range.
+__device__ __forceinline__ int load_page(const Params& p, int b, int slot) {
+  const int pg = __ldg(p.table + (long long)b * p.max_pages + slot);
+  if ((unsigned)pg < (unsigned)p.num_pages) return pg;
+  atomicOr(p.status, kStatusBadIndex);
+  return -1;
+}
+
+__device__ __forceinline__ bool visible(const Params& p, int pos, int j) {
+  return j <= pos && (j > pos - p.window || j < p.sinks);
+}
+
+// The key tiles of KT positions that rows at positions p0 .. p1 see: tiles 0 .. n1-1 hold the
+// first tokens, tiles w0 .. the window; count of both. tile(i) is the i-th of them.
+template <int KT>
+struct TileRange {
+  int n1, w0, count;
+  __device__ __forceinline__ TileRange(const Params& p, int p0, int p1) {
+    const int kend = p1 + 1;
+    const int wstart = max(0, p0 - p.window + 1);
+    const int send = min(p.sinks, kend);
+    n1 = (send + KT - 1) / KT;
+    w0 = wstart / KT;
+    if (w0 <= n1) n1 = w0 = 0;
+    count = kend <= 0 ? 0 : n1 + (kend + KT - 1) / KT - w0;
+  }
+  __device__ __forceinline__ int tile(int i) const { return i < n1 ? i : w0 + i - n1; }
+};
+// Keys k0 .. k1-1 are visible to every row at positions p0 .. p1 (no mask needed).
+__device__ __forceinline__ bool all_visible(const Params& p, int p0, int p1, int k0, int k1) {
+  return k1 - 1 <= p0 && (k0 > p1 - p.window || k1 <= p.sinks);
+}
+
+// Whether sequence rows `n` x g are this launch's.
+__device__ __forceinline__ bool mine(const Params& p, int n) {
+  return n > 0 && n * p.g > p.lo && n * p.g <= p.hi;
+}
+
+// Row tiles of this launch's sequences, `per` tokens each: finds the sequence and tile of linear
+// index `x` (every warp does the search by itself; all lanes return the same). False when x is
+// past the last tile.
+__device__ __forceinline__ bool find_tile(const Params& p, int per, int x, int* b_out, int* tile_out) {
+  const int lane = threadIdx.x & 31;
+  int before = 0;
+  for (int base = 0; base < p.B; base += 32) {
+    const int b = base + lane;
+    int cnt = 0;
+    if (b < p.B) {
+      const int t0 = p.starts[b], t1 = p.starts[b + 1];
+      if (t0 >= 0 && t1 > t0 && t1 <= p.tokens && mine(p, t1 - t0)) cnt = (t1 - t0 + per - 1) / per;
+    }
+    int incl = cnt;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += y;
+    }
+    const unsigned hit = __ballot_sync(0xffffffffu, x < before + incl);
+    if (hit) {
+      const int l = __ffs(hit) - 1;
+      const int upto = __shfl_sync(0xffffffffu, incl, l), c = __shfl_sync(0xffffffffu, cnt, l);
+      *b_out = base + l;
+      // the last tiles of a prompt see the most keys: first
+      *tile_out = c - 1 - (x - (before + upto - c));
+      return true;
+    }
+    before += __shfl_sync(0xffffffffu, incl, 31);
+  }
+  return false;
+}
+
+// One row computed by one warp straight from the definition, skipping every key that the row does
+// not see. The tiled kernels multiply such keys' values by a zero weight, which is not zero when
+// the value is infinite or NaN; a row whose result is not finite is therefore taken again here
+// (and stays NaN only if a key that it sees makes it so). Slow, and off every ordinary path.
+template <typename T>
+__device__ __noinline__ void exact_row(const Params& p, int d, int dv, int b, int pos, int token,
+                                       int head) {
+  const int lane = threadIdx.x & 31, hk = head / p.g;
+  const T* q = static_cast<const T*>(p.q) + ((long long)token * p.Hq + head) * d;
+  const T* r = p.r ? static_cast<const T*>(p.r) + ((long long)token * p.Hq + head) * d : nullptr;
+  const T* kp = static_cast<const T*>(p.k);
+  const T* vp = static_cast<const T*>(p.v);
+  float m = -CUDART_INF_F, d1 = 0.f, d2 = 0.f, o1[4] = {}, o2[4] = {};
+  const TileRange<32> range(p, pos, pos);
+  for (int i = 0; i < range.count; ++i) {
+    const int j = range.tile(i) * 32 + lane;
+    const bool see = visible(p, pos, j);
+    float s = -CUDART_INF_F, t = 0.f;
+    long long slot = -1;
+    if (see) {
+      const int pg = load_page(p, b, j >> p.page_shift);
+      s = 0.f;
+      if (pg >= 0) {
+        slot = ((long long)pg * p.Hkv + hk) * p.page + (j & (p.page - 1));
+        for (int c = 0; c < d; ++c) {
+          const float kv = ldf(kp, slot * d + c);
+          s = fmaf(ldf(q, c), kv, s);
+          if (r) t = fmaf(ldf(r, c), kv, t);
+        }
+      }
+      s *= p.inv_h;
+    }
+    float tm = s;
+    for (int o = 16; o; o >>= 1) {
+      const float y = __shfl_xor_sync(0xffffffffu, tm, o);
+      tm = (tm != tm || y != y) ? CUDART_NAN_F : fmaxf(tm, y);
+    }
+    const float mn = (m != m || tm != tm) ? CUDART_NAN_F : fmaxf(m, tm);
+    if (mn == -CUDART_INF_F) continue;
+    const float sc = m == -CUDART_INF_F ? 0.f : expf(m - mn);
+    const float w = see ? expf(s - mn) : 0.f, wt = see ? w * t : 0.f;
+    m = mn;
+    float a = w, e = wt;
+    for (int o = 16; o; o >>= 1) {
+      a += __shfl_xor_sync(0xffffffffu, a, o);
+      e += __shfl_xor_sync(0xffffffffu, e, o);
+    }
+    d1 = fmaf(d1, sc, a);
+    d2 = fmaf(d2, sc, e);
+    for (int c = 0; c < 4; ++c) { o1[c] *= sc; o2[c] *= sc; }
+    for (int l = 0; l < 32; ++l) {
+      const float wl = __shfl_sync(0xffffffffu, w, l), tl = __shfl_sync(0xffffffffu, wt, l);
+      const long long sl = __shfl_sync(0xffffffffu, slot, l);
+      if (sl < 0) continue;
+      for (int c = 0; c < 4; ++c)
+        if (lane + 32 * c < dv) {
+          const float x = ldf(vp, sl * dv + lane + 32 * c);
+          o1[c] = fmaf(wl, x, o1[c]);
+          o2[c] = fmaf(tl, x, o2[c]);
+        }
+    }
+  }
+  const float inv = d1 == 0.f ? 0.f : 1.f / d1, f1 = (1.f + d2 * inv) * inv;
+  T* out = static_cast<T*>(p.out) + ((long long)token * p.Hq + head) * dv;
+  for (int c = 0; c < 4; ++c)
+    if (lane + 32 * c < dv)
+      stf(out, lane + 32 * c, r ? fmaf(o1[c], f1, -o2[c] * inv) : o1[c] * inv);
+}
+
+// Launchers (each returns the launch error, if any).
+// CUDA cores, every supported size (one set per type): the attention; mass += the rows' weights from
+// q, k and the finished lse; the join of the splits' partial results into out and lse.
+cudaError_t attend_cc_f32(const Params& p, int d, int dv, cudaStream_t s);
+cudaError_t attend_cc_bf16(const Params& p, int d, int dv, cudaStream_t s);
+cudaError_t mass_cc_f32(const Params& p, int d, cudaStream_t s);
+cudaError_t mass_cc_bf16(const Params& p, int d, cudaStream_t s);
+cudaError_t join_f32(const Params& p, int d, int dv, cudaStream_t s);
+cudaError_t join_bf16(const Params& p, int d, int dv, cudaStream_t s);
+inline cudaError_t launch_attend_cc(const Params& p, int d, int dv, int dtype, cudaStream_t s) {
+  return dtype == LLA_F32 ? attend_cc_f32(p, d, dv, s) : attend_cc_bf16(p, d, dv, s);
+}
+inline cudaError_t launch_mass_cc(const Params& p, int d, int dtype, cudaStream_t s) {
+  return dtype == LLA_F32 ? mass_cc_f32(p, d, s) : mass_cc_bf16(p, d, s);
+}
+inline cudaError_t launch_join(const Params& p, int d, int dv, int dtype, cudaStream_t s) {
+  return dtype == LLA_F32 ? join_f32(p, d, dv, s) : join_bf16(p, d, dv, s);
+}
+cudaError_t launch_append(const Params& p, const void* k_new, const void* v_new, int d, int dv,
+                          int dtype, cudaStream_t s);
+// `p` is the source cache; the other arguments the destination and the choice.
+cudaError_t launch_evict(const Params& p, void* k, void* v, float* mass, const int* table, int* lens,
+                         int max_pages, int num_pages, int budget, int sinks, int recent, int* kept,
+                         int d, int dv, int dtype, cudaStream_t s);
+
+}  // namespace paged
+}  // namespace lla

@@ -1,0 +1,233 @@
+// C ABI of the paged-cache operators: argument validation, choice of kernels and splits, scratch.
+#include <cmath>
+
+#include "lla_paged.cuh"
+
+namespace lla {
+namespace paged {
+namespace {
+
+bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+bool head_size(int d) { return d == 16 || d == 32 || d == 64 || d == 128; }
+
+// Fields of the cache description that do not depend on pointers.
+int check_cache_shape(const lla_paged_cache* c) {
+  if (!c) return LLA_ERR_INVALID_ARG;
+  if (c->num_seqs < 0 || c->kv_heads <= 0 || c->max_pages < 0 || c->num_pages < 0)
+    return LLA_ERR_INVALID_ARG;
+  if (c->dtype != LLA_F32 && c->dtype != LLA_BF16) return LLA_ERR_INVALID_ARG;
+  for (int r : c->reserved)
+    if (r != 0) return LLA_ERR_INVALID_ARG;
+  if (!head_size(c->d) || !head_size(c->dv)) return LLA_ERR_UNSUPPORTED;
+  if (c->page_size < 16 || c->page_size > 1024 || (c->page_size & (c->page_size - 1)))
+    return LLA_ERR_UNSUPPORTED;
+  if ((long long)c->max_pages * c->page_size >= kNoWindow) return LLA_ERR_UNSUPPORTED;
+  if ((long long)c->num_pages * c->kv_heads >= (1LL << 31)) return LLA_ERR_UNSUPPORTED;
+  if (c->num_seqs > 65535 || c->kv_heads > 65535) return LLA_ERR_UNSUPPORTED;
+  return LLA_OK;
+}
+
+int check_cache_pointers(const lla_paged_cache* c, bool need_mass) {
+  if (!c->k_pages || !c->v_pages || !c->page_table || !c->lens) return LLA_ERR_INVALID_ARG;
+  if (!aligned16(c->k_pages) || !aligned16(c->v_pages)) return LLA_ERR_INVALID_ARG;
+  if (need_mass && !c->mass) return LLA_ERR_INVALID_ARG;
+  return LLA_OK;
+}
+
+Params cache_params(const lla_paged_cache* c) {
+  Params p = {};
+  p.k = c->k_pages;
+  p.v = c->v_pages;
+  p.mass = c->mass;
+  p.table = c->page_table;
+  p.lens = c->lens;
+  p.B = c->num_seqs;
+  p.Hkv = p.Hq = c->kv_heads;
+  p.g = 1;
+  p.page = c->page_size;
+  while ((1 << p.page_shift) < c->page_size) ++p.page_shift;
+  p.max_pages = c->max_pages;
+  p.num_pages = c->num_pages;
+  p.window = kNoWindow;
+  p.split = 1;
+  p.hi = 0x7fffffff;
+  return p;
+}
+
+int check_query(const lla_paged_cache* c, const lla_paged_query* a) {
+  int st = check_cache_shape(c);
+  if (st != LLA_OK) return st;
+  if (!a || a->tokens < 0 || a->max_new < 0 || a->q_heads <= 0 || a->window < 0 || a->sinks < 0)
+    return LLA_ERR_INVALID_ARG;
+  for (int r : a->reserved)
+    if (r != 0) return LLA_ERR_INVALID_ARG;
+  if (!(std::isfinite(a->h) && a->h > 0.f)) return LLA_ERR_INVALID_ARG;
+  if (a->path < LLA_PATH_AUTO || a->path > LLA_PATH_TENSOR_CORE) return LLA_ERR_INVALID_ARG;
+  if (a->q_heads % c->kv_heads != 0) return LLA_ERR_INVALID_ARG;
+  if ((long long)a->tokens * a->q_heads >= (1LL << 31) || a->tokens >= kNoWindow)
+    return LLA_ERR_UNSUPPORTED;
+  return LLA_OK;
+}
+
+constexpr size_t kAlign = 256;
+size_t align_up(size_t x) { return (x + kAlign - 1) / kAlign * kAlign; }
+
+// How one call runs: its splits and scratch.
+struct Plan {
+  int split = 1;
+  size_t part_s = 0, part_o = 0, lse = 0;  // byte offsets
+  size_t bytes = 0;
+};
+
+Plan make_plan(const lla_paged_cache* c, const lla_paged_query* a) {
+  Plan pl;
+  const int g = a->q_heads / c->kv_heads;
+  const long long cap = (long long)c->max_pages * c->page_size;
+  const long long max_new = a->max_new < a->tokens ? a->max_new : a->tokens;
+  const long long reach = a->window ? (long long)a->window + a->sinks + max_new : cap;
+  const long long keys = reach < cap ? reach : cap;
+  const long long rows = max_new * g, BM = rows <= 16 ? 16 : 64;
+  const long long per = g < BM ? BM / g : 1, slices = (g + BM - 1) / BM;
+  const long long tiles = ((a->tokens + per - 1) / per > c->num_seqs ? (a->tokens + per - 1) / per : c->num_seqs) * slices * c->kv_heads;
+  // Few row tiles: their keys are split over blocks, down to 256 keys each, until two waves of
+  // SMs have work.
+  long long split = tiles > 0 ? (304 + tiles - 1) / tiles : 1;
+  if (split > (keys + 255) / 256) split = (keys + 255) / 256;
+  pl.split = split < 1 ? 1 : (int)split;
+  const size_t all = (size_t)a->tokens * a->q_heads;
+  size_t at = 0;
+  if (pl.split > 1) {
+    pl.part_s = at;
+    at += align_up(all * pl.split * sizeof(float4));
+    pl.part_o = at;
+    at += align_up(all * pl.split * (a->r ? 2 : 1) * c->dv * sizeof(float));
+  }
+  if (a->track_mass && !a->lse) {
+    pl.lse = at;
+    at += align_up(all * sizeof(float));
+  }
+  pl.bytes = at;
+  return pl;
+}
+
+int run_attention(const lla_paged_cache* c, const lla_paged_query* a, const Plan& pl, char* ws,
+                  cudaStream_t s) {
+  Params p = cache_params(c);
+  if (device_status(&p.status) != cudaSuccess) return LLA_ERR_CUDA;
+  p.q = a->q;
+  p.r = a->r;
+  p.out = a->out;
+  p.lse = a->lse;
+  p.starts = a->starts;
+  p.tokens = a->tokens;
+  p.Hq = a->q_heads;
+  p.g = a->q_heads / c->kv_heads;
+  p.window = a->window && a->window < kNoWindow ? a->window : kNoWindow;
+  p.sinks = a->sinks < kNoWindow ? a->sinks : kNoWindow;
+  p.inv_h = 1.f / a->h;
+  const long long rows = (long long)a->max_new * p.g;
+  p.max_rows = rows < 0x7fffffffLL ? (int)rows : 0x7fffffff;
+  p.split = pl.split;
+  if (pl.split > 1) {
+    p.part_s = reinterpret_cast<float4*>(ws + pl.part_s);
+    p.part_o = reinterpret_cast<float*>(ws + pl.part_o);
+  }
+  if (a->track_mass && !a->lse) p.lse = reinterpret_cast<float*>(ws + pl.lse);
+  if (launch_attend_cc(p, c->d, c->dv, c->dtype, s) != cudaSuccess) return LLA_ERR_CUDA;
+  if (pl.split > 1 && launch_join(p, c->d, c->dv, c->dtype, s) != cudaSuccess) return LLA_ERR_CUDA;
+  if (a->track_mass && launch_mass_cc(p, c->d, c->dtype, s) != cudaSuccess) return LLA_ERR_CUDA;
+  return LLA_OK;
+}
+
+}  // namespace
+}  // namespace paged
+}  // namespace lla
+
+using namespace lla;
+using namespace lla::paged;
+
+extern "C" {
+
+int lla_paged_append(const lla_paged_cache* cache, const void* k_new, const void* v_new,
+                     const int* starts, int tokens, void* stream) {
+  int st = check_cache_shape(cache);
+  if (st != LLA_OK) return st;
+  if (tokens < 0) return LLA_ERR_INVALID_ARG;
+  if ((long long)tokens * cache->kv_heads >= (1LL << 31) || tokens >= kNoWindow)
+    return LLA_ERR_UNSUPPORTED;
+  if (tokens == 0 || cache->num_seqs == 0) return LLA_OK;
+  st = check_cache_pointers(cache, false);
+  if (st != LLA_OK) return st;
+  if (!k_new || !v_new || !starts || !aligned16(k_new) || !aligned16(v_new)) return LLA_ERR_INVALID_ARG;
+  Params p = cache_params(cache);
+  if (device_status(&p.status) != cudaSuccess) return LLA_ERR_CUDA;
+  p.starts = starts;
+  p.tokens = tokens;
+  return launch_append(p, k_new, v_new, cache->d, cache->dv, cache->dtype,
+                       static_cast<cudaStream_t>(stream)) == cudaSuccess
+             ? LLA_OK
+             : LLA_ERR_CUDA;
+}
+
+size_t lla_paged_workspace_size(const lla_paged_cache* cache, const lla_paged_query* query) {
+  if (check_query(cache, query) != LLA_OK) return 0;
+  if (query->tokens == 0 || cache->num_seqs == 0) return 0;
+  return make_plan(cache, query).bytes;
+}
+
+int lla_paged_attention(const lla_paged_cache* cache, const lla_paged_query* query, void* workspace,
+                        size_t workspace_bytes, void* stream) {
+  int st = check_query(cache, query);
+  if (st != LLA_OK) return st;
+  if (query->tokens == 0 || cache->num_seqs == 0) return LLA_OK;
+  if (query->max_new == 0) return LLA_ERR_INVALID_ARG;
+  st = check_cache_pointers(cache, query->track_mass != 0);
+  if (st != LLA_OK) return st;
+  if (!query->q || !query->out || !query->starts || !aligned16(query->q) || !aligned16(query->out) ||
+      (query->r && !aligned16(query->r)))
+    return LLA_ERR_INVALID_ARG;
+  const Plan pl = make_plan(cache, query);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (workspace || pl.bytes == 0) {
+    if (workspace && ((reinterpret_cast<uintptr_t>(workspace) % 256) != 0 || workspace_bytes < pl.bytes))
+      return LLA_ERR_INVALID_ARG;
+    return run_attention(cache, query, pl, static_cast<char*>(workspace), s);
+  }
+  if (ensure_pool() != cudaSuccess) return LLA_ERR_CUDA;
+  void* ws = nullptr;
+  if (cudaMallocAsync(&ws, pl.bytes, s) != cudaSuccess) return LLA_ERR_CUDA;
+  st = run_attention(cache, query, pl, static_cast<char*>(ws), s);
+  if (cudaFreeAsync(ws, s) != cudaSuccess && st == LLA_OK) st = LLA_ERR_CUDA;
+  return st;
+}
+
+int lla_paged_evict(const lla_paged_cache* from, const lla_paged_cache* to, int budget, int sinks,
+                    int recent, int* kept, void* stream) {
+  int st = check_cache_shape(from);
+  if (st == LLA_OK) st = check_cache_shape(to);
+  if (st != LLA_OK) return st;
+  if (to->num_seqs != from->num_seqs || to->kv_heads != from->kv_heads ||
+      to->page_size != from->page_size || to->d != from->d || to->dv != from->dv ||
+      to->dtype != from->dtype)
+    return LLA_ERR_INVALID_ARG;
+  if (budget < 1 || sinks < 0 || recent < 0 || (long long)sinks + recent > budget)
+    return LLA_ERR_INVALID_ARG;
+  const long long cap = (long long)from->max_pages * from->page_size;
+  if ((budget < cap ? budget : cap) > (long long)to->max_pages * to->page_size)
+    return LLA_ERR_INVALID_ARG;
+  if (from->num_seqs == 0) return LLA_OK;
+  st = check_cache_pointers(from, true);
+  if (st == LLA_OK) st = check_cache_pointers(to, true);
+  if (st != LLA_OK) return st;
+  if (!kept || from->lens == to->lens || from->page_table == to->page_table)
+    return LLA_ERR_INVALID_ARG;
+  Params p = cache_params(from);
+  if (device_status(&p.status) != cudaSuccess) return LLA_ERR_CUDA;
+  return launch_evict(p, to->k_pages, to->v_pages, to->mass, to->page_table, to->lens, to->max_pages,
+                      to->num_pages, budget, sinks, recent, kept, from->d, from->dv, from->dtype,
+                      static_cast<cudaStream_t>(stream)) == cudaSuccess
+             ? LLA_OK
+             : LLA_ERR_CUDA;
+}
+
+}  // extern "C"

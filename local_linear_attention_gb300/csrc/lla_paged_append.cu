@@ -1,0 +1,70 @@
+// Append: the new tokens' keys and values into the slots of a paged cache, their accumulated
+// weight set to zero. Pure data movement, bound by HBM (each byte read once, written once) and,
+// for the few rows of a decode step, by the launch: one launch, 16-byte accesses, one warp per
+// group of rows; a row's slot costs one page-table load, which its lanes share.
+#include "lla_paged.cuh"
+
+namespace lla {
+namespace paged {
+namespace {
+
+// A row is one (token, key/value head): kv = 16-byte words of its key, vv of its value. LPR lanes
+// (a power of two) share a row.
+template <int LPR>
+__global__ void __launch_bounds__(256) append_kernel(Params p, const uint4* __restrict__ kn,
+                                                     const uint4* __restrict__ vn, int kw, int vw) {
+  const long long row = ((long long)blockIdx.x * 256 + threadIdx.x) / LPR;
+  const int l = threadIdx.x % LPR;
+  if (row >= (long long)p.tokens * p.Hkv) return;
+  const int token = (int)(row / p.Hkv), hk = (int)(row % p.Hkv);
+  // The new row does not depend on where it goes: fetched before the searches below.
+  uint4 a[2], c[2];
+  const int na = (kw + LPR - 1 - l) / LPR, nc = (vw + LPR - 1 - l) / LPR;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    if (i < na) a[i] = kn[row * kw + l + i * LPR];
+    if (i < nc) c[i] = vn[row * vw + l + i * LPR];
+  }
+  int b = 0, e = p.B;  // the last sequence with starts[b] <= token
+  while (e - b > 1) {
+    const int mid = (b + e) / 2;
+    if (__ldg(p.starts + mid) <= token) b = mid;
+    else e = mid;
+  }
+  const Seq sq = load_seq(p, b);
+  const int j = sq.first + token - sq.t0;
+  if (token < sq.t0 || token >= sq.t0 + sq.n || j < 0) return;
+  const int pg = load_page(p, b, j >> p.page_shift);
+  if (pg < 0) return;
+  const long long slot = ((long long)pg * p.Hkv + hk) * p.page + (j & (p.page - 1));
+  uint4* kd = static_cast<uint4*>(p.k) + slot * kw;
+  uint4* vd = static_cast<uint4*>(p.v) + slot * vw;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    if (i < na) kd[l + i * LPR] = a[i];
+    if (i < nc) vd[l + i * LPR] = c[i];
+  }
+  if (l == 0 && p.mass) p.mass[slot] = 0.f;
+}
+
+}  // namespace
+
+cudaError_t launch_append(const Params& p, const void* k_new, const void* v_new, int d, int dv,
+                          int dtype, cudaStream_t s) {
+  const int eb = dtype == LLA_F32 ? 4 : 2, kw = d * eb / 16, vw = dv * eb / 16;
+  const int most = kw > vw ? kw : vw;  // 2 .. 32 words; each lane moves at most two of each
+  auto go = [&](auto kern, int lpr) {
+    const long long blocks = ((long long)p.tokens * p.Hkv * lpr + 255) / 256;
+    kern<<<(unsigned)blocks, 256, 0, s>>>(p, static_cast<const uint4*>(k_new),
+                                          static_cast<const uint4*>(v_new), kw, vw);
+  };
+  if (most <= 4) go(append_kernel<2>, 2);
+  else if (most <= 8) go(append_kernel<4>, 4);
+  else if (most <= 16) go(append_kernel<8>, 8);
+  else go(append_kernel<16>, 16);
+  count_launch();
+  return cudaGetLastError();
+}
+
+}  // namespace paged
+}  // namespace lla
