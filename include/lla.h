@@ -366,7 +366,7 @@ int lla_profile_collect(float* stage_ms, int max_stages, int* n_calls);
  *
  * Supported: d, dv in {16, 32, 64, 128}; page_size a power of two in 16 .. 1024; max_pages *
  * page_size < 2^30; tokens < 2^30, tokens * q_heads < 2^31, num_pages * kv_heads < 2^31, num_seqs and kv_heads
- * at most 65535 (LLA_ERR_UNSUPPORTED otherwise). What only the device can see is checked there: a
+ * at most 65535, their product < 2^28 (LLA_ERR_UNSUPPORTED otherwise). What only the device can see is checked there: a
  * page index outside 0 .. num_pages-1, a length beyond the table, or starts that descend or pass
  * `tokens` are recorded in the status word (lla_stream_status: LLA_ERR_INVALID_ARG); nothing out of
  * range is read or written, and the outputs of that sequence are unspecified. Slots that no row
@@ -397,8 +397,8 @@ int lla_paged_append(const lla_paged_cache* cache, const void* k_new, const void
  *               of the cache's type. q_heads is a multiple of kv_heads: query heads hk*g ..
  *               hk*g + g-1 read key/value head hk, g = q_heads / kv_heads.
  *   lse         [tokens, q_heads] fp32 or NULL: log of the sum of exp(q.k/h) over the visible keys.
- *   max_new     at least the largest number of new tokens of a sequence (it sizes the launch; the
- *               rows of a sequence with more are unspecified).
+ *   max_new     at least the largest number of new tokens of a sequence (it sizes the launch; a
+ *               sequence with more may be reported as a bad index, its rows unspecified).
  *   window      0, or how many last positions a token sees, its own included; sinks: the first
  *               positions that stay visible besides. The token at position i sees positions
  *               j <= i with window == 0, j > i - window or j < sinks.

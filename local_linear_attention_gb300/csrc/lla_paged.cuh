@@ -38,9 +38,11 @@ struct Params {
   int lo, hi;         // this launch takes the sequences with lo < rows <= hi
   // Split of each row's keys over blocks, and its partial results (split > 1).
   int split;
-  float* part_o;     // [split][tokens * Hq][nbranch][dv]   unnormalised O1 (and O2)
-  float4* part_s;    // [split][tokens * Hq]   {m, d1, d2, 0} with m the maximum of q.k (raw)
-  float* logits;     // [B][Hkv][row_cap][keys_cap]  raw q.k of the few-rows kernel (weight tracking)
+  float* part_o;     // [split][rows][branches][dv]   unnormalised O1 (and O2)
+  float4* part_s;    // [split][rows]   {m, d1, d2, 0} with m the maximum of q.k (raw)
+                     // rows: tokens * Hq, or B * Hkv * rows_limit of the few-rows kernel
+  float* logits;     // [B * Hkv][row_cap][keys_cap]  raw q.k of the few-rows kernel, by the key's
+                     // place among the visible 16-key steps (weight tracking)
   int row_cap, keys_cap;
 };
 
@@ -223,6 +225,10 @@ inline cudaError_t launch_mass_cc(const Params& p, int d, int dtype, cudaStream_
 inline cudaError_t launch_join(const Params& p, int d, int dv, int dtype, cudaStream_t s) {
   return dtype == LLA_F32 ? join_f32(p, d, dv, s) : join_bf16(p, d, dv, s);
 }
+// Sequences of few rows (p.hi = rows_limit of them at most), bf16 with d = dv = 64 or 128: the
+// attention, the join of its splits and, with p.logits, the weight tracking.
+inline int rows_limit(bool probe) { return probe ? 8 : 16; }
+cudaError_t launch_attend_rows(const Params& p, int d, cudaStream_t s);
 cudaError_t launch_append(const Params& p, const void* k_new, const void* v_new, int d, int dv,
                           int dtype, cudaStream_t s);
 // `p` is the source cache; the other arguments the destination and the choice.

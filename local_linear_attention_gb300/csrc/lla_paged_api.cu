@@ -23,7 +23,8 @@ int check_cache_shape(const lla_paged_cache* c) {
     return LLA_ERR_UNSUPPORTED;
   if ((long long)c->max_pages * c->page_size >= kNoWindow) return LLA_ERR_UNSUPPORTED;
   if ((long long)c->num_pages * c->kv_heads >= (1LL << 31)) return LLA_ERR_UNSUPPORTED;
-  if (c->num_seqs > 65535 || c->kv_heads > 65535) return LLA_ERR_UNSUPPORTED;
+  if (c->num_seqs > 65535 || c->kv_heads > 65535 || (long long)c->num_seqs * c->kv_heads >= (1LL << 28))
+    return LLA_ERR_UNSUPPORTED;
   return LLA_OK;
 }
 
@@ -72,10 +73,13 @@ int check_query(const lla_paged_cache* c, const lla_paged_query* a) {
 constexpr size_t kAlign = 256;
 size_t align_up(size_t x) { return (x + kAlign - 1) / kAlign * kAlign; }
 
-// How one call runs: its splits and scratch.
+// How one call runs: the kernels it takes, their splits and scratch (byte offsets).
 struct Plan {
-  int split = 1;
-  size_t part_s = 0, part_o = 0, lse = 0;  // byte offsets
+  bool rows = false;   // the few-rows kernel takes the sequences of at most rows_limit rows
+  bool tiles = false;  // the tiled kernel the others
+  int rows_split = 1, tiles_split = 1;
+  int row_cap = 0, keys_cap = 0;
+  size_t rows_s = 0, rows_o = 0, logits = 0, tiles_s = 0, tiles_o = 0, lse = 0;
   size_t bytes = 0;
 };
 
@@ -85,27 +89,47 @@ Plan make_plan(const lla_paged_cache* c, const lla_paged_query* a) {
   const long long cap = (long long)c->max_pages * c->page_size;
   const long long max_new = a->max_new < a->tokens ? a->max_new : a->tokens;
   const long long reach = a->window ? (long long)a->window + a->sinks + max_new : cap;
-  const long long keys = reach < cap ? reach : cap;
-  const long long rows = max_new * g, BM = rows <= 16 ? 16 : 64;
-  const long long per = g < BM ? BM / g : 1, slices = (g + BM - 1) / BM;
-  const long long tiles = ((a->tokens + per - 1) / per > c->num_seqs ? (a->tokens + per - 1) / per : c->num_seqs) * slices * c->kv_heads;
-  // Few row tiles: their keys are split over blocks, down to 256 keys each, until two waves of
-  // SMs have work.
-  long long split = tiles > 0 ? (304 + tiles - 1) / tiles : 1;
-  if (split > (keys + 255) / 256) split = (keys + 255) / 256;
-  pl.split = split < 1 ? 1 : (int)split;
-  const size_t all = (size_t)a->tokens * a->q_heads;
+  const long long keys = reach < cap ? reach : cap;  // most keys that a row may see
+  const long long rows = max_new * g, pairs = (long long)c->num_seqs * c->kv_heads;
+  const bool tc = c->dtype == LLA_BF16 && c->d == c->dv && c->d >= 64 && a->path != LLA_PATH_CUDA_CORE;
+  const int limit = rows_limit(a->r != nullptr);
+  const int branches = a->r ? 2 : 1;
+  pl.rows = tc && g <= limit;
+  pl.tiles = !pl.rows || rows > limit;
   size_t at = 0;
-  if (pl.split > 1) {
-    pl.part_s = at;
-    at += align_up(all * pl.split * sizeof(float4));
-    pl.part_o = at;
-    at += align_up(all * pl.split * (a->r ? 2 : 1) * c->dv * sizeof(float));
+  auto take = [&](size_t bytes) { const size_t o = at; at += align_up(bytes); return o; };
+  auto splits = [&](long long blocks, long long want, long long least) {
+    long long n = blocks > 0 ? (want + blocks - 1) / blocks : 1;
+    if (n > keys / least) n = keys / least;
+    return n < 1 ? 1 : n > 512 ? 512 : (int)n;
+  };
+  if (pl.rows) {
+    pl.row_cap = (int)(rows < limit ? rows : limit);
+    // Blocks of 4 warps, 2 (d = 128) or 3 (d = 64) resident on each of 152 SMs: a wave or two of
+    // them, but no block with fewer than 256 keys (its start and join would cost more).
+    pl.rows_split = splits(pairs, c->d == 128 ? 608 : 912, 256);
+    if (pl.rows_split > 1) {
+      pl.rows_s = take((size_t)pairs * limit * pl.rows_split * sizeof(float4));
+      pl.rows_o = take((size_t)pairs * limit * pl.rows_split * branches * c->dv * sizeof(float));
+    }
+    if (a->track_mass) {
+      pl.keys_cap = (int)((keys + 64 < cap ? keys + 64 : cap) + 15) / 16 * 16;
+      pl.logits = take((size_t)pairs * pl.row_cap * pl.keys_cap * sizeof(float));
+    }
   }
-  if (a->track_mass && !a->lse) {
-    pl.lse = at;
-    at += align_up(all * sizeof(float));
+  if (pl.tiles) {
+    const long long BM = rows <= 16 ? 16 : 64;
+    const long long per = g < BM ? BM / g : 1, slices = (g + BM - 1) / BM;
+    const long long by_tokens = (a->tokens + per - 1) / per;
+    const long long tiles = (by_tokens > c->num_seqs ? by_tokens : c->num_seqs) * slices * c->kv_heads;
+    pl.tiles_split = splits(tiles, 304, 256);
+    if (pl.tiles_split > 1) {
+      const size_t all = (size_t)a->tokens * a->q_heads * pl.tiles_split;
+      pl.tiles_s = take(all * sizeof(float4));
+      pl.tiles_o = take(all * branches * c->dv * sizeof(float));
+    }
   }
+  if (a->track_mass && !a->lse) pl.lse = take((size_t)a->tokens * a->q_heads * sizeof(float));
   pl.bytes = at;
   return pl;
 }
@@ -127,15 +151,34 @@ int run_attention(const lla_paged_cache* c, const lla_paged_query* a, const Plan
   p.inv_h = 1.f / a->h;
   const long long rows = (long long)a->max_new * p.g;
   p.max_rows = rows < 0x7fffffffLL ? (int)rows : 0x7fffffff;
-  p.split = pl.split;
-  if (pl.split > 1) {
-    p.part_s = reinterpret_cast<float4*>(ws + pl.part_s);
-    p.part_o = reinterpret_cast<float*>(ws + pl.part_o);
-  }
   if (a->track_mass && !a->lse) p.lse = reinterpret_cast<float*>(ws + pl.lse);
-  if (launch_attend_cc(p, c->d, c->dv, c->dtype, s) != cudaSuccess) return LLA_ERR_CUDA;
-  if (pl.split > 1 && launch_join(p, c->d, c->dv, c->dtype, s) != cudaSuccess) return LLA_ERR_CUDA;
-  if (a->track_mass && launch_mass_cc(p, c->d, c->dtype, s) != cudaSuccess) return LLA_ERR_CUDA;
+  if (pl.rows) {
+    Params f = p;
+    f.lo = 0;
+    f.hi = pl.row_cap;
+    f.split = pl.rows_split;
+    f.row_cap = pl.row_cap;
+    if (pl.rows_split > 1) {
+      f.part_s = reinterpret_cast<float4*>(ws + pl.rows_s);
+      f.part_o = reinterpret_cast<float*>(ws + pl.rows_o);
+    }
+    if (a->track_mass) {
+      f.keys_cap = pl.keys_cap;
+      f.logits = reinterpret_cast<float*>(ws + pl.logits);
+    }
+    if (launch_attend_rows(f, c->d, s) != cudaSuccess) return LLA_ERR_CUDA;
+  }
+  if (pl.tiles) {
+    p.lo = pl.rows ? pl.row_cap : 0;
+    p.split = pl.tiles_split;
+    if (p.split > 1) {
+      p.part_s = reinterpret_cast<float4*>(ws + pl.tiles_s);
+      p.part_o = reinterpret_cast<float*>(ws + pl.tiles_o);
+    }
+    if (launch_attend_cc(p, c->d, c->dv, c->dtype, s) != cudaSuccess) return LLA_ERR_CUDA;
+    if (p.split > 1 && launch_join(p, c->d, c->dv, c->dtype, s) != cudaSuccess) return LLA_ERR_CUDA;
+    if (a->track_mass && launch_mass_cc(p, c->d, c->dtype, s) != cudaSuccess) return LLA_ERR_CUDA;
+  }
   return LLA_OK;
 }
 
