@@ -229,6 +229,8 @@ inline cudaError_t launch_join(const Params& p, int d, int dv, int dtype, cudaSt
 // attention, the join of its splits and, with p.logits, the weight tracking.
 inline int rows_limit(bool probe) { return probe ? 8 : 16; }
 cudaError_t launch_attend_rows(const Params& p, int d, cudaStream_t s);
+// Sequences of many rows, bf16 with d = dv = 64 or 128 and g <= 128.
+cudaError_t launch_attend_tc(const Params& p, int d, cudaStream_t s);
 cudaError_t launch_append(const Params& p, const void* k_new, const void* v_new, int d, int dv,
                           int dtype, cudaStream_t s);
 // `p` is the source cache; the other arguments the destination and the choice.

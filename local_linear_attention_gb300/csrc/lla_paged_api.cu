@@ -76,7 +76,8 @@ size_t align_up(size_t x) { return (x + kAlign - 1) / kAlign * kAlign; }
 // How one call runs: the kernels it takes, their splits and scratch (byte offsets).
 struct Plan {
   bool rows = false;   // the few-rows kernel takes the sequences of at most rows_limit rows
-  bool tiles = false;  // the tiled kernel the others
+  bool tiles = false;  // a tiled kernel the others: tensor cores (tc) or CUDA cores
+  bool tc = false;
   int rows_split = 1, tiles_split = 1;
   int row_cap = 0, keys_cap = 0;
   size_t rows_s = 0, rows_o = 0, logits = 0, tiles_s = 0, tiles_o = 0, lse = 0;
@@ -118,8 +119,9 @@ Plan make_plan(const lla_paged_cache* c, const lla_paged_query* a) {
     }
   }
   if (pl.tiles) {
-    const long long BM = rows <= 16 ? 16 : 64;
-    const long long per = g < BM ? BM / g : 1, slices = (g + BM - 1) / BM;
+    pl.tc = tc && g <= 128;
+    const long long BM = pl.tc ? (a->r ? 128 : 256) : rows <= 16 ? 16 : 64;
+    const long long per = pl.tc ? 128 / g * (a->r ? 1 : 2) : g < BM ? BM / g : 1, slices = (g + BM - 1) / BM;
     const long long by_tokens = (a->tokens + per - 1) / per;
     const long long tiles = (by_tokens > c->num_seqs ? by_tokens : c->num_seqs) * slices * c->kv_heads;
     pl.tiles_split = splits(tiles, 304, 256);
@@ -175,7 +177,8 @@ int run_attention(const lla_paged_cache* c, const lla_paged_query* a, const Plan
       p.part_s = reinterpret_cast<float4*>(ws + pl.tiles_s);
       p.part_o = reinterpret_cast<float*>(ws + pl.tiles_o);
     }
-    if (launch_attend_cc(p, c->d, c->dv, c->dtype, s) != cudaSuccess) return LLA_ERR_CUDA;
+    if ((pl.tc ? launch_attend_tc(p, c->d, s) : launch_attend_cc(p, c->d, c->dv, c->dtype, s)) != cudaSuccess)
+      return LLA_ERR_CUDA;
     if (p.split > 1 && launch_join(p, c->d, c->dv, c->dtype, s) != cudaSuccess) return LLA_ERR_CUDA;
     if (a->track_mass && launch_mass_cc(p, c->d, c->dtype, s) != cudaSuccess) return LLA_ERR_CUDA;
   }
