@@ -180,7 +180,8 @@ int run_attention(const lla_paged_cache* c, const lla_paged_query* a, const Plan
     if ((pl.tc ? launch_attend_tc(p, c->d, s) : launch_attend_cc(p, c->d, c->dv, c->dtype, s)) != cudaSuccess)
       return LLA_ERR_CUDA;
     if (p.split > 1 && launch_join(p, c->d, c->dv, c->dtype, s) != cudaSuccess) return LLA_ERR_CUDA;
-    if (a->track_mass && launch_mass_cc(p, c->d, c->dtype, s) != cudaSuccess) return LLA_ERR_CUDA;
+    if (a->track_mass && (pl.tc ? launch_mass_tc(p, c->d, s) : launch_mass_cc(p, c->d, c->dtype, s)) != cudaSuccess)
+      return LLA_ERR_CUDA;
   }
   return LLA_OK;
 }

@@ -1,0 +1,300 @@
+// Weight tracking of sequences with many rows, bf16, d = 64 or 128, on the tensor cores:
+//   mass[j] += sum over the rows i that see key j of exp(q_i.k_j / h - lse_i),
+// from the finished lse. The product is taken transposed, S^T = K Q^T (128 keys x 128 rows in
+// tensor memory, a thread per key), so that a key's sum runs along a thread's registers: no
+// shuffles, no atomics, and a CTA that owns its keys adds its row blocks up in one fixed order.
+// What bounds it: the exponentials, one per (row, key) pair (16 a cycle and SM); the product is
+// half as long. Two CTAs a SM (two score buffers each) hide each other's waits.
+// An item is a 128-key tile of one key/value head; CTAs take items in turn (their number depends on
+// the lengths, which only the device knows). Warps 0-3 and 4-7: two consumer groups, alternate row
+// blocks; 8: TMA loader (keys by page fragment; queries as [per tokens][g heads] boxes, rows in the
+// order token * g + head); 9: MMA issuer. All mbarrier waits are bounded.
+#include "lla_paged.cuh"
+#include "lla_tc_ptx.cuh"
+#include "lla_tmap.cuh"
+
+namespace lla {
+namespace paged {
+namespace {
+
+using namespace tc;
+
+constexpr int KT = 128, BR = 128;
+constexpr int NTHREADS = 320;
+constexpr float kLog2e = 1.4426950408889634f;
+
+template <int D>
+struct Cfg {
+  static constexpr int tile = KT * D * 2;
+  static constexpr int sm_q = tile;                  // two stages of row blocks
+  static constexpr int sm_lse = 3 * tile;            // [8 warps][128] lse * log2(e)
+  static constexpr int sm_sum = sm_lse + 8 * BR * 4; // [2][2 groups][128]
+  static constexpr int sm_bar = sm_sum + 2 * 2 * KT * 4;
+  static constexpr int bytes = sm_bar + 128 + 1024;
+};
+static_assert(2 * (Cfg<128>::bytes + 1024) <= 227 * 1024, "two CTAs a SM");
+
+struct Barriers {
+  uint64_t kfull, qfull[2], qempty[2], sfull[2], sfree[2], done;
+};
+static_assert(sizeof(Barriers) <= 128, "barrier region");
+
+__device__ __forceinline__ float ex2(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
+// Key tile `x` of this launch's sequences (as find_tile, over keys).
+__device__ __forceinline__ bool find_keys(const Params& p, int x, int* b_out, int* tile_out) {
+  const int lane = threadIdx.x & 31, cap = p.max_pages << p.page_shift;
+  int before = 0;
+  for (int base = 0; base < p.B; base += 32) {
+    const int b = base + lane;
+    int cnt = 0;
+    if (b < p.B) {
+      const int t0 = p.starts[b], t1 = p.starts[b + 1];
+      if (t0 >= 0 && t1 > t0 && t1 <= p.tokens && mine(p, t1 - t0))
+        cnt = (min(max(p.lens[b], 0), cap) + KT - 1) / KT;
+    }
+    int incl = cnt;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += y;
+    }
+    const unsigned hit = __ballot_sync(0xffffffffu, x < before + incl);
+    if (hit) {
+      const int l = __ffs(hit) - 1;
+      const int upto = __shfl_sync(0xffffffffu, incl, l), c = __shfl_sync(0xffffffffu, cnt, l);
+      *b_out = base + l;
+      *tile_out = x - (before + upto - c);  // the first keys of a prompt have the most rows: first
+      return true;
+    }
+    before += __shfl_sync(0xffffffffu, incl, 31);
+  }
+  return false;
+}
+
+template <int D>
+__global__ void __launch_bounds__(NTHREADS, 2)
+mass_tc_kernel(Params p, const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap qmap) {
+  using C = Cfg<D>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  Barriers& bar = *reinterpret_cast<Barriers*>(smem + C::sm_bar);
+  __shared__ uint32_t tmem_base_s;
+  __shared__ int abort_flag;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int per = BR / p.g, width = per * p.g;  // tokens and rows of a block
+  int* const status = p.status;
+  constexpr int TO = kStatusTimeout;
+
+  // The rows past `width` of the row-block stages are never loaded: zeros.
+  for (int e = tid; e < 2 * (D / 64) * (BR - width) * 8; e += NTHREADS) {
+    const int c = e & 7, row = width + (e >> 3) % (BR - width), half = (e >> 3) / (BR - width);
+    *reinterpret_cast<uint4*>(smem + C::sm_q + half * 16384 + row * 128 + c * 16) = make_uint4(0u, 0u, 0u, 0u);
+  }
+  if (tid == 0) {
+    mbar_init(&bar.kfull, 1);
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&bar.qfull[s], 1);
+      mbar_init(&bar.qempty[s], 1);
+      mbar_init(&bar.sfull[s], 1);
+      mbar_init(&bar.sfree[s], 4);
+    }
+    mbar_init(&bar.done, 1);
+    abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 9) {
+    tmem_alloc(&tmem_base_s, 256);
+    tmem_relinquish();
+  }
+  fence_proxy_async_smem();
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tbase = tmem_base_s;
+  volatile int* abort_p = &abort_flag;
+
+  int done = 0, items = 0;  // row blocks and items so far (every thread counts the same)
+  bool used = false;
+  for (int x = blockIdx.x;; x += gridDim.x) {
+    int b, tile;
+    if (!find_keys(p, x / p.Hkv, &b, &tile)) break;
+    const int hk = x % p.Hkv;
+    const Seq sq = load_seq(p, b);
+    const int k0 = tile * KT;
+    // blocks of rows that see any of these keys
+    const int from = max(0, k0 - sq.first) / per;
+    int last = sq.n - 1;
+    if (k0 >= p.sinks) last = (int)min((long long)last, (long long)k0 + KT - 2 + p.window - sq.first);
+    const int nblk = last < 0 ? 0 : last / per - from + 1;
+    if (nblk <= 0) continue;
+    used = true;
+
+    if (warp == 9) {
+      if (lane == 0) {
+        const uint64_t kd = smem_desc_sw128(smem_u32(smem), 1024);
+        const uint64_t qd = smem_desc_sw128(smem_u32(smem + C::sm_q), 1024);
+        constexpr uint32_t id = idesc_bf16(KT, BR, false, false);
+        bool ok = mbar_wait(&bar.kfull, items & 1, status, TO, abort_p);
+        for (int i = 0; i < nblk && ok; ++i) {
+          const int c = done + i, st = c & 1;
+          ok = mbar_wait(&bar.qfull[st], (c >> 1) & 1, status, TO, abort_p) &&
+               (c < 2 || mbar_wait(&bar.sfree[st], ((c >> 1) - 1) & 1, status, TO, abort_p));
+          if (!ok) break;
+          tc_fence_after();
+#pragma unroll
+          for (int s = 0; s < D / 16; ++s) {
+            const uint32_t o = (s >> 2) * 1024 + (s & 3) * 2;
+            mma_ss(tbase + st * BR, kd + o, qd + (uint64_t)(st * (C::tile >> 4)) + o, id, s > 0);
+          }
+          mma_commit(&bar.sfull[st]);
+          mma_commit(&bar.qempty[st]);
+        }
+        if (!ok) *abort_p = 1;
+      }
+      __syncwarp();
+    } else if (warp == 8) {
+      const int frag = min(p.page, KT), nfrag = KT / frag;
+      const int j = k0 + lane * frag;
+      int c2 = p.num_pages * p.Hkv;  // out of range: zeros
+      if (lane < nfrag && j < sq.len) {
+        const int pg = load_page(p, b, j >> p.page_shift);
+        if (pg >= 0) c2 = pg * p.Hkv + hk;
+      }
+      if (lane == 0) mbar_arrive_expect_tx(&bar.kfull, C::tile);
+      __syncwarp();
+      if (lane < nfrag)
+        for (int c = 0; c < D / 64; ++c)
+          tma_load_3d(smem + c * 16384 + lane * frag * 128, &kmap, c * 64, j & (p.page - 1), c2, &bar.kfull);
+      if (lane == 0) {
+        int issued = 0;
+        for (int i = 0; i < nblk; ++i) {
+          const int c = done + i, st = c & 1;
+          if (c >= 2 && !mbar_wait(&bar.qempty[st], ((c >> 1) - 1) & 1, status, TO, abort_p)) break;
+          mbar_arrive_expect_tx(&bar.qfull[st], width * D * 2);
+          for (int h = 0; h < D / 64; ++h)
+            tma_load_3d(smem + C::sm_q + st * C::tile + h * 16384, &qmap, h * 64, hk * p.g,
+                        sq.t0 + (from + i) * per, &bar.qfull[st]);
+          issued = i + 1;
+        }
+        // the copies of this item have landed before the CTA goes on (or leaves)
+        volatile int never = 0;
+        mbar_wait(&bar.kfull, items & 1, status, TO, &never);
+        for (int i = max(0, issued - 2); i < issued; ++i) {
+          const int c = done + i;
+          mbar_wait(&bar.qfull[c & 1], (c >> 1) & 1, status, TO, &never);
+        }
+      }
+      __syncwarp();
+    } else {
+      const int grp = warp >> 2, r = (warp & 3) * 32 + lane;
+      const uint32_t lanes = tbase + ((uint32_t)((warp & 3) * 32) << 16);
+      float* const lse = reinterpret_cast<float*>(smem + C::sm_lse) + warp * BR;
+      const float c2 = p.inv_h * kLog2e;
+      const int j = k0 + r;
+      float got = 0.f;
+      for (int i = (done ^ grp) & 1; i < nblk; i += 2) {  // block counts of this group's parity
+        const int c = done + i, tok0 = (from + i) * per;
+        // this block's lse (the warp's own copy)
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const int row = u * 32 + lane, t = tok0 + row / p.g;
+          lse[row] = row < width && t < sq.n
+                         ? p.lse[(long long)(sq.t0 + t) * p.Hq + hk * p.g + row % p.g] * kLog2e
+                         : CUDART_INF_F;
+        }
+        __syncwarp();
+        if (!warp_wait(&bar.sfull[grp], (c >> 1) & 1, status, TO, abort_p)) break;
+        tc_fence_after();
+        const int p0 = sq.first + tok0, p1 = p0 + per - 1;
+        const bool full = width == BR && tok0 + per <= sq.n && all_visible(p, p0, p1, k0, k0 + KT);
+        int pos = p0, u = 0;
+#pragma unroll 1
+        for (int cc = 0; cc < BR; cc += 32) {
+          uint32_t s[32];
+          tmem_ld32(lanes + grp * BR + cc, s);
+          tmem_ld_wait();
+          float a[4] = {};
+          if (full) {
+#pragma unroll
+            for (int e = 0; e < 32; e += 4) {
+              const float4 l = *reinterpret_cast<const float4*>(lse + cc + e);
+              a[0] += ex2(fmaf(__uint_as_float(s[e]), c2, -l.x));
+              a[1] += ex2(fmaf(__uint_as_float(s[e + 1]), c2, -l.y));
+              a[2] += ex2(fmaf(__uint_as_float(s[e + 2]), c2, -l.z));
+              a[3] += ex2(fmaf(__uint_as_float(s[e + 3]), c2, -l.w));
+            }
+          } else {
+#pragma unroll
+            for (int e = 0; e < 32; ++e) {
+              const bool row = cc + e < width && pos - sq.first < sq.n;
+              if (row && visible(p, pos, j)) a[e & 3] += ex2(fmaf(__uint_as_float(s[e]), c2, -lse[cc + e]));
+              if (++u == p.g) { u = 0; ++pos; }
+            }
+          }
+          got += (a[0] + a[1]) + (a[2] + a[3]);
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bar.sfree[grp]);
+      }
+      reinterpret_cast<float*>(smem + C::sm_sum)[((items & 1) * 2 + grp) * KT + r] = got;
+    }
+    __syncthreads();  // the item's sums are there, its scores have been read
+    if (*abort_p) break;
+    if (tid < KT && k0 + tid < sq.len) {
+      const float* sum = reinterpret_cast<const float*>(smem + C::sm_sum) + (items & 1) * 2 * KT;
+      const int j = k0 + tid, pg = load_page(p, b, j >> p.page_shift);
+      if (pg >= 0) p.mass[((long long)pg * p.Hkv + hk) * p.page + (j & (p.page - 1))] += sum[tid] + sum[KT + tid];
+    }
+    done += nblk;
+    ++items;
+  }
+  if (warp == 9 && lane == 0 && used) {
+    mma_commit(&bar.done);
+    volatile int never = 0;
+    mbar_wait(&bar.done, 0, status, TO, &never);
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 9) {
+    tc_fence_after();
+    tmem_dealloc(tbase, 256);
+  }
+}
+
+template <int D>
+cudaError_t launch_t(const Params& p, cudaStream_t s) {
+  CUtensorMap kmap, qmap;
+  cudaError_t err = encode_page_map(p, p.k, D, &kmap);
+  if (err != cudaSuccess) return err;
+  auto encode = tensor_map_encoder();
+  const cuuint32_t ones[3] = {1, 1, 1};
+  const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)p.Hq, (cuuint64_t)p.tokens};
+  const cuuint64_t str[2] = {(cuuint64_t)D * 2, (cuuint64_t)p.Hq * D * 2};
+  const cuuint32_t box[3] = {64, (cuuint32_t)p.g, (cuuint32_t)(BR / p.g)};
+  if (encode(&qmap, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(p.q), dims, str, box, ones,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+    return cudaErrorInvalidValue;
+  auto kern = mass_tc_kernel<D>;
+  err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D>::bytes);
+  if (err != cudaSuccess) return err;
+  const long long most = ((((long long)p.max_pages << p.page_shift) + KT - 1) / KT) * p.B * p.Hkv;
+  kern<<<(unsigned)(most < 304 ? most : 304), NTHREADS, Cfg<D>::bytes, s>>>(p, kmap, qmap);
+  count_launch();
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_mass_tc(const Params& p, int d, cudaStream_t s) {
+  return d == 128 ? launch_t<128>(p, s) : launch_t<64>(p, s);
+}
+
+}  // namespace paged
+}  // namespace lla

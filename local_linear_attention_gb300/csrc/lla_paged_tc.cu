@@ -460,27 +460,11 @@ attend_tc_kernel(Params p, const __grid_constant__ CUtensorMap kmap,
   }
 }
 
-// Tensor maps of the pages ([num_pages * Hkv][page][d] bf16; boxes of one page fragment x 64
-// features, 128-byte swizzled).
-cudaError_t page_maps(const Params& p, int d, CUtensorMap* kmap, CUtensorMap* vmap) {
-  auto encode = tensor_map_encoder();
-  if (!encode) return cudaErrorNotSupported;
-  const cuuint32_t ones[3] = {1, 1, 1};
-  const cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)p.page, (cuuint64_t)p.num_pages * p.Hkv};
-  const cuuint64_t str[2] = {(cuuint64_t)d * 2, (cuuint64_t)p.page * d * 2};
-  const cuuint32_t box[3] = {64, (cuuint32_t)(p.page < KT ? p.page : KT), 1};
-  for (int t = 0; t < 2; ++t)
-    if (encode(t ? vmap : kmap, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, t ? p.v : p.k, dims, str, box, ones,
-               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
-      return cudaErrorInvalidValue;
-  return cudaSuccess;
-}
-
 template <int D, bool PROBE>
 cudaError_t launch_tc_t(const Params& p, cudaStream_t s) {
   CUtensorMap kmap, vmap;
-  cudaError_t err = page_maps(p, D, &kmap, &vmap);
+  cudaError_t err = encode_page_map(p, p.k, D, &kmap);
+  if (err == cudaSuccess) err = encode_page_map(p, p.v, D, &vmap);
   if (err != cudaSuccess) return err;
   auto kern = attend_tc_kernel<D, PROBE>;
   err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D>::bytes);
@@ -494,6 +478,22 @@ cudaError_t launch_tc_t(const Params& p, cudaStream_t s) {
 }
 
 }  // namespace
+
+// Tensor map of the pages ([num_pages * Hkv][page][d] bf16; boxes of one page fragment x 64
+// features, 128-byte swizzled).
+cudaError_t encode_page_map(const Params& p, void* pages, int d, CUtensorMap* map) {
+  auto encode = tensor_map_encoder();
+  if (!encode) return cudaErrorNotSupported;
+  const cuuint32_t ones[3] = {1, 1, 1};
+  const cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)p.page, (cuuint64_t)p.num_pages * p.Hkv};
+  const cuuint64_t str[2] = {(cuuint64_t)d * 2, (cuuint64_t)p.page * d * 2};
+  const cuuint32_t box[3] = {64, (cuuint32_t)(p.page < 128 ? p.page : 128), 1};
+  return encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, pages, dims, str, box, ones,
+                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
+             ? cudaSuccess
+             : cudaErrorInvalidValue;
+}
 
 cudaError_t launch_attend_tc(const Params& p, int d, cudaStream_t s) {
   if (p.r) return d == 128 ? launch_tc_t<128, true>(p, s) : launch_tc_t<64, true>(p, s);
