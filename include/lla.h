@@ -358,7 +358,8 @@ int lla_profile_collect(float* stage_ms, int max_stages, int* n_calls);
  * weight that each slot has received so far. Position j of sequence b is slot j % page_size of page
  * page_table[b * max_pages + j / page_size]; lens[b] (0 .. max_pages * page_size) counts the
  * sequence's positions. Pages may come in any order and may be shared by sequences that only read
- * them. All pointers are device memory; k_pages, v_pages 16-byte aligned.
+ * them. All pointers are device memory; k_pages, v_pages and mass 16-byte
+ * aligned.
  *
  * New tokens of all sequences lie one after the other, as [tokens, heads, size] rows: sequence b's
  * are starts[b] .. starts[b+1]-1 (device memory, [num_seqs + 1], ascending, at most `tokens`), and
@@ -405,6 +406,7 @@ int lla_paged_append(const lla_paged_cache* cache, const void* k_new, const void
  *   track_mass  nonzero: cache->mass of every visible slot grows by the softmax weights that the
  *               new tokens' rows give it, summed over the tokens and the g heads (with a probe too:
  *               its signed correction is not counted). The sums do not depend on scheduling.
+ *               Sequences that track may not share pages (their sums would be lost).
  *   path        lla_path: AUTO, CUDA_CORE or TENSOR_CORE.
  */
 typedef struct lla_paged_query {

@@ -19,5 +19,6 @@ _BINDING = {
 def __getattr__(name):
     if name in _BINDING:
         from . import binding
-        return getattr(binding, name)
+        globals()[name] = getattr(binding, name)  # found without this function from now on
+        return globals()[name]
     raise AttributeError(name)

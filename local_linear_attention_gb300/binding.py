@@ -9,6 +9,7 @@ from __future__ import annotations
 import contextlib
 import ctypes
 import os
+import struct
 
 import torch
 
@@ -56,19 +57,10 @@ class Options(ctypes.Structure):
                 ("reserved", ctypes.c_int * 3)]
 
 
-class _CacheStruct(ctypes.Structure):
-    """lla_paged_cache."""
-    _fields_ = [(n, ctypes.c_void_p) for n in ("k_pages", "v_pages", "mass", "page_table", "lens")] + \
-        [(n, ctypes.c_int) for n in ("num_seqs", "kv_heads", "page_size", "max_pages", "num_pages",
-                                     "d", "dv", "dtype")] + [("reserved", ctypes.c_int * 2)]
-
-
-class _QueryStruct(ctypes.Structure):
-    """lla_paged_query."""
-    _fields_ = [(n, ctypes.c_void_p) for n in ("q", "r", "out", "lse", "starts")] + \
-        [(n, ctypes.c_int) for n in ("tokens", "max_new", "q_heads")] + [("h", ctypes.c_float)] + \
-        [(n, ctypes.c_int) for n in ("window", "sinks", "track_mass", "path")] + \
-        [("reserved", ctypes.c_int * 2)]
+# lla_paged_cache and lla_paged_query, packed in native alignment: a decode step makes these calls
+# once per layer, and struct.pack takes a third of the time of a ctypes.Structure.
+_CACHE = struct.Struct("@5P10i")
+_QUERY = struct.Struct("@5P3if6i")
 
 
 def _options(path=0, form=0, cg=None, test_fault=0):
@@ -127,10 +119,10 @@ def _load():
         "lla_decode_ex": (i, [vp, vp, vp, vp, i, i, i, i, i, f, f, i, op, vp]),
         "lla_parallax_decode_ex": (i, [vp, vp, vp, vp, vp, i, i, i, i, i, f, i, op, vp]),
         "lla_parallax_backward_ex": (i, [vp] * 9 + [i, i, i, i, i, f, i, op, vp]),
-        "lla_paged_append": (i, [ctypes.POINTER(_CacheStruct), vp, vp, vp, i, vp]),
-        "lla_paged_workspace_size": (sz, [ctypes.POINTER(_CacheStruct), ctypes.POINTER(_QueryStruct)]),
-        "lla_paged_attention": (i, [ctypes.POINTER(_CacheStruct), ctypes.POINTER(_QueryStruct), vp, sz, vp]),
-        "lla_paged_evict": (i, [ctypes.POINTER(_CacheStruct), ctypes.POINTER(_CacheStruct), i, i, i, vp, vp]),
+        "lla_paged_append": (i, [vp, vp, vp, vp, i, vp]),
+        "lla_paged_workspace_size": (sz, [vp, vp]),
+        "lla_paged_attention": (i, [vp, vp, vp, sz, vp]),
+        "lla_paged_evict": (i, [vp, vp, i, i, i, vp, vp]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -381,85 +373,90 @@ class PagedCache:
     the cache keeps references, and whoever writes new lengths or page numbers into them changes
     what later calls see. `page_table` may be a row range of a larger table."""
 
-    __slots__ = ("k_pages", "v_pages", "page_table", "lens", "mass", "_struct", "_ref", "_device")
+    __slots__ = ("k_pages", "v_pages", "page_table", "lens", "mass", "num_seqs", "kv_heads", "d", "dv",
+                 "dtype", "device", "_packed", "_index")
 
     def __init__(self, k_pages, v_pages, page_table, lens, mass=None):
-        if k_pages.dim() != 4 or v_pages.dim() != 4 or v_pages.shape[:3] != k_pages.shape[:3]:
+        k_shape, v_shape, t_shape = k_pages.shape, v_pages.shape, page_table.shape
+        if len(k_shape) != 4 or len(v_shape) != 4 or v_shape[:3] != k_shape[:3]:
             raise ValueError("expected k_pages [num_pages, kv_heads, page_size, d] and v_pages "
                              "[num_pages, kv_heads, page_size, dv]")
-        if k_pages.dtype != v_pages.dtype or k_pages.dtype not in DTYPE_CODES:
+        dtype, device = k_pages.dtype, k_pages.device
+        if v_pages.dtype != dtype or dtype not in DTYPE_CODES:
             raise ValueError("k_pages and v_pages must share one dtype: float32 or bfloat16")
-        if page_table.dim() != 2 or page_table.dtype != torch.int32:
+        if len(t_shape) != 2 or page_table.dtype != torch.int32:
             raise ValueError("page_table must be int32 [num_seqs, max_pages]")
-        if lens.dim() != 1 or lens.dtype != torch.int32 or lens.shape[0] != page_table.shape[0]:
+        if lens.dtype != torch.int32 or lens.shape != t_shape[:1]:
             raise ValueError("lens must be int32 [num_seqs]")
-        if mass is not None and (mass.shape != k_pages.shape[:3] or mass.dtype != torch.float32):
+        if mass is not None and (mass.shape != k_shape[:3] or mass.dtype != torch.float32):
             raise ValueError("mass must be float32 [num_pages, kv_heads, page_size]")
-        device = k_pages.device
         for t in (k_pages, v_pages, page_table, lens) if mass is None else \
                 (k_pages, v_pages, page_table, lens, mass):
-            if not t.is_cuda or t.device != device or not t.is_contiguous():
-                raise ValueError("the cache's tensors must be contiguous, on one CUDA device")
-        num_pages, kv_heads, page, d = k_pages.shape
+            if t.device != device or not t.is_contiguous():
+                raise ValueError("the cache's tensors must be contiguous, on one device")
+        if device.type != "cuda":
+            raise ValueError("liblla runs on CUDA tensors only")
+        num_pages, self.kv_heads, page, self.d = k_shape
+        self.num_seqs, max_pages = t_shape
+        self.dv = v_shape[3]
         self.k_pages, self.v_pages, self.mass = k_pages, v_pages, mass
-        self.page_table, self.lens, self._device = page_table, lens, device
-        self._struct = _CacheStruct(
-            k_pages.data_ptr(), v_pages.data_ptr(), None if mass is None else mass.data_ptr(),
-            page_table.data_ptr(), lens.data_ptr(), page_table.shape[0], kv_heads, page,
-            page_table.shape[1], num_pages, d, v_pages.shape[3], DTYPE_CODES[k_pages.dtype])
-        self._ref = ctypes.byref(self._struct)
+        self.page_table, self.lens, self.dtype, self.device = page_table, lens, dtype, device
+        self._index = device.index
+        self._packed = _CACHE.pack(
+            k_pages.data_ptr(), v_pages.data_ptr(), 0 if mass is None else mass.data_ptr(),
+            page_table.data_ptr(), lens.data_ptr(), self.num_seqs, self.kv_heads, page, max_pages,
+            num_pages, self.d, self.dv, DTYPE_CODES[dtype], 0, 0)
 
 
-def _on_stream(stream):
-    """Allocations of a call on another stream than the current one belong to that stream."""
-    if stream is None or not isinstance(stream, torch.cuda.Stream):
-        return contextlib.nullcontext()
-    return torch.cuda.stream(stream)
-
-
-def _paged_rows(name, x, cache, heads, size, tokens=None):
-    if x.dim() != 3 or x.shape[2] != size or (heads is not None and x.shape[1] != heads) or \
-            (tokens is not None and x.shape[0] != tokens):
-        raise ValueError(f"{name} must be [tokens, {heads or 'heads'}, {size}]")
-    if x.dtype != cache.k_pages.dtype or x.device != cache._device or not x.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous tensor of the cache's dtype and device")
+def _paged_rows(name, x, cache, shape):
+    if x.shape != shape or x.dtype != cache.dtype or x.device != cache.device or not x.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {cache.dtype} tensor of shape {shape} on {cache.device}")
 
 
 def _paged_starts(starts, cache):
-    if starts.dtype != torch.int32 or starts.dim() != 1 or starts.device != cache._device or \
-            starts.shape[0] != cache._struct.num_seqs + 1 or not starts.is_contiguous():
-        raise ValueError("starts must be int32 [num_seqs + 1] on the cache's device")
+    if starts.dtype != torch.int32 or starts.shape != (cache.num_seqs + 1,) or \
+            starts.device != cache.device or not starts.is_contiguous():
+        raise ValueError("starts must be a contiguous int32 [num_seqs + 1] tensor on the cache's device")
+
+
+def _paged_stream(cache, stream):
+    """The raw stream of a call: `stream`, or the current one of the cache's device."""
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(cache._index)
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+
+
+def _on_stream(stream):
+    """What a call on another stream than the current one allocates belongs to that stream."""
+    return torch.cuda.stream(stream) if isinstance(stream, torch.cuda.Stream) else contextlib.nullcontext()
 
 
 def lla_paged_append(k, v, cache: PagedCache, starts, stream=None):
     """Writes the new tokens' keys k [tokens, kv_heads, d] and values v [tokens, kv_heads, dv] into
     their slots of the cache and sets their mass, if it has one, to zero. Sequence b's tokens are
     rows starts[b] .. starts[b+1]-1 and its last positions (cache.lens counts them already)."""
-    s = cache._struct
-    _paged_rows("k", k, cache, s.kv_heads, s.d)
-    _paged_rows("v", v, cache, s.kv_heads, s.dv, k.shape[0])
+    tokens = k.shape[0]
+    _paged_rows("k", k, cache, (tokens, cache.kv_heads, cache.d))
+    _paged_rows("v", v, cache, (tokens, cache.kv_heads, cache.dv))
     _paged_starts(starts, cache)
-    st = _load().lla_paged_append(cache._ref, k.data_ptr(), v.data_ptr(), starts.data_ptr(),
-                                  k.shape[0], _stream_ptr(stream))
-    _check(st, "lla_paged_append")
+    st = _load().lla_paged_append(cache._packed, k.data_ptr(), v.data_ptr(), starts.data_ptr(), tokens,
+                                  _paged_stream(cache, stream))
+    if st:
+        raise LlaError(st, "lla_paged_append")
 
 
 def _paged_query(q, cache, starts, h, r, max_new, window, sinks, track_mass, out, lse, path):
-    s = cache._struct
-    _paged_rows("q", q, cache, None, s.d)
+    if len(q.shape) != 3:
+        raise ValueError("q must be [tokens, q_heads, d]")
     tokens, heads, _ = q.shape
+    _paged_rows("q", q, cache, (tokens, heads, cache.d))
     if r is not None:
-        _paged_rows("r", r, cache, heads, s.d, tokens)
+        _paged_rows("r", r, cache, (tokens, heads, cache.d))
     _paged_starts(starts, cache)
-    if out is not None:
-        _check_out(out, (tokens, heads, s.dv), q)
-    if lse is not None and (lse.shape != (tokens, heads) or lse.dtype != torch.float32 or
-                            lse.device != q.device or not lse.is_contiguous()):
-        raise ValueError("lse must be a contiguous float32 [tokens, q_heads] tensor")
-    ptr = lambda t: None if t is None else t.data_ptr()  # noqa: E731
-    return _QueryStruct(q.data_ptr(), ptr(r), ptr(out), ptr(lse), starts.data_ptr(), tokens,
-                        tokens if max_new is None else int(max_new), heads, float(h), int(window),
-                        int(sinks), 1 if track_mass else 0, int(path))
+    return _QUERY.pack(q.data_ptr(), 0 if r is None else r.data_ptr(), 0 if out is None else out.data_ptr(),
+                       0 if lse is None else lse.data_ptr(), starts.data_ptr(), tokens,
+                       tokens if max_new is None else max_new, heads, h, window, sinks,
+                       1 if track_mass else 0, path, 0, 0)
 
 
 def lla_paged_attention(q, cache: PagedCache, starts, h: float, r=None, max_new=None, window=0,
@@ -471,16 +468,28 @@ def lla_paged_attention(q, cache: PagedCache, starts, h: float, r=None, max_new=
     them (window = 0) or the last `window` and the first `sinks`. track_mass adds the weights to
     cache.mass. max_new: a bound of the tokens of one sequence (default: all); giving it lets a
     decode step run as one."""
-    with _on_stream(stream):
-        if out is None:
-            out = torch.empty(q.shape[0], q.shape[1], cache._struct.dv, dtype=q.dtype, device=q.device)
-        if lse is None:
-            lse = torch.empty(q.shape[0], q.shape[1], dtype=torch.float32, device=q.device)
+    if out is None or lse is None:
+        if stream is not None:
+            with _on_stream(stream):
+                out = q.new_empty(q.shape[0], q.shape[1], cache.dv) if out is None else out
+                lse = q.new_empty(q.shape[0], q.shape[1], dtype=torch.float32) if lse is None else lse
+        else:
+            if out is None:
+                out = torch.empty((q.shape[0], q.shape[1], cache.dv), dtype=q.dtype, device=q.device) \
+                    if cache.dv != cache.d else torch.empty_like(q)
+            if lse is None:
+                lse = torch.empty(q.shape[:2], dtype=torch.float32, device=q.device)
     query = _paged_query(q, cache, starts, h, r, max_new, window, sinks, track_mass, out, lse, path)
-    wp, wb = (None, 0) if workspace is None else (
+    tokens, heads, _ = q.shape
+    _paged_rows("out", out, cache, (tokens, heads, cache.dv))
+    if lse.shape != (tokens, heads) or lse.dtype != torch.float32 or lse.device != cache.device \
+            or not lse.is_contiguous():
+        raise ValueError("lse must be a contiguous float32 [tokens, q_heads] tensor on the cache's device")
+    wp, wb = (0, 0) if workspace is None else (
         workspace.data_ptr(), workspace.numel() * workspace.element_size())
-    st = _load().lla_paged_attention(cache._ref, ctypes.byref(query), wp, wb, _stream_ptr(stream))
-    _check(st, "lla_paged_attention")
+    st = _load().lla_paged_attention(cache._packed, query, wp, wb, _paged_stream(cache, stream))
+    if st:
+        raise LlaError(st, "lla_paged_attention")
     return out, lse
 
 
@@ -489,7 +498,7 @@ def lla_paged_workspace_size(q, cache: PagedCache, starts, h: float, r=None, max
     """Bytes of device scratch that lla_paged_attention takes for these arguments (as `workspace`,
     or from the stream-ordered allocator)."""
     query = _paged_query(q, cache, starts, h, r, max_new, window, sinks, track_mass, None, lse, path)
-    return int(_load().lla_paged_workspace_size(cache._ref, ctypes.byref(query)))
+    return int(_load().lla_paged_workspace_size(cache._packed, query))
 
 
 def lla_paged_evict(cache: PagedCache, to: PagedCache, budget: int, sinks=0, recent=0, kept=None,
@@ -500,18 +509,21 @@ def lla_paged_evict(cache: PagedCache, to: PagedCache, budget: int, sinks=0, rec
     last)."""
     if cache.mass is None or to.mass is None:
         raise ValueError("eviction needs the mass of both caches")
-    if cache._device != to._device:
+    if cache.device != to.device:
         raise ValueError("the caches must be on one device")
-    shape = (cache._struct.num_seqs, cache._struct.kv_heads, int(budget))
+    if budget < 1:
+        raise ValueError("budget must be at least 1")
+    shape = (cache.num_seqs, cache.kv_heads, budget)
     if kept is None:
         with _on_stream(stream):
-            kept = torch.empty(shape, dtype=torch.int32, device=cache._device)
-    elif tuple(kept.shape) != shape or kept.dtype != torch.int32 or kept.device != cache._device \
+            kept = torch.empty(shape, dtype=torch.int32, device=cache.device)
+    elif kept.shape != shape or kept.dtype != torch.int32 or kept.device != cache.device \
             or not kept.is_contiguous():
         raise ValueError(f"kept must be a contiguous int32 tensor of shape {shape}")
-    st = _load().lla_paged_evict(cache._ref, to._ref, int(budget), int(sinks), int(recent),
-                                 kept.data_ptr(), _stream_ptr(stream))
-    _check(st, "lla_paged_evict")
+    st = _load().lla_paged_evict(cache._packed, to._packed, budget, sinks, recent, kept.data_ptr(),
+                                 _paged_stream(cache, stream))
+    if st:
+        raise LlaError(st, "lla_paged_evict")
     return kept
 
 

@@ -18,6 +18,9 @@ namespace paged {
 
 constexpr int kNoWindow = 1 << 30;  // lengths stay below this (checked on the host)
 
+// Raises the dynamic shared memory limit of a kernel on the current device (lla_paged_api.cu).
+cudaError_t ensure_smem(const void* kern, size_t bytes);
+
 // Passed to kernels by value.
 struct Params {
   const void* q;      // [tokens, Hq, d]
@@ -208,6 +211,52 @@ __device__ __noinline__ void exact_row(const Params& p, int d, int dv, int b, in
       stf(out, lane + 32 * c, r ? fmaf(o1[c], f1, -o2[c] * inv) : o1[c] * inv);
 }
 
+// ------------------------------------------------------------------------------------- launches
+// Launches `kern` on `s`. `smem` bytes of dynamic shared memory (the opt-in above 48 KB is set once
+// per kernel and device: an attribute of the function, which stays); `cluster` blocks per cluster
+// (1: none); `after`: the kernel may be set up while the stream's previous kernel drains, and waits
+// itself (wait_previous) before it reads what that one wrote.
+template <typename... KArgs, typename... Args>
+cudaError_t launch(void (*kern)(KArgs...), dim3 grid, int threads, size_t smem, int cluster, bool after,
+                   cudaStream_t s, Args&&... args) {
+  if (smem > 40 * 1024) {  // 48 KB, less what the kernel declares
+    cudaError_t err = ensure_smem(reinterpret_cast<const void*>(kern), smem);
+    if (err != cudaSuccess) return err;
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute at[2];
+  int n = 0;
+  if (cluster > 1) {
+    at[n].id = cudaLaunchAttributeClusterDimension;
+    at[n].val.clusterDim.x = (unsigned)cluster;
+    at[n].val.clusterDim.y = at[n].val.clusterDim.z = 1;
+    ++n;
+  }
+  if (after) {
+    at[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[n].val.programmaticStreamSerializationAllowed = 1;
+    ++n;
+  }
+  cfg.attrs = at;
+  cfg.numAttrs = n;
+  const cudaError_t err = cudaLaunchKernelEx(&cfg, kern, KArgs(args)...);
+  if (err == cudaSuccess) count_launch();
+  return err;
+}
+// A kernel that may be set up early: everything before this call may not touch what the previous
+// kernel of the stream writes (or reads, where this one writes it).
+__device__ __forceinline__ void wait_previous() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+// From here on the next kernel of the stream may be set up (it still waits for this one's end).
+__device__ __forceinline__ void let_next() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
 // Launchers (each returns the launch error, if any).
 // CUDA cores, every supported size (one set per type): the attention; mass += the rows' weights from
 // q, k and the finished lse; the join of the splits' partial results into out and lse.
@@ -228,6 +277,7 @@ inline cudaError_t launch_join(const Params& p, int d, int dv, int dtype, cudaSt
 }
 // Sequences of few rows (p.hi = rows_limit of them at most), bf16 with d = dv = 64 or 128: the
 // attention, the join of its splits and, with p.logits, the weight tracking.
+constexpr int kRowsCluster = 8;  // splits that join within a cluster (the portable size)
 inline int rows_limit(bool probe) { return probe ? 8 : 16; }
 cudaError_t launch_attend_rows(const Params& p, int d, cudaStream_t s);
 // Sequences of many rows, bf16 with d = dv = 64 or 128 and g <= 128.

@@ -1,10 +1,30 @@
 // C ABI of the paged-cache operators: argument validation, choice of kernels and splits, scratch.
 #include <cmath>
+#include <mutex>
 
 #include "lla_paged.cuh"
 
 namespace lla {
 namespace paged {
+
+// A kernel's limit is raised once per device and size: remembering it saves most of a microsecond
+// per launch. (Only a cache of what the driver already holds: a lost entry sets it again.)
+cudaError_t ensure_smem(const void* kern, size_t bytes) {
+  struct Entry { const void* kern; int dev; size_t bytes; };
+  constexpr int N = 256;
+  static std::mutex mu;
+  static Entry table[N];
+  int dev = 0;
+  cudaError_t err = cudaGetDevice(&dev);
+  if (err != cudaSuccess) return err;
+  Entry& e = table[(reinterpret_cast<uintptr_t>(kern) / 16 * 31 + dev) % N];
+  std::lock_guard<std::mutex> lk(mu);
+  if (e.kern == kern && e.dev == dev && e.bytes >= bytes) return cudaSuccess;
+  err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+  if (err == cudaSuccess) e = {kern, dev, bytes};
+  return err;
+}
+
 namespace {
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
@@ -31,7 +51,7 @@ int check_cache_shape(const lla_paged_cache* c) {
 int check_cache_pointers(const lla_paged_cache* c, bool need_mass) {
   if (!c->k_pages || !c->v_pages || !c->page_table || !c->lens) return LLA_ERR_INVALID_ARG;
   if (!aligned16(c->k_pages) || !aligned16(c->v_pages)) return LLA_ERR_INVALID_ARG;
-  if (need_mass && !c->mass) return LLA_ERR_INVALID_ARG;
+  if (need_mass && (!c->mass || !aligned16(c->mass))) return LLA_ERR_INVALID_ARG;
   return LLA_OK;
 }
 
@@ -99,17 +119,22 @@ Plan make_plan(const lla_paged_cache* c, const lla_paged_query* a) {
   pl.tiles = !pl.rows || rows > limit;
   size_t at = 0;
   auto take = [&](size_t bytes) { const size_t o = at; at += align_up(bytes); return o; };
-  auto splits = [&](long long blocks, long long want, long long least) {
-    long long n = blocks > 0 ? (want + blocks - 1) / blocks : 1;
+  auto splits = [&](long long blocks, long long want, long long least, bool up = true) {
+    long long n = blocks > 0 ? (want + (up ? blocks - 1 : 0)) / blocks : 1;
     if (n > keys / least) n = keys / least;
     return n < 1 ? 1 : n > 512 ? 512 : (int)n;
   };
   if (pl.rows) {
     pl.row_cap = (int)(rows < limit ? rows : limit);
-    // Blocks of 4 warps, 2 (d = 128) or 3 (d = 64) resident on each of 152 SMs: a wave or two of
-    // them, but no block with fewer than 256 keys (its start and join would cost more).
-    pl.rows_split = splits(pairs, c->d == 128 ? 608 : 912, 256);
-    if (pl.rows_split > 1) {
+    // Two blocks per SM first, down to 128 keys each (one sequence, 8 heads of 64, L 1000: 5.0 us
+    // with 7 blocks a head, 7.6 with 2); then, so that uneven lengths level out, four waves of them,
+    // but no block under 1024 keys (48 sequences, 4 heads, window 1024: 30 us with 2 blocks a head,
+    // 47 with 7). More than a cluster of 8 only where its blocks would have over 1024 keys each:
+    // below that, the launch that joins costs more than shorter blocks save.
+    const int fill = splits(pairs, 304, 128), level = splits(pairs, c->d == 128 ? 1216 : 1824, 1024);
+    pl.rows_split = fill > level ? fill : level;
+    if (pl.rows_split > kRowsCluster && keys <= kRowsCluster * 1024) pl.rows_split = kRowsCluster;
+    if (pl.rows_split > kRowsCluster) {
       pl.rows_s = take((size_t)pairs * limit * pl.rows_split * sizeof(float4));
       pl.rows_o = take((size_t)pairs * limit * pl.rows_split * branches * c->dv * sizeof(float));
     }
@@ -124,7 +149,10 @@ Plan make_plan(const lla_paged_cache* c, const lla_paged_query* a) {
     const long long per = pl.tc ? 128 / g * (a->r ? 1 : 2) : g < BM ? BM / g : 1, slices = (g + BM - 1) / BM;
     const long long by_tokens = (a->tokens + per - 1) / per;
     const long long tiles = (by_tokens > c->num_seqs ? by_tokens : c->num_seqs) * slices * c->kv_heads;
-    pl.tiles_split = splits(tiles, 304, 256);
+    // Few tiles: their keys are split until every SM has a block, down to 1024 keys (the start of a
+    // block and the partial results cost about 8 of its 128-key steps); CUDA cores, whose steps are
+    // longer and whose blocks share an SM, down to 256 and for two blocks.
+    pl.tiles_split = pl.tc ? splits(tiles, 152, 1024, false) : splits(tiles, 304, 256);
     if (pl.tiles_split > 1) {
       const size_t all = (size_t)a->tokens * a->q_heads * pl.tiles_split;
       pl.tiles_s = take(all * sizeof(float4));
@@ -160,7 +188,7 @@ int run_attention(const lla_paged_cache* c, const lla_paged_query* a, const Plan
     f.hi = pl.row_cap;
     f.split = pl.rows_split;
     f.row_cap = pl.row_cap;
-    if (pl.rows_split > 1) {
+    if (pl.rows_split > kRowsCluster) {
       f.part_s = reinterpret_cast<float4*>(ws + pl.rows_s);
       f.part_o = reinterpret_cast<float*>(ws + pl.rows_o);
     }

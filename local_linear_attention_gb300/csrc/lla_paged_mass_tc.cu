@@ -281,13 +281,9 @@ cudaError_t launch_t(const Params& p, cudaStream_t s) {
              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
     return cudaErrorInvalidValue;
-  auto kern = mass_tc_kernel<D>;
-  err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D>::bytes);
-  if (err != cudaSuccess) return err;
   const long long most = ((((long long)p.max_pages << p.page_shift) + KT - 1) / KT) * p.B * p.Hkv;
-  kern<<<(unsigned)(most < 304 ? most : 304), NTHREADS, Cfg<D>::bytes, s>>>(p, kmap, qmap);
-  count_launch();
-  return cudaGetLastError();
+  return launch(mass_tc_kernel<D>, dim3((unsigned)(most < 304 ? most : 304)), NTHREADS, Cfg<D>::bytes, 1, false, s,
+                p, kmap, qmap);
 }
 
 }  // namespace

@@ -12,13 +12,20 @@
 // warps take 16-key steps in turn, each warp with a ring of STAGES steps of its own (keys and
 // values, 16-byte asynchronous copies, chunk c of row r at c ^ (r & 7): ldmatrix without bank
 // conflicts) and its own running maximum, so the main loop has no block-wide barrier. The warps'
-// results are joined through shared memory, the blocks' by join_rows_kernel (a fixed order, so
-// results do not depend on scheduling).
+// results are joined through shared memory. Up to 8 blocks of a pair form a cluster and join
+// through distributed shared memory: one launch, no scratch. Where a few long sequences need more
+// blocks than that, their partial results go through scratch to join_rows_kernel. Either way the
+// order is fixed, so results do not depend on scheduling.
+// Weight tracking: the attention leaves its logits in scratch and mass_rows_kernel adds up
+// exp(s - lse) once the rows' lse is known. (Done by the attention's own blocks after their join,
+// the same pass took 60 us longer at B32 L16384 d128: 128 threads a block waiting for scratch.)
 // Rows: 16 without a probe. With one, rows 0-7 of the MMA are q and rows 8-15 the same rows' r:
 // the accumulator fragment gives a thread s and t of one row, p goes back as row i and p t as row
 // i + 8, and O1, O2 come out of one product, so the probe costs no extra matrix work.
 // Rounding: p and p t enter the second product as bf16 (the values are bf16 already; fp32 operands
 // have no matrix path at this rate); d1, d2 are fp32 sums of the unrounded weights.
+#include <cooperative_groups.h>
+
 #include "lla_paged.cuh"
 #include "lla_tc_ptx.cuh"
 
@@ -37,11 +44,13 @@ constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 template <int D>
 struct Cfg {
-  static constexpr int stages = D == 128 ? 3 : 4;
+  static constexpr int stages = D == 128 ? 2 : 3;
   static constexpr int step_bytes = KT * D * 2;            // keys, or values
   static constexpr int warp_bytes = stages * 2 * step_bytes;
-  static constexpr int join_bytes = NW * 16 * (D + 4) * 4; // the warps' O, reusing the rings
-  static constexpr int bytes = NW * warp_bytes > join_bytes ? NW * warp_bytes : join_bytes;
+  static constexpr int join_bytes = NW * 16 * (D + 4) * 4; // the warps' O, reusing the rings,
+  static constexpr int fin = join_bytes;                   // and the block's, [16][D]
+  static constexpr int bytes = NW * warp_bytes;
+  static_assert(fin + 16 * D * 4 <= bytes, "join regions");
 };
 
 __device__ __forceinline__ void ldmatrix4(uint32_t (&r)[4], uint32_t addr) {
@@ -70,15 +79,48 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   return r;
 }
 
-template <int D, bool PROBE, bool LOGITS>
+// A finished row's sums, o1[c] and o2[c] its unnormalised columns lane * VC + c: writes out and lse.
+template <int D, bool PROBE>
+__device__ __forceinline__ void write_row(const Params& p, const Seq& sq, int b, int hk, int r, float top,
+                                           float s1, float s2, const float (&o1)[D / 32],
+                                           const float (&o2)[D / 32]) {
+  constexpr int VC = D / 32;
+  const int lane = threadIdx.x & 31;
+  const int token = sq.t0 + r / p.g, head = hk * p.g + r % p.g;
+  const float inv = s1 == 0.f ? 0.f : 1.f / s1, f1 = (1.f + s2 * inv) * inv;
+  __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.out) + ((long long)token * p.Hq + head) * D + lane * VC;
+  float bad = 0.f;
+  uint32_t w[VC / 2];
+#pragma unroll
+  for (int c = 0; c < VC; c += 2) {
+    const float y0 = PROBE ? fmaf(o1[c], f1, -o2[c] * inv) : o1[c] * inv;
+    const float y1 = PROBE ? fmaf(o1[c + 1], f1, -o2[c + 1] * inv) : o1[c + 1] * inv;
+    bad += (y0 + y1) * 0.f;
+    w[c / 2] = pack_bf16(y0, y1);
+  }
+  if (VC == 4) *reinterpret_cast<uint2*>(dst) = make_uint2(w[0], w[VC / 2 - 1]);
+  else *reinterpret_cast<uint32_t*>(dst) = w[0];
+  if (p.lse && lane == 0)
+    p.lse[(long long)token * p.Hq + head] =
+        s1 == 0.f ? -CUDART_INF_F : (top * (p.inv_h * kLog2e) + log2f(s1)) * kLn2;
+  if (__any_sync(0xffffffffu, !(bad == 0.f))) {
+    __syncwarp();
+    exact_row<__nv_bfloat16>(p, D, D, b, sq.first + r / p.g, token, head);
+  }
+}
+
+// CLUSTER: the blocks of a pair are one cluster and join there.
+template <int D, bool PROBE, bool LOGITS, bool CLUSTER>
 __global__ void __launch_bounds__(NW * 32) attend_rows_kernel(Params p) {
   using C = Cfg<D>;
   constexpr int ROWS = PROBE ? 8 : 16, NR = PROBE ? 1 : 2;  // rows; rows per thread
   constexpr int CH = D / 8;                                 // 16-byte chunks per key
   extern __shared__ __align__(1024) uint8_t smem[];
   __shared__ float4 stats[NW][16];
+  __shared__ float4 fin_stats[16];  // the block's {m, d1, d2}
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int pair = blockIdx.x, b = pair / p.Hkv, hk = pair % p.Hkv, part = blockIdx.y;
+  // the parts of a pair follow one another: clusters are made of neighbours
+  const int pair = blockIdx.x / p.split, b = pair / p.Hkv, hk = pair % p.Hkv, part = blockIdx.x % p.split;
   const Seq sq = load_seq(p, b);
   if (!mine(p, sq.n)) {
     if (sq.n > 0 && sq.n * p.g > p.max_rows) atomicOr(p.status, kStatusBadIndex);  // beyond max_new
@@ -93,10 +135,12 @@ __global__ void __launch_bounds__(NW * 32) attend_rows_kernel(Params p) {
   const __nv_bfloat16* vg = static_cast<const __nv_bfloat16*>(p.v);
   uint8_t* const ring = smem + warp * C::warp_bytes;
 
-  auto page_of = [&](int it) {
-    if (it >= i1) return -1;
-    const int j = range.tile(it) * KT;
-    return j < sq.len ? load_page(p, b, j >> p.page_shift) : -1;
+  // Pages of this warp's next 32 steps, one per lane: one load's latency for all of them.
+  int pages = 0, page_at = 0;
+  auto load_pages = [&](int first) {
+    const int it = first + lane * NW, j = it < i1 ? range.tile(it) * KT : sq.len;
+    pages = j < sq.len ? load_page(p, b, j >> p.page_shift) : -1;
+    page_at = 0;
   };
   // Copies step `it` (page pg) into a stage: positions past the sequence's end, and those of a bad
   // page, become zeros.
@@ -118,13 +162,12 @@ __global__ void __launch_bounds__(NW * 32) attend_rows_kernel(Params p) {
     }
     cp_async_commit();
   };
-  int pg_next = page_of(i0 + warp);
   int it_next = i0 + warp;
+  load_pages(it_next);
   auto advance = [&](int stage) {
-    const int pg = pg_next;
-    issue(it_next, pg, stage);
+    if (page_at == 32) load_pages(it_next);
+    issue(it_next, __shfl_sync(0xffffffffu, pages, page_at++), stage);
     it_next += NW;
-    pg_next = page_of(it_next);  // one step ahead: its latency is not in front of a copy
   };
 #pragma unroll
   for (int s = 0; s < C::stages - 1; ++s) advance(s);
@@ -265,6 +308,7 @@ __global__ void __launch_bounds__(NW * 32) attend_rows_kernel(Params p) {
     if (++stage == C::stages) stage = 0;
   }
   cp_async_wait<0>();
+  let_next();
   __syncthreads();  // the rings are free
 
   // Join of the four warps through shared memory: O [warp][16][D + 4], {m, d1, d2}.
@@ -307,8 +351,16 @@ __global__ void __launch_bounds__(NW * 32) attend_rows_kernel(Params p) {
         if (PROBE) o2[c] = fmaf(os[(i * 16 + r + 8) * OP + lane * VC + c], f, o2[c]);
       }
     }
-    if (p.split > 1) {
-      const long long id = ((long long)part * gridDim.x + pair) * ROWS + r;
+    if (CLUSTER) {
+      if (lane == 0) fin_stats[r] = make_float4(top, s1, s2, 0.f);
+      float* dst = reinterpret_cast<float*>(smem + C::fin) + r * D + lane * VC;
+#pragma unroll
+      for (int c = 0; c < VC; ++c) {
+        dst[c] = o1[c];
+        if (PROBE) dst[8 * D + c] = o2[c];
+      }
+    } else if (p.split > 1) {
+      const long long id = ((long long)part * p.B * p.Hkv + pair) * ROWS + r;
       if (lane == 0) p.part_s[id] = make_float4(top, s1, s2, 0.f);
       float* dst = p.part_o + id * (PROBE ? 2 : 1) * D + lane * VC;
 #pragma unroll
@@ -316,25 +368,41 @@ __global__ void __launch_bounds__(NW * 32) attend_rows_kernel(Params p) {
         dst[c] = o1[c];
         if (PROBE) dst[D + c] = o2[c];
       }
-      continue;
+    } else {
+      write_row<D, PROBE>(p, sq, b, hk, r, top, s1, s2, o1, o2);
     }
-    const int token = sq.t0 + r / p.g, head = hk * p.g + r % p.g;
-    const float inv = s1 == 0.f ? 0.f : 1.f / s1, f1 = (1.f + s2 * inv) * inv;
-    __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.out) + ((long long)token * p.Hq + head) * D + lane * VC;
-    float bad = 0.f;
+  }
+  if constexpr (CLUSTER) {
+    namespace cg = cooperative_groups;
+    cg::cluster_group cluster = cg::this_cluster();
+    cluster.sync();
+    for (int r = warp * p.split + part; r < nrows; r += NW * p.split) {  // this warp's rows
+      float4 st[kRowsCluster];
+      float top = -CUDART_INF_F;
 #pragma unroll
-    for (int c = 0; c < VC; c += 2) {
-      const float y0 = PROBE ? fmaf(o1[c], f1, -o2[c] * inv) : o1[c] * inv;
-      const float y1 = PROBE ? fmaf(o1[c + 1], f1, -o2[c + 1] * inv) : o1[c + 1] * inv;
-      bad += (y0 + y1) * 0.f;
-      *reinterpret_cast<uint32_t*>(dst + c) = pack_bf16(y0, y1);
+      for (int i = 0; i < kRowsCluster; ++i)
+        if (i < p.split) {
+          st[i] = *cluster.map_shared_rank(&fin_stats[r], i);
+          top = fmaxf(top, st[i].x);
+        }
+      const float ref = top == -CUDART_INF_F ? 0.f : top * c2;
+      float s1 = 0.f, s2 = 0.f, o1[VC] = {}, o2[VC] = {};
+#pragma unroll
+      for (int i = 0; i < kRowsCluster; ++i)
+        if (i < p.split) {
+          const float f = ex2(fmaf(st[i].x, c2, -ref));
+          s1 = fmaf(st[i].y, f, s1);
+          s2 = fmaf(st[i].z, f, s2);
+          const float* src = reinterpret_cast<const float*>(cluster.map_shared_rank(smem, i) + C::fin) + r * D + lane * VC;
+#pragma unroll
+          for (int c = 0; c < VC; ++c) {
+            o1[c] = fmaf(src[c], f, o1[c]);
+            if (PROBE) o2[c] = fmaf(src[8 * D + c], f, o2[c]);
+          }
+        }
+      write_row<D, PROBE>(p, sq, b, hk, r, top, s1, s2, o1, o2);
     }
-    if (p.lse && lane == 0)
-      p.lse[(long long)token * p.Hq + head] = s1 == 0.f ? -CUDART_INF_F : (ref + log2f(s1)) * kLn2;
-    if (__any_sync(0xffffffffu, !(bad == 0.f))) {
-      __syncwarp();
-      exact_row<__nv_bfloat16>(p, D, D, b, p0 + r / p.g, token, head);
-    }
+    cluster.sync();  // this block's sums have been read
   }
 }
 
@@ -345,6 +413,7 @@ __global__ void __launch_bounds__(128) join_rows_kernel(Params p) {
   const int lane = threadIdx.x & 31;
   const long long id = (long long)blockIdx.x * 4 + (threadIdx.x >> 5);
   const int pairs = p.B * p.Hkv;
+  wait_previous();  // by every thread: this kernel ends after the attention has
   const int pair = (int)(id / p.row_cap), r = (int)(id % p.row_cap);
   if (pair >= pairs) return;
   const int b = pair / p.Hkv, hk = pair % p.Hkv;
@@ -368,75 +437,64 @@ __global__ void __launch_bounds__(128) join_rows_kernel(Params p) {
       if (PROBE) o2[c] = fmaf(src[D + c], f, o2[c]);
     }
   }
-  const int token = sq.t0 + r / p.g, head = hk * p.g + r % p.g;
-  const float inv = s1 == 0.f ? 0.f : 1.f / s1, f1 = (1.f + s2 * inv) * inv;
-  __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.out) + ((long long)token * p.Hq + head) * D + lane * VC;
-  float bad = 0.f;
-#pragma unroll
-  for (int c = 0; c < VC; c += 2) {
-    const float y0 = PROBE ? fmaf(o1[c], f1, -o2[c] * inv) : o1[c] * inv;
-    const float y1 = PROBE ? fmaf(o1[c + 1], f1, -o2[c + 1] * inv) : o1[c + 1] * inv;
-    bad += (y0 + y1) * 0.f;
-    *reinterpret_cast<uint32_t*>(dst + c) = pack_bf16(y0, y1);
-  }
-  if (p.lse && lane == 0)
-    p.lse[(long long)token * p.Hq + head] = s1 == 0.f ? -CUDART_INF_F : (ref + log2f(s1)) * kLn2;
-  if (__any_sync(0xffffffffu, !(bad == 0.f))) {
-    __syncwarp();
-    exact_row<__nv_bfloat16>(p, D, D, b, sq.first + r / p.g, token, head);
-  }
+  write_row<D, PROBE>(p, sq, b, hk, r, top, s1, s2, o1, o2);
 }
 
 // mass += the rows' weights, from the logits that the attention wrote (4 bytes a row and key,
-// against 2 d bytes a key to read the keys again and the products) and the finished lse. One
-// thread per key.
+// against 2 d bytes a key to read the keys again and the products) and the finished lse. A thread
+// takes four keys, whose loads (a row's four logits are one 16-byte word) are all in flight at once.
 __global__ void __launch_bounds__(256) mass_rows_kernel(Params p) {
   __shared__ float lse[16];
+  wait_previous();
   const int pair = blockIdx.x, b = pair / p.Hkv, hk = pair % p.Hkv;
   const Seq sq = load_seq(p, b);
   if (!mine(p, sq.n)) return;
   const TileRange<KT> range(p, sq.first, sq.len - 1);
   const int nrows = sq.n * p.g, count = range.count * KT;
-  if (blockIdx.y * 256 >= count) return;
+  if (blockIdx.y * 1024 >= count) return;
   if (threadIdx.x < nrows) {
     const int r = threadIdx.x;
     lse[r] = p.lse[(long long)(sq.t0 + r / p.g) * p.Hq + hk * p.g + r % p.g] * kLog2e;
   }
   __syncthreads();
   const float c2 = p.inv_h * kLog2e;
-  for (int i = blockIdx.y * 256 + threadIdx.x; i < count; i += gridDim.y * 256) {
+  for (int i = (blockIdx.y * 256 + threadIdx.x) * 4; i < count; i += gridDim.y * 1024) {
     const int j = range.tile(i / KT) * KT + i % KT;
     if (j >= sq.len) continue;
-    const float* src = p.logits + (long long)pair * p.row_cap * p.keys_cap + i;
-    float got = 0.f;
-    for (int r = 0; r < nrows; ++r) {
-      const float x = src[(long long)r * p.keys_cap];
-      if (x != -CUDART_INF_F) got += ex2(fmaf(x, c2, -lse[r]));  // -inf: the row does not see it
-    }
     const int pg = load_page(p, b, j >> p.page_shift);
-    if (pg >= 0) p.mass[((long long)pg * p.Hkv + hk) * p.page + (j & (p.page - 1))] += got;
+    if (pg < 0) continue;
+    float4* dst = reinterpret_cast<float4*>(p.mass + ((long long)pg * p.Hkv + hk) * p.page + (j & (p.page - 1)));
+    const float4 old = *dst;
+    float got[4] = {};
+    const float* src = p.logits + (long long)pair * p.row_cap * p.keys_cap + i;
+#pragma unroll 4
+    for (int r = 0; r < nrows; ++r) {
+      const float4 x = *reinterpret_cast<const float4*>(src + (long long)r * p.keys_cap);
+      const float y[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (y[e] != -CUDART_INF_F) got[e] += ex2(fmaf(y[e], c2, -lse[r]));  // -inf: not visible
+    }
+    *dst = make_float4(old.x + got[0], old.y + got[1], old.z + got[2], old.w + got[3]);
   }
 }
 
 template <int D, bool PROBE, bool LOGITS>
 cudaError_t launch_rows_t(const Params& p, cudaStream_t s) {
-  auto kern = attend_rows_kernel<D, PROBE, LOGITS>;
-  cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D>::bytes);
-  if (err != cudaSuccess) return err;
   const unsigned pairs = (unsigned)p.B * p.Hkv;
-  kern<<<dim3(pairs, p.split), NW * 32, Cfg<D>::bytes, s>>>(p);
-  count_launch();
-  if (p.split > 1) {
+  if ((long long)pairs * p.split > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+  const bool cluster = p.split > 1 && p.split <= kRowsCluster;
+  auto kern = cluster ? attend_rows_kernel<D, PROBE, LOGITS, true> : attend_rows_kernel<D, PROBE, LOGITS, false>;
+  cudaError_t err = launch(kern, dim3(pairs * p.split), NW * 32, Cfg<D>::bytes, cluster ? p.split : 1, false, s, p);
+  if (err == cudaSuccess && !cluster && p.split > 1) {
     const long long rows = (long long)pairs * p.row_cap;
-    join_rows_kernel<D, PROBE><<<(unsigned)((rows + 3) / 4), 128, 0, s>>>(p);
-    count_launch();
+    err = launch(join_rows_kernel<D, PROBE>, dim3((unsigned)((rows + 3) / 4)), 128, 0, 1, true, s, p);
   }
-  if (LOGITS) {
-    const int blocks = (p.keys_cap + 255) / 256;
-    mass_rows_kernel<<<dim3(pairs, blocks < 4096 ? blocks : 4096), 256, 0, s>>>(p);
-    count_launch();
+  if (err == cudaSuccess && LOGITS) {
+    const int blocks = (p.keys_cap + 1023) / 1024;
+    err = launch(mass_rows_kernel, dim3(pairs, blocks < 4096 ? blocks : 4096), 256, 0, 1, true, s, p);
   }
-  return cudaGetLastError();
+  return err;
 }
 
 template <int D>

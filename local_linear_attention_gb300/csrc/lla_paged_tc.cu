@@ -4,23 +4,26 @@
 // One pass over the keys with a running row maximum. Per 128-key tile a CTA runs two 128-row score
 // products and two 128-row value products, X and Y:
 //   softmax attention: X and Y are two blocks of 128 rows (tokens x grouped heads of one key/value
-//     head), S = Q K^T, P = exp(S - m), O += P V, each block with its own softmax warpgroup, so one
+//     head), S = Q K^T, P = exp(S - m), O += P V, each block with its own softmax warps, so one
 //     block's exponentials run while the tensor core works for the other;
 //   with a probe: X is Q, Y is R of the same 128 rows; P1 = exp(S_X - m), P2 = P1 .* S_Y, O1 += P1 V,
-//     O2 += P2 V. Each warpgroup takes 64 of a tile's 128 keys; the row maximum goes through shared
-//     memory.
-// Warps 0-3 and 4-7: the two softmax warpgroups (a thread is a row, so row sums need no shuffles);
-// 8: TMA loader (one lane per page fragment: a tile spans 128 / page_size pages; rows past the
-// sequence's end and bad pages are loaded as zeros by an out-of-range coordinate); 9: MMA issuer.
+//     O2 += P2 V.
+// Warps 0-15: softmax, a thread is a row and 64 (probe: 32) of a tile's keys, the row maximum goes
+// through shared memory. (With 8 warps and whole rows per thread the exponential chain of one warp
+// per scheduler was exposed.) 16: TMA loader (one lane per page fragment: a tile
+// spans 128 / page_size pages; rows past the sequence's end and bad pages are loaded as zeros by an
+// out-of-range coordinate); 17 and 18: the MMA issuers of X and Y.
 // Tensor memory: S_X, S_Y (128 columns each), O_X, O_Y (d each); bf16 P has columns of its own at
 // d = 64, and overwrites its S at d = 128 (512 columns are all there are), where the next S product
 // is issued behind the P V product that reads them.
 // The accumulators are rescaled only when a row's maximum grows by more than 2^8 (the weights then
 // stay below 2^8, exact in scale; d1 is fp32): after the first tiles this hardly happens.
 // Rounding: p and p t enter the value products as bf16, d1 and d2 sum the unrounded fp32 weights.
-// What bounds it: the tensor pipe and the exponentials are near balance at d = 128 (2048 cycles of
-// MMA against 2048 of ex2 per 256 rows x 128 keys).
+// What bounds it at d = 128: the chain softmax - value product - next score product of each block
+// against 2048 cycles of MMA per 256 rows x 128 keys.
 // All mbarrier waits are bounded.
+#include <type_traits>
+
 #include "lla_paged.cuh"
 #include "lla_tc_ptx.cuh"
 #include "lla_tmap.cuh"
@@ -32,7 +35,8 @@ namespace {
 using namespace tc;
 
 constexpr int BM = 128, KT = 128;
-constexpr int NTHREADS = 320;
+constexpr int NSOFT = 16;                 // softmax warps
+constexpr int NTHREADS = (NSOFT + 3) * 32;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 template <int D>
@@ -41,8 +45,8 @@ struct Cfg {
   static constexpr int stages = D == 128 ? 4 : 8;
   static constexpr int sm_y = tile, sm_ring = 2 * tile;
   static constexpr int sm_bar = sm_ring + stages * tile;
-  static constexpr int sm_x = sm_bar + 512;      // row exchange: [2 buffers][2 groups][128] maxima
-  static constexpr int bytes = sm_x + 2048 + 1024;  // 1024: aligning the base
+  static constexpr int sm_x = sm_bar + 512;      // row exchange: [2 buffers][4 groups][128]
+  static constexpr int bytes = sm_x + 4096 + 1024;  // 1024: aligning the base
   static constexpr bool overlay = D == 128;
   static constexpr uint32_t t_o = 256, t_p = overlay ? 0 : 384, p_stride = overlay ? 128 : 64;
 };
@@ -50,8 +54,8 @@ static_assert(Cfg<128>::bytes <= 227 * 1024 && Cfg<64>::bytes <= 227 * 1024, "sh
 
 struct Barriers {
   uint64_t full[8], empty[8];
-  uint64_t sfull[2], sfree[2], pfull[2], pvdone[2];
-  uint64_t rowx, done;
+  uint64_t sfull[2], sfree[2], pfull[2][2], pvdone[2];
+  uint64_t rowx[2], done[2];
 };
 static_assert(sizeof(Barriers) <= 512, "barrier region");
 
@@ -66,6 +70,36 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   return r;
 }
 
+// Packed pairs of fp32 (one instruction per pair on this architecture).
+__device__ __forceinline__ uint64_t pair(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ void unpair(uint64_t x, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(x));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.ftz.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+
 template <int D, bool PROBE>
 __global__ void __launch_bounds__(NTHREADS, 1)
 attend_tc_kernel(Params p, const __grid_constant__ CUtensorMap kmap,
@@ -76,7 +110,7 @@ attend_tc_kernel(Params p, const __grid_constant__ CUtensorMap kmap,
   Barriers& bar = *reinterpret_cast<Barriers*>(smem + C::sm_bar);
   __shared__ uint32_t tmem_base_s;
   __shared__ int abort_flag;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   const int hk = blockIdx.x % p.Hkv, part = blockIdx.y;
   const int per = BM / p.g, tokens = PROBE ? per : 2 * per;  // tokens per block and per tile
   int b, tile;
@@ -107,19 +141,20 @@ attend_tc_kernel(Params p, const __grid_constant__ CUtensorMap kmap,
     *reinterpret_cast<uint4*>(smem + h * C::tile + (c >> 3) * 16384 + r * 128 + (((c & 7) ^ (r & 7)) * 16)) = x;
   }
   if (tid == 0) {
-    for (int s = 0; s < C::stages; ++s) { mbar_init(&bar.full[s], 1); mbar_init(&bar.empty[s], 1); }
+    for (int s = 0; s < C::stages; ++s) { mbar_init(&bar.full[s], 1); mbar_init(&bar.empty[s], 2); }
     for (int s = 0; s < 2; ++s) {
       mbar_init(&bar.sfull[s], 1);
-      mbar_init(&bar.sfree[s], PROBE ? 8 : 4);
-      mbar_init(&bar.pfull[s], PROBE ? 8 : 4);
+      mbar_init(&bar.sfree[s], PROBE ? 16 : 8);
+      mbar_init(&bar.pfull[s][0], PROBE ? 8 : 4);
+      mbar_init(&bar.pfull[s][1], PROBE ? 8 : 4);
+      mbar_init(&bar.rowx[s], PROBE ? 16 : 8);
       mbar_init(&bar.pvdone[s], 1);
+      mbar_init(&bar.done[s], 1);
     }
-    mbar_init(&bar.rowx, 8);
-    mbar_init(&bar.done, 1);
     abort_flag = 0;
     fence_mbar_init();
   }
-  if (warp == 9) {
+  if (warp == NSOFT + 1) {
     tmem_alloc(&tmem_base_s, 512);
     tmem_relinquish();
   }
@@ -127,81 +162,85 @@ attend_tc_kernel(Params p, const __grid_constant__ CUtensorMap kmap,
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tbase = tmem_base_s;
+  const uint32_t tbase = __shfl_sync(0xffffffffu, tmem_base_s, 0);
   volatile int* abort_p = &abort_flag;
   int* const status = p.status;
   constexpr int TO = kStatusTimeout;
 
-  if (warp == 9) {
-    // ------------------------------------------------------------------ MMA issuer
-    if (lane == 0 && n > 0) {
-      const uint64_t xd = smem_desc_sw128(smem_u32(smem), 1024);
+  if (warp > NSOFT) {
+    // ------------------------------------------------------------------ MMA issuers, one per block
+    const int h = warp - NSOFT - 1;
+    if (n > 0) {
+      const uint64_t xd = smem_desc_sw128(smem_u32(smem + h * C::tile), 1024);
       const uint64_t kd = smem_desc_sw128(smem_u32(smem + C::sm_ring), 1024);
       const uint64_t vd = smem_desc_sw128_mn(smem_u32(smem + C::sm_ring), 16384, 1024);
+      const uint32_t ts = tbase + h * 128, to = tbase + C::t_o + h * D, tp = tbase + C::t_p + h * C::p_stride;
       constexpr uint32_t id_s = idesc_bf16(BM, KT, false, false);
       constexpr uint32_t id_o = idesc_bf16(BM, D, false, true);
       constexpr uint32_t tile16 = C::tile >> 4;
       auto stage = [](int i) { return (uint32_t)(i % C::stages); };
       auto parity = [](int i) { return (uint32_t)((i / C::stages) & 1); };
-      auto scores = [&](int h, int i) {  // S_h = (X or Y) K_i^T
-        const uint64_t a = xd + (uint64_t)(h * tile16), k = kd + (uint64_t)(stage(2 * i) * tile16);
-#pragma unroll
-        for (int s = 0; s < D / 16; ++s) {
-          const uint32_t o = (s >> 2) * 1024 + (s & 3) * 2;
-          mma_ss(tbase + h * 128, a + o, k + o, id_s, s > 0);
-        }
-        mma_commit(&bar.sfull[h]);
-      };
-      auto values = [&](int h, int i) {  // O_h += P_h V_i
-        const uint64_t v = vd + (uint64_t)(stage(2 * i + 1) * tile16);
-#pragma unroll
-        for (int s = 0; s < KT / 16; ++s)
-          mma_ts(tbase + C::t_o + h * D, tbase + C::t_p + h * C::p_stride + s * 8,
-                 v + (uint64_t)(s * (2048 >> 4)), id_o, (i > 0 || s > 0) ? 1u : 0u);
-        mma_commit(&bar.pvdone[h]);
-      };
-      auto wait = [&](uint64_t* x, uint32_t par) { return mbar_wait(x, par, status, TO, abort_p); };
-      bool ok = wait(&bar.full[0], 0);
-      if (ok) {
+      auto wait = [&](uint64_t* x, uint32_t par) { return warp_wait(x, par, status, TO, abort_p); };
+      auto scores = [&](int i) {  // S = (X or Y) K_i^T
+        const uint32_t st = stage(2 * i);
+        const uint64_t k = kd + (uint64_t)(st * tile16);
         tc_fence_after();
-        scores(0, 0);
-        scores(1, 0);
-        mma_commit(&bar.empty[0]);
-      }
+        if (elect_one()) {
+#pragma unroll
+          for (int s = 0; s < D / 16; ++s) {
+            const uint32_t o = (s >> 2) * 1024 + (s & 3) * 2;
+            mma_ss(ts, xd + o, k + o, id_s, s > 0);
+          }
+          mma_commit(&bar.sfull[h]);
+          mma_commit(&bar.empty[st]);
+        }
+        __syncwarp();
+      };
+      auto values = [&](int i, auto half) {  // O += P V_i over 64 keys
+        const uint32_t st = stage(2 * i + 1);
+        const uint64_t v = vd + (uint64_t)(st * tile16);
+        tc_fence_after();
+        if (elect_one()) {
+#pragma unroll
+          for (int u = 0; u < KT / 32; ++u) {
+            const int s = half * (KT / 32) + u;
+            mma_ts(to, tp + s * 8, v + (uint64_t)(s * (2048 >> 4)), id_o, (i > 0 || s > 0) ? 1u : 0u);
+          }
+          if (half) {
+            mma_commit(&bar.pvdone[h]);
+            mma_commit(&bar.empty[st]);
+          }
+        }
+        __syncwarp();
+      };
+      uint64_t* const pfull = bar.pfull[PROBE ? 0 : h];
+      bool ok = wait(&bar.full[0], 0);
+      if (ok) scores(0);
       for (int i = 0; i < n && ok; ++i) {
         const bool more = i + 1 < n;
         if (more) ok = wait(&bar.full[stage(2 * i + 2)], parity(2 * i + 2));
         if (!C::overlay && more && ok) {
           // S has its own columns: the next scores as soon as the softmax has read these
-          for (int h = 0; h < 2 && ok; ++h) {
-            ok = wait(&bar.sfree[h], i & 1);
-            tc_fence_after();
-            if (ok) scores(h, i + 1);
-          }
-          if (ok) mma_commit(&bar.empty[stage(2 * i + 2)]);
+          ok = wait(&bar.sfree[h], i & 1);
+          if (ok) scores(i + 1);
         }
         ok = ok && wait(&bar.full[stage(2 * i + 1)], parity(2 * i + 1));
-        for (int h = 0; h < 2 && ok; ++h) {
-          if (!PROBE || h == 0) ok = wait(&bar.pfull[h], i & 1);
-          if (!ok) break;
-          tc_fence_after();
-          values(h, i);
-          if (h == 1) mma_commit(&bar.empty[stage(2 * i + 1)]);
-          // P overwrote S: the next scores follow the product that reads P (MMAs run in order)
-          if (C::overlay && more && !(PROBE && h == 0)) {
-            if (PROBE) scores(0, i + 1);
-            scores(h, i + 1);
-            if (h == 1) mma_commit(&bar.empty[stage(2 * i + 2)]);
-          }
-        }
+        // The weights of 64 keys at a time: the first product runs while the others are computed.
+        ok = ok && wait(&pfull[0], i & 1);
+        if (ok) values(i, std::integral_constant<int, 0>{});
+        ok = ok && wait(&pfull[1], i & 1);
+        if (ok) values(i, std::integral_constant<int, 1>{});
+        // P overwrote S: the next scores follow the product that reads P (MMAs run in order).
+        if (C::overlay && more && ok) scores(i + 1);
       }
       if (!ok) *abort_p = 1;
-      mma_commit(&bar.done);
+      if (elect_one()) mma_commit(&bar.done[h]);
+      __syncwarp();
       volatile int never = 0;
-      mbar_wait(&bar.done, 0, status, TO, &never);
+      mbar_wait(&bar.done[h], 0, status, TO, &never);
     }
     __syncwarp();
-  } else if (warp == 8) {
+  } else if (warp == NSOFT) {
     // ------------------------------------------------------------------ K/V loader
     const int frag = min(p.page, KT), nfrag = KT / frag;
     if (lane == 0) {
@@ -242,34 +281,40 @@ attend_tc_kernel(Params p, const __grid_constant__ CUtensorMap kmap,
     __syncwarp();
   } else {
     // ------------------------------------------------------------------ softmax + output
-    const int grp = warp >> 2, r = (warp & 3) * 32 + lane;
+    // A group is four warps, one per tensor-memory lane quarter. Softmax attention: groups 0 and 1
+    // take the two halves of block X's keys, 2 and 3 of block Y's. Probe: four quarters of the keys.
+    constexpr int NG = PROBE ? 4 : 2;              // groups that share a row
+    constexpr int NC = KT / NG;                    // keys of a tile per thread
+    const int r = (warp & 3) * 32 + lane;
+    const int h = PROBE ? 0 : warp >> 3;           // the row block of this thread's row
+    const int sub = PROBE ? warp >> 2 : (warp >> 2) & 1;
     const uint32_t lanes = tbase + ((uint32_t)((warp & 3) * 32) << 16);
-    const int h = PROBE ? 0 : grp;                 // which row block this thread's row is in
     const int t = token_of(h, r);
     const int pos = t >= 0 ? p0 + t : p1;          // rows that do not exist are not written
     const int q0 = PROBE ? p0 : min(p0 + h * per, p1), q1 = PROBE ? p1 : min(q0 + per - 1, p1);
     const float c2 = p.inv_h * kLog2e, slack = 8.f / c2;
     float m = -CUDART_INF_F, d1 = 0.f, d2 = 0.f;
+    // Exchange among the groups of a row: x[buffer][group][row].
     float* const xm = reinterpret_cast<float*>(smem + C::sm_x);
+    auto slot = [&](int buf, int g) -> float& { return xm[(buf * 4 + (PROBE ? g : h * 2 + g)) * 128 + r]; };
     int xphase = 0;  // phases of rowx used so far
     auto exchange = [&]() {
       __syncwarp();
-      if (lane == 0) mbar_arrive(&bar.rowx);
-      return warp_wait(&bar.rowx, (xphase++) & 1, status, TO, abort_p);
+      if (lane == 0) mbar_arrive(&bar.rowx[h]);
+      return warp_wait(&bar.rowx[h], (xphase++) & 1, status, TO, abort_p);
     };
     bool ok = true;
-    constexpr int NC = PROBE ? 64 : 128;           // keys of a tile per thread
     for (int i = 0; i < n; ++i) {
       ok = warp_wait(&bar.sfull[h], i & 1, status, TO, abort_p);
       if (PROBE) ok = ok && warp_wait(&bar.sfull[1], i & 1, status, TO, abort_p);
       if (!ok) break;
       tc_fence_after();
-      uint32_t s[NC / 32][32], tt[PROBE ? 2 : 1][32];
+      uint32_t s[NC / 32][32], tt[PROBE ? NC / 32 : 1][32];
 #pragma unroll
-      for (int c = 0; c < NC / 32; ++c) tmem_ld32(lanes + h * 128 + (PROBE ? grp * 64 : 0) + c * 32, s[c]);
+      for (int c = 0; c < NC / 32; ++c) tmem_ld32(lanes + h * 128 + sub * NC + c * 32, s[c]);
       if constexpr (PROBE) {
 #pragma unroll
-        for (int c = 0; c < 2; ++c) tmem_ld32(lanes + 128 + grp * 64 + c * 32, tt[c]);
+        for (int c = 0; c < NC / 32; ++c) tmem_ld32(lanes + 128 + sub * NC + c * 32, tt[c]);
       }
       tmem_ld_wait();
       if (!C::overlay) {
@@ -280,31 +325,38 @@ attend_tc_kernel(Params p, const __grid_constant__ CUtensorMap kmap,
           if (PROBE) mbar_arrive(&bar.sfree[1]);
         }
       }
-      const int k0 = range.tile(i0 + i) * KT, kb = k0 + (PROBE ? grp * 64 : 0);
+      const int k0 = range.tile(i0 + i) * KT, kb = k0 + sub * NC;
       if (!all_visible(p, q0, q1, k0, k0 + KT)) {
         // column c is visible when c <= hi and (c > lo or c < first)
         const int hi = pos - kb, lo = pos - p.window - kb, first = p.sinks - kb;
 #pragma unroll
         for (int c = 0; c < NC; ++c)
-          if (!(c <= hi && (c > lo || c < first))) s[c >> 5][c & 31] = 0xFF800000u;
+          if (!(c <= hi && (c > lo || c < first))) {
+            s[c >> 5][c & 31] = 0xFF800000u;
+            if constexpr (PROBE) tt[c >> 5][c & 31] = 0u;  // of a slot that may hold anything
+          }
       }
-      float tm = -CUDART_INF_F;
+      float t4[4] = {-CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F};
 #pragma unroll
-      for (int c = 0; c < NC; ++c) tm = fmaxf(tm, __uint_as_float(s[c >> 5][c & 31]));
-      if (PROBE) {
-        float* buf = xm + (i & 1) * 256;
-        buf[grp * 128 + r] = tm;
-        if (!(ok = exchange())) break;  // also: both groups have read S_X and S_Y
-        tm = fmaxf(buf[r], buf[128 + r]);
-      }
-      if (!C::overlay && i > 0) {
-        // the products that read the previous P (overlay: they precede this S in the pipe)
-        ok = warp_wait(&bar.pvdone[h], (i - 1) & 1, status, TO, abort_p);
-        if (PROBE) ok = ok && warp_wait(&bar.pvdone[1], (i - 1) & 1, status, TO, abort_p);
-        if (!ok) break;
+      for (int c = 0; c < NC; c += 2)
+        t4[(c >> 1) & 3] = max3(t4[(c >> 1) & 3], __uint_as_float(s[c >> 5][c & 31]), __uint_as_float(s[c >> 5][(c & 31) + 1]));
+      float tm = fmaxf(max3(t4[0], t4[1], t4[2]), t4[3]);
+      slot(i & 1, sub) = tm;
+      if (!(ok = exchange())) break;  // also: every group has read its scores, which P may overwrite
+#pragma unroll
+      for (int g = 0; g < NG; ++g) tm = fmaxf(tm, slot(i & 1, g));
+      // The products that read the previous P and O: where P overwrites S they precede this S in the
+      // pipe; otherwise they are waited for before O is rescaled or P written.
+      bool drained = C::overlay || i == 0;
+      auto drain = [&]() {
+        if (drained) return true;
+        drained = true;
+        bool d = warp_wait(&bar.pvdone[h], (i - 1) & 1, status, TO, abort_p);
+        if (PROBE) d = d && warp_wait(&bar.pvdone[1], (i - 1) & 1, status, TO, abort_p);
         tc_fence_after();
-      }
-      const bool grow = tm > m + slack || (m == -CUDART_INF_F && tm > m);
+        return d;
+      };
+      const bool grow = tm > m + slack || (m == -CUDART_INF_F && tm > m);  // alike in every group
       if (__any_sync(0xffffffffu, grow)) {
         float sc = 1.f;
         if (grow) {
@@ -314,9 +366,11 @@ attend_tc_kernel(Params p, const __grid_constant__ CUtensorMap kmap,
           d2 *= sc;
         }
         if (i > 0) {
-          const uint32_t o = lanes + C::t_o + grp * D;  // with a probe: each group one accumulator
+          if (!(ok = drain())) break;
+          // half of O_X or O_Y per group
+          const uint32_t o = lanes + C::t_o + (PROBE ? sub >> 1 : h) * D + (sub & 1) * (D / 2);
 #pragma unroll
-          for (int c = 0; c < D; c += 16) {
+          for (int c = 0; c < D / 2; c += 16) {
             uint32_t x[16];
             tmem_ld16(o + c, x);
             tmem_ld_wait();
@@ -326,56 +380,71 @@ attend_tc_kernel(Params p, const __grid_constant__ CUtensorMap kmap,
           }
         }
       }
-      const float ref = m == -CUDART_INF_F ? 0.f : m * c2;
-#pragma unroll
-      for (int c = 0; c < NC / 32; ++c) {
-        uint32_t w[16], wt[PROBE ? 16 : 1];
-        float sum = 0.f, sumt = 0.f;
-#pragma unroll
-        for (int e = 0; e < 32; e += 2) {
-          const float y0 = ex2(fmaf(__uint_as_float(s[c][e]), c2, -ref));
-          const float y1 = ex2(fmaf(__uint_as_float(s[c][e + 1]), c2, -ref));
-          sum += y0 + y1;
-          w[e / 2] = pack_bf16(y0, y1);
-          if constexpr (PROBE) {
-            const float z0 = s[c][e] == 0xFF800000u ? 0.f : y0 * __uint_as_float(tt[c][e]);
-            const float z1 = s[c][e + 1] == 0xFF800000u ? 0.f : y1 * __uint_as_float(tt[c][e + 1]);
-            sumt += z0 + z1;
-            wt[e / 2] = pack_bf16(z0, z1);
-          }
-        }
-        d1 += sum;
-        d2 += sumt;
-        tmem_st16(lanes + C::t_p + h * C::p_stride + (PROBE ? grp * 32 : 0) + c * 16, w);
-        if constexpr (PROBE) tmem_st16(lanes + C::t_p + C::p_stride + grp * 32 + c * 16, wt);
-      }
       if (k0 + KT > sq.len) {
         // the last page's slots past the sequence's end may hold anything: their weight is zero,
-        // and so must be the values (both groups write the same zeros; the products wait for both)
+        // and so must be the values
         const int x = 2 * i + 1, st = x % C::stages;
         if (!(ok = warp_wait(&bar.full[st], (x / C::stages) & 1, status, TO, abort_p))) break;
-        for (int e = tid & 127; e < (k0 + KT - sq.len) * (D / 8); e += 128) {
+        // every warp zeroes every row: its own arrival below is then enough for the products it lets go
+        for (int e = lane; e < (k0 + KT - sq.len) * (D / 8); e += 32) {
           const int row = sq.len - k0 + e / (D / 8), c = e % (D / 8);
           *reinterpret_cast<uint4*>(smem + C::sm_ring + st * C::tile + (c >> 3) * 16384 + row * 128 + (c & 7) * 16) =
               make_uint4(0u, 0u, 0u, 0u);
         }
         fence_proxy_async_smem();
       }
+      const float ref = m == -CUDART_INF_F ? 0.f : m * c2;
+      const uint64_t c22 = pair(c2, c2), ref2 = pair(-ref, -ref);
+      uint64_t sum[2] = {}, sumt[2] = {};  // pairs of partial sums
+#pragma unroll
+      for (int c = 0; c < NC / 32; ++c) {
+        uint32_t w[16], wt[PROBE ? 16 : 1];
+#pragma unroll
+        for (int e = 0; e < 32; e += 2) {
+          const uint64_t x = fma2(pair(__uint_as_float(s[c][e]), __uint_as_float(s[c][e + 1])), c22, ref2);
+          float y0, y1;
+          unpair(x, y0, y1);
+          y0 = ex2(y0);
+          y1 = ex2(y1);
+          const uint64_t y = pair(y0, y1);
+          sum[(e >> 1) & 1] = add2(sum[(e >> 1) & 1], y);
+          w[e / 2] = pack_bf16(y0, y1);
+          if constexpr (PROBE) {
+            const uint64_t z = mul2(y, pair(__uint_as_float(tt[c][e]), __uint_as_float(tt[c][e + 1])));
+            sumt[(e >> 1) & 1] = add2(sumt[(e >> 1) & 1], z);
+            float z0, z1;
+            unpair(z, z0, z1);
+            wt[e / 2] = pack_bf16(z0, z1);
+          }
+        }
+        if (!(ok = drain())) break;
+        tmem_st16(lanes + C::t_p + h * C::p_stride + sub * (NC / 2) + c * 16, w);
+        if constexpr (PROBE) tmem_st16(lanes + C::t_p + C::p_stride + sub * (NC / 2) + c * 16, wt);
+      }
+      if (!ok) break;
       tmem_st_wait();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&bar.pfull[h]);
+      if (lane == 0) mbar_arrive(&bar.pfull[h][PROBE ? sub >> 1 : sub]);
+      float a0, a1;
+      unpair(add2(sum[0], sum[1]), a0, a1);
+      d1 += a0 + a1;
+      unpair(add2(sumt[0], sumt[1]), a0, a1);
+      d2 += a0 + a1;
     }
 
-    if (PROBE && ok) {  // the groups' sums
-      float* buf = xm;
+    if (ok) {  // the groups' sums
       ok = exchange();  // the last maxima have been read
       if (ok) {
-        buf[grp * 128 + r] = d1;
-        buf[256 + grp * 128 + r] = d2;
+        slot(0, sub) = d1;
+        slot(1, sub) = d2;
         ok = exchange();
-        d1 = buf[r] + buf[128 + r];
-        d2 = buf[256 + r] + buf[384 + r];
+        d1 = d2 = 0.f;
+#pragma unroll
+        for (int g = 0; g < NG; ++g) {
+          d1 += slot(0, g);
+          d2 += slot(1, g);
+        }
       }
     }
     if (ok && n > 0) {
@@ -388,10 +457,9 @@ attend_tc_kernel(Params p, const __grid_constant__ CUtensorMap kmap,
       const long long id = t >= 0 ? rowid(t, r) : 0;
       const long long pid = (long long)part * p.tokens * p.Hq + id;
       float bad = 0.f;
-      constexpr int NO = PROBE ? D / 2 : D;  // output columns per thread
-      const int c0 = PROBE ? grp * NO : 0;
+      constexpr int NO = D / NG;  // output columns per thread
 #pragma unroll 1
-      for (int c = c0; c < c0 + NO; c += 16) {
+      for (int c = sub * NO; c < (sub + 1) * NO; c += 16) {
         uint32_t a[16], e[16];
         if (n > 0) {
           tmem_ld16(lanes + C::t_o + h * D + c, a);
@@ -427,20 +495,20 @@ attend_tc_kernel(Params p, const __grid_constant__ CUtensorMap kmap,
         dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
         dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
       }
-      if (t >= 0 && (!PROBE || grp == 0)) {
+      if (t >= 0 && sub == 0) {
         if (p.split > 1) p.part_s[pid] = make_float4(m, d1, d2, 0.f);
         else if (p.lse) p.lse[id] = d1 == 0.f ? -CUDART_INF_F : (m * c2 + log2f(d1)) * kLn2;
       }
       if (p.split == 1) {
-        // rows that are not finite, again by themselves (with a probe: once both groups have
-        // written their columns, by the first)
-        if (PROBE) {
-          ok = exchange();  // the sums have been read
-          if (ok) xm[grp * 128 + r] = bad;
-          ok = ok && exchange();
-          bad = xm[r] + xm[128 + r];
-        }
-        unsigned again = __ballot_sync(0xffffffffu, ok && t >= 0 && !(bad == 0.f) && (!PROBE || grp == 0));
+        // rows that are not finite, again by themselves: once every group has written its columns,
+        // by the first
+        ok = exchange();  // the sums have been read
+        if (ok) slot(0, sub) = bad;
+        ok = ok && exchange();
+        bad = 0.f;
+#pragma unroll
+        for (int g = 0; g < NG; ++g) bad += slot(0, g);
+        unsigned again = __ballot_sync(0xffffffffu, ok && t >= 0 && !(bad == 0.f) && sub == 0);
         while (again) {
           const int row = (warp & 3) * 32 + __ffs(again) - 1;
           again &= again - 1;
@@ -454,7 +522,7 @@ attend_tc_kernel(Params p, const __grid_constant__ CUtensorMap kmap,
 
   tc_fence_before();
   __syncthreads();
-  if (warp == 9) {
+  if (warp == NSOFT + 1) {
     tc_fence_after();
     tmem_dealloc(tbase, 512);
   }
@@ -466,15 +534,11 @@ cudaError_t launch_tc_t(const Params& p, cudaStream_t s) {
   cudaError_t err = encode_page_map(p, p.k, D, &kmap);
   if (err == cudaSuccess) err = encode_page_map(p, p.v, D, &vmap);
   if (err != cudaSuccess) return err;
-  auto kern = attend_tc_kernel<D, PROBE>;
-  err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D>::bytes);
-  if (err != cudaSuccess) return err;
   const int per = BM / p.g * (PROBE ? 1 : 2);
   const long long blocks = ((long long)p.tokens / per + p.B) * p.Hkv;
   if (blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-  kern<<<dim3((unsigned)blocks, p.split), NTHREADS, Cfg<D>::bytes, s>>>(p, kmap, vmap);
-  count_launch();
-  return cudaGetLastError();
+  return launch(attend_tc_kernel<D, PROBE>, dim3((unsigned)blocks, p.split), NTHREADS, Cfg<D>::bytes, 1, false, s,
+                p, kmap, vmap);
 }
 
 }  // namespace

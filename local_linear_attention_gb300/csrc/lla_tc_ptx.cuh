@@ -323,6 +323,19 @@ __host__ __device__ constexpr uint32_t idesc_bf16(int M, int N, bool a_mn_major,
          | ((uint32_t)(M >> 4) << 24);    // M / 16
 }
 
+// One lane of the (converged) warp: true for it only. Code that the whole warp runs and in which
+// only the instruction itself is under elect_one() keeps addresses and descriptors in uniform
+// registers; in a branch on the lane index every operand is moved there before each MMA.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(p));
+  return p != 0;
+}
+
 // ----------------------------------------------------------------------------- MMA
 // D[tmem] (+)= A[smem] x B[smem], issued by one thread. (Ordered against the other volatile
 // asm statements -- barrier waits, fences, commits -- without a memory clobber, so the compiler

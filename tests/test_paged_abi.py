@@ -17,18 +17,32 @@ def lla():
     return binding
 
 
+class CacheStruct(ctypes.Structure):
+    """lla_paged_cache, field by field."""
+    _fields_ = [(n, ctypes.c_void_p) for n in ("k_pages", "v_pages", "mass", "page_table", "lens")] + \
+        [(n, ctypes.c_int) for n in ("num_seqs", "kv_heads", "page_size", "max_pages", "num_pages", "d", "dv",
+                                     "dtype")] + [("reserved", ctypes.c_int * 2)]
+
+
+class QueryStruct(ctypes.Structure):
+    """lla_paged_query, field by field."""
+    _fields_ = [(n, ctypes.c_void_p) for n in ("q", "r", "out", "lse", "starts")] + \
+        [(n, ctypes.c_int) for n in ("tokens", "max_new", "q_heads")] + [("h", ctypes.c_float)] + \
+        [(n, ctypes.c_int) for n in ("window", "sinks", "track_mass", "path")] + [("reserved", ctypes.c_int * 2)]
+
+
 def cache(lla, **kw):
     f = dict(k_pages=256, v_pages=512, mass=768, page_table=1024, lens=1280, num_seqs=2, kv_heads=2,
              page_size=16, max_pages=8, num_pages=20, d=64, dv=64, dtype=1)
     f.update(kw)
-    return lla._CacheStruct(**f)
+    return CacheStruct(**f)
 
 
 def query(lla, **kw):
     f = dict(q=256, r=None, out=512, lse=None, starts=768, tokens=4, max_new=2, q_heads=4, h=8.0, window=0,
              sinks=0, track_mass=0, path=0)
     f.update(kw)
-    return lla._QueryStruct(**f)
+    return QueryStruct(**f)
 
 
 def attend(lla, c, q, ws=None, n=0):
@@ -36,7 +50,14 @@ def attend(lla, c, q, ws=None, n=0):
 
 
 def test_struct_sizes(lla):
-    assert ctypes.sizeof(lla._CacheStruct) == 80 and ctypes.sizeof(lla._QueryStruct) == 80
+    """The binding packs the same bytes."""
+    assert lla._CACHE.size == ctypes.sizeof(CacheStruct) and lla._QUERY.size == ctypes.sizeof(QueryStruct)
+    got = CacheStruct.from_buffer_copy(lla._CACHE.pack(*range(15)))
+    flat = [getattr(got, f[0]) or 0 for f in CacheStruct._fields_[:-1]] + list(got.reserved)
+    assert flat == list(range(15))
+    got = QueryStruct.from_buffer_copy(lla._QUERY.pack(1, 2, 3, 4, 5, 6, 7, 8, 9.0, *range(10, 16)))
+    flat = [getattr(got, f[0]) for f in QueryStruct._fields_[:-1]] + list(got.reserved)
+    assert flat == [1, 2, 3, 4, 5, 6, 7, 8, 9.0, *range(10, 16)]
 
 
 @pytest.mark.parametrize("kw,status", [
