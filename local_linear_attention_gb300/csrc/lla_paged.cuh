@@ -283,7 +283,8 @@ cudaError_t launch_attend_rows(const Params& p, int d, cudaStream_t s);
 // Sequences of many rows, bf16 with d = dv = 64 or 128 and g <= 128.
 cudaError_t launch_attend_tc(const Params& p, int d, cudaStream_t s);
 cudaError_t launch_mass_tc(const Params& p, int d, cudaStream_t s);
-cudaError_t encode_page_map(const Params& p, void* pages, int d, CUtensorMap* map);
+int tc_tokens(int d, bool probe, int g);  // tokens per block of launch_attend_tc
+cudaError_t encode_page_map(const Params& p, void* pages, int d, int kt, CUtensorMap* map);
 cudaError_t launch_append(const Params& p, const void* k_new, const void* v_new, int d, int dv,
                           int dtype, cudaStream_t s);
 // `p` is the source cache; the other arguments the destination and the choice.

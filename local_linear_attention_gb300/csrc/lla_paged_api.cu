@@ -145,14 +145,15 @@ Plan make_plan(const lla_paged_cache* c, const lla_paged_query* a) {
   }
   if (pl.tiles) {
     pl.tc = tc && g <= 128;
-    const long long BM = pl.tc ? (a->r ? 128 : 256) : rows <= 16 ? 16 : 64;
-    const long long per = pl.tc ? 128 / g * (a->r ? 1 : 2) : g < BM ? BM / g : 1, slices = (g + BM - 1) / BM;
+    const long long BM = pl.tc ? 128 : rows <= 16 ? 16 : 64;
+    const long long per = pl.tc ? tc_tokens(c->d, a->r != nullptr, g) : g < BM ? BM / g : 1;
+    const long long slices = (g + BM - 1) / BM;
     const long long by_tokens = (a->tokens + per - 1) / per;
     const long long tiles = (by_tokens > c->num_seqs ? by_tokens : c->num_seqs) * slices * c->kv_heads;
     // Few tiles: their keys are split until every SM has a block, down to 1024 keys (the start of a
     // block and the partial results cost about 8 of its 128-key steps); CUDA cores, whose steps are
-    // longer and whose blocks share an SM, down to 256 and for two blocks.
-    pl.tiles_split = pl.tc ? splits(tiles, 152, 1024, false) : splits(tiles, 304, 256);
+    // longer and whose blocks share an SM, down to one step of 64 and for two blocks.
+    pl.tiles_split = pl.tc ? splits(tiles, c->d == 128 ? 152 : 304, 1024, false) : splits(tiles, 304, 64);
     if (pl.tiles_split > 1) {
       const size_t all = (size_t)a->tokens * a->q_heads * pl.tiles_split;
       pl.tiles_s = take(all * sizeof(float4));

@@ -270,7 +270,7 @@ mass_tc_kernel(Params p, const __grid_constant__ CUtensorMap kmap, const __grid_
 template <int D>
 cudaError_t launch_t(const Params& p, cudaStream_t s) {
   CUtensorMap kmap, qmap;
-  cudaError_t err = encode_page_map(p, p.k, D, &kmap);
+  cudaError_t err = encode_page_map(p, p.k, D, KT, &kmap);
   if (err != cudaSuccess) return err;
   auto encode = tensor_map_encoder();
   const cuuint32_t ones[3] = {1, 1, 1};

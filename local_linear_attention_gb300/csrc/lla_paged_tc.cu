@@ -1,26 +1,28 @@
 // Attention over a paged cache for sequences with many rows (prompts and chunks), bf16, d = dv = 64
 // or 128, on the tensor cores (tcgen05, tensor memory, TMA).
 //
-// One pass over the keys with a running row maximum. Per 128-key tile a CTA runs two 128-row score
-// products and two 128-row value products, X and Y:
-//   softmax attention: X and Y are two blocks of 128 rows (tokens x grouped heads of one key/value
-//     head), S = Q K^T, P = exp(S - m), O += P V, each block with its own softmax warps, so one
-//     block's exponentials run while the tensor core works for the other;
-//   with a probe: X is Q, Y is R of the same 128 rows; P1 = exp(S_X - m), P2 = P1 .* S_Y, O1 += P1 V,
-//     O2 += P2 V.
-// Warps 0-15: softmax, a thread is a row and 64 (probe: 32) of a tile's keys, the row maximum goes
-// through shared memory. (With 8 warps and whole rows per thread the exponential chain of one warp
-// per scheduler was exposed.) 16: TMA loader (one lane per page fragment: a tile
-// spans 128 / page_size pages; rows past the sequence's end and bad pages are loaded as zeros by an
-// out-of-range coordinate); 17 and 18: the MMA issuers of X and Y.
-// Tensor memory: S_X, S_Y (128 columns each), O_X, O_Y (d each); bf16 P has columns of its own at
-// d = 64, and overwrites its S at d = 128 (512 columns are all there are), where the next S product
-// is issued behind the P V product that reads them.
+// One pass over the keys with a running row maximum. Per tile of KT keys and block of 128 rows
+// (tokens x grouped heads of one key/value head): S = Q K^T, P = exp(S - m), O += P V; with a probe
+// also T = R K^T, P2 = P .* T, O2 += P2 V. "Operand" below: Q of a block, or R.
+//   d = 128: one CTA per SM with two operands (512 tensor-memory columns: two S, two O). Softmax
+//     attention takes two row blocks, whose softmax and matrix products alternate: while one
+//     block's weights are computed the tensor core works for the other, and both read one key tile.
+//   d = 64: two CTAs per SM of 256 columns each, which alternate by themselves: one row block with
+//     128-key tiles, or with a probe Q and R with 64-key tiles.
+// Warps: softmax (a thread is a row and KT / NG of a tile's keys; the NG groups of four warps that
+// share a row block pass the row maximum through shared memory), then a TMA loader (one lane per
+// page fragment; rows past the sequence's end and bad pages are loaded as zeros by an out-of-range
+// coordinate) and one MMA issuer. Its code is warp-uniform with only the instructions under
+// elect_one(): issued from a branch on the lane index, an MMA took 75 cycles of operand moves
+// against 64 of tensor pipe, and that was the bound (chunk of 2048 at 32768, d = 128: 1.06 -> 0.85
+// ms). One issuer serves both blocks in turn; with an issuer each, their products interleave,
+// finish together and the two softmax phases run in step instead of alternating.
+// bf16 P has columns of its own where there is room (d = 64 without a probe: the next scores are
+// issued as soon as these are read), else it overwrites its S and the next score product is issued
+// behind the value product that reads P (MMAs run in order).
 // The accumulators are rescaled only when a row's maximum grows by more than 2^8 (the weights then
 // stay below 2^8, exact in scale; d1 is fp32): after the first tiles this hardly happens.
 // Rounding: p and p t enter the value products as bf16, d1 and d2 sum the unrounded fp32 weights.
-// What bounds it at d = 128: the chain softmax - value product - next score product of each block
-// against 2048 cycles of MMA per 256 rows x 128 keys.
 // All mbarrier waits are bounded.
 #include <type_traits>
 
@@ -34,28 +36,39 @@ namespace {
 
 using namespace tc;
 
-constexpr int BM = 128, KT = 128;
-constexpr int NSOFT = 16;                 // softmax warps
-constexpr int NTHREADS = (NSOFT + 3) * 32;
+constexpr int BM = 128;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
-template <int D>
+template <int D, bool PROBE>
 struct Cfg {
-  static constexpr int tile = BM * D * 2;        // bytes of a [128][D] bf16 tile: D/64 blocks of 16 KiB
-  static constexpr int stages = D == 128 ? 4 : 8;
-  static constexpr int sm_y = tile, sm_ring = 2 * tile;
+  static constexpr int kt = D == 64 && PROBE ? 64 : 128;       // keys per tile
+  static constexpr int blocks = D == 128 && !PROBE ? 2 : 1;    // row blocks
+  static constexpr int ops = blocks * (PROBE ? 2 : 1);         // operands: Q of each block, or Q and R
+  static constexpr int groups = D == 128 && PROBE ? 4 : 2;     // groups of four warps per row block
+  static constexpr int nsoft = blocks * groups * 4;            // softmax warps
+  static constexpr int threads = (nsoft + 2) * 32;
+  static constexpr int ctas = D == 64 ? 2 : 1;                 // per SM
+  static constexpr bool overlay = D == 128 || PROBE;           // P overwrites S
+  // tensor memory: S [ops][kt], O [ops][D], and P [ops][kt/2] unless it overlays S
+  static constexpr uint32_t t_o = ops * kt, t_p = overlay ? 0 : t_o + ops * D;
+  static constexpr uint32_t p_stride = overlay ? kt : kt / 2;
+  static constexpr uint32_t cols = D == 64 ? 256 : 512;
+  static_assert((overlay ? t_o + ops * D : t_p + ops * kt / 2) <= cols, "tensor memory");
+  // shared memory: operands [ops][D/64][128 rows][128 B], ring of key and value tiles
+  // [D/64][kt rows][128 B], barriers, row exchange [2 buffers][nsoft/4 groups][128]
+  static constexpr int op_bytes = BM * D * 2, tile = kt * D * 2, half = kt * 128;
+  static constexpr int stages = D == 128 ? 4 : PROBE ? 8 : 5;
+  static constexpr int sm_ring = ops * op_bytes;
   static constexpr int sm_bar = sm_ring + stages * tile;
-  static constexpr int sm_x = sm_bar + 512;      // row exchange: [2 buffers][4 groups][128]
-  static constexpr int bytes = sm_x + 4096 + 1024;  // 1024: aligning the base
-  static constexpr bool overlay = D == 128;
-  static constexpr uint32_t t_o = 256, t_p = overlay ? 0 : 384, p_stride = overlay ? 128 : 64;
+  static constexpr int sm_x = sm_bar + 512;
+  static constexpr int bytes = sm_x + 2 * (nsoft / 4) * BM * 4 + 1024;  // 1024: aligning the base
+  static_assert(ctas * (bytes + 1024) <= 227 * 1024, "shared memory");
 };
-static_assert(Cfg<128>::bytes <= 227 * 1024 && Cfg<64>::bytes <= 227 * 1024, "shared memory");
 
 struct Barriers {
   uint64_t full[8], empty[8];
   uint64_t sfull[2], sfree[2], pfull[2][2], pvdone[2];
-  uint64_t rowx[2], done[2];
+  uint64_t rowx[2], done;
 };
 static_assert(sizeof(Barriers) <= 512, "barrier region");
 
@@ -101,10 +114,11 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
 }
 
 template <int D, bool PROBE>
-__global__ void __launch_bounds__(NTHREADS, 1)
+__global__ void __launch_bounds__((Cfg<D, PROBE>::threads), (Cfg<D, PROBE>::ctas))
 attend_tc_kernel(Params p, const __grid_constant__ CUtensorMap kmap,
                  const __grid_constant__ CUtensorMap vmap) {
-  using C = Cfg<D>;
+  using C = Cfg<D, PROBE>;
+  constexpr int KT = C::kt;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   Barriers& bar = *reinterpret_cast<Barriers*>(smem + C::sm_bar);
@@ -112,7 +126,7 @@ attend_tc_kernel(Params p, const __grid_constant__ CUtensorMap kmap,
   __shared__ int abort_flag;
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   const int hk = blockIdx.x % p.Hkv, part = blockIdx.y;
-  const int per = BM / p.g, tokens = PROBE ? per : 2 * per;  // tokens per block and per tile
+  const int per = BM / p.g, tokens = C::blocks * per;  // tokens per row block and per CTA
   int b, tile;
   if (!find_tile(p, tokens, blockIdx.x / p.Hkv, &b, &tile)) return;
   const Seq sq = load_seq(p, b);
@@ -122,40 +136,40 @@ attend_tc_kernel(Params p, const __grid_constant__ CUtensorMap kmap,
   const int chunk = (range.count + p.split - 1) / p.split;
   const int i0 = min(range.count, part * chunk), n = min(range.count, i0 + chunk) - i0;
 
-  // Row r of block h: token and head; -1 when there is none.
+  // Row r of row block h: its token within the CTA, -1 when there is none.
   auto token_of = [&](int h, int r) {
-    const int t = (PROBE ? 0 : h * per) + r / p.g;
+    const int t = h * per + r / p.g;
     return r < per * p.g && t < ntok ? t : -1;
   };
   auto rowid = [&](int t, int r) -> long long {
     return (long long)(sq.t0 + tok0 + t) * p.Hq + hk * p.g + r % p.g;
   };
 
-  // X and Y tiles in the 128-byte swizzled layout (rows that do not exist are zero).
-  for (int e = tid; e < 2 * BM * (D / 8); e += NTHREADS) {
-    const int h = e / (BM * (D / 8)), r = (e / (D / 8)) % BM, c = e % (D / 8);
-    const int t = token_of(h, r);
-    const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(PROBE && h ? p.r : p.q);
+  // Operands in the 128-byte swizzled layout (rows that do not exist are zero).
+  for (int e = tid; e < C::ops * BM * (D / 8); e += C::threads) {
+    const int o = e / (BM * (D / 8)), r = (e / (D / 8)) % BM, c = e % (D / 8);
+    const int t = token_of(PROBE ? 0 : o, r);
+    const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(PROBE && o ? p.r : p.q);
     uint4 x = make_uint4(0u, 0u, 0u, 0u);
     if (t >= 0) x = *reinterpret_cast<const uint4*>(src + rowid(t, r) * D + c * 8);
-    *reinterpret_cast<uint4*>(smem + h * C::tile + (c >> 3) * 16384 + r * 128 + (((c & 7) ^ (r & 7)) * 16)) = x;
+    *reinterpret_cast<uint4*>(smem + o * C::op_bytes + (c >> 3) * 16384 + r * 128 + (((c & 7) ^ (r & 7)) * 16)) = x;
   }
   if (tid == 0) {
-    for (int s = 0; s < C::stages; ++s) { mbar_init(&bar.full[s], 1); mbar_init(&bar.empty[s], 2); }
+    for (int s = 0; s < C::stages; ++s) { mbar_init(&bar.full[s], 1); mbar_init(&bar.empty[s], 1); }
     for (int s = 0; s < 2; ++s) {
       mbar_init(&bar.sfull[s], 1);
-      mbar_init(&bar.sfree[s], PROBE ? 16 : 8);
-      mbar_init(&bar.pfull[s][0], PROBE ? 8 : 4);
-      mbar_init(&bar.pfull[s][1], PROBE ? 8 : 4);
-      mbar_init(&bar.rowx[s], PROBE ? 16 : 8);
+      mbar_init(&bar.sfree[s], C::groups * 4);
+      mbar_init(&bar.pfull[s][0], C::groups * 2);
+      mbar_init(&bar.pfull[s][1], C::groups * 2);
       mbar_init(&bar.pvdone[s], 1);
-      mbar_init(&bar.done[s], 1);
+      mbar_init(&bar.rowx[s], C::groups * 4);
     }
+    mbar_init(&bar.done, 1);
     abort_flag = 0;
     fence_mbar_init();
   }
-  if (warp == NSOFT + 1) {
-    tmem_alloc(&tmem_base_s, 512);
+  if (warp == C::nsoft + 1) {
+    tmem_alloc(&tmem_base_s, C::cols);
     tmem_relinquish();
   }
   fence_proxy_async_smem();
@@ -167,80 +181,89 @@ attend_tc_kernel(Params p, const __grid_constant__ CUtensorMap kmap,
   int* const status = p.status;
   constexpr int TO = kStatusTimeout;
 
-  if (warp > NSOFT) {
-    // ------------------------------------------------------------------ MMA issuers, one per block
-    const int h = warp - NSOFT - 1;
+  if (warp == C::nsoft + 1) {
+    // ------------------------------------------------------------------ MMA issuer
     if (n > 0) {
-      const uint64_t xd = smem_desc_sw128(smem_u32(smem + h * C::tile), 1024);
+      const uint64_t xd = smem_desc_sw128(smem_u32(smem), 1024);
       const uint64_t kd = smem_desc_sw128(smem_u32(smem + C::sm_ring), 1024);
-      const uint64_t vd = smem_desc_sw128_mn(smem_u32(smem + C::sm_ring), 16384, 1024);
-      const uint32_t ts = tbase + h * 128, to = tbase + C::t_o + h * D, tp = tbase + C::t_p + h * C::p_stride;
+      const uint64_t vd = smem_desc_sw128_mn(smem_u32(smem + C::sm_ring), C::half, 1024);
       constexpr uint32_t id_s = idesc_bf16(BM, KT, false, false);
       constexpr uint32_t id_o = idesc_bf16(BM, D, false, true);
       constexpr uint32_t tile16 = C::tile >> 4;
       auto stage = [](int i) { return (uint32_t)(i % C::stages); };
       auto parity = [](int i) { return (uint32_t)((i / C::stages) & 1); };
       auto wait = [&](uint64_t* x, uint32_t par) { return warp_wait(x, par, status, TO, abort_p); };
-      auto scores = [&](int i) {  // S = (X or Y) K_i^T
+      // S_o = operand o x K_i^T for operands o .. o + count - 1; the last ones of a tile free its stage
+      auto scores = [&](auto o0, auto count, int i) {
         const uint32_t st = stage(2 * i);
         const uint64_t k = kd + (uint64_t)(st * tile16);
         tc_fence_after();
         if (elect_one()) {
 #pragma unroll
-          for (int s = 0; s < D / 16; ++s) {
-            const uint32_t o = (s >> 2) * 1024 + (s & 3) * 2;
-            mma_ss(ts, xd + o, k + o, id_s, s > 0);
+          for (int o = o0; o < o0 + count; ++o) {
+#pragma unroll
+            for (int s = 0; s < D / 16; ++s)
+              mma_ss(tbase + o * KT, xd + (uint64_t)(o * (C::op_bytes >> 4) + (s >> 2) * 1024 + (s & 3) * 2),
+                     k + (uint64_t)((s >> 2) * (C::half >> 4) + (s & 3) * 2), id_s, s > 0);
+            mma_commit(&bar.sfull[o]);
           }
-          mma_commit(&bar.sfull[h]);
-          mma_commit(&bar.empty[st]);
+          if (o0 + count == C::ops) mma_commit(&bar.empty[st]);
         }
         __syncwarp();
       };
-      auto values = [&](int i, auto half) {  // O += P V_i over 64 keys
+      // O_o += P_o V_i over one half of the tile's keys
+      auto values = [&](auto o0, auto count, int i, auto half) {
         const uint32_t st = stage(2 * i + 1);
         const uint64_t v = vd + (uint64_t)(st * tile16);
         tc_fence_after();
         if (elect_one()) {
 #pragma unroll
-          for (int u = 0; u < KT / 32; ++u) {
-            const int s = half * (KT / 32) + u;
-            mma_ts(to, tp + s * 8, v + (uint64_t)(s * (2048 >> 4)), id_o, (i > 0 || s > 0) ? 1u : 0u);
+          for (int o = o0; o < o0 + count; ++o) {
+#pragma unroll
+            for (int u = 0; u < KT / 32; ++u) {
+              const int s = half * (KT / 32) + u;
+              mma_ts(tbase + C::t_o + o * D, tbase + C::t_p + o * C::p_stride + s * 8,
+                     v + (uint64_t)(s * (2048 >> 4)), id_o, (i > 0 || s > 0) ? 1u : 0u);
+            }
+            if (half) mma_commit(&bar.pvdone[o]);
           }
-          if (half) {
-            mma_commit(&bar.pvdone[h]);
-            mma_commit(&bar.empty[st]);
-          }
+          if (half && o0 + count == C::ops) mma_commit(&bar.empty[st]);
         }
         __syncwarp();
       };
-      uint64_t* const pfull = bar.pfull[PROBE ? 0 : h];
+      using I0 = std::integral_constant<int, 0>;
+      using I1 = std::integral_constant<int, 1>;
+      using Per = std::integral_constant<int, PROBE ? 2 : 1>;  // operands of a row block
+      // The weights of half a tile at a time: the first product runs while the others are computed.
+      auto block = [&](auto h, auto o, int i, bool more) {
+        bool ok = wait(&bar.pfull[h][0], i & 1);
+        if (ok) values(o, Per{}, i, I0{});
+        ok = ok && wait(&bar.pfull[h][1], i & 1);
+        if (ok) values(o, Per{}, i, I1{});
+        if (ok && C::overlay && more) scores(o, Per{}, i + 1);
+        return ok;
+      };
       bool ok = wait(&bar.full[0], 0);
-      if (ok) scores(0);
+      if (ok) scores(I0{}, std::integral_constant<int, C::ops>{}, 0);
       for (int i = 0; i < n && ok; ++i) {
         const bool more = i + 1 < n;
         if (more) ok = wait(&bar.full[stage(2 * i + 2)], parity(2 * i + 2));
-        if (!C::overlay && more && ok) {
-          // S has its own columns: the next scores as soon as the softmax has read these
-          ok = wait(&bar.sfree[h], i & 1);
-          if (ok) scores(i + 1);
+        if (!C::overlay && more && ok) {  // one operand with S of its own
+          ok = wait(&bar.sfree[0], i & 1);
+          if (ok) scores(I0{}, I1{}, i + 1);
         }
         ok = ok && wait(&bar.full[stage(2 * i + 1)], parity(2 * i + 1));
-        // The weights of 64 keys at a time: the first product runs while the others are computed.
-        ok = ok && wait(&pfull[0], i & 1);
-        if (ok) values(i, std::integral_constant<int, 0>{});
-        ok = ok && wait(&pfull[1], i & 1);
-        if (ok) values(i, std::integral_constant<int, 1>{});
-        // P overwrote S: the next scores follow the product that reads P (MMAs run in order).
-        if (C::overlay && more && ok) scores(i + 1);
+        ok = ok && block(I0{}, I0{}, i, more);
+        if (C::blocks == 2) ok = ok && block(I1{}, std::integral_constant<int, C::blocks - 1>{}, i, more);
       }
       if (!ok) *abort_p = 1;
-      if (elect_one()) mma_commit(&bar.done[h]);
+      if (elect_one()) mma_commit(&bar.done);
       __syncwarp();
       volatile int never = 0;
-      mbar_wait(&bar.done[h], 0, status, TO, &never);
+      mbar_wait(&bar.done, 0, status, TO, &never);
     }
     __syncwarp();
-  } else if (warp == NSOFT) {
+  } else if (warp == C::nsoft) {
     // ------------------------------------------------------------------ K/V loader
     const int frag = min(p.page, KT), nfrag = KT / frag;
     if (lane == 0) {
@@ -266,7 +289,7 @@ attend_tc_kernel(Params p, const __grid_constant__ CUtensorMap kmap,
           uint8_t* dst = smem + C::sm_ring + st * C::tile + lane * frag * 128;
 #pragma unroll
           for (int c = 0; c < D / 64; ++c)
-            tma_load_3d(dst + c * 16384, kv ? &vmap : &kmap, c * 64, j & (p.page - 1), c2, &bar.full[st]);
+            tma_load_3d(dst + c * C::half, kv ? &vmap : &kmap, c * 64, j & (p.page - 1), c2, &bar.full[st]);
         }
         issued = x + 1;
       }
@@ -281,13 +304,11 @@ attend_tc_kernel(Params p, const __grid_constant__ CUtensorMap kmap,
     __syncwarp();
   } else {
     // ------------------------------------------------------------------ softmax + output
-    // A group is four warps, one per tensor-memory lane quarter. Softmax attention: groups 0 and 1
-    // take the two halves of block X's keys, 2 and 3 of block Y's. Probe: four quarters of the keys.
-    constexpr int NG = PROBE ? 4 : 2;              // groups that share a row
-    constexpr int NC = KT / NG;                    // keys of a tile per thread
+    // A group is four warps, one per tensor-memory lane quarter.
+    constexpr int NG = C::groups;                  // groups that share a row block
+    constexpr int NC = KT / NG;                    // keys of a tile per thread: 64 or 32
     const int r = (warp & 3) * 32 + lane;
-    const int h = PROBE ? 0 : warp >> 3;           // the row block of this thread's row
-    const int sub = PROBE ? warp >> 2 : (warp >> 2) & 1;
+    const int h = (warp >> 2) / NG, sub = (warp >> 2) % NG;  // row block, group within it
     const uint32_t lanes = tbase + ((uint32_t)((warp & 3) * 32) << 16);
     const int t = token_of(h, r);
     const int pos = t >= 0 ? p0 + t : p1;          // rows that do not exist are not written
@@ -296,7 +317,7 @@ attend_tc_kernel(Params p, const __grid_constant__ CUtensorMap kmap,
     float m = -CUDART_INF_F, d1 = 0.f, d2 = 0.f;
     // Exchange among the groups of a row: x[buffer][group][row].
     float* const xm = reinterpret_cast<float*>(smem + C::sm_x);
-    auto slot = [&](int buf, int g) -> float& { return xm[(buf * 4 + (PROBE ? g : h * 2 + g)) * 128 + r]; };
+    auto slot = [&](int buf, int g) -> float& { return xm[((buf * C::blocks + h) * NG + g) * BM + r]; };
     int xphase = 0;  // phases of rowx used so far
     auto exchange = [&]() {
       __syncwarp();
@@ -311,19 +332,16 @@ attend_tc_kernel(Params p, const __grid_constant__ CUtensorMap kmap,
       tc_fence_after();
       uint32_t s[NC / 32][32], tt[PROBE ? NC / 32 : 1][32];
 #pragma unroll
-      for (int c = 0; c < NC / 32; ++c) tmem_ld32(lanes + h * 128 + sub * NC + c * 32, s[c]);
+      for (int c = 0; c < NC / 32; ++c) tmem_ld32(lanes + h * KT + sub * NC + c * 32, s[c]);
       if constexpr (PROBE) {
 #pragma unroll
-        for (int c = 0; c < NC / 32; ++c) tmem_ld32(lanes + 128 + sub * NC + c * 32, tt[c]);
+        for (int c = 0; c < NC / 32; ++c) tmem_ld32(lanes + KT + sub * NC + c * 32, tt[c]);
       }
       tmem_ld_wait();
       if (!C::overlay) {
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(&bar.sfree[h]);
-          if (PROBE) mbar_arrive(&bar.sfree[1]);
-        }
+        if (lane == 0) mbar_arrive(&bar.sfree[h]);
       }
       const int k0 = range.tile(i0 + i) * KT, kb = k0 + sub * NC;
       if (!all_visible(p, q0, q1, k0, k0 + KT)) {
@@ -351,8 +369,7 @@ attend_tc_kernel(Params p, const __grid_constant__ CUtensorMap kmap,
       auto drain = [&]() {
         if (drained) return true;
         drained = true;
-        bool d = warp_wait(&bar.pvdone[h], (i - 1) & 1, status, TO, abort_p);
-        if (PROBE) d = d && warp_wait(&bar.pvdone[1], (i - 1) & 1, status, TO, abort_p);
+        const bool d = warp_wait(&bar.pvdone[h], (i - 1) & 1, status, TO, abort_p);
         tc_fence_after();
         return d;
       };
@@ -367,10 +384,11 @@ attend_tc_kernel(Params p, const __grid_constant__ CUtensorMap kmap,
         }
         if (i > 0) {
           if (!(ok = drain())) break;
-          // half of O_X or O_Y per group
-          const uint32_t o = lanes + C::t_o + (PROBE ? sub >> 1 : h) * D + (sub & 1) * (D / 2);
+          // the row block's accumulators, an equal part per group
+          constexpr int part_cols = (PROBE ? 2 : 1) * D / NG;
+          const uint32_t o = lanes + C::t_o + h * D + sub * part_cols;
 #pragma unroll
-          for (int c = 0; c < D / 2; c += 16) {
+          for (int c = 0; c < part_cols; c += 16) {
             uint32_t x[16];
             tmem_ld16(o + c, x);
             tmem_ld_wait();
@@ -388,7 +406,7 @@ attend_tc_kernel(Params p, const __grid_constant__ CUtensorMap kmap,
         // every warp zeroes every row: its own arrival below is then enough for the products it lets go
         for (int e = lane; e < (k0 + KT - sq.len) * (D / 8); e += 32) {
           const int row = sq.len - k0 + e / (D / 8), c = e % (D / 8);
-          *reinterpret_cast<uint4*>(smem + C::sm_ring + st * C::tile + (c >> 3) * 16384 + row * 128 + (c & 7) * 16) =
+          *reinterpret_cast<uint4*>(smem + C::sm_ring + st * C::tile + (c >> 3) * C::half + row * 128 + (c & 7) * 16) =
               make_uint4(0u, 0u, 0u, 0u);
         }
         fence_proxy_async_smem();
@@ -425,7 +443,7 @@ attend_tc_kernel(Params p, const __grid_constant__ CUtensorMap kmap,
       tmem_st_wait();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&bar.pfull[h][PROBE ? sub >> 1 : sub]);
+      if (lane == 0) mbar_arrive(&bar.pfull[h][sub / (NG / 2)]);
       float a0, a1;
       unpair(add2(sum[0], sum[1]), a0, a1);
       d1 += a0 + a1;
@@ -522,42 +540,44 @@ attend_tc_kernel(Params p, const __grid_constant__ CUtensorMap kmap,
 
   tc_fence_before();
   __syncthreads();
-  if (warp == NSOFT + 1) {
+  if (warp == C::nsoft + 1) {
     tc_fence_after();
-    tmem_dealloc(tbase, 512);
+    tmem_dealloc(tbase, C::cols);
   }
 }
 
 template <int D, bool PROBE>
 cudaError_t launch_tc_t(const Params& p, cudaStream_t s) {
+  using C = Cfg<D, PROBE>;
   CUtensorMap kmap, vmap;
-  cudaError_t err = encode_page_map(p, p.k, D, &kmap);
-  if (err == cudaSuccess) err = encode_page_map(p, p.v, D, &vmap);
+  cudaError_t err = encode_page_map(p, p.k, D, C::kt, &kmap);
+  if (err == cudaSuccess) err = encode_page_map(p, p.v, D, C::kt, &vmap);
   if (err != cudaSuccess) return err;
-  const int per = BM / p.g * (PROBE ? 1 : 2);
-  const long long blocks = ((long long)p.tokens / per + p.B) * p.Hkv;
+  const long long blocks = ((long long)p.tokens / (BM / p.g * C::blocks) + p.B) * p.Hkv;
   if (blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-  return launch(attend_tc_kernel<D, PROBE>, dim3((unsigned)blocks, p.split), NTHREADS, Cfg<D>::bytes, 1, false, s,
-                p, kmap, vmap);
+  return launch(attend_tc_kernel<D, PROBE>, dim3((unsigned)blocks, p.split), C::threads, C::bytes, 1, false, s, p,
+                kmap, vmap);
 }
 
 }  // namespace
 
-// Tensor map of the pages ([num_pages * Hkv][page][d] bf16; boxes of one page fragment x 64
-// features, 128-byte swizzled).
-cudaError_t encode_page_map(const Params& p, void* pages, int d, CUtensorMap* map) {
+// Tensor map of the pages ([num_pages * Hkv][page][d] bf16; boxes of one page fragment, at most
+// kt rows, x 64 features, 128-byte swizzled).
+cudaError_t encode_page_map(const Params& p, void* pages, int d, int kt, CUtensorMap* map) {
   auto encode = tensor_map_encoder();
   if (!encode) return cudaErrorNotSupported;
   const cuuint32_t ones[3] = {1, 1, 1};
   const cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)p.page, (cuuint64_t)p.num_pages * p.Hkv};
   const cuuint64_t str[2] = {(cuuint64_t)d * 2, (cuuint64_t)p.page * d * 2};
-  const cuuint32_t box[3] = {64, (cuuint32_t)(p.page < 128 ? p.page : 128), 1};
+  const cuuint32_t box[3] = {64, (cuuint32_t)(p.page < kt ? p.page : kt), 1};
   return encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, pages, dims, str, box, ones,
                 CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
              ? cudaSuccess
              : cudaErrorInvalidValue;
 }
+
+int tc_tokens(int d, bool probe, int g) { return BM / g * (d == 128 && !probe ? 2 : 1); }
 
 cudaError_t launch_attend_tc(const Params& p, int d, cudaStream_t s) {
   if (p.r) return d == 128 ? launch_tc_t<128, true>(p, s) : launch_tc_t<64, true>(p, s);
