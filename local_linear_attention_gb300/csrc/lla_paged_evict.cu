@@ -45,20 +45,20 @@ __device__ __forceinline__ uint32_t order_key(float x) {
 }
 
 // Inclusive prefix sums of x over the block (every thread calls); *total gets the block's sum.
-__device__ __forceinline__ long long block_scan(long long x, long long* warp_sums, long long* total) {
+__device__ __forceinline__ int block_scan(int x, int* warp_sums, int* total) {
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const long long y = __shfl_up_sync(0xffffffffu, x, o);
+    const int y = __shfl_up_sync(0xffffffffu, x, o);
     if (lane >= o) x += y;
   }
   __syncthreads();  // the previous call's readers are done
   if (lane == 31) warp_sums[w] = x;
   __syncthreads();
-  long long before = 0, all = 0;
+  int before = 0, all = 0;
 #pragma unroll
   for (int i = 0; i < NT / 32; ++i) {
-    const long long y = warp_sums[i];
+    const int y = warp_sums[i];
     if (i < w) before += y;
     all += y;
   }
@@ -69,36 +69,45 @@ __device__ __forceinline__ long long block_scan(long long x, long long* warp_sum
 // STAGED: the CTA's keys fit its dynamic shared memory; otherwise they are read again per pass.
 template <bool STAGED>
 __global__ void __launch_bounds__(NT) select_kernel(Params p, Evict e) {
-  extern __shared__ uint32_t keys[];
-  __shared__ int hist[BINS];
-  __shared__ long long warp_sums[NT / 32];
-  __shared__ long long totals;        // this CTA's counts: (above T) << 32 | (equal to T)
+  extern __shared__ __align__(16) uint32_t keys[];
+  __shared__ __align__(16) int hist[BINS];
+  __shared__ int warp_sums[NT / 32];
+  __shared__ int2 warp_counts[NT / 32], totals;  // positions above T, equal to T
   __shared__ int found_bin, found_above;
   cg::cluster_group cluster = cg::this_cluster();
   const int C = cluster.num_blocks(), rank = cluster.block_rank();
+  auto sync = [&]() {
+    if (C == 1) __syncthreads();
+    else cluster.sync();
+  };
   const int pair = blockIdx.x / C, b = pair / p.Hkv, hk = pair % p.Hkv;
-  const int tid = threadIdx.x;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int cap = p.max_pages << p.page_shift;
   const int raw = p.lens[b], n = min(max(raw, 0), cap);
   if (raw != n && tid == 0) atomicOr(p.status, kStatusBadIndex);
   const int m = min(n, e.budget);
-  const int chunk = ((n + C - 1) / C + 31) / 32 * 32;
-  const int c0 = min(n, rank * chunk), c1 = min(n, c0 + chunk);
+  // this CTA's positions c0 .. c1-1, and each warp's share of them (multiples of 32 and 128)
+  const int share = ((n + C - 1) / C + 127) / 128 * 128;
+  const int c0 = min(n, rank * share), c1 = min(n, c0 + share);
   if (hk == 0 && rank == 0 && tid == 0) e.lens[b] = m;
 
-  auto read = [&](int j) -> uint32_t {
+  // Keys of positions j .. j+3 (j a multiple of 4: one page, one 16-byte load).
+  auto read4 = [&](int j) -> uint4 {
     const int pg = load_page(p, b, j >> p.page_shift);
-    return pg < 0 ? 0u : order_key(p.mass[((long long)pg * p.Hkv + hk) * p.page + (j & (p.page - 1))]);
+    if (pg < 0) return make_uint4(0u, 0u, 0u, 0u);
+    const float4 x = *reinterpret_cast<const float4*>(p.mass + ((long long)pg * p.Hkv + hk) * p.page + (j & (p.page - 1)));
+    return make_uint4(order_key(x.x), order_key(x.y), order_key(x.z), order_key(x.w));
   };
   // candidates: positions lo .. hi-1; `need` of them are kept
   const bool all = n <= e.budget;
   const int lo = all ? 0 : e.sinks, hi = all ? n : n - e.recent;
   int need = all ? n : m - e.sinks - e.recent;
   if (STAGED && !all) {
-    for (int j = c0 + tid; j < c1; j += NT) keys[j - c0] = read(j);
+#pragma unroll 4
+    for (int j = c0 + tid * 4; j < c1; j += NT * 4) *reinterpret_cast<uint4*>(keys + j - c0) = read4(j);
     __syncthreads();
   }
-  auto key = [&](int j) { return STAGED ? keys[j - c0] : read(j); };
+  auto keys4 = [&](int j) { return STAGED ? *reinterpret_cast<const uint4*>(keys + j - c0) : read4(j); };
 
   uint32_t T = 0xFFFFFFFFu;  // above every key: no candidate is kept
   if (!all && need > 0) {    // uniform over the cluster
@@ -110,70 +119,109 @@ __global__ void __launch_bounds__(NT) select_kernel(Params p, Evict e) {
       for (int i = tid; i < BINS; i += NT) hist[i] = 0;
       __syncthreads();
       const int down = shift - bits;
-      for (int j = max(c0, lo) + tid; j < min(c1, hi); j += NT) {
-        const uint32_t u = key(j);
-        if (pass == 0 || (u >> shift) == (T >> shift)) atomicAdd(&hist[(u >> down) & ((1u << bits) - 1u)], 1);
+#pragma unroll 2
+      for (int j = c0 + tid * 4; j < c1; j += NT * 4) {
+        const uint4 k = keys4(j);
+        const uint32_t u[4] = {k.x, k.y, k.z, k.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (j + i >= lo && j + i < hi && (pass == 0 || (u[i] >> shift) == (T >> shift)))
+            atomicAdd(&hist[(u[i] >> down) & ((1u << bits) - 1u)], 1);
       }
-      cluster.sync();
+      sync();
       // thread t sums bins 4t' .. 4t'+3 over the cluster, t' = NT-1-t: prefix sums run from the top
       const int top = (NT - 1 - tid) * 4;
       int c[4] = {};
       for (int r = 0; r < C; ++r) {
-        const int4 x = *reinterpret_cast<const int4*>(cluster.map_shared_rank(hist, r) + top);
+        const int4 x = *reinterpret_cast<const int4*>((C == 1 ? hist : cluster.map_shared_rank(hist, r)) + top);
         c[0] += x.x; c[1] += x.y; c[2] += x.z; c[3] += x.w;
       }
-      long long sum;
-      const long long upto = block_scan(c[0] + c[1] + c[2] + c[3], warp_sums, &sum);
-      const int above = (int)upto - (c[0] + c[1] + c[2] + c[3]);
-      if (above < need && need <= (int)upto) {  // exactly one thread: the need-th largest is here
+      int sum;
+      const int upto = block_scan(c[0] + c[1] + c[2] + c[3], warp_sums, &sum);
+      const int above = upto - (c[0] + c[1] + c[2] + c[3]);
+      if (above < need && need <= upto) {  // exactly one thread: the need-th largest is here
         int a = above, bin = 3;
         while (a + c[bin] < need) a += c[bin--];
         found_bin = top + bin;
         found_above = a;
       }
-      cluster.sync();  // found_* set; every CTA has read the histograms
+      sync();  // found_* set; every CTA has read the histograms
       T |= (uint32_t)found_bin << down;
       need -= found_above;
       shift = down;
     }
   }
   // Kept: protected positions and candidates above T, and the first `need` candidates equal to T
-  // (`all`: every position counts as protected).
-  auto flags = [&](int j) -> long long {
-    if (j >= c1) return 0;
-    if (all || j < lo || j >= hi) return 1ll << 32;
-    const uint32_t u = key(j);
-    return u > T ? 1ll << 32 : (u == T && T != 0xFFFFFFFFu) ? 1ll : 0ll;
+  // (`all`: every position counts as protected). A warp counts its positions, the block and the
+  // cluster add up the counts before it, and the warp numbers its kept positions by ballots.
+  const int own = (share / (NT / 32) + 31) / 32 * 32;
+  const int w0 = min(c1, c0 + warp * own), w1 = min(c1, w0 + own);
+  auto kinds = [&](int j, unsigned& gt, unsigned& eq) {  // of positions j .. j+31, this lane's j + lane
+    const int i = j + lane;
+    bool g = false, q = false;
+    if (i < w1) {
+      if (all || i < lo || i >= hi) {
+        g = true;
+      } else {
+        uint32_t u;
+        if (STAGED) {
+          u = keys[i - c0];
+        } else {
+          const int pg = load_page(p, b, i >> p.page_shift);
+          u = pg < 0 ? 0u : order_key(p.mass[((long long)pg * p.Hkv + hk) * p.page + (i & (p.page - 1))]);
+        }
+        g = u > T;
+        q = u == T && T != 0xFFFFFFFFu;
+      }
+    }
+    gt = __ballot_sync(0xffffffffu, g);
+    eq = __ballot_sync(0xffffffffu, q);
   };
-  long long mine_ = 0;
-  for (int j = c0 + tid; j < c1; j += NT) mine_ += flags(j);
-  long long total;
-  block_scan(mine_, warp_sums, &total);
+  int2 mine_ = make_int2(0, 0);
+  for (int j = w0; j < w1; j += 32) {
+    unsigned gt, eq;
+    kinds(j, gt, eq);
+    mine_.x += __popc(gt);
+    mine_.y += __popc(eq);
+  }
+  if (lane == 0) warp_counts[warp] = mine_;
+  __syncthreads();
+  int2 before = make_int2(0, 0), total = before;
+  for (int w = 0; w < NT / 32; ++w) {
+    const int2 x = warp_counts[w];
+    if (w < warp) before = make_int2(before.x + x.x, before.y + x.y);
+    total = make_int2(total.x + x.x, total.y + x.y);
+  }
   if (tid == 0) totals = total;
-  cluster.sync();
-  long long before = 0;
-  for (int r = 0; r < rank; ++r) before += *cluster.map_shared_rank(&totals, r);
+  if (C > 1) {
+    cluster.sync();
+    for (int r = 0; r < rank; ++r) {
+      const int2 x = *cluster.map_shared_rank(&totals, r);
+      before = make_int2(before.x + x.x, before.y + x.y);
+    }
+  }
+  let_next();
   const int want = all ? 0 : need;  // positions equal to T to keep
   int* kept = e.kept + (long long)pair * e.budget;
-  for (int j0 = c0; j0 < c1; j0 += NT) {
-    const int j = j0 + tid;
-    const long long f = flags(j);
-    long long sum;
-    const long long x = before + block_scan(f, warp_sums, &sum) - f;
-    const int eq = (int)(x & 0xFFFFFFFFll), gt = (int)(x >> 32);
-    if (f >> 32 || ((f & 1) && eq < want)) {
-      const int at = gt + min(eq, want);
-      if (at < m) kept[at] = j;
+  const unsigned lower = (1u << lane) - 1u;
+  for (int j = w0; j < w1; j += 32) {
+    unsigned gt, eq;
+    kinds(j, gt, eq);
+    const int g = before.x + __popc(gt & lower), q = before.y + __popc(eq & lower);
+    if (((gt >> lane) & 1u) || (((eq >> lane) & 1u) && q < want)) {
+      const int at = g + min(q, want);
+      if (at < m) kept[at] = j + lane;
     }
-    before += sum;
+    before = make_int2(before.x + __popc(gt), before.y + __popc(eq));
   }
   for (int i = m + rank * NT + tid; i < e.budget; i += C * NT) kept[i] = -1;
-  cluster.sync();  // `totals` stays readable until every CTA is done
+  if (C > 1) cluster.sync();  // `totals` stays readable until every CTA is done
 }
 
 // A warp moves 32 kept rows of one (sequence, head): keys of kw and values of vw 16-byte words.
 __global__ void __launch_bounds__(256) gather_kernel(Params p, Evict e, int kw, int vw, int blocks) {
   const int lane = threadIdx.x & 31;
+  wait_previous();
   const int pair = blockIdx.x / blocks, b = pair / p.Hkv, hk = pair % p.Hkv;
   const int i0 = (blockIdx.x % blocks) * 256 + (threadIdx.x & ~31);
   const int i = i0 + lane;
@@ -226,38 +274,22 @@ cudaError_t launch_evict(const Params& p, void* k, void* v, float* mass, const i
   const Evict e{k, v, mass, table, lens, kept, max_pages, num_pages, budget, sinks, recent};
   const long long pairs = (long long)p.B * p.Hkv;
   const long long cap = (long long)p.max_pages << p.page_shift;
-  // A cluster per (sequence, head), large enough to give every SM a CTA but no CTA fewer than 1024
-  // positions (below that the cluster's barriers cost more than they share).
+  // A cluster per (sequence, head), large enough to give every SM a CTA but no CTA fewer than 2048
+  // positions (below that the cluster's barriers cost more than it shares).
   int C = 1;
-  while (C < 8 && pairs * C < 152 && cap / (2 * C) >= 1024) C *= 2;
-  const long long share = ((cap + C - 1) / C + 31) / 32 * 32;
+  while (C < 8 && pairs * C < 152 && cap / (2 * C) >= 2048) C *= 2;
+  const long long share = ((cap + C - 1) / C + 127) / 128 * 128;
   const bool staged = share * 4 <= 160 * 1024;
-  const size_t bytes = staged ? (size_t)share * 4 : 0;
-  auto kern = staged ? select_kernel<true> : select_kernel<false>;
-  cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
-  if (err != cudaSuccess) return err;
   if (pairs * C > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(pairs * C));
-  cfg.blockDim = dim3(NT);
-  cfg.dynamicSmemBytes = bytes;
-  cfg.stream = s;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = (unsigned)C;
-  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  err = cudaLaunchKernelEx(&cfg, kern, p, e);
+  cudaError_t err = launch(staged ? select_kernel<true> : select_kernel<false>, dim3((unsigned)(pairs * C)), NT,
+                           staged ? (size_t)share * 4 : 0, C, false, s, p, e);
   if (err != cudaSuccess) return err;
-  count_launch();
   const int eb = dtype == LLA_F32 ? 4 : 2;
   const long long most = budget < cap ? budget : cap;
   const int blocks = (int)((most + 255) / 256);
   if (pairs * blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-  gather_kernel<<<(unsigned)(pairs * blocks), 256, 0, s>>>(p, e, d * eb / 16, dv * eb / 16, blocks);
-  count_launch();
-  return cudaGetLastError();
+  return launch(gather_kernel, dim3((unsigned)(pairs * blocks)), 256, 0, 1, true, s, p, e, d * eb / 16, dv * eb / 16,
+                blocks);
 }
 
 }  // namespace paged

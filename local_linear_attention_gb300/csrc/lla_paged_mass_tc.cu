@@ -27,7 +27,7 @@ template <int D>
 struct Cfg {
   static constexpr int tile = KT * D * 2;
   static constexpr int sm_q = tile;                  // two stages of row blocks
-  static constexpr int sm_lse = 3 * tile;            // [8 warps][128] lse * log2(e)
+  static constexpr int sm_lse = 3 * tile;            // [8 warps][128] -lse * log2(e)
   static constexpr int sm_sum = sm_lse + 8 * BR * 4; // [2][2 groups][128]
   static constexpr int sm_bar = sm_sum + 2 * 2 * KT * 4;
   static constexpr int bytes = sm_bar + 128 + 1024;
@@ -38,12 +38,6 @@ struct Barriers {
   uint64_t kfull, qfull[2], qempty[2], sfull[2], sfree[2], done;
 };
 static_assert(sizeof(Barriers) <= 128, "barrier region");
-
-__device__ __forceinline__ float ex2(float x) {
-  float r;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-  return r;
-}
 
 // Key tile `x` of this launch's sequences (as find_tile, over keys).
 __device__ __forceinline__ bool find_keys(const Params& p, int x, int* b_out, int* tile_out) {
@@ -197,50 +191,69 @@ mass_tc_kernel(Params p, const __grid_constant__ CUtensorMap kmap, const __grid_
       const float c2 = p.inv_h * kLog2e;
       const int j = k0 + r;
       float got = 0.f;
+      auto release = [&](int buf) {  // the scores have been read
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bar.sfree[buf]);
+      };
       for (int i = (done ^ grp) & 1; i < nblk; i += 2) {  // block counts of this group's parity
         const int c = done + i, tok0 = (from + i) * per;
-        // this block's lse (the warp's own copy)
+        // this block's -lse log2(e) (the warp's own copy)
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
           const int row = u * 32 + lane, t = tok0 + row / p.g;
           lse[row] = row < width && t < sq.n
-                         ? p.lse[(long long)(sq.t0 + t) * p.Hq + hk * p.g + row % p.g] * kLog2e
-                         : CUDART_INF_F;
+                         ? p.lse[(long long)(sq.t0 + t) * p.Hq + hk * p.g + row % p.g] * -kLog2e
+                         : -CUDART_INF_F;
         }
         __syncwarp();
         if (!warp_wait(&bar.sfull[grp], (c >> 1) & 1, status, TO, abort_p)) break;
         tc_fence_after();
         const int p0 = sq.first + tok0, p1 = p0 + per - 1;
-        const bool full = width == BR && tok0 + per <= sq.n && all_visible(p, p0, p1, k0, k0 + KT);
-        int pos = p0, u = 0;
-#pragma unroll 1
-        for (int cc = 0; cc < BR; cc += 32) {
-          uint32_t s[32];
-          tmem_ld32(lanes + grp * BR + cc, s);
-          tmem_ld_wait();
-          float a[4] = {};
-          if (full) {
+        // (the columns past `width` are zero scores with -lse = -infinity: nothing)
+        const bool full = tok0 + per <= sq.n && all_visible(p, p0, p1, k0, k0 + KT);
+        uint32_t s[2][32];
+        tmem_ld32(lanes + grp * BR, s[0]);
+        if (full) {
+          // the next 32 columns are on their way while these are added up
+          uint64_t a[2] = {};
+          const uint64_t c22 = pair(c2, c2);
+#pragma unroll
+          for (int q = 0; q < BR / 32; ++q) {
+            tmem_ld_wait();
+            if (q + 1 < BR / 32) tmem_ld32(lanes + grp * BR + (q + 1) * 32, s[(q + 1) & 1]);
+            else release(grp);
+            const uint32_t(&x)[32] = s[q & 1];
 #pragma unroll
             for (int e = 0; e < 32; e += 4) {
-              const float4 l = *reinterpret_cast<const float4*>(lse + cc + e);
-              a[0] += ex2(fmaf(__uint_as_float(s[e]), c2, -l.x));
-              a[1] += ex2(fmaf(__uint_as_float(s[e + 1]), c2, -l.y));
-              a[2] += ex2(fmaf(__uint_as_float(s[e + 2]), c2, -l.z));
-              a[3] += ex2(fmaf(__uint_as_float(s[e + 3]), c2, -l.w));
+              const float4 l = *reinterpret_cast<const float4*>(lse + q * 32 + e);
+              float y[4];
+              unpair(fma2(pair(__uint_as_float(x[e]), __uint_as_float(x[e + 1])), c22, pair(l.x, l.y)), y[0], y[1]);
+              unpair(fma2(pair(__uint_as_float(x[e + 2]), __uint_as_float(x[e + 3])), c22, pair(l.z, l.w)), y[2], y[3]);
+              a[0] = add2(a[0], pair(ex2(y[0]), ex2(y[1])));
+              a[1] = add2(a[1], pair(ex2(y[2]), ex2(y[3])));
             }
-          } else {
+          }
+          float y0, y1;
+          unpair(add2(a[0], a[1]), y0, y1);
+          got += y0 + y1;
+        } else {
+          int pos = p0, u = 0;
+          float a = 0.f;
+#pragma unroll 1
+          for (int cc = 0; cc < BR; cc += 32) {
+            if (cc) tmem_ld32(lanes + grp * BR + cc, s[0]);
+            tmem_ld_wait();
 #pragma unroll
             for (int e = 0; e < 32; ++e) {
               const bool row = cc + e < width && pos - sq.first < sq.n;
-              if (row && visible(p, pos, j)) a[e & 3] += ex2(fmaf(__uint_as_float(s[e]), c2, -lse[cc + e]));
+              if (row && visible(p, pos, j)) a += ex2(fmaf(__uint_as_float(s[0][e]), c2, lse[cc + e]));
               if (++u == p.g) { u = 0; ++pos; }
             }
           }
-          got += (a[0] + a[1]) + (a[2] + a[3]);
+          got += a;
+          release(grp);
         }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bar.sfree[grp]);
       }
       reinterpret_cast<float*>(smem + C::sm_sum)[((items & 1) * 2 + grp) * KT + r] = got;
     }

@@ -44,7 +44,9 @@ struct Cfg {
   static constexpr int kt = D == 64 && PROBE ? 64 : 128;       // keys per tile
   static constexpr int blocks = D == 128 && !PROBE ? 2 : 1;    // row blocks
   static constexpr int ops = blocks * (PROBE ? 2 : 1);         // operands: Q of each block, or Q and R
-  static constexpr int groups = D == 128 && PROBE ? 4 : 2;     // groups of four warps per row block
+  // groups of four warps per row block (d = 64, prompts of B4 T4096, 8 heads: 127 us with two, 138
+  // with one; with a probe 222 with two of 32 keys a thread, 195 with one of 64 and no exchange)
+  static constexpr int groups = D == 128 ? (PROBE ? 4 : 2) : (PROBE ? 1 : 2);
   static constexpr int nsoft = blocks * groups * 4;            // softmax warps
   static constexpr int threads = (nsoft + 2) * 32;
   static constexpr int ctas = D == 64 ? 2 : 1;                 // per SM
@@ -72,41 +74,6 @@ struct Barriers {
 };
 static_assert(sizeof(Barriers) <= 512, "barrier region");
 
-__device__ __forceinline__ float ex2(float x) {
-  float r;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-  return r;
-}
-__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
-}
-
-// Packed pairs of fp32 (one instruction per pair on this architecture).
-__device__ __forceinline__ uint64_t pair(float lo, float hi) {
-  uint64_t r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
-  return r;
-}
-__device__ __forceinline__ void unpair(uint64_t x, float& lo, float& hi) {
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(x));
-}
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
-}
-__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("add.rn.ftz.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float r;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
@@ -159,8 +126,8 @@ attend_tc_kernel(Params p, const __grid_constant__ CUtensorMap kmap,
     for (int s = 0; s < 2; ++s) {
       mbar_init(&bar.sfull[s], 1);
       mbar_init(&bar.sfree[s], C::groups * 4);
-      mbar_init(&bar.pfull[s][0], C::groups * 2);
-      mbar_init(&bar.pfull[s][1], C::groups * 2);
+      mbar_init(&bar.pfull[s][0], C::groups == 1 ? 4 : C::groups * 2);
+      mbar_init(&bar.pfull[s][1], C::groups == 1 ? 4 : C::groups * 2);
       mbar_init(&bar.pvdone[s], 1);
       mbar_init(&bar.rowx[s], C::groups * 4);
     }
@@ -320,6 +287,7 @@ attend_tc_kernel(Params p, const __grid_constant__ CUtensorMap kmap,
     auto slot = [&](int buf, int g) -> float& { return xm[((buf * C::blocks + h) * NG + g) * BM + r]; };
     int xphase = 0;  // phases of rowx used so far
     auto exchange = [&]() {
+      if (NG == 1) return true;
       __syncwarp();
       if (lane == 0) mbar_arrive(&bar.rowx[h]);
       return warp_wait(&bar.rowx[h], (xphase++) & 1, status, TO, abort_p);
@@ -359,10 +327,12 @@ attend_tc_kernel(Params p, const __grid_constant__ CUtensorMap kmap,
       for (int c = 0; c < NC; c += 2)
         t4[(c >> 1) & 3] = max3(t4[(c >> 1) & 3], __uint_as_float(s[c >> 5][c & 31]), __uint_as_float(s[c >> 5][(c & 31) + 1]));
       float tm = fmaxf(max3(t4[0], t4[1], t4[2]), t4[3]);
-      slot(i & 1, sub) = tm;
-      if (!(ok = exchange())) break;  // also: every group has read its scores, which P may overwrite
+      if (NG > 1) {
+        slot(i & 1, sub) = tm;
+        if (!(ok = exchange())) break;  // also: every group has read its scores, which P may overwrite
 #pragma unroll
-      for (int g = 0; g < NG; ++g) tm = fmaxf(tm, slot(i & 1, g));
+        for (int g = 0; g < NG; ++g) tm = fmaxf(tm, slot(i & 1, g));
+      }
       // The products that read the previous P and O: where P overwrites S they precede this S in the
       // pipe; otherwise they are waited for before O is rescaled or P written.
       bool drained = C::overlay || i == 0;
@@ -438,12 +408,15 @@ attend_tc_kernel(Params p, const __grid_constant__ CUtensorMap kmap,
         if (!(ok = drain())) break;
         tmem_st16(lanes + C::t_p + h * C::p_stride + sub * (NC / 2) + c * 16, w);
         if constexpr (PROBE) tmem_st16(lanes + C::t_p + C::p_stride + sub * (NC / 2) + c * 16, wt);
+        // half of the tile's weights are there: with this group's last, or, alone, halfway
+        if (c + 1 == NC / 32 || (NG == 1 && c + 1 == NC / 64)) {
+          tmem_st_wait();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bar.pfull[h][NG == 1 ? c / (NC / 64) : sub / ((NG + 1) / 2)]);
+        }
       }
       if (!ok) break;
-      tmem_st_wait();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&bar.pfull[h][sub / (NG / 2)]);
       float a0, a1;
       unpair(add2(sum[0], sum[1]), a0, a1);
       d1 += a0 + a1;
@@ -451,7 +424,7 @@ attend_tc_kernel(Params p, const __grid_constant__ CUtensorMap kmap,
       d2 += a0 + a1;
     }
 
-    if (ok) {  // the groups' sums
+    if (NG > 1 && ok) {  // the groups' sums
       ok = exchange();  // the last maxima have been read
       if (ok) {
         slot(0, sub) = d1;
@@ -520,12 +493,14 @@ attend_tc_kernel(Params p, const __grid_constant__ CUtensorMap kmap,
       if (p.split == 1) {
         // rows that are not finite, again by themselves: once every group has written its columns,
         // by the first
-        ok = exchange();  // the sums have been read
-        if (ok) slot(0, sub) = bad;
-        ok = ok && exchange();
-        bad = 0.f;
+        if (NG > 1) {
+          ok = exchange();  // the sums have been read
+          if (ok) slot(0, sub) = bad;
+          ok = ok && exchange();
+          bad = 0.f;
 #pragma unroll
-        for (int g = 0; g < NG; ++g) bad += slot(0, g);
+          for (int g = 0; g < NG; ++g) bad += slot(0, g);
+        }
         unsigned again = __ballot_sync(0xffffffffu, ok && t >= 0 && !(bad == 0.f) && sub == 0);
         while (again) {
           const int row = (warp & 3) * 32 + __ffs(again) - 1;
