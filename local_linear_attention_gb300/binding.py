@@ -468,23 +468,22 @@ def lla_paged_attention(q, cache: PagedCache, starts, h: float, r=None, max_new=
     them (window = 0) or the last `window` and the first `sinks`. track_mass adds the weights to
     cache.mass. max_new: a bound of the tokens of one sequence (default: all); giving it lets a
     decode step run as one."""
-    if out is None or lse is None:
-        if stream is not None:
-            with _on_stream(stream):
-                out = q.new_empty(q.shape[0], q.shape[1], cache.dv) if out is None else out
-                lse = q.new_empty(q.shape[0], q.shape[1], dtype=torch.float32) if lse is None else lse
-        else:
-            if out is None:
-                out = torch.empty((q.shape[0], q.shape[1], cache.dv), dtype=q.dtype, device=q.device) \
-                    if cache.dv != cache.d else torch.empty_like(q)
-            if lse is None:
-                lse = torch.empty(q.shape[:2], dtype=torch.float32, device=q.device)
-    query = _paged_query(q, cache, starts, h, r, max_new, window, sinks, track_mass, out, lse, path)
-    tokens, heads, _ = q.shape
-    _paged_rows("out", out, cache, (tokens, heads, cache.dv))
-    if lse.shape != (tokens, heads) or lse.dtype != torch.float32 or lse.device != cache.device \
-            or not lse.is_contiguous():
+    if out is not None:
+        _paged_rows("out", out, cache, (*q.shape[:2], cache.dv))
+    if lse is not None and (lse.shape != q.shape[:2] or lse.dtype != torch.float32 or
+                            lse.device != cache.device or not lse.is_contiguous()):
         raise ValueError("lse must be a contiguous float32 [tokens, q_heads] tensor on the cache's device")
+    if stream is None:
+        if out is None:
+            out = torch.empty_like(q) if cache.dv == cache.d else \
+                torch.empty((*q.shape[:2], cache.dv), dtype=q.dtype, device=q.device)
+        if lse is None:
+            lse = torch.empty(q.shape[:2], dtype=torch.float32, device=q.device)
+    else:
+        with _on_stream(stream):
+            out = q.new_empty((*q.shape[:2], cache.dv)) if out is None else out
+            lse = q.new_empty(q.shape[:2], dtype=torch.float32) if lse is None else lse
+    query = _paged_query(q, cache, starts, h, r, max_new, window, sinks, track_mass, out, lse, path)
     wp, wb = (0, 0) if workspace is None else (
         workspace.data_ptr(), workspace.numel() * workspace.element_size())
     st = _load().lla_paged_attention(cache._packed, query, wp, wb, _paged_stream(cache, stream))

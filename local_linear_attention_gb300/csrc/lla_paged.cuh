@@ -40,6 +40,7 @@ struct Params {
   float inv_h;
   int max_rows;       // most rows (new tokens x g) of any sequence, as the caller states
   int lo, hi;         // this launch takes the sequences with lo < rows <= hi
+  int beside;         // few-rows kernel: launched behind the tensor-core kernel, may overlap it
   // Split of each row's keys over blocks, and its partial results (split > 1).
   int split;
   float* part_o;     // [split][rows][branches][dv]   unnormalised O1 (and O2)

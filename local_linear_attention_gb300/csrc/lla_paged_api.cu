@@ -150,10 +150,10 @@ Plan make_plan(const lla_paged_cache* c, const lla_paged_query* a) {
     const long long slices = (g + BM - 1) / BM;
     const long long by_tokens = (a->tokens + per - 1) / per;
     const long long tiles = (by_tokens > c->num_seqs ? by_tokens : c->num_seqs) * slices * c->kv_heads;
-    // Few tiles: their keys are split until every SM has a block, down to 1024 keys (the start of a
-    // block and the partial results cost about 8 of its 128-key steps); CUDA cores, whose steps are
+    // Few tiles: their keys are split until every SM has a block, down to 512 keys (the start of a
+    // block and the partial results cost about 4 of its 128-key steps); CUDA cores, whose steps are
     // longer and whose blocks share an SM, down to one step of 64 and for two blocks.
-    pl.tiles_split = pl.tc ? splits(tiles, c->d == 128 ? 152 : 304, 1024, false) : splits(tiles, 304, 64);
+    pl.tiles_split = pl.tc ? splits(tiles, c->d == 128 ? 152 : 304, 512, false) : splits(tiles, 304, 64);
     if (pl.tiles_split > 1) {
       const size_t all = (size_t)a->tokens * a->q_heads * pl.tiles_split;
       pl.tiles_s = take(all * sizeof(float4));
@@ -183,12 +183,22 @@ int run_attention(const lla_paged_cache* c, const lla_paged_query* a, const Plan
   const long long rows = (long long)a->max_new * p.g;
   p.max_rows = rows < 0x7fffffffLL ? (int)rows : 0x7fffffff;
   if (a->track_mass && !a->lse) p.lse = reinterpret_cast<float*>(ws + pl.lse);
+  Params f = p;  // the few-rows kernel's
+  p.lo = pl.rows ? pl.row_cap : 0;
+  p.split = pl.tiles_split;
+  if (pl.tiles) {
+    if (p.split > 1) {
+      p.part_s = reinterpret_cast<float4*>(ws + pl.tiles_s);
+      p.part_o = reinterpret_cast<float*>(ws + pl.tiles_o);
+    }
+    if ((pl.tc ? launch_attend_tc(p, c->d, s) : launch_attend_cc(p, c->d, c->dv, c->dtype, s)) != cudaSuccess)
+      return LLA_ERR_CUDA;
+  }
   if (pl.rows) {
-    Params f = p;
     f.lo = 0;
-    f.hi = pl.row_cap;
+    f.hi = f.row_cap = pl.row_cap;
     f.split = pl.rows_split;
-    f.row_cap = pl.row_cap;
+    f.beside = pl.tiles && pl.tc;
     if (pl.rows_split > kRowsCluster) {
       f.part_s = reinterpret_cast<float4*>(ws + pl.rows_s);
       f.part_o = reinterpret_cast<float*>(ws + pl.rows_o);
@@ -200,14 +210,6 @@ int run_attention(const lla_paged_cache* c, const lla_paged_query* a, const Plan
     if (launch_attend_rows(f, c->d, s) != cudaSuccess) return LLA_ERR_CUDA;
   }
   if (pl.tiles) {
-    p.lo = pl.rows ? pl.row_cap : 0;
-    p.split = pl.tiles_split;
-    if (p.split > 1) {
-      p.part_s = reinterpret_cast<float4*>(ws + pl.tiles_s);
-      p.part_o = reinterpret_cast<float*>(ws + pl.tiles_o);
-    }
-    if ((pl.tc ? launch_attend_tc(p, c->d, s) : launch_attend_cc(p, c->d, c->dv, c->dtype, s)) != cudaSuccess)
-      return LLA_ERR_CUDA;
     if (p.split > 1 && launch_join(p, c->d, c->dv, c->dtype, s) != cudaSuccess) return LLA_ERR_CUDA;
     if (a->track_mass && (pl.tc ? launch_mass_tc(p, c->d, s) : launch_mass_cc(p, c->d, c->dtype, s)) != cudaSuccess)
       return LLA_ERR_CUDA;

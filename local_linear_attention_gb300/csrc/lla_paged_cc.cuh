@@ -45,14 +45,22 @@ __device__ __forceinline__ float4 ld4(const __nv_bfloat16* p) {
                      __uint_as_float(w.y << 16), __uint_as_float(w.y & 0xFFFF0000u));
 }
 
-// Stages rows of a [.., W] array as fp32; addr(row) gives a row's first element or nullptr (zeros).
-template <int W, int PITCH, typename T, typename Addr>
-__device__ __forceinline__ void stage(float* dst, int rows, Addr addr) {
-  for (int e = threadIdx.x; e < rows * (W / 4); e += NT) {
-    const int row = e / (W / 4), c = (e % (W / 4)) * 4;
-    const T* src = addr(row);
-    const float4 x = src ? ld4(src + c) : make_float4(0.f, 0.f, 0.f, 0.f);
-    *reinterpret_cast<float4*>(dst + row * PITCH + c) = x;
+// Stages ROWS rows of a [.., W] array as fp32; addr(row) gives a row's first element or nullptr
+// (zeros). All loads of a thread are issued before the first store.
+template <int W, int PITCH, int ROWS, typename T, typename Addr>
+__device__ __forceinline__ void stage(float* dst, Addr addr) {
+  constexpr int N = (ROWS * (W / 4) + NT - 1) / NT;
+  float4 x[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const int e = threadIdx.x + i * NT, row = e / (W / 4), c = (e % (W / 4)) * 4;
+    const T* src = row < ROWS ? addr(row) : nullptr;
+    x[i] = src ? ld4(src + c) : make_float4(0.f, 0.f, 0.f, 0.f);
+  }
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const int e = threadIdx.x + i * NT, row = e / (W / 4), c = (e % (W / 4)) * 4;
+    if (row < ROWS) *reinterpret_cast<float4*>(dst + row * PITCH + c) = x[i];
   }
 }
 
@@ -98,9 +106,9 @@ __global__ void __launch_bounds__(NT) attend_cc_kernel(Params p) {
   auto rowid = [&](int row) -> long long {             // row of q, r, out (flat [tokens * Hq])
     return (long long)(sq.t0 + tok0 + row / width) * p.Hq + hk * p.g + u0 + row % width;
   };
-  stage<D, S::QP, T>(sm + S::q, BM, [&](int row) { return row < nrows ? qg + rowid(row) * D : (const T*)nullptr; });
+  stage<D, S::QP, BM, T>(sm + S::q, [&](int row) { return row < nrows ? qg + rowid(row) * D : (const T*)nullptr; });
   if (PROBE)
-    stage<D, S::QP, T>(sm + S::r, BM, [&](int row) { return row < nrows ? rg + rowid(row) * D : (const T*)nullptr; });
+    stage<D, S::QP, BM, T>(sm + S::r, [&](int row) { return row < nrows ? rg + rowid(row) * D : (const T*)nullptr; });
 
   const int p0 = sq.first + tok0, p1 = p0 + ntok - 1;
   const TileRange<KT> range(p, p0, p1);
@@ -134,8 +142,8 @@ __global__ void __launch_bounds__(NT) attend_cc_kernel(Params p) {
       const int pg = load_page(p, b, j >> p.page_shift);
       return pg < 0 ? -1 : ((long long)pg * p.Hkv + hk) * p.page + (j & (p.page - 1));
     };
-    stage<D, S::KP, T>(sm + S::k, KT, [&](int row) { const long long s = slot(row); return s < 0 ? (const T*)nullptr : kg + s * D; });
-    stage<DV, DV, T>(sm + S::v, KT, [&](int row) { const long long s = slot(row); return s < 0 ? (const T*)nullptr : vg + s * DV; });
+    stage<D, S::KP, KT, T>(sm + S::k, [&](int row) { const long long s = slot(row); return s < 0 ? (const T*)nullptr : kg + s * D; });
+    stage<DV, DV, KT, T>(sm + S::v, [&](int row) { const long long s = slot(row); return s < 0 ? (const T*)nullptr : vg + s * DV; });
     __syncthreads();
     float s[RM][4] = {}, t[PROBE ? RM : 1][4] = {};
     dots<RM, D, S::KP>(sm + S::q + ty * RM * S::QP, sm + S::k + tx * S::KP, s);
@@ -260,7 +268,7 @@ __global__ void __launch_bounds__(NT) mass_cc_kernel(Params p) {
   if (k0 >= sq.len || !mine(p, sq.n)) return;
   const T* qg = static_cast<const T*>(p.q);
   const T* kg = static_cast<const T*>(p.k);
-  stage<D, S::KP, T>(sm + S::k, KT, [&](int row) {
+  stage<D, S::KP, KT, T>(sm + S::k, [&](int row) {
     const int j = k0 + row;
     const int pg = j < sq.len ? load_page(p, b, j >> p.page_shift) : -1;
     return pg < 0 ? (const T*)nullptr : kg + (((long long)pg * p.Hkv + hk) * p.page + (j & (p.page - 1))) * D;
@@ -271,7 +279,7 @@ __global__ void __launch_bounds__(NT) mass_cc_kernel(Params p) {
     const int p0 = sq.first + r0 / p.g, p1 = sq.first + min(rows - 1, r0 + BM - 1) / p.g;
     if (p1 < k0 || !(k0 + KT > p0 - p.window || k0 < p.sinks)) continue;
     __syncthreads();
-    stage<D, S::QP, T>(sm + S::q, BM, [&](int row) {
+    stage<D, S::QP, BM, T>(sm + S::q, [&](int row) {
       const int x = r0 + row;
       return x < rows ? qg + ((long long)(sq.t0 + x / p.g) * p.Hq + hk * p.g + x % p.g) * D : (const T*)nullptr;
     });
@@ -321,15 +329,17 @@ __global__ void __launch_bounds__(128) join_kernel(Params p, int d) {
   const Seq sq = load_seq(p, b);
   if (token < sq.t0 || token >= sq.t0 + sq.n || !mine(p, sq.n)) return;
   float m = -CUDART_INF_F;
-  for (int s = 0; s < p.split; ++s) m = fmaxf(m, p.part_s[s * rows + id].x);
+  for (int s = lane; s < p.split; s += 32) m = fmaxf(m, p.part_s[s * rows + id].x);
+#pragma unroll
+  for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
   const float ref = m == -CUDART_INF_F ? 0.f : m;
   float d1 = 0.f, d2 = 0.f;
   constexpr int NC = (DV + 31) / 32;
   float o1[NC] = {}, o2[NC] = {};
+#pragma unroll 4
   for (int s = 0; s < p.split; ++s) {
     const float4 st = p.part_s[s * rows + id];
-    const float sc = expf((st.x - ref) * p.inv_h);
-    if (st.x == -CUDART_INF_F) continue;
+    const float sc = expf((st.x - ref) * p.inv_h);  // 0 where the split saw nothing
     d1 = fmaf(st.y, sc, d1);
     d2 = fmaf(st.z, sc, d2);
     const float* src = p.part_o + (s * rows + id) * (PROBE ? 2 : 1) * DV;

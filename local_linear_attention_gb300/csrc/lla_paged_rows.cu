@@ -110,6 +110,10 @@ __global__ void __launch_bounds__(NW * 32) attend_rows_kernel(Params p) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   // the parts of a pair follow one another: clusters are made of neighbours
   const int pair = blockIdx.x / p.split, b = pair / p.Hkv, hk = pair % p.Hkv, part = blockIdx.x % p.split;
+  let_next();
+  // Set up behind the tiled kernel of the same call, this one may run beside its last blocks (they
+  // share no output); one thread's wait makes the end of this grid the end of both.
+  if (p.beside && blockIdx.x == 0 && threadIdx.x == 0) wait_previous();
   const Seq sq = load_seq(p, b);
   if (!mine(p, sq.n)) {
     if (sq.n > 0 && sq.n * p.g > p.max_rows) atomicOr(p.status, kStatusBadIndex);  // beyond max_new
@@ -297,7 +301,6 @@ __global__ void __launch_bounds__(NW * 32) attend_rows_kernel(Params p) {
     if (++stage == C::stages) stage = 0;
   }
   cp_async_wait<0>();
-  let_next();
   __syncthreads();  // the rings are free
 
   // Join of the four warps through shared memory: O [warp][16][D + 4], {m, d1, d2}.
@@ -474,7 +477,7 @@ cudaError_t launch_rows_t(const Params& p, cudaStream_t s) {
   if ((long long)pairs * p.split > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
   const bool cluster = p.split > 1 && p.split <= kRowsCluster;
   auto kern = cluster ? attend_rows_kernel<D, PROBE, LOGITS, true> : attend_rows_kernel<D, PROBE, LOGITS, false>;
-  cudaError_t err = launch(kern, dim3(pairs * p.split), NW * 32, Cfg<D>::bytes, cluster ? p.split : 1, false, s, p);
+  cudaError_t err = launch(kern, dim3(pairs * p.split), NW * 32, Cfg<D>::bytes, cluster ? p.split : 1, p.beside != 0, s, p);
   if (err == cudaSuccess && !cluster && p.split > 1) {
     const long long rows = (long long)pairs * p.row_cap;
     err = launch(join_rows_kernel<D, PROBE>, dim3((unsigned)((rows + 3) / 4)), 128, 0, 1, true, s, p);

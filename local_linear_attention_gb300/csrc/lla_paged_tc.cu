@@ -93,6 +93,7 @@ attend_tc_kernel(Params p, const __grid_constant__ CUtensorMap kmap,
   __shared__ int abort_flag;
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   const int hk = blockIdx.x % p.Hkv, part = blockIdx.y;
+  let_next();  // the few-rows kernel of the same call, which does not depend on this one
   const int per = BM / p.g, tokens = C::blocks * per;  // tokens per row block and per CTA
   int b, tile;
   if (!find_tile(p, tokens, blockIdx.x / p.Hkv, &b, &tile)) return;
