@@ -34,7 +34,7 @@ struct Params {
   const int* table;   // [B, max_pages]
   const int* lens;    // [B]
   int* status;
-  int B, tokens, Hq, Hkv, g;
+  int B, tokens, Hq, Hkv, g, d, dv;
   int page, page_shift, max_pages, num_pages;
   int window, sinks;  // window = kNoWindow when there is none
   float inv_h;
@@ -148,8 +148,8 @@ __device__ __forceinline__ bool find_tile(const Params& p, int per, int x, int* 
 // the value is infinite or NaN; a row whose result is not finite is therefore taken again here
 // (and stays NaN only if a key that it sees makes it so). Slow, and off every ordinary path.
 template <typename T>
-__device__ __noinline__ void exact_row(const Params& p, int d, int dv, int b, int pos, int token,
-                                       int head) {
+__device__ __noinline__ void exact_row(const Params& p, int b, int pos, int token, int head) {
+  const int d = p.d, dv = p.dv;
   const int lane = threadIdx.x & 31, hk = head / p.g;
   const T* q = static_cast<const T*>(p.q) + ((long long)token * p.Hq + head) * d;
   const T* r = p.r ? static_cast<const T*>(p.r) + ((long long)token * p.Hq + head) * d : nullptr;
@@ -301,26 +301,29 @@ cudaError_t attend_cc_f32(const Params& p, int d, int dv, cudaStream_t s);
 cudaError_t attend_cc_bf16(const Params& p, int d, int dv, cudaStream_t s);
 cudaError_t mass_cc_f32(const Params& p, int d, cudaStream_t s);
 cudaError_t mass_cc_bf16(const Params& p, int d, cudaStream_t s);
-cudaError_t join_f32(const Params& p, int d, int dv, cudaStream_t s);
-cudaError_t join_bf16(const Params& p, int d, int dv, cudaStream_t s);
+cudaError_t join_f32(const Params& p, int dv, cudaStream_t s);
+cudaError_t join_bf16(const Params& p, int dv, cudaStream_t s);
 inline cudaError_t launch_attend_cc(const Params& p, int d, int dv, int dtype, cudaStream_t s) {
   return dtype == LLA_F32 ? attend_cc_f32(p, d, dv, s) : attend_cc_bf16(p, d, dv, s);
 }
 inline cudaError_t launch_mass_cc(const Params& p, int d, int dtype, cudaStream_t s) {
   return dtype == LLA_F32 ? mass_cc_f32(p, d, s) : mass_cc_bf16(p, d, s);
 }
-inline cudaError_t launch_join(const Params& p, int d, int dv, int dtype, cudaStream_t s) {
-  return dtype == LLA_F32 ? join_f32(p, d, dv, s) : join_bf16(p, d, dv, s);
+inline cudaError_t launch_join(const Params& p, int dv, int dtype, cudaStream_t s) {
+  return dtype == LLA_F32 ? join_f32(p, dv, s) : join_bf16(p, dv, s);
 }
-// Sequences of few rows (p.hi = rows_limit of them at most), bf16 with d = dv = 64 or 128: the
-// attention, the join of its splits and, with p.logits, the weight tracking.
+// The tensor-core kernels (bf16) are built for head sizes D = 64 and 128 and take smaller ones
+// padded with zeros in shared memory: zero features add nothing to a product. D of a call:
+inline int padded(int d) { return d > 64 ? 128 : 64; }
+// Sequences of few rows (p.hi = rows_limit of them at most): the attention, the join of its splits
+// and, with p.logits, the weight tracking. D = padded(max(d, dv)).
 constexpr int kRowsCluster = 8;  // splits that join within a cluster (the portable size)
 inline int rows_limit(bool probe) { return probe ? 8 : 16; }
-cudaError_t launch_attend_rows(const Params& p, int d, cudaStream_t s);
-// Sequences of many rows, bf16 with d = dv = 64 or 128 and g <= 128.
-cudaError_t launch_attend_tc(const Params& p, int d, cudaStream_t s);
-cudaError_t launch_mass_tc(const Params& p, int d, cudaStream_t s);
-int tc_tokens(int d, bool probe, int g);  // tokens per block of launch_attend_tc
+cudaError_t launch_attend_rows(const Params& p, int D, cudaStream_t s);
+// Sequences of many rows, g <= 128; launch_mass_tc with D = padded(d).
+cudaError_t launch_attend_tc(const Params& p, int D, cudaStream_t s);
+cudaError_t launch_mass_tc(const Params& p, int D, cudaStream_t s);
+int tc_tokens(int D, bool probe, int g);  // tokens per block of launch_attend_tc
 cudaError_t encode_page_map(const Params& p, void* pages, int d, int kt, CUtensorMap* map);
 cudaError_t launch_append(const Params& p, const void* k_new, const void* v_new, int d, int dv,
                           int dtype, cudaStream_t s);

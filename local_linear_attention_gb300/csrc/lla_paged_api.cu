@@ -67,6 +67,8 @@ Params cache_params(const lla_paged_cache* c) {
   p.g = 1;
   p.page = c->page_size;
   while ((1 << p.page_shift) < c->page_size) ++p.page_shift;
+  p.d = c->d;
+  p.dv = c->dv;
   p.max_pages = c->max_pages;
   p.num_pages = c->num_pages;
   p.window = kNoWindow;
@@ -98,6 +100,7 @@ struct Plan {
   bool rows = false;   // the few-rows kernel takes the sequences of at most rows_limit rows
   bool tiles = false;  // a tiled kernel the others: tensor cores (tc) or CUDA cores
   bool tc = false;
+  int D = 0;           // head size of the tensor-core kernels
   int rows_split = 1, tiles_split = 1;
   int row_cap = 0, keys_cap = 0;
   size_t rows_s = 0, rows_o = 0, logits = 0, tiles_s = 0, tiles_o = 0, lse = 0;
@@ -112,7 +115,8 @@ Plan make_plan(const lla_paged_cache* c, const lla_paged_query* a) {
   const long long reach = a->window ? (long long)a->window + a->sinks + max_new : cap;
   const long long keys = reach < cap ? reach : cap;  // most keys that a row may see
   const long long rows = max_new * g, pairs = (long long)c->num_seqs * c->kv_heads;
-  const bool tc = c->dtype == LLA_BF16 && c->d == c->dv && c->d >= 64 && a->path != LLA_PATH_CUDA_CORE;
+  const bool tc = c->dtype == LLA_BF16 && a->path != LLA_PATH_CUDA_CORE;
+  pl.D = padded(c->d > c->dv ? c->d : c->dv);
   const int limit = rows_limit(a->r != nullptr);
   const int branches = a->r ? 2 : 1;
   pl.rows = tc && g <= limit;
@@ -131,12 +135,12 @@ Plan make_plan(const lla_paged_cache* c, const lla_paged_query* a) {
     // but no block under 1024 keys (48 sequences, 4 heads, window 1024: 30 us with 2 blocks a head,
     // 47 with 7). More than a cluster of 8 only where its blocks would have over 1024 keys each:
     // below that, the launch that joins costs more than shorter blocks save.
-    const int fill = splits(pairs, 304, 128), level = splits(pairs, c->d == 128 ? 1216 : 1824, 1024);
+    const int fill = splits(pairs, 304, 128), level = splits(pairs, pl.D == 128 ? 1216 : 1824, 1024);
     pl.rows_split = fill > level ? fill : level;
     if (pl.rows_split > kRowsCluster && keys <= kRowsCluster * 1024) pl.rows_split = kRowsCluster;
     if (pl.rows_split > kRowsCluster) {
       pl.rows_s = take((size_t)pairs * limit * pl.rows_split * sizeof(float4));
-      pl.rows_o = take((size_t)pairs * limit * pl.rows_split * branches * c->dv * sizeof(float));
+      pl.rows_o = take((size_t)pairs * limit * pl.rows_split * branches * pl.D * sizeof(float));
     }
     if (a->track_mass) {
       pl.keys_cap = (int)((keys + 64 < cap ? keys + 64 : cap) + 15) / 16 * 16;
@@ -146,14 +150,14 @@ Plan make_plan(const lla_paged_cache* c, const lla_paged_query* a) {
   if (pl.tiles) {
     pl.tc = tc && g <= 128;
     const long long BM = pl.tc ? 128 : rows <= 16 ? 16 : 64;
-    const long long per = pl.tc ? tc_tokens(c->d, a->r != nullptr, g) : g < BM ? BM / g : 1;
+    const long long per = pl.tc ? tc_tokens(pl.D, a->r != nullptr, g) : g < BM ? BM / g : 1;
     const long long slices = (g + BM - 1) / BM;
     const long long by_tokens = (a->tokens + per - 1) / per;
     const long long tiles = (by_tokens > c->num_seqs ? by_tokens : c->num_seqs) * slices * c->kv_heads;
     // Few tiles: their keys are split until every SM has a block, down to 512 keys (the start of a
     // block and the partial results cost about 4 of its 128-key steps); CUDA cores, whose steps are
     // longer and whose blocks share an SM, down to one step of 64 and for two blocks.
-    pl.tiles_split = pl.tc ? splits(tiles, c->d == 128 ? 152 : 304, 512, false) : splits(tiles, 304, 64);
+    pl.tiles_split = pl.tc ? splits(tiles, pl.D == 128 ? 152 : 304, 512, false) : splits(tiles, 304, 64);
     if (pl.tiles_split > 1) {
       const size_t all = (size_t)a->tokens * a->q_heads * pl.tiles_split;
       pl.tiles_s = take(all * sizeof(float4));
@@ -191,7 +195,7 @@ int run_attention(const lla_paged_cache* c, const lla_paged_query* a, const Plan
       p.part_s = reinterpret_cast<float4*>(ws + pl.tiles_s);
       p.part_o = reinterpret_cast<float*>(ws + pl.tiles_o);
     }
-    if ((pl.tc ? launch_attend_tc(p, c->d, s) : launch_attend_cc(p, c->d, c->dv, c->dtype, s)) != cudaSuccess)
+    if ((pl.tc ? launch_attend_tc(p, pl.D, s) : launch_attend_cc(p, c->d, c->dv, c->dtype, s)) != cudaSuccess)
       return LLA_ERR_CUDA;
   }
   if (pl.rows) {
@@ -207,11 +211,11 @@ int run_attention(const lla_paged_cache* c, const lla_paged_query* a, const Plan
       f.keys_cap = pl.keys_cap;
       f.logits = reinterpret_cast<float*>(ws + pl.logits);
     }
-    if (launch_attend_rows(f, c->d, s) != cudaSuccess) return LLA_ERR_CUDA;
+    if (launch_attend_rows(f, pl.D, s) != cudaSuccess) return LLA_ERR_CUDA;
   }
   if (pl.tiles) {
-    if (p.split > 1 && launch_join(p, c->d, c->dv, c->dtype, s) != cudaSuccess) return LLA_ERR_CUDA;
-    if (a->track_mass && (pl.tc ? launch_mass_tc(p, c->d, s) : launch_mass_cc(p, c->d, c->dtype, s)) != cudaSuccess)
+    if (p.split > 1 && launch_join(p, c->dv, c->dtype, s) != cudaSuccess) return LLA_ERR_CUDA;
+    if (a->track_mass && (pl.tc ? launch_mass_tc(p, padded(c->d), s) : launch_mass_cc(p, c->d, c->dtype, s)) != cudaSuccess)
       return LLA_ERR_CUDA;
   }
   return LLA_OK;

@@ -251,7 +251,7 @@ __global__ void __launch_bounds__(NT) attend_cc_kernel(Params p) {
     const int row = ((threadIdx.x >> 5) * 2 + (bit >> 4)) * RM + (bit & 15);
     const long long id = rowid(row);
     __syncwarp();
-    exact_row<T>(p, D, DV, b, p0 + row / width, (int)(id / p.Hq), (int)(id % p.Hq));
+    exact_row<T>(p, b, p0 + row / width, (int)(id / p.Hq), (int)(id % p.Hq));
   }
 }
 
@@ -314,7 +314,7 @@ __global__ void __launch_bounds__(NT) mass_cc_kernel(Params p) {
 
 // One warp per row: o and lse from the splits' {m, d1, d2}, O1 (and O2).
 template <typename T, int DV, bool PROBE>
-__global__ void __launch_bounds__(128) join_kernel(Params p, int d) {
+__global__ void __launch_bounds__(128) join_kernel(Params p) {
   const int lane = threadIdx.x & 31;
   const long long rows = (long long)p.tokens * p.Hq;
   const long long id = (long long)blockIdx.x * 4 + (threadIdx.x >> 5);
@@ -364,7 +364,7 @@ __global__ void __launch_bounds__(128) join_kernel(Params p, int d) {
   if (p.lse && lane == 0) p.lse[id] = d1 == 0.f ? -CUDART_INF_F : m * p.inv_h + logf(d1);
   if (__any_sync(0xffffffffu, !(bad == 0.f))) {
     __syncwarp();
-    exact_row<T>(p, d, DV, b, sq.first + token - sq.t0, token, (int)(id % p.Hq));
+    exact_row<T>(p, b, sq.first + token - sq.t0, token, (int)(id % p.Hq));
   }
 }
 
@@ -434,21 +434,21 @@ cudaError_t pick_mass(const Params& p, int d, cudaStream_t s) {
 }
 
 template <typename T, int DV>
-cudaError_t launch_join_t(const Params& p, int d, cudaStream_t s) {
+cudaError_t launch_join_t(const Params& p, cudaStream_t s) {
   const long long blocks = ((long long)p.tokens * p.Hq + 3) / 4;
-  if (p.r) join_kernel<T, DV, true><<<(unsigned)blocks, 128, 0, s>>>(p, d);
-  else join_kernel<T, DV, false><<<(unsigned)blocks, 128, 0, s>>>(p, d);
+  if (p.r) join_kernel<T, DV, true><<<(unsigned)blocks, 128, 0, s>>>(p);
+  else join_kernel<T, DV, false><<<(unsigned)blocks, 128, 0, s>>>(p);
   count_launch();
   return cudaGetLastError();
 }
 
 template <typename T>
-cudaError_t pick_join(const Params& p, int d, int dv, cudaStream_t s) {
+cudaError_t pick_join(const Params& p, int dv, cudaStream_t s) {
   switch (dv) {
-    case 16: return launch_join_t<T, 16>(p, d, s);
-    case 32: return launch_join_t<T, 32>(p, d, s);
-    case 64: return launch_join_t<T, 64>(p, d, s);
-    default: return launch_join_t<T, 128>(p, d, s);
+    case 16: return launch_join_t<T, 16>(p, s);
+    case 32: return launch_join_t<T, 32>(p, s);
+    case 64: return launch_join_t<T, 64>(p, s);
+    default: return launch_join_t<T, 128>(p, s);
   }
 }
 

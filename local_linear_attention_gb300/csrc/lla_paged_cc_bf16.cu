@@ -11,8 +11,8 @@ cudaError_t attend_cc_bf16(const Params& p, int d, int dv, cudaStream_t s) {
 cudaError_t mass_cc_bf16(const Params& p, int d, cudaStream_t s) {
   return pick_mass<__nv_bfloat16>(p, d, s);
 }
-cudaError_t join_bf16(const Params& p, int d, int dv, cudaStream_t s) {
-  return pick_join<__nv_bfloat16>(p, d, dv, s);
+cudaError_t join_bf16(const Params& p, int dv, cudaStream_t s) {
+  return pick_join<__nv_bfloat16>(p, dv, s);
 }
 
 }  // namespace paged

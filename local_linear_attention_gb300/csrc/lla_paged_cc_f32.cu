@@ -11,8 +11,8 @@ cudaError_t attend_cc_f32(const Params& p, int d, int dv, cudaStream_t s) {
 cudaError_t mass_cc_f32(const Params& p, int d, cudaStream_t s) {
   return pick_mass<float>(p, d, s);
 }
-cudaError_t join_f32(const Params& p, int d, int dv, cudaStream_t s) {
-  return pick_join<float>(p, d, dv, s);
+cudaError_t join_f32(const Params& p, int dv, cudaStream_t s) {
+  return pick_join<float>(p, dv, s);
 }
 
 }  // namespace paged

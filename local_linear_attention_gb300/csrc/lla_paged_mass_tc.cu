@@ -1,4 +1,4 @@
-// Weight tracking of sequences with many rows, bf16, d = 64 or 128, on the tensor cores:
+// Weight tracking of sequences with many rows, bf16, d up to D = 64 or 128, on the tensor cores:
 //   mass[j] += sum over the rows i that see key j of exp(q_i.k_j / h - lse_i),
 // from the finished lse. The product is taken transposed, S^T = K Q^T (128 keys x 128 rows in
 // tensor memory, a thread per key), so that a key's sum runs along a thread's registers: no
@@ -283,12 +283,12 @@ mass_tc_kernel(Params p, const __grid_constant__ CUtensorMap kmap, const __grid_
 template <int D>
 cudaError_t launch_t(const Params& p, cudaStream_t s) {
   CUtensorMap kmap, qmap;
-  cudaError_t err = encode_page_map(p, p.k, D, KT, &kmap);
+  cudaError_t err = encode_page_map(p, p.k, p.d, KT, &kmap);
   if (err != cudaSuccess) return err;
   auto encode = tensor_map_encoder();
   const cuuint32_t ones[3] = {1, 1, 1};
-  const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)p.Hq, (cuuint64_t)p.tokens};
-  const cuuint64_t str[2] = {(cuuint64_t)D * 2, (cuuint64_t)p.Hq * D * 2};
+  const cuuint64_t dims[3] = {(cuuint64_t)p.d, (cuuint64_t)p.Hq, (cuuint64_t)p.tokens};
+  const cuuint64_t str[2] = {(cuuint64_t)p.d * 2, (cuuint64_t)p.Hq * p.d * 2};
   const cuuint32_t box[3] = {64, (cuuint32_t)p.g, (cuuint32_t)(BR / p.g)};
   if (encode(&qmap, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(p.q), dims, str, box, ones,
              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
@@ -301,8 +301,8 @@ cudaError_t launch_t(const Params& p, cudaStream_t s) {
 
 }  // namespace
 
-cudaError_t launch_mass_tc(const Params& p, int d, cudaStream_t s) {
-  return d == 128 ? launch_t<128>(p, s) : launch_t<64>(p, s);
+cudaError_t launch_mass_tc(const Params& p, int D, cudaStream_t s) {
+  return D == 128 ? launch_t<128>(p, s) : launch_t<64>(p, s);
 }
 
 }  // namespace paged

@@ -1,5 +1,6 @@
 // Attention over a paged cache for sequences with few rows (new tokens x grouped heads): a decode
-// step, or a few speculated tokens. bf16, d = dv = 64 or 128.
+// step, or a few speculated tokens. bf16, head sizes up to D = 64 or 128 (smaller ones padded with
+// zeros as they are copied to shared memory).
 //
 // What bounds it: HBM. Each cached key and value is read once for all rows of its key/value head
 // and takes part in at most 32 row products per element, an order below the ridge point, so what
@@ -77,7 +78,7 @@ __device__ __forceinline__ void write_row(const Params& p, const Seq& sq, int b,
   const int lane = threadIdx.x & 31;
   const int token = sq.t0 + r / p.g, head = hk * p.g + r % p.g;
   const float inv = s1 == 0.f ? 0.f : 1.f / s1, f1 = (1.f + s2 * inv) * inv;
-  __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.out) + ((long long)token * p.Hq + head) * D + lane * VC;
+  __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.out) + ((long long)token * p.Hq + head) * p.dv + lane * VC;
   float bad = 0.f;
   uint32_t w[VC / 2];
 #pragma unroll
@@ -87,14 +88,16 @@ __device__ __forceinline__ void write_row(const Params& p, const Seq& sq, int b,
     bad += (y0 + y1) * 0.f;
     w[c / 2] = pack_bf16(y0, y1);
   }
-  if (VC == 4) *reinterpret_cast<uint2*>(dst) = make_uint2(w[0], w[VC / 2 - 1]);
-  else *reinterpret_cast<uint32_t*>(dst) = w[0];
+  if (lane * VC < p.dv) {
+    if (VC == 4) *reinterpret_cast<uint2*>(dst) = make_uint2(w[0], w[VC / 2 - 1]);
+    else *reinterpret_cast<uint32_t*>(dst) = w[0];
+  }
   if (p.lse && lane == 0)
     p.lse[(long long)token * p.Hq + head] =
         s1 == 0.f ? -CUDART_INF_F : (top * (p.inv_h * kLog2e) + log2f(s1)) * kLn2;
   if (__any_sync(0xffffffffu, !(bad == 0.f))) {
     __syncwarp();
-    exact_row<__nv_bfloat16>(p, D, D, b, sq.first + r / p.g, token, head);
+    exact_row<__nv_bfloat16>(p, b, sq.first + r / p.g, token, head);
   }
 }
 
@@ -142,15 +145,16 @@ __global__ void __launch_bounds__(NW * 32) attend_rows_kernel(Params p) {
       const int j0 = range.tile(it) * KT;
       const long long slot = ((long long)max(pg, 0) * p.Hkv + hk) * p.page + (j0 & (p.page - 1));
       const int live = pg < 0 ? 0 : sq.len - j0;
+      const __nv_bfloat16* ks = kg + slot * p.d;
+      const __nv_bfloat16* vs = vg + slot * p.dv;
       uint8_t* dst = ring + stage * 2 * C::step_bytes;
 #pragma unroll
       for (int e = lane; e < KT * CH; e += 32) {
         const int row = e / CH, c = e % CH;
-        const uint32_t n = row < live ? 16u : 0u;
+        const bool k_in = row < live && c * 8 < p.d, v_in = row < live && c * 8 < p.dv;
         const int off = row * (D * 2) + ((c ^ (row & 7)) * 16);
-        const long long at = n ? (slot + row) * D + c * 8 : 0;
-        cp_async16(dst + off, kg + at, n);
-        cp_async16(dst + C::step_bytes + off, vg + at, n);
+        cp_async16(dst + off, k_in ? ks + row * p.d + c * 8 : kg, k_in ? 16u : 0u);
+        cp_async16(dst + C::step_bytes + off, v_in ? vs + row * p.dv + c * 8 : vg, v_in ? 16u : 0u);
       }
     }
     cp_async_commit();
@@ -171,17 +175,18 @@ __global__ void __launch_bounds__(NW * 32) attend_rows_kernel(Params p) {
     const int r0 = lane >> 2, cc = (lane & 3) * 2;
     auto row = [&](const void* base, int r) -> const uint32_t* {
       return reinterpret_cast<const uint32_t*>(static_cast<const __nv_bfloat16*>(base) +
-             ((long long)(sq.t0 + r / p.g) * p.Hq + hk * p.g + r % p.g) * D + cc);
+             ((long long)(sq.t0 + r / p.g) * p.Hq + hk * p.g + r % p.g) * p.d + cc);
     };
     const uint32_t* x = r0 < nrows ? row(p.q, r0) : nullptr;
     const uint32_t* y = PROBE ? (r0 < nrows ? row(p.r, r0) : nullptr)
                               : (r0 + 8 < nrows ? row(p.q, r0 + 8) : nullptr);
 #pragma unroll
     for (int ks = 0; ks < D / 16; ++ks) {
-      a[ks][0] = x ? x[ks * 8] : 0u;
-      a[ks][2] = x ? x[ks * 8 + 4] : 0u;
-      a[ks][1] = y ? y[ks * 8] : 0u;
-      a[ks][3] = y ? y[ks * 8 + 4] : 0u;
+      const bool in = ks * 16 < p.d;
+      a[ks][0] = in && x ? x[ks * 8] : 0u;
+      a[ks][2] = in && x ? x[ks * 8 + 4] : 0u;
+      a[ks][1] = in && y ? y[ks * 8] : 0u;
+      a[ks][3] = in && y ? y[ks * 8 + 4] : 0u;
     }
   }
   int pos[NR];
@@ -497,8 +502,8 @@ cudaError_t pick(const Params& p, cudaStream_t s) {
 
 }  // namespace
 
-cudaError_t launch_attend_rows(const Params& p, int d, cudaStream_t s) {
-  return d == 128 ? pick<128>(p, s) : pick<64>(p, s);
+cudaError_t launch_attend_rows(const Params& p, int D, cudaStream_t s) {
+  return D == 128 ? pick<128>(p, s) : pick<64>(p, s);
 }
 
 }  // namespace paged

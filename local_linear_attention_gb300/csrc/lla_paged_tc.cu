@@ -1,5 +1,5 @@
-// Attention over a paged cache for sequences with many rows (prompts and chunks), bf16, d = dv = 64
-// or 128, on the tensor cores (tcgen05, tensor memory, TMA).
+// Attention over a paged cache for sequences with many rows (prompts and chunks), bf16, head sizes
+// up to D = 64 or 128 (smaller ones padded with zeros: the tensor maps fill them in), on the tensor cores (tcgen05, tensor memory, TMA).
 //
 // One pass over the keys with a running row maximum. Per tile of KT keys and block of 128 rows
 // (tokens x grouped heads of one key/value head): S = Q K^T, P = exp(S - m), O += P V; with a probe
@@ -119,7 +119,7 @@ attend_tc_kernel(Params p, const __grid_constant__ CUtensorMap kmap,
     const int t = token_of(PROBE ? 0 : o, r);
     const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(PROBE && o ? p.r : p.q);
     uint4 x = make_uint4(0u, 0u, 0u, 0u);
-    if (t >= 0) x = *reinterpret_cast<const uint4*>(src + rowid(t, r) * D + c * 8);
+    if (t >= 0 && c * 8 < p.d) x = *reinterpret_cast<const uint4*>(src + rowid(t, r) * p.d + c * 8);
     *reinterpret_cast<uint4*>(smem + o * C::op_bytes + (c >> 3) * 16384 + r * 128 + (((c & 7) ^ (r & 7)) * 16)) = x;
   }
   if (tid == 0) {
@@ -461,13 +461,13 @@ attend_tc_kernel(Params p, const __grid_constant__ CUtensorMap kmap,
 #pragma unroll
           for (int u = 0; u < 16; ++u) a[u] = e[u] = 0u;
         }
-        if (t < 0) continue;
+        if (t < 0 || c >= p.dv) continue;
         if (p.split > 1) {
-          float* dst = p.part_o + pid * (PROBE ? 2 : 1) * D + c;
+          float* dst = p.part_o + pid * (PROBE ? 2 : 1) * p.dv + c;
 #pragma unroll
           for (int u = 0; u < 16; u += 4) {
             *reinterpret_cast<uint4*>(dst + u) = make_uint4(a[u], a[u + 1], a[u + 2], a[u + 3]);
-            if (PROBE) *reinterpret_cast<uint4*>(dst + D + u) = make_uint4(e[u], e[u + 1], e[u + 2], e[u + 3]);
+            if (PROBE) *reinterpret_cast<uint4*>(dst + p.dv + u) = make_uint4(e[u], e[u + 1], e[u + 2], e[u + 3]);
           }
           continue;
         }
@@ -483,7 +483,7 @@ attend_tc_kernel(Params p, const __grid_constant__ CUtensorMap kmap,
           bad += (y0 + y1) * 0.f;
           w[u / 2] = pack_bf16(y0, y1);
         }
-        uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out) + id * D + c);
+        uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out) + id * p.dv + c);
         dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
         dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
       }
@@ -508,7 +508,7 @@ attend_tc_kernel(Params p, const __grid_constant__ CUtensorMap kmap,
           again &= again - 1;
           const int tk = token_of(h, row);
           __syncwarp();
-          exact_row<__nv_bfloat16>(p, D, D, b, p0 + tk, sq.t0 + tok0 + tk, hk * p.g + row % p.g);
+          exact_row<__nv_bfloat16>(p, b, p0 + tk, sq.t0 + tok0 + tk, hk * p.g + row % p.g);
         }
       }
     }
@@ -526,8 +526,8 @@ template <int D, bool PROBE>
 cudaError_t launch_tc_t(const Params& p, cudaStream_t s) {
   using C = Cfg<D, PROBE>;
   CUtensorMap kmap, vmap;
-  cudaError_t err = encode_page_map(p, p.k, D, C::kt, &kmap);
-  if (err == cudaSuccess) err = encode_page_map(p, p.v, D, C::kt, &vmap);
+  cudaError_t err = encode_page_map(p, p.k, p.d, C::kt, &kmap);
+  if (err == cudaSuccess) err = encode_page_map(p, p.v, p.dv, C::kt, &vmap);
   if (err != cudaSuccess) return err;
   const long long blocks = ((long long)p.tokens / (BM / p.g * C::blocks) + p.B) * p.Hkv;
   if (blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
@@ -538,7 +538,7 @@ cudaError_t launch_tc_t(const Params& p, cudaStream_t s) {
 }  // namespace
 
 // Tensor map of the pages ([num_pages * Hkv][page][d] bf16; boxes of one page fragment, at most
-// kt rows, x 64 features, 128-byte swizzled).
+// kt rows, x 64 features, 128-byte swizzled; features past d are zeros).
 cudaError_t encode_page_map(const Params& p, void* pages, int d, int kt, CUtensorMap* map) {
   auto encode = tensor_map_encoder();
   if (!encode) return cudaErrorNotSupported;
@@ -553,11 +553,11 @@ cudaError_t encode_page_map(const Params& p, void* pages, int d, int kt, CUtenso
              : cudaErrorInvalidValue;
 }
 
-int tc_tokens(int d, bool probe, int g) { return BM / g * (d == 128 && !probe ? 2 : 1); }
+int tc_tokens(int D, bool probe, int g) { return BM / g * (D == 128 && !probe ? 2 : 1); }
 
-cudaError_t launch_attend_tc(const Params& p, int d, cudaStream_t s) {
-  if (p.r) return d == 128 ? launch_tc_t<128, true>(p, s) : launch_tc_t<64, true>(p, s);
-  return d == 128 ? launch_tc_t<128, false>(p, s) : launch_tc_t<64, false>(p, s);
+cudaError_t launch_attend_tc(const Params& p, int D, cudaStream_t s) {
+  if (p.r) return D == 128 ? launch_tc_t<128, true>(p, s) : launch_tc_t<64, true>(p, s);
+  return D == 128 ? launch_tc_t<128, false>(p, s) : launch_tc_t<64, false>(p, s);
 }
 
 }  // namespace paged

@@ -64,7 +64,8 @@ BATCHES = {
 @pytest.mark.parametrize("dtype,d,dv,Hq,Hkv,page", [
     (F32, 64, 64, 4, 2, 16), (F32, 16, 128, 3, 1, 64), (BF, 64, 64, 4, 4, 16), (BF, 128, 128, 8, 2, 32),
     (BF, 64, 64, 5, 1, 128), (BF, 128, 128, 21, 3, 256), (BF, 32, 16, 2, 1, 16), (BF, 128, 64, 6, 2, 64),
-    (BF, 64, 64, 40, 2, 64)])
+    (BF, 64, 64, 40, 2, 64), (BF, 16, 128, 4, 4, 16), (BF, 64, 32, 12, 4, 32), (BF, 16, 64, 30, 2, 128),
+    (F32, 32, 16, 300, 2, 16), (BF, 64, 16, 260, 2, 16)])
 def test_attention(lla, dtype, d, dv, Hq, Hkv, page, batch, probe):
     lens, news = BATCHES[batch]
     run_and_check(lla, Problem(lens, news, Hq, Hkv, d, dv, page, dtype, probe, seed=d + Hq + page))
