@@ -112,6 +112,13 @@ mass_tc_kernel(Params p, const __grid_constant__ CUtensorMap kmap, const __grid_
   const uint32_t tbase = tmem_base_s;
   volatile int* abort_p = &abort_flag;
 
+  int lse_tok[4], lse_head[4];  // of rows lane, lane + 32, ..: token within the block, grouped head
+#pragma unroll
+  for (int u = 0; u < 4; ++u) {
+    const int row = u * 32 + lane;
+    lse_tok[u] = row < width ? row / p.g : -1;
+    lse_head[u] = row % p.g;
+  }
   int done = 0, items = 0;  // row blocks and items so far (every thread counts the same)
   bool used = false;
   for (int x = blockIdx.x;; x += gridDim.x) {
@@ -196,17 +203,25 @@ mass_tc_kernel(Params p, const __grid_constant__ CUtensorMap kmap, const __grid_
         __syncwarp();
         if (lane == 0) mbar_arrive(&bar.sfree[buf]);
       };
-      for (int i = (done ^ grp) & 1; i < nblk; i += 2) {  // block counts of this group's parity
-        const int c = done + i, tok0 = (from + i) * per;
-        // this block's -lse log2(e) (the warp's own copy)
+      // -lse log2(e) of a block's rows, four to a lane (-infinity past the rows there are); loaded a
+      // block ahead, so that its latency is not in front of the sums
+      float ahead[4];
+      auto load_lse = [&](int i) {
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
-          const int row = u * 32 + lane, t = tok0 + row / p.g;
-          lse[row] = row < width && t < sq.n
-                         ? p.lse[(long long)(sq.t0 + t) * p.Hq + hk * p.g + row % p.g] * -kLog2e
+          const int t = (from + i) * per + lse_tok[u];
+          ahead[u] = i < nblk && lse_tok[u] >= 0 && t < sq.n
+                         ? p.lse[(long long)(sq.t0 + t) * p.Hq + hk * p.g + lse_head[u]] * -kLog2e
                          : -CUDART_INF_F;
         }
+      };
+      load_lse((done ^ grp) & 1);
+      for (int i = (done ^ grp) & 1; i < nblk; i += 2) {  // block counts of this group's parity
+        const int c = done + i, tok0 = (from + i) * per;
+#pragma unroll
+        for (int u = 0; u < 4; ++u) lse[u * 32 + lane] = ahead[u];
         __syncwarp();
+        load_lse(i + 2);
         if (!warp_wait(&bar.sfull[grp], (c >> 1) & 1, status, TO, abort_p)) break;
         tc_fence_after();
         const int p0 = sq.first + tok0, p1 = p0 + per - 1;
