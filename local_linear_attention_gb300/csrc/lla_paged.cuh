@@ -44,6 +44,7 @@ struct Params {
   // Split of each row's keys over blocks, and its partial results (split > 1).
   int split;
   float* part_o;     // [split][rows][branches][dv]   unnormalised O1 (and O2)
+  int4* pieces;      // tensor-core kernel: [split CTAs][2] {sequence, tile, head, there is one}
   float4* part_s;    // [split][rows]   {m, d1, d2, 0} with m the maximum of q.k (raw)
                      // rows: tokens * Hq, or B * Hkv * rows_limit of the few-rows kernel
   float* logits;     // [B * Hkv][row_cap][keys_cap]  raw q.k of the few-rows kernel, by the key's
@@ -145,8 +146,8 @@ __device__ __forceinline__ bool find_tile(const Params& p, int per, int x, int* 
 
 // One row computed by one warp straight from the definition, skipping every key that the row does
 // not see. The tiled kernels multiply such keys' values by a zero weight, which is not zero when
-// the value is infinite or NaN; a row whose result is not finite is therefore taken again here
-// (and stays NaN only if a key that it sees makes it so). Slow, and off every ordinary path.
+// the value is infinite or NaN; a row whose result is not finite is therefore taken again here, out
+// and lse (and stays NaN only if a key that it sees makes it so). Slow, and off every ordinary path.
 template <typename T>
 __device__ __noinline__ void exact_row(const Params& p, int b, int pos, int token, int head) {
   const int d = p.d, dv = p.dv;
@@ -210,6 +211,8 @@ __device__ __noinline__ void exact_row(const Params& p, int b, int pos, int toke
   for (int c = 0; c < 4; ++c)
     if (lane + 32 * c < dv)
       stf(out, lane + 32 * c, r ? fmaf(o1[c], f1, -o2[c] * inv) : o1[c] * inv);
+  if (p.lse && lane == 0)
+    p.lse[(long long)token * p.Hq + head] = d1 == 0.f ? -CUDART_INF_F : m + logf(d1);
 }
 
 // ------------------------------------------------------------------------------------- arithmetic
@@ -320,10 +323,18 @@ inline int padded(int d) { return d > 64 ? 128 : 64; }
 constexpr int kRowsCluster = 8;  // splits that join within a cluster (the portable size)
 inline int rows_limit(bool probe) { return probe ? 8 : 16; }
 cudaError_t launch_attend_rows(const Params& p, int D, cudaStream_t s);
-// Sequences of many rows, g <= 128; launch_mass_tc with D = padded(d).
+// Sequences of many rows: the attention on p.split CTAs, the join of the tiles that their shares
+// cut; the weight tracking (D = padded(d)).
+struct TcPlan {
+  int ctas = 0;            // 0: not for these kernels
+  size_t rows = 0;         // rows of partial results (part_s, part_o), row_floats of part_o each
+  int row_floats = 0;
+};
+TcPlan plan_tc(int D, bool probe, long long tokens, int B, int Hkv, int g, long long keys);
 cudaError_t launch_attend_tc(const Params& p, int D, cudaStream_t s);
+cudaError_t launch_join_tc(const Params& p, int D, cudaStream_t s);
 cudaError_t launch_mass_tc(const Params& p, int D, cudaStream_t s);
-int tc_tokens(int D, bool probe, int g);  // tokens per block of launch_attend_tc
+cudaError_t encode_query_map(const Params& p, const void* q, CUtensorMap* map);
 cudaError_t encode_page_map(const Params& p, void* pages, int d, int kt, CUtensorMap* map);
 cudaError_t launch_append(const Params& p, const void* k_new, const void* v_new, int d, int dv,
                           int dtype, cudaStream_t s);

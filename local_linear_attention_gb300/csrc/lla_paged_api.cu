@@ -103,7 +103,7 @@ struct Plan {
   int D = 0;           // head size of the tensor-core kernels
   int rows_split = 1, tiles_split = 1;
   int row_cap = 0, keys_cap = 0;
-  size_t rows_s = 0, rows_o = 0, logits = 0, tiles_s = 0, tiles_o = 0, lse = 0;
+  size_t rows_s = 0, rows_o = 0, logits = 0, pieces = 0, tiles_s = 0, tiles_o = 0, lse = 0;
   size_t bytes = 0;
 };
 
@@ -123,8 +123,8 @@ Plan make_plan(const lla_paged_cache* c, const lla_paged_query* a) {
   pl.tiles = !pl.rows || rows > limit;
   size_t at = 0;
   auto take = [&](size_t bytes) { const size_t o = at; at += align_up(bytes); return o; };
-  auto splits = [&](long long blocks, long long want, long long least, bool up = true) {
-    long long n = blocks > 0 ? (want + (up ? blocks - 1 : 0)) / blocks : 1;
+  auto splits = [&](long long blocks, long long want, long long least) {
+    long long n = blocks > 0 ? (want + blocks - 1) / blocks : 1;
     if (n > keys / least) n = keys / least;
     return n < 1 ? 1 : n > 512 ? 512 : (int)n;
   };
@@ -148,20 +148,24 @@ Plan make_plan(const lla_paged_cache* c, const lla_paged_query* a) {
     }
   }
   if (pl.tiles) {
-    pl.tc = tc && g <= 128;
-    const long long BM = pl.tc ? 128 : rows <= 16 ? 16 : 64;
-    const long long per = pl.tc ? tc_tokens(pl.D, a->r != nullptr, g) : g < BM ? BM / g : 1;
-    const long long slices = (g + BM - 1) / BM;
-    const long long by_tokens = (a->tokens + per - 1) / per;
-    const long long tiles = (by_tokens > c->num_seqs ? by_tokens : c->num_seqs) * slices * c->kv_heads;
-    // Few tiles: their keys are split until every SM has a block, down to 512 keys (the start of a
-    // block and the partial results cost about 4 of its 128-key steps); CUDA cores, whose steps are
-    // longer and whose blocks share an SM, down to one step of 64 and for two blocks.
-    pl.tiles_split = pl.tc ? splits(tiles, pl.D == 128 ? 152 : 304, 512, false) : splits(tiles, 304, 64);
-    if (pl.tiles_split > 1) {
-      const size_t all = (size_t)a->tokens * a->q_heads * pl.tiles_split;
-      pl.tiles_s = take(all * sizeof(float4));
-      pl.tiles_o = take(all * branches * c->dv * sizeof(float));
+    const TcPlan t = tc ? plan_tc(pl.D, a->r != nullptr, a->tokens, c->num_seqs, c->kv_heads, g, keys) : TcPlan();
+    pl.tc = t.ctas > 0;
+    if (pl.tc) {
+      pl.tiles_split = t.ctas;
+      pl.pieces = take((size_t)t.ctas * 2 * sizeof(int4));
+      pl.tiles_s = take(t.rows * sizeof(float4));
+      pl.tiles_o = take(t.rows * t.row_floats * sizeof(float));
+    } else {
+      // CUDA cores: few tiles' keys are split until every SM has two blocks, down to one step of 64.
+      const long long BM = rows <= 16 ? 16 : 64, per = g < BM ? BM / g : 1, slices = (g + BM - 1) / BM;
+      const long long by_tokens = (a->tokens + per - 1) / per;
+      const long long tiles = (by_tokens > c->num_seqs ? by_tokens : c->num_seqs) * slices * c->kv_heads;
+      pl.tiles_split = splits(tiles, 304, 64);
+      if (pl.tiles_split > 1) {
+        const size_t all = (size_t)a->tokens * a->q_heads * pl.tiles_split;
+        pl.tiles_s = take(all * sizeof(float4));
+        pl.tiles_o = take(all * branches * c->dv * sizeof(float));
+      }
     }
   }
   if (a->track_mass && !a->lse) pl.lse = take((size_t)a->tokens * a->q_heads * sizeof(float));
@@ -191,10 +195,11 @@ int run_attention(const lla_paged_cache* c, const lla_paged_query* a, const Plan
   p.lo = pl.rows ? pl.row_cap : 0;
   p.split = pl.tiles_split;
   if (pl.tiles) {
-    if (p.split > 1) {
+    if (pl.tc || p.split > 1) {
       p.part_s = reinterpret_cast<float4*>(ws + pl.tiles_s);
       p.part_o = reinterpret_cast<float*>(ws + pl.tiles_o);
     }
+    if (pl.tc) p.pieces = reinterpret_cast<int4*>(ws + pl.pieces);
     if ((pl.tc ? launch_attend_tc(p, pl.D, s) : launch_attend_cc(p, c->d, c->dv, c->dtype, s)) != cudaSuccess)
       return LLA_ERR_CUDA;
   }
@@ -214,7 +219,9 @@ int run_attention(const lla_paged_cache* c, const lla_paged_query* a, const Plan
     if (launch_attend_rows(f, pl.D, s) != cudaSuccess) return LLA_ERR_CUDA;
   }
   if (pl.tiles) {
-    if (p.split > 1 && launch_join(p, c->dv, c->dtype, s) != cudaSuccess) return LLA_ERR_CUDA;
+    if (pl.tc ? launch_join_tc(p, pl.D, s) != cudaSuccess
+              : p.split > 1 && launch_join(p, c->dv, c->dtype, s) != cudaSuccess)
+      return LLA_ERR_CUDA;
     if (a->track_mass && (pl.tc ? launch_mass_tc(p, padded(c->d), s) : launch_mass_cc(p, c->d, c->dtype, s)) != cudaSuccess)
       return LLA_ERR_CUDA;
   }

@@ -300,15 +300,8 @@ cudaError_t launch_t(const Params& p, cudaStream_t s) {
   CUtensorMap kmap, qmap;
   cudaError_t err = encode_page_map(p, p.k, p.d, KT, &kmap);
   if (err != cudaSuccess) return err;
-  auto encode = tensor_map_encoder();
-  const cuuint32_t ones[3] = {1, 1, 1};
-  const cuuint64_t dims[3] = {(cuuint64_t)p.d, (cuuint64_t)p.Hq, (cuuint64_t)p.tokens};
-  const cuuint64_t str[2] = {(cuuint64_t)p.d * 2, (cuuint64_t)p.Hq * p.d * 2};
-  const cuuint32_t box[3] = {64, (cuuint32_t)p.g, (cuuint32_t)(BR / p.g)};
-  if (encode(&qmap, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(p.q), dims, str, box, ones,
-             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
-    return cudaErrorInvalidValue;
+  err = encode_query_map(p, p.q, &qmap);
+  if (err != cudaSuccess) return err;
   const long long most = ((((long long)p.max_pages << p.page_shift) + KT - 1) / KT) * p.B * p.Hkv;
   return launch(mass_tc_kernel<D>, dim3((unsigned)(most < 304 ? most : 304)), NTHREADS, Cfg<D>::bytes, 1, false, s,
                 p, kmap, qmap);
