@@ -377,45 +377,46 @@ class PagedCache:
                  "dtype", "device", "_packed", "_index")
 
     def __init__(self, k_pages, v_pages, page_table, lens, mass=None):
-        k_shape, v_shape, t_shape = k_pages.shape, v_pages.shape, page_table.shape
-        if len(k_shape) != 4 or len(v_shape) != 4 or v_shape[:3] != k_shape[:3]:
+        k_shape, v_shape, device, dtype = k_pages.shape, v_pages.shape, k_pages.device, k_pages.dtype
+        tensors = (k_pages, v_pages, page_table, lens) if mass is None else (k_pages, v_pages, page_table, lens, mass)
+        if len(k_shape) != 4 or v_shape[:3] != k_shape[:3] or len(v_shape) != 4:
             raise ValueError("expected k_pages [num_pages, kv_heads, page_size, d] and v_pages "
                              "[num_pages, kv_heads, page_size, dv]")
-        dtype, device = k_pages.dtype, k_pages.device
-        if v_pages.dtype != dtype or dtype not in DTYPE_CODES:
+        code = DTYPE_CODES.get(dtype)
+        if code is None or v_pages.dtype != dtype:
             raise ValueError("k_pages and v_pages must share one dtype: float32 or bfloat16")
+        t_shape = page_table.shape
         if len(t_shape) != 2 or page_table.dtype != torch.int32:
             raise ValueError("page_table must be int32 [num_seqs, max_pages]")
         if lens.dtype != torch.int32 or lens.shape != t_shape[:1]:
             raise ValueError("lens must be int32 [num_seqs]")
         if mass is not None and (mass.shape != k_shape[:3] or mass.dtype != torch.float32):
             raise ValueError("mass must be float32 [num_pages, kv_heads, page_size]")
-        for t in (k_pages, v_pages, page_table, lens) if mass is None else \
-                (k_pages, v_pages, page_table, lens, mass):
-            if t.device != device or not t.is_contiguous():
-                raise ValueError("the cache's tensors must be contiguous, on one device")
-        if device.type != "cuda":
+        index = k_pages.get_device()  # -1: not on a CUDA device
+        if index < 0:
             raise ValueError("liblla runs on CUDA tensors only")
+        for t in tensors:
+            if t.get_device() != index or not t.is_contiguous():
+                raise ValueError("the cache's tensors must be contiguous, on one device")
         num_pages, self.kv_heads, page, self.d = k_shape
         self.num_seqs, max_pages = t_shape
         self.dv = v_shape[3]
         self.k_pages, self.v_pages, self.mass = k_pages, v_pages, mass
-        self.page_table, self.lens, self.dtype, self.device = page_table, lens, dtype, device
-        self._index = device.index
+        self.page_table, self.lens, self.dtype, self.device, self._index = page_table, lens, dtype, device, index
         self._packed = _CACHE.pack(
             k_pages.data_ptr(), v_pages.data_ptr(), 0 if mass is None else mass.data_ptr(),
             page_table.data_ptr(), lens.data_ptr(), self.num_seqs, self.kv_heads, page, max_pages,
-            num_pages, self.d, self.dv, DTYPE_CODES[dtype], 0, 0)
+            num_pages, self.d, self.dv, code, 0, 0)
 
 
 def _paged_rows(name, x, cache, shape):
-    if x.shape != shape or x.dtype != cache.dtype or x.device != cache.device or not x.is_contiguous():
+    if x.shape != shape or x.dtype != cache.dtype or x.get_device() != cache._index or not x.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {cache.dtype} tensor of shape {shape} on {cache.device}")
 
 
 def _paged_starts(starts, cache):
     if starts.dtype != torch.int32 or starts.shape != (cache.num_seqs + 1,) or \
-            starts.device != cache.device or not starts.is_contiguous():
+            starts.get_device() != cache._index or not starts.is_contiguous():
         raise ValueError("starts must be a contiguous int32 [num_seqs + 1] tensor on the cache's device")
 
 
@@ -446,12 +447,13 @@ def lla_paged_append(k, v, cache: PagedCache, starts, stream=None):
 
 
 def _paged_query(q, cache, starts, h, r, max_new, window, sinks, track_mass, out, lse, path):
-    if len(q.shape) != 3:
-        raise ValueError("q must be [tokens, q_heads, d]")
-    tokens, heads, _ = q.shape
-    _paged_rows("q", q, cache, (tokens, heads, cache.d))
+    shape = q.shape
+    if len(shape) != 3 or shape[2] != cache.d or q.dtype != cache.dtype or q.get_device() != cache._index or \
+            not q.is_contiguous():
+        raise ValueError(f"q must be a contiguous {cache.dtype} tensor [tokens, q_heads, {cache.d}] on {cache.device}")
+    tokens, heads, _ = shape
     if r is not None:
-        _paged_rows("r", r, cache, (tokens, heads, cache.d))
+        _paged_rows("r", r, cache, shape)
     _paged_starts(starts, cache)
     return _QUERY.pack(q.data_ptr(), 0 if r is None else r.data_ptr(), 0 if out is None else out.data_ptr(),
                        0 if lse is None else lse.data_ptr(), starts.data_ptr(), tokens,
@@ -468,21 +470,22 @@ def lla_paged_attention(q, cache: PagedCache, starts, h: float, r=None, max_new=
     them (window = 0) or the last `window` and the first `sinks`. track_mass adds the weights to
     cache.mass. max_new: a bound of the tokens of one sequence (default: all); giving it lets a
     decode step run as one."""
+    shape = q.shape
     if out is not None:
-        _paged_rows("out", out, cache, (*q.shape[:2], cache.dv))
-    if lse is not None and (lse.shape != q.shape[:2] or lse.dtype != torch.float32 or
-                            lse.device != cache.device or not lse.is_contiguous()):
+        _paged_rows("out", out, cache, (*shape[:2], cache.dv))
+    if lse is not None and (lse.shape != shape[:2] or lse.dtype != torch.float32 or
+                            lse.get_device() != cache._index or not lse.is_contiguous()):
         raise ValueError("lse must be a contiguous float32 [tokens, q_heads] tensor on the cache's device")
     if stream is None:
         if out is None:
             out = torch.empty_like(q) if cache.dv == cache.d else \
-                torch.empty((*q.shape[:2], cache.dv), dtype=q.dtype, device=q.device)
+                torch.empty((*shape[:2], cache.dv), dtype=q.dtype, device=cache.device)
         if lse is None:
-            lse = torch.empty(q.shape[:2], dtype=torch.float32, device=q.device)
+            lse = torch.empty(shape[:2], dtype=torch.float32, device=cache.device)
     else:
         with _on_stream(stream):
-            out = q.new_empty((*q.shape[:2], cache.dv)) if out is None else out
-            lse = q.new_empty(q.shape[:2], dtype=torch.float32) if lse is None else lse
+            out = q.new_empty((*shape[:2], cache.dv)) if out is None else out
+            lse = q.new_empty(shape[:2], dtype=torch.float32) if lse is None else lse
     query = _paged_query(q, cache, starts, h, r, max_new, window, sinks, track_mass, out, lse, path)
     wp, wb = (0, 0) if workspace is None else (
         workspace.data_ptr(), workspace.numel() * workspace.element_size())
@@ -508,7 +511,7 @@ def lla_paged_evict(cache: PagedCache, to: PagedCache, budget: int, sinks=0, rec
     last)."""
     if cache.mass is None or to.mass is None:
         raise ValueError("eviction needs the mass of both caches")
-    if cache.device != to.device:
+    if cache._index != to._index:
         raise ValueError("the caches must be on one device")
     if budget < 1:
         raise ValueError("budget must be at least 1")
@@ -516,7 +519,7 @@ def lla_paged_evict(cache: PagedCache, to: PagedCache, budget: int, sinks=0, rec
     if kept is None:
         with _on_stream(stream):
             kept = torch.empty(shape, dtype=torch.int32, device=cache.device)
-    elif kept.shape != shape or kept.dtype != torch.int32 or kept.device != cache.device \
+    elif kept.shape != shape or kept.dtype != torch.int32 or kept.get_device() != cache._index \
             or not kept.is_contiguous():
         raise ValueError(f"kept must be a contiguous int32 tensor of shape {shape}")
     st = _load().lla_paged_evict(cache._packed, to._packed, budget, sinks, recent, kept.data_ptr(),

@@ -79,7 +79,7 @@ mass_tc_kernel(Params p, const __grid_constant__ CUtensorMap kmap, const __grid_
   Barriers& bar = *reinterpret_cast<Barriers*>(smem + C::sm_bar);
   __shared__ uint32_t tmem_base_s;
   __shared__ int abort_flag;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   const int per = BR / p.g, width = per * p.g;  // tokens and rows of a block
   int* const status = p.status;
   constexpr int TO = kStatusTimeout;
@@ -109,7 +109,7 @@ mass_tc_kernel(Params p, const __grid_constant__ CUtensorMap kmap, const __grid_
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tbase = tmem_base_s;
+  const uint32_t tbase = __shfl_sync(0xffffffffu, tmem_base_s, 0);
   volatile int* abort_p = &abort_flag;
 
   int lse_tok[4], lse_head[4];  // of rows lane, lane + 32, ..: token within the block, grouped head
@@ -136,17 +136,19 @@ mass_tc_kernel(Params p, const __grid_constant__ CUtensorMap kmap, const __grid_
     used = true;
 
     if (warp == 9) {
-      if (lane == 0) {
-        const uint64_t kd = smem_desc_sw128(smem_u32(smem), 1024);
-        const uint64_t qd = smem_desc_sw128(smem_u32(smem + C::sm_q), 1024);
-        constexpr uint32_t id = idesc_bf16(KT, BR, false, false);
-        bool ok = mbar_wait(&bar.kfull, items & 1, status, TO, abort_p);
-        for (int i = 0; i < nblk && ok; ++i) {
-          const int c = done + i, st = c & 1;
-          ok = mbar_wait(&bar.qfull[st], (c >> 1) & 1, status, TO, abort_p) &&
-               (c < 2 || mbar_wait(&bar.sfree[st], ((c >> 1) - 1) & 1, status, TO, abort_p));
-          if (!ok) break;
-          tc_fence_after();
+      // Warp-uniform, only the instructions under elect_one() (see lla_paged_tc.cu).
+      const uint64_t kd = smem_desc_sw128(smem_u32(smem), 1024);
+      const uint64_t qd = smem_desc_sw128(smem_u32(smem + C::sm_q), 1024);
+      constexpr uint32_t id = idesc_bf16(KT, BR, false, false);
+      auto wait = [&](uint64_t* x, uint32_t par) { return warp_wait(x, par, status, TO, abort_p); };
+      const int first = __shfl_sync(0xffffffffu, done, 0), count = __shfl_sync(0xffffffffu, nblk, 0);
+      bool ok = wait(&bar.kfull, items & 1);
+      for (int i = 0; i < count && ok; ++i) {
+        const int c = first + i, st = c & 1;
+        ok = wait(&bar.qfull[st], (c >> 1) & 1) && (c < 2 || wait(&bar.sfree[st], ((c >> 1) - 1) & 1));
+        if (!ok) break;
+        tc_fence_after();
+        if (elect_one()) {
 #pragma unroll
           for (int s = 0; s < D / 16; ++s) {
             const uint32_t o = (s >> 2) * 1024 + (s & 3) * 2;
@@ -155,8 +157,9 @@ mass_tc_kernel(Params p, const __grid_constant__ CUtensorMap kmap, const __grid_
           mma_commit(&bar.sfull[st]);
           mma_commit(&bar.qempty[st]);
         }
-        if (!ok) *abort_p = 1;
+        __syncwarp();
       }
+      if (!ok) *abort_p = 1;
       __syncwarp();
     } else if (warp == 8) {
       const int frag = min(p.page, KT), nfrag = KT / frag;
@@ -253,21 +256,26 @@ mass_tc_kernel(Params p, const __grid_constant__ CUtensorMap kmap, const __grid_
           unpair(add2(a[0], a[1]), y0, y1);
           got += y0 + y1;
         } else {
-          int pos = p0, u = 0;
-          float a = 0.f;
-#pragma unroll 1
-          for (int cc = 0; cc < BR; cc += 32) {
-            if (cc) tmem_ld32(lanes + grp * BR + cc, s[0]);
+          // The rows that see key j are a range: e0 <= row < e1. As bits, then a select each (a branch per
+          // row took several times as long).
+          const long long g = p.g, end = j < p.sinks ? width : ((long long)j + p.window - p0) * g;
+          const int e0 = (int)min(max(((long long)j - p0) * g, 0ll), (long long)BR);
+          const int e1 = (int)min(max(end, 0ll), min((long long)width, (long long)(sq.n - tok0) * g));
+          auto below = [](int x) { return x <= 0 ? 0u : x >= 32 ? 0xFFFFFFFFu : (1u << x) - 1u; };
+          float a[2] = {};
+#pragma unroll
+          for (int q = 0; q < BR / 32; ++q) {
             tmem_ld_wait();
+            if (q + 1 < BR / 32) tmem_ld32(lanes + grp * BR + (q + 1) * 32, s[(q + 1) & 1]);
+            else release(grp);
+            const unsigned seen = below(e1 - q * 32) & ~below(e0 - q * 32);
 #pragma unroll
             for (int e = 0; e < 32; ++e) {
-              const bool row = cc + e < width && pos - sq.first < sq.n;
-              if (row && visible(p, pos, j)) a += ex2(fmaf(__uint_as_float(s[0][e]), c2, lse[cc + e]));
-              if (++u == p.g) { u = 0; ++pos; }
+              const float y = ex2(fmaf(__uint_as_float(s[q & 1][e]), c2, lse[q * 32 + e]));
+              a[e & 1] += seen & (1u << e) ? y : 0.f;
             }
           }
-          got += a;
-          release(grp);
+          got += a[0] + a[1];
         }
       }
       reinterpret_cast<float*>(smem + C::sm_sum)[((items & 1) * 2 + grp) * KT + r] = got;
@@ -282,10 +290,12 @@ mass_tc_kernel(Params p, const __grid_constant__ CUtensorMap kmap, const __grid_
     done += nblk;
     ++items;
   }
-  if (warp == 9 && lane == 0 && used) {
-    mma_commit(&bar.done);
+  if (warp == 9 && used) {  // after an abort there may be products in flight
+    if (elect_one()) mma_commit(&bar.done);
+    __syncwarp();
     volatile int never = 0;
     mbar_wait(&bar.done, 0, status, TO, &never);
+    __syncwarp();
   }
   tc_fence_before();
   __syncthreads();
