@@ -201,30 +201,37 @@ __device__ __forceinline__ Place locate(const Params& p, const long long* cost, 
   return {p.B, 0, 0, 0};
 }
 // Whole tile x in the order last tiles of the sequences, last but one, .. (heads innermost): its place,
-// from the sequences' tile counts (a whole warp calls and agrees).
-__device__ __forceinline__ Place by_rank(const Params& p, const int* tiles, int most, long long x) {
+// from the sequences' tile counts (a whole warp calls and agrees; tiles x heads stay below 2^31).
+__device__ __forceinline__ Place by_rank(const Params& p, const int* tiles, int most, unsigned x) {
   const int lane = threadIdx.x & 31;
+  const unsigned row = x / p.Hkv;
+  const int hk = (int)(x - row * p.Hkv);
   auto upto = [&](int r) {  // tiles of rank below r
-    long long n = 0;
-    for (int i = lane; i < p.B; i += 32) n += min(tiles[i], r);
-#pragma unroll
-    for (int o = 16; o; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
-    return n * p.Hkv;
+    unsigned n = 0;
+    for (int i = 0; i < p.B; i += 32)
+      n += __reduce_add_sync(0xffffffffu, i + lane < p.B ? (unsigned)min(tiles[i + lane], r) : 0u);
+    return n;
   };
-  int lo = 0, hi = most;  // the rank r with upto(r) <= x < upto(r + 1)
+  int lo = 0, hi = most;  // the rank r with upto(r) <= row < upto(r + 1)
+  unsigned below = 0;
   while (hi - lo > 1) {
     const int mid = (lo + hi) / 2;
-    if (upto(mid) <= x) lo = mid;
-    else hi = mid;
+    const unsigned n = upto(mid);
+    if (n <= row) {
+      lo = mid;
+      below = n;
+    } else {
+      hi = mid;
+    }
   }
-  x -= upto(lo);
-  const int hk = (int)(x % p.Hkv);
-  long long k = x / p.Hkv;  // the k-th sequence with more than lo tiles
+  int k = (int)(row - below);  // the k-th sequence with more than lo tiles
   for (int base = 0; base < p.B; base += 32) {
-    const unsigned has = __ballot_sync(0xffffffffu, base + lane < p.B && tiles[base + lane] > lo);
-    if (k < __popc(has)) {
-      const int l = __fns(has, 0, (int)k + 1);
-      return {base + l, tiles[base + l] - 1 - lo, hk, 0};
+    const bool mine_ = base + lane < p.B && tiles[base + lane] > lo;
+    const unsigned has = __ballot_sync(0xffffffffu, mine_);
+    const unsigned it = __ballot_sync(0xffffffffu, mine_ && __popc(has & ((1u << lane) - 1u)) == k);
+    if (it) {
+      const int b = base + __ffs(it) - 1;
+      return {b, tiles[b] - 1 - lo, hk, 0};
     }
     k -= __popc(has);
   }
@@ -494,7 +501,7 @@ attend_tc_kernel(Params p, const __grid_constant__ CUtensorMap kmap, const __gri
       w.none = 1;
       if (most > 0) {
         const long long at = (long long)k * gridDim.x + (k & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
-        const Place t = at < ntiles ? by_rank(p, tiles_s, most, at) : Place{p.B, 0, 0, 0};
+        const Place t = at < ntiles ? by_rank(p, tiles_s, most, (unsigned)at) : Place{p.B, 0, 0, 0};
         if (t.b < p.B) {
           const Seq sq = load_seq(p, t.b);
           const Tile x(sq, t.tile, tokens);
@@ -532,6 +539,17 @@ attend_tc_kernel(Params p, const __grid_constant__ CUtensorMap kmap, const __gri
       if (w.none) break;
       if (w.n == 0) continue;
       const Tile x(Seq{w.t0, w.seq_n, w.len, w.first}, w.tile, tokens);
+      // Step i's first key, and this lane's page fragment of it: the page number is read a step ahead.
+      auto first_key = [&](int i) {
+        const int it = w.i0 + i;
+        return (it < w.n1 ? it : w.w0 + it - w.n1) * KT;
+      };
+      auto page_row = [&](int i) {  // row of the tensor map; out of range: zeros
+        const int j = first_key(i) + lane * frag;
+        const int pg = i < w.n && lane < nfrag && j < w.len ? load_page(p, w.b, j >> p.page_shift) : -1;
+        return pg >= 0 ? pg * p.Hkv + w.hk : p.num_pages * p.Hkv;
+      };
+      int c2_next = page_row(0);
       if (pieces > 0) ok = wait(&bar.opempty, (pieces - 1) & 1);
       if (!ok) break;
       ++pieces;
@@ -544,17 +562,13 @@ attend_tc_kernel(Params p, const __grid_constant__ CUtensorMap kmap, const __gri
       }
       __syncwarp();
       for (int i = 0; i < w.n && ok; ++i) {
-        const int it = w.i0 + i, k0 = (it < w.n1 ? it : w.w0 + it - w.n1) * KT, j = k0 + lane * frag;
+        const int k0 = first_key(i), j = k0 + lane * frag, c2 = c2_next;
+        c2_next = page_row(i + 1);
         int info = k0 | (k0 + KT > w.len ? 4 : 0);
 #pragma unroll
         for (int h = 0; h < C::blocks; ++h) {
           const int q0 = min(x.p0 + h * per, x.p1);
           if (!all_visible(p, q0, min(q0 + per - 1, x.p1), k0, k0 + KT)) info |= 1 << h;
-        }
-        int c2 = p.num_pages * p.Hkv;  // out of range: zeros
-        if (lane < nfrag && j < w.len) {
-          const int pg = load_page(p, w.b, j >> p.page_shift);
-          if (pg >= 0) c2 = pg * p.Hkv + w.hk;
         }
         for (int kv = 0; kv < 2 && ok; ++kv) {
           const int y = 2 * (base + i) + kv, st = y % C::stages;
