@@ -145,9 +145,7 @@ __device__ __forceinline__ bool find_tile(const Params& p, int per, int x, int* 
 }
 
 // One row computed by one warp straight from the definition, skipping every key that the row does
-// not see. The tiled kernels multiply such keys' values by a zero weight, which is not zero when
-// the value is infinite or NaN; a row whose result is not finite is therefore taken again here, out
-// and lse (and stays NaN only if a key that it sees makes it so). Slow, and off every ordinary path.
+// not see (see repair_row). Slow, and off every ordinary path.
 template <typename T>
 __device__ __noinline__ void exact_row(const Params& p, int b, int pos, int token, int head) {
   const int d = p.d, dv = p.dv;
@@ -213,6 +211,47 @@ __device__ __noinline__ void exact_row(const Params& p, int b, int pos, int toke
       stf(out, lane + 32 * c, r ? fmaf(o1[c], f1, -o2[c] * inv) : o1[c] * inv);
   if (p.lse && lane == 0)
     p.lse[(long long)token * p.Hq + head] = d1 == 0.f ? -CUDART_INF_F : m + logf(d1);
+}
+
+// Whether a key that the row at position `pos` does not see, in the KT-key tiles that its row block
+// (positions p0 .. p1) goes over, has a value that is not finite. One warp.
+template <typename T, int KT>
+__device__ __noinline__ bool hides_bad(const Params& p, const Seq& sq, int b, int hk, int pos, int p0, int p1) {
+  const int lane = threadIdx.x & 31;
+  const TileRange<KT> range(p, p0, p1);
+  const T* vp = static_cast<const T*>(p.v);
+  for (int base = 0; base < range.count; base += 32) {
+    const int k0 = base + lane < range.count ? range.tile(base + lane) * KT : 0;
+    unsigned masked = __ballot_sync(0xffffffffu, base + lane < range.count && !all_visible(p, pos, pos, k0, k0 + KT));
+    while (masked) {
+      const int t0 = __shfl_sync(0xffffffffu, k0, __ffs(masked) - 1);
+      masked &= masked - 1;
+      bool bad = false;
+      for (int j = t0; j < min(t0 + KT, sq.len); ++j) {
+        if (visible(p, pos, j)) continue;
+        const int pg = load_page(p, b, j >> p.page_shift);
+        if (pg < 0) continue;
+        const long long slot = ((long long)pg * p.Hkv + hk) * p.page + (j & (p.page - 1));
+        for (int c = lane; c < p.dv; c += 32) bad |= !isfinite(ldf(vp, slot * p.dv + c));
+      }
+      if (__any_sync(0xffffffffu, bad)) return true;
+    }
+  }
+  return false;
+}
+
+// A row that came out not finite (d1: its sum of weights), by one warp. The kernels multiply the values
+// of keys that a row does not see by a zero weight, which is not zero when such a value is infinite
+// or NaN; and a weight may pass the range of fp32 where the reference it is taken against is a step
+// old (d1 is infinite then). Either way the row is taken again from the definition. A NaN sum of
+// weights comes from a key that the row sees, and so does everything else that is not finite: those
+// rows stay as they are.
+template <typename T, int KT>
+__device__ __forceinline__ void repair_row(const Params& p, const Seq& sq, int b, int pos, int p0, int p1, int token,
+                                           int head, float d1) {
+  __syncwarp();
+  if (isnan(d1)) return;
+  if (isinf(d1) || hides_bad<T, KT>(p, sq, b, head / p.g, pos, p0, p1)) exact_row<T>(p, b, pos, token, head);
 }
 
 // ------------------------------------------------------------------------------------- arithmetic

@@ -230,6 +230,7 @@ __global__ void __launch_bounds__(NT) attend_cc_kernel(Params p) {
     const float inv = d1[i] == 0.f ? 0.f : 1.f / d1[i], f1 = (1.f + d2[i] * inv) * inv;
     float bad = 0.f;
     if (row < nrows) {
+      bad = d1[i] * 0.f;
       T* dst = static_cast<T*>(p.out) + rowid(row) * DV;
 #pragma unroll
       for (int c = 0; c < VC; ++c) {
@@ -246,12 +247,16 @@ __global__ void __launch_bounds__(NT) attend_cc_kernel(Params p) {
     if (hit >> 16) again |= 1u << (16 + i);
   }
   while (again) {  // the warp holds rows of two ty
-    const int bit = __ffs(again) - 1;
+    const int bit = __ffs(again) - 1, i = bit & 15;
     again &= again - 1;
-    const int row = ((threadIdx.x >> 5) * 2 + (bit >> 4)) * RM + (bit & 15);
+    const int row = ((threadIdx.x >> 5) * 2 + (bit >> 4)) * RM + i;
+    float sum = 0.f;
+#pragma unroll
+    for (int u = 0; u < RM; ++u)
+      if (u == i) sum = d1[u];
+    sum = __shfl_sync(0xffffffffu, sum, bit & 16);
     const long long id = rowid(row);
-    __syncwarp();
-    exact_row<T>(p, b, p0 + row / width, (int)(id / p.Hq), (int)(id % p.Hq));
+    repair_row<T, KT>(p, sq, b, p0 + row / width, p0, p1, (int)(id / p.Hq), (int)(id % p.Hq), sum);
   }
 }
 
@@ -363,8 +368,9 @@ __global__ void __launch_bounds__(128) join_kernel(Params p) {
     }
   if (p.lse && lane == 0) p.lse[id] = d1 == 0.f ? -CUDART_INF_F : m * p.inv_h + logf(d1);
   if (__any_sync(0xffffffffu, !(bad == 0.f))) {
-    __syncwarp();
-    exact_row<T>(p, b, sq.first + token - sq.t0, token, (int)(id % p.Hq));
+    const int first = sq.first + (token - sq.t0) / 64 * 64;  // (a block's rows are at most 64 tokens)
+    repair_row<T, KT>(p, sq, b, sq.first + token - sq.t0, max(first - 64, sq.first), min(first + 127, sq.len - 1),
+                      token, (int)(id % p.Hq), d1);
   }
 }
 

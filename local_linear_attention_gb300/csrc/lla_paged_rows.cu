@@ -96,8 +96,7 @@ __device__ __forceinline__ void write_row(const Params& p, const Seq& sq, int b,
     p.lse[(long long)token * p.Hq + head] =
         s1 == 0.f ? -CUDART_INF_F : (top * (p.inv_h * kLog2e) + log2f(s1)) * kLn2;
   if (__any_sync(0xffffffffu, !(bad == 0.f))) {
-    __syncwarp();
-    exact_row<__nv_bfloat16>(p, b, sq.first + r / p.g, token, head);
+    repair_row<__nv_bfloat16, KT>(p, sq, b, sq.first + r / p.g, sq.first, sq.len - 1, token, head, s1);
   }
 }
 

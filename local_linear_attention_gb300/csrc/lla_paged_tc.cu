@@ -38,6 +38,7 @@ using namespace tc;
 
 constexpr int BM = 128;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+constexpr float kTooFar = 100.f;  // a weight of 2^100: its products and sums may leave fp32
 
 template <int D, bool PROBE>
 struct Cfg {
@@ -716,9 +717,11 @@ attend_tc_kernel(Params p, const __grid_constant__ CUtensorMap kmap, const __gri
       if (__any_sync(0xffffffffu, grow)) {
         float sc = 1.f;
         if (grow) {
+          const float m_old = m;
           sc = ex2((m - top) * c2);  // 0 from -infinity
           m = top;
-          d1 *= sc;
+          // beyond what the last step's weights could hold: the row is taken again at the end
+          d1 = (top - m_old) * c2 > kTooFar && m_old != -CUDART_INF_F ? CUDART_INF_F : d1 * sc;
           d2 *= sc;
         }
         if (i > 0) {
@@ -793,6 +796,7 @@ attend_tc_kernel(Params p, const __grid_constant__ CUtensorMap kmap, const __gri
       d1 += a0 + a1;
       unpair(add2(sumt[0], sumt[1]), a0, a1);
       d2 += a0 + a1;
+      if ((tm - m) * c2 > kTooFar) d1 = CUDART_INF_F;  // weights too large to go on with (see repair_row)
     }
 
     if (NG > 1 && ok) {  // the groups' sums
@@ -882,10 +886,11 @@ attend_tc_kernel(Params p, const __grid_constant__ CUtensorMap kmap, const __gri
     }
     unsigned again = __ballot_sync(0xffffffffu, ok && there && !(bad == 0.f) && sub == 0);
     while (again) {
-      const int row = (warp & 3) * 32 + __ffs(again) - 1, tk = h * per + row / p.g;
+      const int l = __ffs(again) - 1, row = (warp & 3) * 32 + l, tk = h * per + row / p.g;
       again &= again - 1;
-      __syncwarp();
-      exact_row<__nv_bfloat16>(p, w->b, tile.p0 + tk, t0 + tile.tok0 + tk, hk * p.g + row % p.g);
+      const Seq sq{t0, w->seq_n, w->len, w->first};
+      repair_row<__nv_bfloat16, KT>(p, sq, w->b, tile.p0 + tk, tile.p0, tile.p1, t0 + tile.tok0 + tk, hk * p.g + row % p.g,
+                                    __shfl_sync(0xffffffffu, d1, l));
     }
     give_back(k);
     if (NG > 1 && ok) ok = exchange();  // and these
@@ -934,7 +939,7 @@ __global__ void __launch_bounds__(256) join_tc_kernel(Params p) {
     for (int i = 0; i < n; ++i) {
       const float4 st = p.part_s[at(i, row)];
       const float f = ex2(fmaf(st.x, c2, -ref));
-      s1 = fmaf(st.y, f, s1);
+      s1 = isinf(st.y) ? st.y : fmaf(st.y, f, s1);  // (infinite: see repair_row; times f it might be NaN)
       s2 = fmaf(st.z, f, s2);
       const float* src = p.part_o + at(i, row) * (PROBE ? 2 : 1) * D + lane * VC;
       if (lane * VC < p.dv) {
@@ -959,8 +964,7 @@ __global__ void __launch_bounds__(256) join_tc_kernel(Params p) {
     if (p.lse && lane == 0)
       p.lse[(long long)token * p.Hq + head] = s1 == 0.f ? -CUDART_INF_F : (top * c2 + log2f(s1)) * kLn2;
     if (__any_sync(0xffffffffu, !(bad == 0.f))) {
-      __syncwarp();
-      exact_row<__nv_bfloat16>(p, b, tile.p0 + t, token, head);
+      repair_row<__nv_bfloat16, C::kt>(p, sq, b, tile.p0 + t, tile.p0, tile.p1, token, head, s1);
     }
   }
 }

@@ -138,6 +138,47 @@ def test_a_value_that_is_not_finite_reaches_only_the_rows_that_see_it(lla, dtype
     assert out[good:].isnan().all() and lse[good:].isnan().all()
 
 
+@pytest.mark.parametrize("dtype,d,news", [(BF, 64, [300]), (BF, 128, [300]), (BF, 128, [1]), (F32, 32, [20])])
+def test_a_key_that_is_not_finite_far_back(lla, dtype, d, news):
+    """Every row sees it: all are NaN, and the call does not take its time over them."""
+    P = Problem([30000], news, 8, 2, d, d, 64, dtype, False, seed=22)
+    pg, off = P.slots(0)
+    P.k[pg[7], 0, off[7], 0] = math.nan
+    cache, q, r, starts = P.cuda(lla)
+    begin, end = torch.cuda.Event(True), torch.cuda.Event(True)
+    for _ in range(2):
+        begin.record()
+        out, lse = lla.lla_paged_attention(q, cache, starts, P.h, max_new=news[0])
+        end.record()
+    assert lla.lla_stream_status() == 0
+    assert out[:, :4].isnan().all() and lse[:, :4].isnan().all()
+    assert out[:, 4:].isfinite().all() and lse[:, 4:].isfinite().all()
+    assert begin.elapsed_time(end) < 100.0  # ms; rows taken again one by one would need seconds
+
+
+@pytest.mark.parametrize("probe", [False, True])
+@pytest.mark.parametrize("d", [64, 128])
+def test_logits_that_grow_from_tile_to_tile(lla, d, probe):
+    """Later keys outweigh everything before them by far more than the range of fp32."""
+    P = Problem([1500], [260], 4, 2, d, d, 64, BF, probe, seed=23)
+    pg, off = P.slots(0)
+    scale = torch.linspace(0.1, 30.0, 1500) ** 2
+    base = P.k[pg[0], 0, off[0]].clone()
+    P.k[pg, 0, off] = (base[None] * scale[:, None]).bfloat16()
+    P.q = (base.sign()[None, None] * P.q.abs()).bfloat16()  # q.k > 0 and growing with the position
+    run_and_check(lla, P)
+
+
+def test_more_sequences_than_the_tensor_core_kernel_schedules(lla):
+    P = Problem([20 + i % 13 for i in range(2100)], [2] * 2100, 9, 1, 64, 64, 16, BF, False, seed=24)
+    run_and_check(lla, P, track=False)
+
+
+def test_workspace_of_a_chunk(lla):
+    for d, probe in ((64, True), (128, False)):
+        run_and_check(lla, Problem([900, 5000], [150, 300], 4, 2, d, d, 32, BF, probe, seed=25), workspace=True)
+
+
 def test_rows_before_the_first_position_see_nothing(lla):
     """More new tokens than positions: the first rows have positions below zero."""
     for dtype, d, news in ((BF, 64, [5, 1]), (BF, 128, [200, 3]), (F32, 64, [70, 2])):
