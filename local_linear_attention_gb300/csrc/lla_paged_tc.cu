@@ -62,13 +62,13 @@ struct Cfg {
   static constexpr uint32_t cols = D == 64 ? 256 : 512;
   static_assert((overlay ? t_o + ops * D : t_p + ops * kt / 2) <= cols, "tensor memory");
   // shared memory: operands [ops][D/64][128 rows][128 B], ring of key and value tiles
-  // [D/64][kt rows][128 B], barriers, row exchange [4 buffers][nsoft/4 groups][128]
+  // [D/64][kt rows][128 B], barriers, row exchange [5 buffers][nsoft/4 groups][128], tile counts
   static constexpr int op_bytes = BM * D * 2, tile = kt * D * 2, half = kt * 128;
   static constexpr int stages = D == 128 ? 4 : PROBE ? 8 : 5;
   static constexpr int sm_ring = ops * op_bytes;
   static constexpr int sm_bar = sm_ring + stages * tile;
   static constexpr int sm_x = sm_bar + 512;
-  static constexpr int sm_tiles = sm_x + 4 * (nsoft / 4) * BM * 4, tiles_bytes = 2048 * 4;
+  static constexpr int sm_tiles = sm_x + 5 * (nsoft / 4) * BM * 4, tiles_bytes = 2048 * 4;
   static constexpr int bytes = sm_tiles + tiles_bytes + 1024;  // 1024: aligning the base
   static_assert(ctas * (bytes + 1024) <= 227 * 1024, "shared memory");
 };
@@ -610,8 +610,8 @@ attend_tc_kernel(Params p, const __grid_constant__ CUtensorMap kmap, const __gri
     const uint32_t lanes = tbase + ((uint32_t)((warp & 3) * 32) << 16);
     const float c2 = p.inv_h * kLog2e, slack = 8.f / c2;
     const bool wide = (reinterpret_cast<uintptr_t>(p.out) & 31) == 0;
-    // Exchange among the groups of a row: x[buffer][group][row], buffers 0 and 1 for the maxima of
-    // alternate steps, 2 and 3 for a piece's sums; between warps of the same rows.
+    // Exchange among the groups of a row: x[buffer][group][row], buffers 0 to 2 for the maxima of steps in
+    // turn, 3 and 4 for a piece's sums; between warps of the same rows.
     float* const xm = reinterpret_cast<float*>(smem + C::sm_x);
     auto slot = [&](int buf, int g) -> float& { return xm[((buf * C::blocks + h) * NG + g) * BM + r]; };
     int xphase = 0;  // phases of rowx used so far
@@ -634,7 +634,7 @@ attend_tc_kernel(Params p, const __grid_constant__ CUtensorMap kmap, const __gri
       sq.first = w->first;
       return Tile(sq, w->tile, tokens);
     };
-    float m = -CUDART_INF_F, d1 = 0.f, d2 = 0.f;
+    float m = -CUDART_INF_F, d1 = 0.f, d2 = 0.f, before = -CUDART_INF_F;
     for (int i = 0; i < n; ++i) {
       const int gi = base + i;
       ok = wait(&bar.sfull[h], gi & 1);
@@ -673,35 +673,38 @@ attend_tc_kernel(Params p, const __grid_constant__ CUtensorMap kmap, const __gri
           }
         }
       }
-      float t4[4] = {-CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F};
+      auto own_max = [&]() {  // over this thread's keys
+        float t4[4] = {-CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F};
 #pragma unroll
-      for (int c = 0; c < NC; c += 2)
-        t4[(c >> 1) & 3] = max3(t4[(c >> 1) & 3], __uint_as_float(s[c >> 5][c & 31]), __uint_as_float(s[c >> 5][(c & 31) + 1]));
-      float tm = fmaxf(max3(t4[0], t4[1], t4[2]), t4[3]);
+        for (int c = 0; c < NC; c += 2)
+          t4[(c >> 1) & 3] = max3(t4[(c >> 1) & 3], __uint_as_float(s[c >> 5][c & 31]), __uint_as_float(s[c >> 5][(c & 31) + 1]));
+        return fmaxf(max3(t4[0], t4[1], t4[2]), t4[3]);
+      };
       // The reference that weights are taken against. The first step of a piece and masked ones take
-      // the row's maximum over all groups. Others keep the reference of the step before, or the
-      // maximum of that step where it had outgrown it by 2^8 (the groups' maxima of the last step are
-      // there without waiting: the scores of this one come after all its weights): a weight is then at
-      // most 2^(growth within a step), which fp32 and bf16 hold up to 2^127; a row beyond that ends
-      // infinite and is taken again by itself. Waiting for the other group's maximum in every step
-      // took 700 of its 2400 cycles.
-      float top;
-      if (NG == 1) {
-        top = tm;
-      } else {
-        slot(gi & 1, sub) = tm;
-        // (with P in columns of its own the scores do not wait for the last weights: always exchange)
-        if (!C::overlay || i == 0 || masked || __any_sync(0xffffffffu, m == -CUDART_INF_F)) {
+      // the row's maximum over all groups. The others do not wait for a maximum: they keep the
+      // reference, or raise it to the maximum of two steps ago where that had outgrown it by 2^8, and
+      // find their own maximum once their weights are on the way. (Of two steps ago, because it was
+      // written before the arrivals that the scores of this step come after.) A weight is then at most
+      // 2^(growth over three steps); past 2^100 the row is given up here and taken again by itself.
+      // With the exchange in every step and the maximum in front of the weights, 1100 of a step's 3400
+      // cycles went there (d = 128).
+      // (With P in columns of its own the scores do not wait for the last weights: always exchanged.)
+      const bool exact = !C::overlay || i == 0 || masked || __any_sync(0xffffffffu, m == -CUDART_INF_F);
+      float tm = -CUDART_INF_F, top = m;
+      if (exact) {
+        top = tm = own_max();
+        if (NG > 1) {
+          slot(gi % 3, sub) = tm;
           ok = exchange();
           if (!ok) break;
-          top = slot(gi & 1, 0);
 #pragma unroll
-          for (int g = 1; g < NG; ++g) top = fmaxf(top, slot(gi & 1, g));
-        } else {
-          top = slot((gi - 1) & 1, 0);
-#pragma unroll
-          for (int g = 1; g < NG; ++g) top = fmaxf(top, slot((gi - 1) & 1, g));
+          for (int g = 0; g < NG; ++g) top = fmaxf(top, slot(gi % 3, g));
         }
+      } else if (NG == 1) {
+        top = before;
+      } else if (i > 1) {
+#pragma unroll
+        for (int g = 0; g < NG; ++g) top = fmaxf(top, slot((gi + 1) % 3, g));
       }
       // The products that read the previous P and O: where P overwrites S they precede this S in the
       // pipe; otherwise they are waited for before O is rescaled or P written.
@@ -796,18 +799,23 @@ attend_tc_kernel(Params p, const __grid_constant__ CUtensorMap kmap, const __gri
       d1 += a0 + a1;
       unpair(add2(sumt[0], sumt[1]), a0, a1);
       d2 += a0 + a1;
+      if (!exact) {
+        tm = own_max();
+        if (NG > 1) slot(gi % 3, sub) = tm;
+      }
+      before = tm;
       if ((tm - m) * c2 > kTooFar) d1 = CUDART_INF_F;  // weights too large to go on with (see repair_row)
     }
 
     if (NG > 1 && ok) {  // the groups' sums
-      slot(2, sub) = d1;
-      slot(3, sub) = d2;
+      slot(3, sub) = d1;
+      slot(4, sub) = d2;
       ok = exchange();
       d1 = d2 = 0.f;
 #pragma unroll
       for (int g = 0; g < NG; ++g) {
-        d1 += slot(2, g);
-        d2 += slot(3, g);
+        d1 += slot(3, g);
+        d2 += slot(4, g);
       }
     }
     if (ok && n > 0) {
@@ -878,11 +886,11 @@ attend_tc_kernel(Params p, const __grid_constant__ CUtensorMap kmap, const __gri
     if (NG > 1) {
       ok = exchange();  // the sums have been read
       if (!ok) break;
-      slot(2, sub) = bad;
+      slot(3, sub) = bad;
       ok = exchange();
       bad = 0.f;
 #pragma unroll
-      for (int g = 0; g < NG; ++g) bad += slot(2, g);
+      for (int g = 0; g < NG; ++g) bad += slot(3, g);
     }
     unsigned again = __ballot_sync(0xffffffffu, ok && there && !(bad == 0.f) && sub == 0);
     while (again) {
