@@ -1,28 +1,31 @@
-// Attention over a paged cache for sequences with many rows (prompts and chunks), bf16, head sizes
-// up to D = 64 or 128 (smaller ones padded with zeros: the tensor maps fill them in), on the tensor cores (tcgen05, tensor memory, TMA).
+// Attention over a paged cache for sequences with many rows (prompts and chunks), bf16, head sizes up
+// to D = 64 or 128 (smaller ones padded with zeros: the tensor maps fill them in), on the tensor
+// cores (tcgen05, tensor memory, TMA).
 //
-// One pass over the keys with a running row maximum. Per tile of KT keys and block of 128 rows
-// (tokens x grouped heads of one key/value head): S = Q K^T, P = exp(S - m), O += P V; with a probe
-// also T = R K^T, P2 = P .* T, O2 += P2 V. "Operand" below: Q of a block, or R.
-//   d = 128: one CTA per SM with two operands (512 tensor-memory columns: two S, two O). Softmax
+// One pass over the keys. Per tile of KT keys and block of 128 rows (tokens x grouped heads of one
+// key/value head): S = Q K^T, P = exp(S - m), O += P V; with a probe also T = R K^T, P2 = P .* T,
+// O2 += P2 V. "Operand" below: Q of a block, or R.
+//   D = 128: one CTA per SM with two operands (512 tensor-memory columns: two S, two O). Softmax
 //     attention takes two row blocks, whose softmax and matrix products alternate: while one
 //     block's weights are computed the tensor core works for the other, and both read one key tile.
-//   d = 64: two CTAs per SM of 256 columns each, which alternate by themselves: one row block with
+//   D = 64: two CTAs per SM of 256 columns each, which alternate by themselves: one row block with
 //     128-key tiles, or with a probe Q and R with 64-key tiles.
-// Warps: softmax (a thread is a row and KT / NG of a tile's keys; the NG groups of four warps that
-// share a row block pass the row maximum through shared memory), then a TMA loader (one lane per
-// page fragment; rows past the sequence's end and bad pages are loaded as zeros by an out-of-range
-// coordinate) and one MMA issuer. Its code is warp-uniform with only the instructions under
-// elect_one(): issued from a branch on the lane index, an MMA took 75 cycles of operand moves
-// against 64 of tensor pipe, and that was the bound (chunk of 2048 at 32768, d = 128: 1.06 -> 0.85
-// ms). One issuer serves both blocks in turn; with an issuer each, their products interleave,
-// finish together and the two softmax phases run in step instead of alternating.
-// bf16 P has columns of its own where there is room (d = 64 without a probe: the next scores are
-// issued as soon as these are read), else it overwrites its S and the next score product is issued
-// behind the value product that reads P (MMAs run in order).
-// The accumulators are rescaled only when a row's maximum grows by more than 2^8 (the weights then
-// stay below 2^8, exact in scale; d1 is fp32): after the first tiles this hardly happens.
+// Warps: softmax (a thread is a row and KT / NG of a tile's keys, NG groups of four warps to a row
+// block), then a TMA loader (one lane per page fragment; rows past the sequence's end and bad pages
+// are loaded as zeros by an out-of-range coordinate) and one MMA issuer. Its code is warp-uniform
+// with only the instructions under elect_one(): issued from a branch on the lane index, an MMA took
+// 75 cycles of operand moves against 64 of tensor pipe, and that was the bound (chunk of 2048 at
+// 32768, D = 128: 1.06 -> 0.85 ms). One issuer serves both blocks in turn; with an issuer each, their
+// products interleave, finish together and the two softmax phases run in step instead of alternating.
+// bf16 P overwrites its S, and the next score product is issued behind the value product that reads
+// P (MMAs run in order). (At D = 64 there is room for P beside S; using it measured 108 against 106
+// us on softmax prompts B4 T4096, 8 heads.)
+// The accumulators are rescaled only when a row's maximum outgrows its reference by more than 2^8;
+// after the first tiles this hardly happens.
 // Rounding: p and p t enter the value products as bf16, d1 and d2 sum the unrounded fp32 weights.
+// What bounds it: at D = 128 the chain softmax - value product - next scores of a block, about 3,100
+// cycles a 128-key step against 2,048 of MMA for the two blocks (chunk of 2048 at 32768, 32 heads
+// over 8: 1.4 PFLOP/s); at D = 64 the N = 64 products (about 59 cycles for 32 of work) and the same chain.
 // All mbarrier waits are bounded.
 #include <type_traits>
 
@@ -45,22 +48,23 @@ struct Cfg {
   static constexpr int kt = D == 64 && PROBE ? 64 : 128;       // keys per tile
   static constexpr int blocks = D == 128 && !PROBE ? 2 : 1;    // row blocks
   static constexpr int ops = blocks * (PROBE ? 2 : 1);         // operands: Q of each block, or Q and R
-  // groups of four warps per row block (d = 64, prompts of B4 T4096, 8 heads: 127 us with two, 138
-  // with one; with a probe 222 with two of 32 keys a thread, 195 with one of 64 and no exchange)
-  static constexpr int groups = D == 128 ? (PROBE ? 4 : 2) : (PROBE ? 1 : 2);
+  // Groups of four warps per row block. One, a thread taking a whole row of the tile, where the
+  // registers allow it: nothing is exchanged then (chunk of 2048 at 32768, D = 128: 779 us with two,
+  // 729 with one; prompts B4 T4096 D = 64: 121 and 108, with a probe 205 and 168). At D = 128 with a
+  // probe a row's scores and probe scores are 256 values: two groups (280 us with four, 269 with two
+  // on five prompts of 500 to 1800 tokens, 40 heads over 8).
+  static constexpr int groups = D == 128 && PROBE ? 2 : 1;
   static constexpr int nsoft = blocks * groups * 4;            // softmax warps
   static constexpr int ctas = D == 64 ? 2 : 1;                 // per SM
   static constexpr int threads = (nsoft + 2) * 32;
-  static constexpr bool overlay = D == 128 || PROBE;           // P overwrites S
-  // tensor memory: S [ops][kt], O [ops][D], and P [ops][kt/2] unless it overlays S
-  static constexpr uint32_t t_o = ops * kt, t_p = overlay ? 0 : t_o + ops * D;
-  static constexpr uint32_t p_stride = overlay ? kt : kt / 2;
-  // Column of key j's weight (j even): over S, each group's weights stay within the columns of its own
-  // scores, which it has read.
+  // tensor memory: S [ops][kt] with P in it, O [ops][D]
+  static constexpr uint32_t t_o = ops * kt;
+  // Column of key j's weight (j even) within S: each group's weights stay within the columns of its
+  // own scores, which it has read.
   static constexpr int nc = kt / groups;
-  static constexpr uint32_t p_col(int j) { return overlay ? j / nc * nc + j % nc / 2 : j / 2; }
+  static constexpr uint32_t p_col(int j) { return j / nc * nc + j % nc / 2; }
   static constexpr uint32_t cols = D == 64 ? 256 : 512;
-  static_assert((overlay ? t_o + ops * D : t_p + ops * kt / 2) <= cols, "tensor memory");
+  static_assert(t_o + ops * D <= cols, "tensor memory");
   // shared memory: operands [ops][D/64][128 rows][128 B], ring of key and value tiles
   // [D/64][kt rows][128 B], barriers, row exchange [5 buffers][nsoft/4 groups][128], tile counts
   static constexpr int op_bytes = BM * D * 2, tile = kt * D * 2, half = kt * 128;
@@ -75,7 +79,7 @@ struct Cfg {
 
 struct Barriers {
   uint64_t full[8], empty[8];
-  uint64_t sfull[2], sfree[2], pfull[2][2], pvdone[2];
+  uint64_t sfull[2], pfull[2][2], pvdone[2];
   uint64_t rowx[2][4], opfull, opempty, workfull[2], workempty[2], done;
 };
 static_assert(sizeof(Barriers) <= 512, "barrier region");
@@ -285,7 +289,6 @@ attend_tc_kernel(Params p, const __grid_constant__ CUtensorMap kmap, const __gri
     for (int s = 0; s < C::stages; ++s) { mbar_init(&bar.full[s], 1); mbar_init(&bar.empty[s], 1); }
     for (int s = 0; s < 2; ++s) {
       mbar_init(&bar.sfull[s], 1);
-      mbar_init(&bar.sfree[s], C::groups * 4);
       mbar_init(&bar.pfull[s][0], C::groups == 1 ? 4 : C::groups * 2);
       mbar_init(&bar.pfull[s][1], C::groups == 1 ? 4 : C::groups * 2);
       mbar_init(&bar.pvdone[s], 1);
@@ -429,7 +432,7 @@ attend_tc_kernel(Params p, const __grid_constant__ CUtensorMap kmap, const __gri
 #pragma unroll
           for (int u = 0; u < KT / 32; ++u) {
             const int s = half * (KT / 32) + u;
-            mma_ts(tbase + C::t_o + o * D, tbase + C::t_p + o * C::p_stride + C::p_col(s * 16),
+            mma_ts(tbase + C::t_o + o * D, tbase + o * KT + C::p_col(s * 16),
                    v + (uint64_t)(s * (2048 >> 4)), id_o, (!first || s > 0) ? 1u : 0u);
           }
           if (half) mma_commit(&bar.pvdone[o]);
@@ -452,29 +455,21 @@ attend_tc_kernel(Params p, const __grid_constant__ CUtensorMap kmap, const __gri
       give_back(k);
       if (n == 0) continue;
       // A row block's value products, half a step's weights at a time (the first product runs while
-      // the others are computed), and where P overwrote S the next scores behind them.
+      // the others are computed), and the next scores behind them.
       auto block = [&](auto h, auto o, int i) {
         const int gi = base + i;
         bool d = wait(&bar.pfull[h][0], gi & 1);
         if (d) values(o, Per{}, gi, i == 0, I0{});
         d = d && wait(&bar.pfull[h][1], gi & 1);
         if (d) values(o, Per{}, gi, i == 0, I1{});
-        if (d && C::overlay && i + 1 < n) scores(o, Per{}, gi + 1, i + 2 == n);
+        if (d && i + 1 < n) scores(o, Per{}, gi + 1, i + 2 == n);
         return d;
       };
       ok = wait(&bar.opfull, pieces++ & 1) && wait(&bar.full[stage(2 * base)], parity(2 * base));
-      // (S of its own: its last scores must have been read; P over S: the value products are issued)
-      if (!C::overlay && base > 0) ok = ok && wait(&bar.sfree[0], (base - 1) & 1);
       if (ok) scores(I0{}, All{}, base, n == 1);
       for (int i = 0; i < n && ok; ++i) {
-        const int gi = base + i, x = 2 * gi;
-        if (i + 1 < n) {
-          ok = wait(&bar.full[stage(x + 2)], parity(x + 2));
-          if (!C::overlay && ok) {  // the next scores as soon as these have been read
-            ok = wait(&bar.sfree[0], gi & 1);
-            if (ok) scores(I0{}, I1{}, gi + 1, i + 2 == n);
-          }
-        }
+        const int x = 2 * (base + i);
+        if (i + 1 < n) ok = wait(&bar.full[stage(x + 2)], parity(x + 2));
         ok = ok && wait(&bar.full[stage(x + 1)], parity(x + 1));
         ok = ok && block(I0{}, I0{}, i);
         if (C::blocks == 2) ok = ok && block(I1{}, Second{}, i);
@@ -649,11 +644,6 @@ attend_tc_kernel(Params p, const __grid_constant__ CUtensorMap kmap, const __gri
         for (int c = 0; c < NC / 32; ++c) tmem_ld32(lanes + KT + sub * NC + c * 32, tt[c]);
       }
       tmem_ld_wait();
-      if (!C::overlay) {
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bar.sfree[h]);
-      }
       const int info = uni(*(volatile int*)&step_s[gi & 7]), k0 = info & ~63, kb = k0 + sub * NC;
       const bool masked = (info >> h) & 1;
       if (masked) {
@@ -688,8 +678,7 @@ attend_tc_kernel(Params p, const __grid_constant__ CUtensorMap kmap, const __gri
       // 2^(growth over three steps); past 2^100 the row is given up here and taken again by itself.
       // With the exchange in every step and the maximum in front of the weights, 1100 of a step's 3400
       // cycles went there (d = 128).
-      // (With P in columns of its own the scores do not wait for the last weights: always exchanged.)
-      const bool exact = !C::overlay || i == 0 || masked || __any_sync(0xffffffffu, m == -CUDART_INF_F);
+      const bool exact = i == 0 || masked || __any_sync(0xffffffffu, m == -CUDART_INF_F);
       float tm = -CUDART_INF_F, top = m;
       if (exact) {
         top = tm = own_max();
@@ -706,16 +695,6 @@ attend_tc_kernel(Params p, const __grid_constant__ CUtensorMap kmap, const __gri
 #pragma unroll
         for (int g = 0; g < NG; ++g) top = fmaxf(top, slot((gi + 1) % 3, g));
       }
-      // The products that read the previous P and O: where P overwrites S they precede this S in the
-      // pipe; otherwise they are waited for before O is rescaled or P written.
-      bool drained = C::overlay || i == 0;
-      auto drain = [&]() {
-        if (drained) return true;
-        drained = true;
-        const bool d = wait(&bar.pvdone[h], (gi - 1) & 1);
-        tc_fence_after();
-        return d;
-      };
       const bool grow = top > m + slack || (m == -CUDART_INF_F && top > m);  // alike in every group
       if (__any_sync(0xffffffffu, grow)) {
         float sc = 1.f;
@@ -728,7 +707,7 @@ attend_tc_kernel(Params p, const __grid_constant__ CUtensorMap kmap, const __gri
           d2 *= sc;
         }
         if (i > 0) {
-          if (!(ok = drain())) break;
+          // (the products that went into them precede this step's scores in the pipe)
           // the row block's accumulators, an equal part per group
           constexpr int part_cols = (PROBE ? 2 : 1) * D / NG;
           const uint32_t o = lanes + C::t_o + h * D + sub * part_cols;
@@ -782,9 +761,8 @@ attend_tc_kernel(Params p, const __grid_constant__ CUtensorMap kmap, const __gri
             wt[e / 2] = pack_bf16(z0, z1);
           }
         }
-        if (!(ok = drain())) break;
-        tmem_st16(lanes + C::t_p + h * C::p_stride + C::p_col(sub * NC) + c * 16, wp);
-        if constexpr (PROBE) tmem_st16(lanes + C::t_p + C::p_stride + C::p_col(sub * NC) + c * 16, wt);
+        tmem_st16(lanes + h * KT + C::p_col(sub * NC) + c * 16, wp);
+        if constexpr (PROBE) tmem_st16(lanes + KT + C::p_col(sub * NC) + c * 16, wt);
         // half of the step's weights are there: with this group's last, or, alone, halfway
         if (c + 1 == NC / 32 || (NG == 1 && c + 1 == NC / 64)) {
           tmem_st_wait();
@@ -835,40 +813,47 @@ attend_tc_kernel(Params p, const __grid_constant__ CUtensorMap kmap, const __gri
     const long long pid = (long long)piece * Sched<D, PROBE>::rows + h * BM + r;
     float bad = (d1 + d2) * 0.f;  // NaN when something is not finite
     constexpr int NO = D / NG;  // output columns per thread
-#pragma unroll
-    for (int c = sub * NO; c < (sub + 1) * NO; c += 16) {
-      uint32_t a[16], e[16];
+#pragma unroll 1
+    for (int c0 = sub * NO; c0 < (sub + 1) * NO; c0 += 32) {
+      uint32_t a[32], e[PROBE ? 32 : 1];
       if (n > 0) {
-        tmem_ld16(lanes + C::t_o + h * D + c, a);
-        if (PROBE) tmem_ld16(lanes + C::t_o + D + c, e);
+        tmem_ld32(lanes + C::t_o + h * D + c0, a);
+        if constexpr (PROBE) tmem_ld32(lanes + C::t_o + D + c0, e);
         tmem_ld_wait();
       } else {
 #pragma unroll
-        for (int u = 0; u < 16; ++u) a[u] = e[u] = 0u;
-      }
-      if (!there || c >= p.dv) continue;
-      if (!whole) {
-        float* dst = p.part_o + pid * (PROBE ? 2 : 1) * D + c;
-#pragma unroll
-        for (int u = 0; u < 16; u += 8) {
-          store32(dst + u, *reinterpret_cast<const uint32_t(*)[8]>(a + u), true);
-          if (PROBE) store32(dst + D + u, *reinterpret_cast<const uint32_t(*)[8]>(e + u), true);
+        for (int u = 0; u < 32; ++u) {
+          a[u] = 0u;
+          if constexpr (PROBE) e[u] = 0u;
         }
-        continue;
       }
-      uint32_t o[8];
 #pragma unroll
-      for (int u = 0; u < 16; u += 2) {
-        float y0 = __uint_as_float(a[u]) * (PROBE ? f1 : inv);
-        float y1 = __uint_as_float(a[u + 1]) * (PROBE ? f1 : inv);
-        if (PROBE) {
-          y0 = fmaf(-__uint_as_float(e[u]), inv, y0);
-          y1 = fmaf(-__uint_as_float(e[u + 1]), inv, y1);
+      for (int q = 0; q < 32; q += 16) {
+        const int c = c0 + q;
+        if (!there || c >= p.dv) continue;
+        if (!whole) {
+          float* dst = p.part_o + pid * (PROBE ? 2 : 1) * D + c;
+#pragma unroll
+          for (int u = 0; u < 16; u += 8) {
+            store32(dst + u, *reinterpret_cast<const uint32_t(*)[8]>(a + q + u), true);
+            if constexpr (PROBE) store32(dst + D + u, *reinterpret_cast<const uint32_t(*)[8]>(e + q + u), true);
+          }
+          continue;
         }
-        bad += (y0 + y1) * 0.f;
-        o[u / 2] = pack_bf16(y0, y1);
+        uint32_t o[8];
+#pragma unroll
+        for (int u = 0; u < 16; u += 2) {
+          float y0 = __uint_as_float(a[q + u]) * (PROBE ? f1 : inv);
+          float y1 = __uint_as_float(a[q + u + 1]) * (PROBE ? f1 : inv);
+          if constexpr (PROBE) {
+            y0 = fmaf(-__uint_as_float(e[q + u]), inv, y0);
+            y1 = fmaf(-__uint_as_float(e[q + u + 1]), inv, y1);
+          }
+          bad += (y0 + y1) * 0.f;
+          o[u / 2] = pack_bf16(y0, y1);
+        }
+        store32(static_cast<__nv_bfloat16*>(p.out) + id * p.dv + c, o, wide);
       }
-      store32(static_cast<__nv_bfloat16*>(p.out) + id * p.dv + c, o, wide);
     }
     tc_fence_before();  // these reads, before the arrivals that let the next piece's products go
     if (there && sub == 0) {
