@@ -58,7 +58,8 @@ extern "C" {
 typedef enum {
   LLA_OK = 0,
   LLA_ERR_INVALID_ARG = 1, /* null/misaligned pointer, bad h/lambda/dtype, negative size       */
-  LLA_ERR_UNSUPPORTED = 2, /* d or dv outside {16, 32, 64}, or B*H*T >= 2^31                     */
+  LLA_ERR_UNSUPPORTED = 2, /* d or dv outside {16, 32, 64}, or B*H*T >= 2^31; for the paged
+                              operators, the limits listed with them                              */
   LLA_ERR_CUDA = 3,        /* a CUDA runtime call or kernel launch failed                         */
   LLA_ERR_NUMERICAL = 4,   /* a ridge solve met a non-positive pivot (rows set to NaN)            */
   LLA_ERR_TIMEOUT = 5      /* a bounded device-side wait gave up (kernel returned early)          */

@@ -587,7 +587,7 @@ const char* lla_status_string(int status) {
   switch (status) {
     case LLA_OK: return "LLA_OK: success";
     case LLA_ERR_INVALID_ARG: return "LLA_ERR_INVALID_ARG: invalid argument";
-    case LLA_ERR_UNSUPPORTED: return "LLA_ERR_UNSUPPORTED: unsupported size (d, dv in {16,32,64}; B*H*T < 2^31)";
+    case LLA_ERR_UNSUPPORTED: return "LLA_ERR_UNSUPPORTED: unsupported size (d, dv in {16,32,64}, paged operators also 128; B*H*T < 2^31)";
     case LLA_ERR_CUDA: return "LLA_ERR_CUDA: a CUDA call or kernel launch failed";
     case LLA_ERR_NUMERICAL: return "LLA_ERR_NUMERICAL: non-positive pivot in a ridge solve";
     case LLA_ERR_TIMEOUT: return "LLA_ERR_TIMEOUT: a bounded device wait gave up";

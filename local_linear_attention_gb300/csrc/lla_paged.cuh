@@ -41,12 +41,14 @@ struct Params {
   int max_rows;       // most rows (new tokens x g) of any sequence, as the caller states
   int lo, hi;         // this launch takes the sequences with lo < rows <= hi
   int beside;         // few-rows kernel: launched behind the tensor-core kernel, may overlap it
-  // Split of each row's keys over blocks, and its partial results (split > 1).
+  // Blocks that share a row's keys (tensor-core kernel: CTAs of the launch), and their partial
+  // results: {m, d1, d2, 0} with m the reference of the weights (raw q.k), and unnormalised O1 (and
+  // O2). CUDA cores and few rows (split > 1): [split][rows], rows = tokens * Hq with O rows of dv, or
+  // B * Hkv * rows_limit with O rows of D. Tensor cores: [CTA][2 slots][rows of a tile], O rows of D.
   int split;
-  float* part_o;     // [split][rows][branches][dv]   unnormalised O1 (and O2)
-  int4* pieces;      // tensor-core kernel: [split CTAs][2] {sequence, tile, head, there is one}
-  float4* part_s;    // [split][rows]   {m, d1, d2, 0} with m the maximum of q.k (raw)
-                     // rows: tokens * Hq, or B * Hkv * rows_limit of the few-rows kernel
+  float* part_o;
+  float4* part_s;
+  int4* pieces;      // tensor-core kernel: [CTA][2 slots] {sequence, tile, head, there is one}
   float* logits;     // [B * Hkv][row_cap][keys_cap]  raw q.k of the few-rows kernel, by the key's
                      // place among the visible 16-key steps (weight tracking)
   int row_cap, keys_cap;
@@ -368,6 +370,7 @@ struct TcPlan {
   int ctas = 0;            // 0: not for these kernels
   size_t rows = 0;         // rows of partial results (part_s, part_o), row_floats of part_o each
   int row_floats = 0;
+  bool cuts = false;       // whether a tile may have enough steps to be cut
 };
 TcPlan plan_tc(int D, bool probe, long long tokens, int B, int Hkv, int g, long long keys);
 cudaError_t launch_attend_tc(const Params& p, int D, cudaStream_t s);

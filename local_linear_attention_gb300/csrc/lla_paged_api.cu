@@ -100,6 +100,7 @@ struct Plan {
   bool rows = false;   // the few-rows kernel takes the sequences of at most rows_limit rows
   bool tiles = false;  // a tiled kernel the others: tensor cores (tc) or CUDA cores
   bool tc = false;
+  bool join = false;   // tensor cores: tiles may be cut
   int D = 0;           // head size of the tensor-core kernels
   int rows_split = 1, tiles_split = 1;
   int row_cap = 0, keys_cap = 0;
@@ -119,7 +120,10 @@ Plan make_plan(const lla_paged_cache* c, const lla_paged_query* a) {
   pl.D = padded(c->d > c->dv ? c->d : c->dv);
   const int limit = rows_limit(a->r != nullptr);
   const int branches = a->r ? 2 : 1;
-  pl.rows = tc && g <= limit;
+  // The few-rows kernel, unless the counts leave no sequence for it: a sequence of at most limit / g
+  // new tokens falls short of max_new by more than all sequences together do.
+  const long long short_of = max_new * c->num_seqs - a->tokens;
+  pl.rows = tc && g <= limit && (rows <= limit || short_of >= max_new - limit / g);
   pl.tiles = !pl.rows || rows > limit;
   size_t at = 0;
   auto take = [&](size_t bytes) { const size_t o = at; at += align_up(bytes); return o; };
@@ -152,6 +156,7 @@ Plan make_plan(const lla_paged_cache* c, const lla_paged_query* a) {
     pl.tc = t.ctas > 0;
     if (pl.tc) {
       pl.tiles_split = t.ctas;
+      pl.join = t.cuts;
       pl.pieces = take((size_t)t.ctas * 2 * sizeof(int4));
       pl.tiles_s = take(t.rows * sizeof(float4));
       pl.tiles_o = take(t.rows * t.row_floats * sizeof(float));
@@ -219,7 +224,7 @@ int run_attention(const lla_paged_cache* c, const lla_paged_query* a, const Plan
     if (launch_attend_rows(f, pl.D, s) != cudaSuccess) return LLA_ERR_CUDA;
   }
   if (pl.tiles) {
-    if (pl.tc ? launch_join_tc(p, pl.D, s) != cudaSuccess
+    if (pl.tc ? pl.join && launch_join_tc(p, pl.D, s) != cudaSuccess
               : p.split > 1 && launch_join(p, c->dv, c->dtype, s) != cudaSuccess)
       return LLA_ERR_CUDA;
     if (a->track_mass && (pl.tc ? launch_mass_tc(p, padded(c->d), s) : launch_mass_cc(p, c->d, c->dtype, s)) != cudaSuccess)

@@ -901,22 +901,26 @@ attend_tc_kernel(Params p, const __grid_constant__ CUtensorMap kmap, const __gri
 // The pieces of a tile that was cut: block x joins the tile whose first piece CTA x has (slot 1); the
 // next CTAs' slots 0 continue it. One warp per row, blocks y apart.
 template <int D, bool PROBE>
-__global__ void __launch_bounds__(256) join_tc_kernel(Params p) {
+__global__ void __launch_bounds__(256, 4) join_tc_kernel(Params p) {
   using C = Cfg<D, PROBE>;
   constexpr int ROWS = Sched<D, PROBE>::rows, VC = D / 32;
   wait_previous();
   const int4 first = p.pieces[blockIdx.x * 2 + 1];
   if (!first.w) return;
+  const int lane = threadIdx.x & 31;
   int n = 1;
-  while (blockIdx.x + n < gridDim.x) {
-    const int4 x = p.pieces[(blockIdx.x + n) * 2];
-    if (!x.w || x.x != first.x || x.y != first.y || x.z != first.z) break;
-    ++n;
+  for (;; n += 32) {  // the CTAs that continue it, 32 looked at together
+    const int c = blockIdx.x + n + lane;
+    const int4 x = c < gridDim.x ? p.pieces[c * 2] : make_int4(0, 0, 0, 0);
+    const unsigned on = __ballot_sync(0xffffffffu, x.w && x.x == first.x && x.y == first.y && x.z == first.z);
+    if (on != 0xffffffffu) {
+      n += __ffs(~on) - 1;
+      break;
+    }
   }
   const int per = BM / p.g, tokens = C::blocks * per, b = first.x, hk = first.z;
   const Seq sq = load_seq(p, b);
   const Tile tile(sq, first.y, tokens);
-  const int lane = threadIdx.x & 31;
   const float c2 = p.inv_h * kLog2e;
   auto at = [&](int i, int row) { return (long long)((blockIdx.x + i) * 2 + (i == 0)) * ROWS + row; };
   for (int row = blockIdx.y * 8 + (threadIdx.x >> 5); row < ROWS; row += gridDim.y * 8) {
@@ -981,12 +985,13 @@ TcPlan plan_t(long long tokens, int B, int Hkv, int g, long long keys) {
   using S = Sched<D, PROBE>;
   // No more CTAs than pieces there can be.
   const long long tiles = (tokens / (BM / g * C::blocks) + B) * Hkv;
-  const long long steps = (keys + C::kt - 1) / C::kt + 2;  // a window may begin and end inside a tile
+  const long long steps = (keys + C::kt - 1) / C::kt + 3;  // first tokens and window may begin and end inside tiles
   const long long most = tiles * ((steps + S::kPiece - 1) / S::kPiece);
   TcPlan t;
   t.ctas = (int)(most < 152 * C::ctas ? most : 152 * C::ctas);
   t.rows = (size_t)t.ctas * 2 * S::rows;
   t.row_floats = (PROBE ? 2 : 1) * D;
+  t.cuts = steps >= 2 * S::kPiece;  // (see locate: both sides of a cut have kPiece steps)
   return t;
 }
 
@@ -1038,7 +1043,7 @@ cudaError_t launch_attend_tc(const Params& p, int D, cudaStream_t s) {
 cudaError_t launch_join_tc(const Params& p, int D, cudaStream_t s) {
   auto kern = p.r ? (D == 128 ? join_tc_kernel<128, true> : join_tc_kernel<64, true>)
                   : (D == 128 ? join_tc_kernel<128, false> : join_tc_kernel<64, false>);
-  return launch(kern, dim3((unsigned)p.split, 16), 256, 0, 1, true, s, p);
+  return launch(kern, dim3((unsigned)p.split, 8), 256, 0, 1, true, s, p);
 }
 
 }  // namespace paged
