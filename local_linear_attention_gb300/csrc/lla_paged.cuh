@@ -44,7 +44,7 @@ struct Params {
   // Blocks that share a row's keys (tensor-core kernel: CTAs of the launch), and their partial
   // results: {m, d1, d2, 0} with m the reference of the weights (raw q.k), and unnormalised O1 (and
   // O2). CUDA cores and few rows (split > 1): [split][rows], rows = tokens * Hq with O rows of dv, or
-  // B * Hkv * rows_limit with O rows of D. Tensor cores: [CTA][2 slots][rows of a tile], O rows of D.
+  // B * Hkv * row_cap with O rows of D. Tensor cores: [CTA][2 slots][rows of a tile], O rows of D.
   int split;
   float* part_o;
   float4* part_s;
@@ -341,15 +341,11 @@ __device__ __forceinline__ void let_next() {
 // Launchers (each returns the launch error, if any).
 // CUDA cores, every supported size (one set per type): the attention; mass += the rows' weights from
 // q, k and the finished lse; the join of the splits' partial results into out and lse.
-cudaError_t attend_cc_f32(const Params& p, int d, int dv, cudaStream_t s);
 cudaError_t attend_cc_bf16(const Params& p, int d, int dv, cudaStream_t s);
 cudaError_t mass_cc_f32(const Params& p, int d, cudaStream_t s);
 cudaError_t mass_cc_bf16(const Params& p, int d, cudaStream_t s);
 cudaError_t join_f32(const Params& p, int dv, cudaStream_t s);
 cudaError_t join_bf16(const Params& p, int dv, cudaStream_t s);
-inline cudaError_t launch_attend_cc(const Params& p, int d, int dv, int dtype, cudaStream_t s) {
-  return dtype == LLA_F32 ? attend_cc_f32(p, d, dv, s) : attend_cc_bf16(p, d, dv, s);
-}
 inline cudaError_t launch_mass_cc(const Params& p, int d, int dtype, cudaStream_t s) {
   return dtype == LLA_F32 ? mass_cc_f32(p, d, s) : mass_cc_bf16(p, d, s);
 }
@@ -364,6 +360,12 @@ inline int padded(int d) { return d > 64 ? 128 : 64; }
 constexpr int kRowsCluster = 8;  // splits that join within a cluster (the portable size)
 inline int rows_limit(bool probe) { return probe ? 8 : 16; }
 cudaError_t launch_attend_rows(const Params& p, int D, cudaStream_t s);
+// fp32: the attention of every sequence in tiles of kF32Rows rows, at most f32_tiles a key/value head;
+// the weight tracking of the sequences of at most p.row_cap rows, whose logits are in p.logits.
+constexpr int kF32Rows = 16, kF32MassRows = 256;
+long long f32_tiles(long long tokens, long long max_new, int B, int g);
+cudaError_t launch_attend_f32(const Params& p, long long tiles, int D, cudaStream_t s);
+cudaError_t launch_mass_f32(const Params& p, cudaStream_t s);
 // Sequences of many rows: the attention on p.split CTAs, the join of the tiles that their shares
 // cut; the weight tracking (D = padded(d)).
 struct TcPlan {

@@ -99,6 +99,7 @@ size_t align_up(size_t x) { return (x + kAlign - 1) / kAlign * kAlign; }
 struct Plan {
   bool rows = false;   // the few-rows kernel takes the sequences of at most rows_limit rows
   bool tiles = false;  // a tiled kernel the others: tensor cores (tc) or CUDA cores
+  long long f32 = 0;   // fp32: one kernel's tiles; `rows` and `tiles` are the weight tracking's parts
   bool tc = false;
   bool join = false;   // tensor cores: tiles may be cut
   int D = 0;           // head size of the tensor-core kernels
@@ -118,12 +119,12 @@ Plan make_plan(const lla_paged_cache* c, const lla_paged_query* a) {
   const long long rows = max_new * g, pairs = (long long)c->num_seqs * c->kv_heads;
   const bool tc = c->dtype == LLA_BF16 && a->path != LLA_PATH_CUDA_CORE;
   pl.D = padded(c->d > c->dv ? c->d : c->dv);
-  const int limit = rows_limit(a->r != nullptr);
+  const int limit = c->dtype == LLA_F32 ? kF32Rows : rows_limit(a->r != nullptr);
   const int branches = a->r ? 2 : 1;
   // The few-rows kernel, unless the counts leave no sequence for it: a sequence of at most limit / g
   // new tokens falls short of max_new by more than all sequences together do.
   const long long short_of = max_new * c->num_seqs - a->tokens;
-  pl.rows = tc && g <= limit && (rows <= limit || short_of >= max_new - limit / g);
+  pl.rows = (tc || c->dtype == LLA_F32) && g <= limit && (rows <= limit || short_of >= max_new - limit / g);
   pl.tiles = !pl.rows || rows > limit;
   size_t at = 0;
   auto take = [&](size_t bytes) { const size_t o = at; at += align_up(bytes); return o; };
@@ -132,6 +133,38 @@ Plan make_plan(const lla_paged_cache* c, const lla_paged_query* a) {
     if (n > keys / least) n = keys / least;
     return n < 1 ? 1 : n > 512 ? 512 : (int)n;
   };
+  if (c->dtype == LLA_F32) {
+    pl.f32 = f32_tiles(a->tokens, max_new, c->num_seqs, g);
+    // As below, but scratch sooner: a step of 32 keys takes a warp longer (3 sequences of 7.7k, 2 heads
+    // of 64, 16 rows: 34 us with 26 blocks a tile, 71 with 8).
+    const long long blocks = pl.f32 * c->kv_heads;
+    const int fill = splits(blocks, 304, 128), level = splits(blocks, 1216, 1024);
+    pl.tiles_split = fill > level ? fill : level;
+    if (pl.tiles_split > kRowsCluster && keys <= kRowsCluster * 256) pl.tiles_split = kRowsCluster;
+    if (pl.tiles_split > kRowsCluster) {
+      const size_t all = (size_t)a->tokens * a->q_heads * pl.tiles_split;
+      pl.tiles_s = take(all * sizeof(float4));
+      pl.tiles_o = take(all * branches * c->dv * sizeof(float));
+    }
+    if (a->track_mass) {
+      // The weights of sequences of up to kF32MassRows rows come from their logits, which cost 8 bytes
+      // of traffic each against 2 d flops to compute them again, where the scratch stays below 512 MB;
+      // those of longer ones from q and k.
+      pl.keys_cap = (int)((keys + 64 < cap ? keys + 64 : cap) + 15) / 16 * 16;
+      const size_t row_bytes = (size_t)pairs * pl.keys_cap * sizeof(float);
+      if (rows <= kF32MassRows && rows * row_bytes <= (size_t)512 << 20) {
+        pl.row_cap = (int)rows;
+        pl.rows = true;
+        pl.tiles = false;
+      } else if (pl.rows) {
+        pl.row_cap = (int)(rows < limit ? rows : limit);
+      }
+      if (pl.rows) pl.logits = take(pl.row_cap * row_bytes);
+    }
+    if (a->track_mass && !a->lse) pl.lse = take((size_t)a->tokens * a->q_heads * sizeof(float));
+    pl.bytes = at;
+    return pl;
+  }
   if (pl.rows) {
     pl.row_cap = (int)(rows < limit ? rows : limit);
     // Two blocks per SM first, down to 128 keys each (one sequence, 8 heads of 64, L 1000: 5.0 us
@@ -143,8 +176,8 @@ Plan make_plan(const lla_paged_cache* c, const lla_paged_query* a) {
     pl.rows_split = fill > level ? fill : level;
     if (pl.rows_split > kRowsCluster && keys <= kRowsCluster * 1024) pl.rows_split = kRowsCluster;
     if (pl.rows_split > kRowsCluster) {
-      pl.rows_s = take((size_t)pairs * limit * pl.rows_split * sizeof(float4));
-      pl.rows_o = take((size_t)pairs * limit * pl.rows_split * branches * pl.D * sizeof(float));
+      pl.rows_s = take((size_t)pairs * pl.row_cap * pl.rows_split * sizeof(float4));
+      pl.rows_o = take((size_t)pairs * pl.row_cap * pl.rows_split * branches * pl.D * sizeof(float));
     }
     if (a->track_mass) {
       pl.keys_cap = (int)((keys + 64 < cap ? keys + 64 : cap) + 15) / 16 * 16;
@@ -178,6 +211,30 @@ Plan make_plan(const lla_paged_cache* c, const lla_paged_query* a) {
   return pl;
 }
 
+int run_f32(const Params& p, const Plan& pl, int track_mass, char* ws, cudaStream_t s) {
+  Params f = p;
+  f.split = pl.tiles_split;
+  f.row_cap = pl.row_cap;
+  f.keys_cap = pl.keys_cap;
+  if (f.split > kRowsCluster) {
+    f.part_s = reinterpret_cast<float4*>(ws + pl.tiles_s);
+    f.part_o = reinterpret_cast<float*>(ws + pl.tiles_o);
+  }
+  if (track_mass && pl.rows) f.logits = reinterpret_cast<float*>(ws + pl.logits);
+  cudaError_t err = launch_attend_f32(f, pl.f32, pl.D, s);
+  if (err == cudaSuccess && f.split > kRowsCluster) err = launch_join(f, p.dv, LLA_F32, s);
+  if (track_mass && pl.rows && err == cudaSuccess) {
+    f.hi = pl.row_cap;
+    err = launch_mass_f32(f, s);
+  }
+  if (track_mass && pl.tiles && err == cudaSuccess) {
+    f.lo = pl.row_cap;
+    f.hi = p.hi;
+    err = launch_mass_cc(f, p.d, LLA_F32, s);
+  }
+  return err == cudaSuccess ? LLA_OK : LLA_ERR_CUDA;
+}
+
 int run_attention(const lla_paged_cache* c, const lla_paged_query* a, const Plan& pl, char* ws,
                   cudaStream_t s) {
   Params p = cache_params(c);
@@ -196,6 +253,7 @@ int run_attention(const lla_paged_cache* c, const lla_paged_query* a, const Plan
   const long long rows = (long long)a->max_new * p.g;
   p.max_rows = rows < 0x7fffffffLL ? (int)rows : 0x7fffffff;
   if (a->track_mass && !a->lse) p.lse = reinterpret_cast<float*>(ws + pl.lse);
+  if (c->dtype == LLA_F32) return run_f32(p, pl, a->track_mass, ws, s);
   Params f = p;  // the few-rows kernel's
   p.lo = pl.rows ? pl.row_cap : 0;
   p.split = pl.tiles_split;
@@ -205,7 +263,7 @@ int run_attention(const lla_paged_cache* c, const lla_paged_query* a, const Plan
       p.part_o = reinterpret_cast<float*>(ws + pl.tiles_o);
     }
     if (pl.tc) p.pieces = reinterpret_cast<int4*>(ws + pl.pieces);
-    if ((pl.tc ? launch_attend_tc(p, pl.D, s) : launch_attend_cc(p, c->d, c->dv, c->dtype, s)) != cudaSuccess)
+    if ((pl.tc ? launch_attend_tc(p, pl.D, s) : attend_cc_bf16(p, c->d, c->dv, s)) != cudaSuccess)
       return LLA_ERR_CUDA;
   }
   if (pl.rows) {

@@ -1,7 +1,7 @@
-// Attention of new tokens over a paged cache on the CUDA cores: every type (fp32, bf16) and head
-// size (16, 32, 64, 128, keys and values independent). bf16 runs here only when asked to
-// (LLA_PATH_CUDA_CORE), with more than 128 heads to a key/value head, or for chunks of more than 2048
-// sequences at once; fp32 always.
+// Attention of new tokens over a paged cache on the CUDA cores, head sizes 16, 32, 64, 128, keys and
+// values independent: the attention of bf16 where it is asked to (LLA_PATH_CUDA_CORE), with more than 128
+// heads to a key/value head, or for chunks of more than 2048 sequences at once; the join of splits and
+// the weight tracking of more than 16 rows, for fp32 too.
 //
 // Mathematics, per row with visible keys j (logit s_j = q.k_j / h, probe t_j = r.k_j):
 //   m = max s, p_j = exp(s_j - m), d1 = sum p, O1 = sum p v, and with a probe d2 = sum p t,
@@ -11,12 +11,9 @@
 // A block takes BM rows (tokens x grouped heads of one key/value head, so that each key tile is
 // read once for all of them) and key tiles of 64 staged in shared memory as fp32. 256 threads form
 // a 16 x 16 grid: thread (ty, tx) computes the logits of BM/16 rows x 4 keys, then the products
-// with the values for BM/16 rows x DV/16 columns. Bound: FP32 FMA (fp32 inputs must not be
-// rounded, so the tensor cores do not serve here).
+// with the values for BM/16 rows x DV/16 columns. Bound: FP32 FMA.
 // BM = 64, or 16 when no sequence brings more than 16 rows: a decode step would waste three
-// quarters of the larger tile. Measured: fp32, 3 sequences of up to 37 new tokens and 2047 positions, 6
-// heads over 2, d 64, dv 32, with a probe and weights: 46 us in three launches, latency; 62 single tokens
-// at 12k to 18k, 16 heads each over 2 of 128, with a probe: 2.3 ms, 22 TFLOP/s.
+// quarters of the larger tile.
 #pragma once
 
 #include "lla_paged.cuh"

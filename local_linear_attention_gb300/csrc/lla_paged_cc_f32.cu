@@ -1,13 +1,10 @@
-// The CUDA-core kernels of attention over a paged cache for fp32 inputs (one translation unit per
-// type, so that they compile in parallel).
+// The CUDA-core kernels behind the fp32 attention over a paged cache (one translation unit per type, so
+// that they compile in parallel).
 #include "lla_paged_cc.cuh"
 
 namespace lla {
 namespace paged {
 
-cudaError_t attend_cc_f32(const Params& p, int d, int dv, cudaStream_t s) {
-  return pick_d<float>(p, d, dv, s);
-}
 cudaError_t mass_cc_f32(const Params& p, int d, cudaStream_t s) {
   return pick_mass<float>(p, d, s);
 }

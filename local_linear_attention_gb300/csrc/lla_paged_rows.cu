@@ -28,23 +28,13 @@
 // i + 8, and O1, O2 come out of one product, so the probe costs no extra matrix work.
 // Rounding: p and p t enter the second product as bf16 (the values are bf16 already; fp32 operands
 // have no matrix path at this rate); d1, d2 are fp32 sums of the unrounded weights.
-#include <cooperative_groups.h>
-
-#include "lla_paged.cuh"
-#include "lla_tc_ptx.cuh"
+#include "lla_paged_rows.cuh"
 
 namespace lla {
 namespace paged {
 namespace {
 
-using tc::cp_async16;
-using tc::cp_async_commit;
-using tc::cp_async_wait;
-using tc::smem_u32;
-
-constexpr int KT = 16;  // keys per step: within one page, since pages hold a multiple of 16
 constexpr int NW = 4;
-constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 template <int D>
 struct Cfg {
@@ -75,37 +65,6 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-// A finished row's sums, o1[c] and o2[c] its unnormalised columns lane * VC + c: writes out and lse.
-template <int D, bool PROBE>
-__device__ __forceinline__ void write_row(const Params& p, const Seq& sq, int b, int hk, int r, float top,
-                                           float s1, float s2, const float (&o1)[D / 32],
-                                           const float (&o2)[D / 32]) {
-  constexpr int VC = D / 32;
-  const int lane = threadIdx.x & 31;
-  const int token = sq.t0 + r / p.g, head = hk * p.g + r % p.g;
-  const float inv = s1 == 0.f ? 0.f : 1.f / s1, f1 = (1.f + s2 * inv) * inv;
-  __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.out) + ((long long)token * p.Hq + head) * p.dv + lane * VC;
-  float bad = 0.f;
-  uint32_t w[VC / 2];
-#pragma unroll
-  for (int c = 0; c < VC; c += 2) {
-    const float y0 = PROBE ? fmaf(o1[c], f1, -o2[c] * inv) : o1[c] * inv;
-    const float y1 = PROBE ? fmaf(o1[c + 1], f1, -o2[c + 1] * inv) : o1[c + 1] * inv;
-    bad += (y0 + y1) * 0.f;
-    w[c / 2] = pack_bf16(y0, y1);
-  }
-  if (lane * VC < p.dv) {
-    if (VC == 4) *reinterpret_cast<uint2*>(dst) = make_uint2(w[0], w[VC / 2 - 1]);
-    else *reinterpret_cast<uint32_t*>(dst) = w[0];
-  }
-  if (p.lse && lane == 0)
-    p.lse[(long long)token * p.Hq + head] =
-        s1 == 0.f ? -CUDART_INF_F : (top * (p.inv_h * kLog2e) + log2f(s1)) * kLn2;
-  if (__any_sync(0xffffffffu, !(bad == 0.f))) {
-    repair_row<__nv_bfloat16, KT>(p, sq, b, sq.first + r / p.g, sq.first, sq.len - 1, token, head, s1);
-  }
-}
-
 // CLUSTER: the blocks of a pair are one cluster and join there.
 template <int D, bool PROBE, bool LOGITS, bool CLUSTER>
 __global__ void __launch_bounds__(NW * 32) attend_rows_kernel(Params p) {
@@ -334,84 +293,16 @@ __global__ void __launch_bounds__(NW * 32) attend_rows_kernel(Params p) {
     *reinterpret_cast<float2*>(dst + 8 * OP) = make_float2(o[n][2], o[n][3]);
   }
   __syncthreads();
-  constexpr int VC = D / 32;  // columns per lane
-  for (int r = warp; r < min(nrows, ROWS); r += NW) {
-    float top = -CUDART_INF_F;
-#pragma unroll
-    for (int i = 0; i < NW; ++i) top = fmaxf(top, stats[i][r].x);
-    const float ref = top == -CUDART_INF_F ? 0.f : top * c2;
-    float s1 = 0.f, s2 = 0.f, o1[VC] = {}, o2[VC] = {};
-#pragma unroll
-    for (int i = 0; i < NW; ++i) {
-      const float4 st = stats[i][r];
-      const float f = ex2(fmaf(st.x, c2, -ref));
-      s1 = fmaf(st.y, f, s1);
-      s2 = fmaf(st.z, f, s2);
-#pragma unroll
-      for (int c = 0; c < VC; ++c) {
-        o1[c] = fmaf(os[(i * 16 + r) * OP + lane * VC + c], f, o1[c]);
-        if (PROBE) o2[c] = fmaf(os[(i * 16 + r + 8) * OP + lane * VC + c], f, o2[c]);
-      }
-    }
-    if (CLUSTER) {
-      if (lane == 0) fin_stats[r] = make_float4(top, s1, s2, 0.f);
-      float* dst = reinterpret_cast<float*>(smem + C::fin) + r * D + lane * VC;
-#pragma unroll
-      for (int c = 0; c < VC; ++c) {
-        dst[c] = o1[c];
-        if (PROBE) dst[8 * D + c] = o2[c];
-      }
-    } else if (p.split > 1) {
-      const long long id = ((long long)part * p.B * p.Hkv + pair) * ROWS + r;
-      if (lane == 0) p.part_s[id] = make_float4(top, s1, s2, 0.f);
-      float* dst = p.part_o + id * (PROBE ? 2 : 1) * D + lane * VC;
-#pragma unroll
-      for (int c = 0; c < VC; ++c) {
-        dst[c] = o1[c];
-        if (PROBE) dst[D + c] = o2[c];
-      }
-    } else {
-      write_row<D, PROBE>(p, sq, b, hk, r, top, s1, s2, o1, o2);
-    }
-  }
-  if constexpr (CLUSTER) {
-    namespace cg = cooperative_groups;
-    cg::cluster_group cluster = cg::this_cluster();
-    cluster.sync();
-    for (int r = warp * p.split + part; r < nrows; r += NW * p.split) {  // this warp's rows
-      float4 st[kRowsCluster];
-      float top = -CUDART_INF_F;
-#pragma unroll
-      for (int i = 0; i < kRowsCluster; ++i)
-        if (i < p.split) {
-          st[i] = *cluster.map_shared_rank(&fin_stats[r], i);
-          top = fmaxf(top, st[i].x);
-        }
-      const float ref = top == -CUDART_INF_F ? 0.f : top * c2;
-      float s1 = 0.f, s2 = 0.f, o1[VC] = {}, o2[VC] = {};
-#pragma unroll
-      for (int i = 0; i < kRowsCluster; ++i)
-        if (i < p.split) {
-          const float f = ex2(fmaf(st[i].x, c2, -ref));
-          s1 = fmaf(st[i].y, f, s1);
-          s2 = fmaf(st[i].z, f, s2);
-          const float* src = reinterpret_cast<const float*>(cluster.map_shared_rank(smem, i) + C::fin) + r * D + lane * VC;
-#pragma unroll
-          for (int c = 0; c < VC; ++c) {
-            o1[c] = fmaf(src[c], f, o1[c]);
-            if (PROBE) o2[c] = fmaf(src[8 * D + c], f, o2[c]);
-          }
-        }
-      write_row<D, PROBE>(p, sq, b, hk, r, top, s1, s2, o1, o2);
-    }
-    cluster.sync();  // this block's sums have been read
-  }
+  const Rows rows{sq.t0, p0, p1, p.g, hk * p.g};
+  auto at = [&](int r) { return ((long long)part * p.B * p.Hkv + pair) * p.row_cap + r; };
+  join_block<__nv_bfloat16, D, PROBE, CLUSTER, NW, ROWS, 16>(p, sq, b, rows, part, nrows, at, D, os, stats,
+                                                             reinterpret_cast<float*>(smem + C::fin), fin_stats);
 }
 
 // One warp per row of the few-rows launch: joins the splits in order.
 template <int D, bool PROBE>
 __global__ void __launch_bounds__(128) join_rows_kernel(Params p) {
-  constexpr int ROWS = PROBE ? 8 : 16, VC = D / 32;
+  constexpr int VC = D / 32;
   const int lane = threadIdx.x & 31;
   const long long id = (long long)blockIdx.x * 4 + (threadIdx.x >> 5);
   const int pairs = p.B * p.Hkv;
@@ -422,7 +313,7 @@ __global__ void __launch_bounds__(128) join_rows_kernel(Params p) {
   const Seq sq = load_seq(p, b);
   if (!mine(p, sq.n) || r >= sq.n * p.g) return;
   const float c2 = p.inv_h * kLog2e;
-  auto at = [&](int s) { return ((long long)s * pairs + pair) * ROWS + r; };
+  auto at = [&](int s) { return ((long long)s * pairs + pair) * p.row_cap + r; };
   float top = -CUDART_INF_F;
   for (int s = 0; s < p.split; ++s) top = fmaxf(top, p.part_s[at(s)].x);
   const float ref = top == -CUDART_INF_F ? 0.f : top * c2;
@@ -439,7 +330,7 @@ __global__ void __launch_bounds__(128) join_rows_kernel(Params p) {
       if (PROBE) o2[c] = fmaf(src[D + c], f, o2[c]);
     }
   }
-  write_row<D, PROBE>(p, sq, b, hk, r, top, s1, s2, o1, o2);
+  write_row<__nv_bfloat16, D, PROBE>(p, sq, b, Rows{sq.t0, sq.first, sq.len - 1, p.g, hk * p.g}, r, top, s1, s2, o1, o2);
 }
 
 // mass += the rows' weights, from the logits that the attention wrote (4 bytes a row and key,
