@@ -276,10 +276,11 @@ cudaError_t launch_evict(const Params& p, void* k, void* v, float* mass, const i
   const Evict e{k, v, mass, table, lens, kept, max_pages, num_pages, budget, sinks, recent};
   const long long pairs = (long long)p.B * p.Hkv;
   const long long cap = (long long)p.max_pages << p.page_shift;
-  // A cluster per (sequence, head), large enough to give every SM a CTA but no CTA fewer than 2048
-  // positions (below that the cluster's barriers cost more than it shares).
+  // A cluster per (sequence, head), large enough to give every SM a CTA but no CTA fewer than 4096
+  // positions (below that the cluster's barriers cost more than it shares: 11 sequences of 28k, 2 heads,
+  // 72 us in all with 3600 a CTA, 65 with 7200).
   int C = 1;
-  while (C < 8 && pairs * C < 152 && cap / (2 * C) >= 2048) C *= 2;
+  while (C < 8 && pairs * C < 152 && cap / (2 * C) >= 4096) C *= 2;
   const long long share = ((cap + C - 1) / C + 127) / 128 * 128;
   const bool staged = share * 4 <= 160 * 1024;
   if (pairs * C > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
