@@ -9,7 +9,8 @@
 // the exponentials would be 30 us). Half a block's scores per buffer, so that the product refills one
 // while the other is read, was slower: its N = 64 products take about as long as N = 128 ones.
 // An item is a 128-key tile of one key/value head; CTAs take items in turn (their number depends on
-// the lengths, which only the device knows). Warps 0-3 and 4-7: two consumer groups, alternate row
+// the lengths, which only the device knows), those with the most rows first where the sequences are few
+// (prompts B4 T4096: the busiest CTA had 1.65 times the mean in the order of the sequences). Warps 0-3 and 4-7: two consumer groups, alternate row
 // blocks; 8: TMA loader (keys by page fragment; queries as [per tokens][g heads] boxes, rows in the
 // order token * g + head); 9: MMA issuer. All mbarrier waits are bounded.
 #include "lla_paged.cuh"
@@ -42,18 +43,44 @@ struct Barriers {
 };
 static_assert(sizeof(Barriers) <= 128, "barrier region");
 
+// Key tiles of sequence b, if it is this launch's.
+__device__ __forceinline__ int key_tiles(const Params& p, int b) {
+  if (b >= p.B) return 0;
+  const int t0 = p.starts[b], t1 = p.starts[b + 1];
+  return t0 >= 0 && t1 > t0 && t1 <= p.tokens && mine(p, t1 - t0)
+             ? (min(max(p.lens[b], 0), p.max_pages << p.page_shift) + KT - 1) / KT
+             : 0;
+}
+
+// Key tiles of up to 32 sequences, the first tiles of all before the second ones: a prompt's first keys
+// have the most rows, so the work of a tile declines along this order. A lane has its sequence's `count`
+// and `below`, how many tiles come before tile number `count`.
+struct Ranks {
+  int count, below;
+  __device__ __forceinline__ explicit Ranks(int n) : count(n), below(0) {
+    for (int l = 0; l < 32; ++l) below += min(count, __shfl_sync(0xffffffffu, count, l));
+  }
+  __device__ __forceinline__ bool find(int x, int* b_out, int* tile_out) const {
+    // sequences that end before x; between two ends every tile number has the same sequences
+    const bool ended = below <= x;
+    const int from = (int)__reduce_max_sync(0xffffffffu, ended ? (unsigned)count : 0u);
+    const int at = (int)__reduce_max_sync(0xffffffffu, ended ? (unsigned)below : 0u);
+    unsigned there = __ballot_sync(0xffffffffu, count > from);
+    if (!there) return false;
+    const int n = __popc(there);
+    *tile_out = from + (x - at) / n;
+    for (int skip = (x - at) % n; skip > 0; --skip) there &= there - 1;
+    *b_out = __ffs(there) - 1;
+    return true;
+  }
+};
+
 // Key tile `x` of this launch's sequences (as find_tile, over keys).
 __device__ __forceinline__ bool find_keys(const Params& p, int x, int* b_out, int* tile_out) {
-  const int lane = threadIdx.x & 31, cap = p.max_pages << p.page_shift;
+  const int lane = threadIdx.x & 31;
   int before = 0;
   for (int base = 0; base < p.B; base += 32) {
-    const int b = base + lane;
-    int cnt = 0;
-    if (b < p.B) {
-      const int t0 = p.starts[b], t1 = p.starts[b + 1];
-      if (t0 >= 0 && t1 > t0 && t1 <= p.tokens && mine(p, t1 - t0))
-        cnt = (min(max(p.lens[b], 0), cap) + KT - 1) / KT;
-    }
+    const int cnt = key_tiles(p, base + lane);
     int incl = cnt;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -124,9 +151,13 @@ mass_tc_kernel(Params p, const __grid_constant__ CUtensorMap kmap, const __grid_
   }
   int done = 0, items = 0;  // row blocks and items so far (every thread counts the same)
   bool used = false;
-  for (int x = blockIdx.x;; x += gridDim.x) {
+  const bool ranked = p.B <= 32;
+  const Ranks ranks(ranked ? key_tiles(p, lane) : 0);
+  for (int turn = 0;; ++turn) {
+    // rows of one item per CTA that run back and forth, which levels a steady decline
+    const int x = turn * gridDim.x + (turn & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
     int b, tile;
-    if (!find_keys(p, x / p.Hkv, &b, &tile)) break;
+    if (!(ranked ? ranks.find(x / p.Hkv, &b, &tile) : find_keys(p, x / p.Hkv, &b, &tile))) break;
     const int hk = x % p.Hkv;
     const Seq sq = load_seq(p, b);
     const int k0 = tile * KT;
