@@ -3,15 +3,15 @@
 // from the finished lse. The product is taken transposed, S^T = K Q^T (128 keys x 128 rows in
 // tensor memory, a thread per key), so that a key's sum runs along a thread's registers: no
 // shuffles, no atomics, and a CTA that owns its keys adds its row blocks up in one fixed order.
-// What bounds it: the exponentials, one per (row, key) pair (16 a cycle and SM); the product is
+// What bounds it: the exponentials, one per (row, key) pair (32 a cycle and SM); the product is
 // half as long. Two CTAs a SM (two score buffers each) hide each other's waits.
-// Measured: prompts B4 T4096, 8 heads of 64, 70 us (268 M row-key pairs, 3.8 T a second; the limit of
-// the exponentials would be 30 us). Half a block's scores per buffer, so that the product refills one
+// Measured: prompts B4 T4096, 8 heads of 64, 60 us (268 M row-key pairs, 4.5 T a second; the limit of
+// the exponentials would be 27 us). Half a block's scores per buffer, so that the product refills one
 // while the other is read, was slower: its N = 64 products take about as long as N = 128 ones.
 // An item is a 128-key tile of one key/value head; CTAs take items in turn (their number depends on
 // the lengths, which only the device knows), those with the most rows first where the sequences are few
-// (prompts B4 T4096: the busiest CTA had 1.65 times the mean in the order of the sequences). Warps 0-3 and 4-7: two consumer groups, alternate row
-// blocks; 8: TMA loader (keys by page fragment; queries as [per tokens][g heads] boxes, rows in the
+// (prompts B4 T4096: the busiest CTA had 1.65 times the mean in the order of the sequences, 75 us).
+// Warps 0-3 and 4-7: two consumer groups, alternate row blocks; 8: TMA loader (keys by page fragment; queries as [per tokens][g heads] boxes, rows in the
 // order token * g + head); 9: MMA issuer. All mbarrier waits are bounded.
 #include "lla_paged.cuh"
 #include "lla_tc_ptx.cuh"
