@@ -11,17 +11,17 @@
 // rows and RG = RT / 4 keys of a step's 32, in the second all RT rows and 4 value columns.
 //
 // Layout: a block of NW warps takes a contiguous share of a tile's keys; its warps take steps of 32 keys
-// in turn, each with a ring of three 8 KB chunks of its own (asynchronous 16-byte copies, two chunks in
-// flight): a step's keys by 64 features (16-byte piece c of row r at c ^ (r & 7): lanes read rows apart
+// in turn, each with two 8 KB chunks of its own (asynchronous 16-byte copies, one chunk in flight
+// behind the one in use; a third chunk a warp would leave an SM six warps instead of eight: 10 % slower): a step's keys by 64 features (16-byte piece c of row r at c ^ (r & 7): lanes read rows apart
 // without bank conflicts), then its values. Every warp has its own running maximum, so the main loop
 // has no block-wide barrier. Warps and clusters join as in the bf16 kernel of few rows, more splits than
 // a cluster has through scratch.
 // The accumulators are rescaled only when a row's maximum outgrows its reference by more than 2^8:
 // sums and weights are fp32 either way, relative to the same reference.
-// Measured: 62 single tokens at 12k to 18k, 16 heads each over 2 of 128, with a probe, 1.07 ms (29 TFLOP/s;
+// Measured: 62 single tokens at 12k to 18k, 16 heads each over 2 of 128, with a probe, 0.92 ms (34 TFLOP/s;
 // 2.3 ms in the block-wide form of lla_paged_cc.cuh, with tiles of 16 rows); prompts of 7 sequences of
-// 3.8k, 4 heads of 128, 0.81 ms (1.13, tiles of 64 rows); 3 sequences of up to 37 new tokens and 2047
-// positions, 6 heads over 2, d 64, dv 32, with a probe and weights, 24 us (47) in two launches. Six warps
+// 3.8k, 4 heads of 128, 0.73 ms (1.13, tiles of 64 rows); 3 sequences of up to 37 new tokens and 2047
+// positions, 6 heads over 2, d 64, dv 32, with a probe and weights, 22 us (47) in two launches. Eight warps
 // an SM (registers and shared memory) wait for their own instructions' results most of the time.
 #include "lla_paged_rows.cuh"
 
@@ -29,9 +29,9 @@ namespace lla {
 namespace paged {
 namespace {
 
-constexpr int NW = 3;       // two blocks on an SM with every RT
+constexpr int NW = 4;       // two blocks on an SM with every RT
 constexpr int STEP = 32;    // keys
-constexpr int STAGES = 3;
+constexpr int STAGES = 2;
 constexpr int CHUNK = 8192; // bytes
 
 template <int D, int RT, bool PROBE>
@@ -44,8 +44,8 @@ struct Cfg {
   static constexpr int q = NW * STAGES * CHUNK;
   static constexpr int w = q + branches * RT * qp * 4;
   static constexpr int bytes = w + NW * branches * STEP * pp * 4;
-  static constexpr int fin = NW * branches * kF32Rows * (D + 4) * 4;  // the join's regions reuse the rings
-  static_assert(fin + branches * kF32Rows * D * 4 <= q, "join regions");
+  static constexpr int fin = NW * branches * kF32Rows * (D + 4) * 4;  // the join's regions reuse all of it
+  static_assert(RT < kF32Rows || fin + branches * kF32Rows * D * 4 <= bytes, "join regions");
   static_assert(2 * (bytes + 3 * 1024) <= 227 * 1024, "two blocks");
 };
 
@@ -134,8 +134,6 @@ __device__ __forceinline__ void attend_tile(const Params& p, const Seq& sq, cons
   Step cur, nxt;
   next_step(cur);
   issue_keys(cur, 0, 0);
-  if (D == 128) issue_keys(cur, 1, 1);
-  else issue_values(cur, 0, 1);
 
   // q and r: [RT][D], zeros past nrows and past d
   for (int e = threadIdx.x; e < C::branches * RT * (D / 4); e += NW * 32) {
@@ -176,15 +174,19 @@ __device__ __forceinline__ void attend_tile(const Params& p, const Seq& sq, cons
   const bool logits = p.logits && sq.n * p.g <= p.row_cap;
   const TileRange<KT> whole(p, sq.first, sq.len - 1);  // the sequence's: a logit's place is its key's there
   int stage = 0;
-  // The next chunk is here; the one two ahead goes on its way, into the stage read last time.
+  // The next chunk is here; the one after it goes on its way, into the stage read last time.
   auto arrive = [&](bool keys, int c) {
-    cp_async_wait<1>();
+    cp_async_wait<0>();
     __syncwarp();
-    const int fill = stage == 0 ? 2 : stage - 1;
-    if (keys) D == 128 ? issue_values(cur, c, fill) : issue_keys(nxt, c, fill);
-    else D == 128 ? issue_keys(nxt, c, fill) : issue_values(nxt, c, fill);
     const uint8_t* at = ring + stage * CHUNK;
-    stage = stage == 2 ? 0 : stage + 1;
+    stage ^= 1;
+    if (keys) {
+      if (c + 1 < C::kc) issue_keys(cur, c + 1, stage);
+      else issue_values(cur, 0, stage);
+    } else {
+      if (c + 1 < C::vc) issue_values(cur, c + 1, stage);
+      else issue_keys(nxt, 0, stage);
+    }
     return at;
   };
   for (int st = warp; st < steps; st += NW) {
@@ -338,7 +340,7 @@ __device__ __forceinline__ void attend_tile(const Params& p, const Seq& sq, cons
 #pragma unroll
     for (int i = 0; i < 4; ++i) stats[warp][i * RG + rg] = make_float4(m[i], d1[i], d2[i], 0.f);
   }
-  __syncthreads();  // the rings are free
+  __syncthreads();  // the rings, q and the weights have been read
   float* os = reinterpret_cast<float*>(smem);
   constexpr int OROWS = C::branches * kF32Rows;
   auto put = [&](const uint64_t (&o)[4], int s, int base) {  // slots 2 s and 2 s + 1
