@@ -109,6 +109,34 @@ struct Plan {
   size_t bytes = 0;
 };
 
+// Blocks to a tile of the fp32 kernel: the number with the least time of a block (its keys in rounds of
+// 128, its start, and beyond a cluster the join through scratch) times the waves of blocks, in halves:
+// two blocks fit an SM and share its FMAs. Clusters stay within a GPC (19 SMs), whose slots their size
+// may not divide. Measured: 34 sequences of 10k, one tile each, 137 us with 20 blocks a tile, 177 with 8
+// (34 clusters where 32 fit); 42 sequences of 3.5k, window 1052, 2 heads, 21 us with 3, 27 with 2, 31 with 4;
+// 62 of 12k to 18k, 2 heads, 895 us with 10, 1099 with 2, 1154 with 64.
+int f32_splits(long long tiles, long long keys, long long rows, int D, bool probe) {
+  if (tiles <= 0) return 1;
+  const double rate = 8.0 * 16 / (rows < 4 ? 4 : rows > 16 ? 16 : rows) * 128 / D * (probe ? 1 : 1.6);  // keys a us
+  const double start = 8 * rate, join = 4 * rate;
+  long long most = keys / 128 < 64 ? keys / 128 : 64;
+  if (most > 16 * 304 / tiles) most = 16 * 304 / tiles;
+  int best = 1;
+  double least = 0;
+  for (int n = 1; n == 1 || n <= most; ++n) {
+    const int slots = n == 1 || n > kRowsCluster ? 304 : 8 * (38 / n * n);
+    const long long halves = (2 * tiles * n + slots - 1) / slots;
+    const double waves = halves < 2 ? 1 : halves * 0.5;
+    const long long rounds = ((keys + n - 1) / n + 127) / 128;
+    const double cost = waves * (rounds * 128 + start) + (n > kRowsCluster ? join : 0);
+    if (n == 1 || cost < least) {
+      least = cost;
+      best = n;
+    }
+  }
+  return best;
+}
+
 Plan make_plan(const lla_paged_cache* c, const lla_paged_query* a) {
   Plan pl;
   const int g = a->q_heads / c->kv_heads;
@@ -135,12 +163,9 @@ Plan make_plan(const lla_paged_cache* c, const lla_paged_query* a) {
   };
   if (c->dtype == LLA_F32) {
     pl.f32 = f32_tiles(a->tokens, max_new, c->num_seqs, g);
-    // As below, but scratch sooner: a step of 32 keys takes a warp longer (3 sequences of 7.7k, 2 heads
-    // of 64, 16 rows: 34 us with 26 blocks a tile, 71 with 8).
-    const long long blocks = pl.f32 * c->kv_heads;
-    const int fill = splits(blocks, 304, 128), level = splits(blocks, 1216, 1024);
-    pl.tiles_split = fill > level ? fill : level;
-    if (pl.tiles_split > kRowsCluster && keys <= kRowsCluster * 256) pl.tiles_split = kRowsCluster;
+    // (the bound counts a part tile for every sequence: as likely as not there is one)
+    const long long likely = pl.f32 - (pl.f32 > 2 * c->num_seqs ? c->num_seqs / 2 : 0);
+    pl.tiles_split = f32_splits(likely * c->kv_heads, keys, rows, pl.D, a->r != nullptr);
     if (pl.tiles_split > kRowsCluster) {
       const size_t all = (size_t)a->tokens * a->q_heads * pl.tiles_split;
       pl.tiles_s = take(all * sizeof(float4));

@@ -18,9 +18,9 @@
 // a cluster has through scratch.
 // The accumulators are rescaled only when a row's maximum outgrows its reference by more than 2^8:
 // sums and weights are fp32 either way, relative to the same reference.
-// Measured: 62 single tokens at 12k to 18k, 16 heads each over 2 of 128, with a probe, 0.92 ms (34 TFLOP/s;
+// Measured: 62 single tokens at 12k to 18k, 16 heads each over 2 of 128, with a probe, 0.90 ms (35 TFLOP/s;
 // 2.3 ms in the block-wide form of lla_paged_cc.cuh, with tiles of 16 rows); prompts of 7 sequences of
-// 3.8k, 4 heads of 128, 0.73 ms (1.13, tiles of 64 rows); 3 sequences of up to 37 new tokens and 2047
+// 3.8k, 4 heads of 128, 0.71 ms (1.13, tiles of 64 rows); 3 sequences of up to 37 new tokens and 2047
 // positions, 6 heads over 2, d 64, dv 32, with a probe and weights, 22 us (47) in two launches. Eight warps
 // an SM (registers and shared memory) wait for their own instructions' results most of the time.
 #include "lla_paged_rows.cuh"
@@ -300,7 +300,7 @@ __device__ __forceinline__ void attend_tile(const Params& p, const Seq& sq, cons
 #pragma unroll 1
     for (int c = 0; c < C::vc; ++c) {
       const uint8_t* vs = arrive(false, c);  // (its warp barrier is the weights' too)
-#pragma unroll 4
+#pragma unroll 8
       for (int k = 0; k < 16; ++k) {
         const int key = D == 128 ? k : 2 * k + (lane >> 4);
         const float4 v = *reinterpret_cast<const float4*>(vs + (D == 128 ? k * 512 + lane * 16 : key * 256 + (lane & 15) * 16));
@@ -472,7 +472,7 @@ cudaError_t launch_t(const Params& p, long long tiles, cudaStream_t s) {
 
 long long f32_tiles(long long tokens, long long max_new, int B, int g) {
   const long long per = g < kF32Rows ? kF32Rows / g : 1, slices = (g + kF32Rows - 1) / kF32Rows;
-  const long long by_tokens = tokens / per + B, by_seqs = (max_new + per - 1) / per * B;
+  const long long by_tokens = per == 1 ? tokens : tokens / per + B, by_seqs = (max_new + per - 1) / per * B;
   return (by_tokens < by_seqs ? by_tokens : by_seqs) * slices;
 }
 
