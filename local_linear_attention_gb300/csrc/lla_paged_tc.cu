@@ -54,6 +54,7 @@ struct Cfg {
   // probe a row's scores and probe scores are 256 values: two groups (280 us with four, 269 with two
   // on five prompts of 500 to 1800 tokens, 40 heads over 8).
   static constexpr int groups = D == 128 && PROBE ? 2 : 1;
+  static_assert(groups <= 2, "a group's weights are one half of a step's, or all");
   static constexpr int nsoft = blocks * groups * 4;            // softmax warps
   static constexpr int ctas = D == 64 ? 2 : 1;                 // per SM
   static constexpr int threads = (nsoft + 2) * 32;
@@ -289,8 +290,8 @@ attend_tc_kernel(Params p, const __grid_constant__ CUtensorMap kmap, const __gri
     for (int s = 0; s < C::stages; ++s) { mbar_init(&bar.full[s], 1); mbar_init(&bar.empty[s], 1); }
     for (int s = 0; s < 2; ++s) {
       mbar_init(&bar.sfull[s], 1);
-      mbar_init(&bar.pfull[s][0], C::groups == 1 ? 4 : C::groups * 2);
-      mbar_init(&bar.pfull[s][1], C::groups == 1 ? 4 : C::groups * 2);
+      mbar_init(&bar.pfull[s][0], C::groups * 4);  // (with two groups the second's rescaling too, see there)
+      mbar_init(&bar.pfull[s][1], 4);
       mbar_init(&bar.pvdone[s], 1);
       for (int q = 0; q < 4; ++q) mbar_init(&bar.rowx[s][q], C::groups);
       mbar_init(&bar.workfull[s], 1);
@@ -722,6 +723,14 @@ attend_tc_kernel(Params p, const __grid_constant__ CUtensorMap kmap, const __gri
           }
         }
       }
+      if (NG > 1 && sub > 0) {
+        // The product with the first half's weights goes into the columns that this group has rescaled
+        // as well, so it waits for this arrival besides those of the first group.
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bar.pfull[h][0]);
+      }
       if (info & 4) {
         // the last page's slots past the sequence's end may hold anything: their weight is zero,
         // and so must be the values
@@ -768,7 +777,7 @@ attend_tc_kernel(Params p, const __grid_constant__ CUtensorMap kmap, const __gri
           tmem_st_wait();
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive(&bar.pfull[h][NG == 1 ? c / (NC / 64) : sub / ((NG + 1) / 2)]);
+          if (lane == 0) mbar_arrive(&bar.pfull[h][NG == 1 ? c / (NC / 64) : sub]);
         }
       }
       if (!ok) break;
