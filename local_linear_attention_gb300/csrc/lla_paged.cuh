@@ -42,8 +42,8 @@ struct Params {
   int lo, hi;         // this launch takes the sequences with lo < rows <= hi
   int beside;         // few-rows kernel: launched behind the tensor-core kernel, may overlap it
   // Blocks that share a row's keys (tensor-core kernel: CTAs of the launch), and their partial
-  // results: {m, d1, d2, 0} with m the reference of the weights (raw q.k), and unnormalised O1 (and
-  // O2). CUDA cores and few rows (split > 1): [split][rows], rows = tokens * Hq with O rows of dv, or
+  // results: {m, d1, d2, d1 of the rounded weights (bf16 with a probe)} with m the reference of the
+  // weights (raw q.k), and unnormalised O1 (and O2). CUDA cores and few rows (split > 1): [split][rows], rows = tokens * Hq with O rows of dv, or
   // B * Hkv * row_cap with O rows of D. Tensor cores: [CTA][2 slots][rows of a tile], O rows of D.
   int split;
   float* part_o;
@@ -267,6 +267,10 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
 }
+
+// The two values of a pair of bf16.
+__device__ __forceinline__ float bf16_lo(uint32_t x) { return __uint_as_float(x << 16); }
+__device__ __forceinline__ float bf16_hi(uint32_t x) { return __uint_as_float(x & 0xFFFF0000u); }
 
 // Packed pairs of fp32 (one instruction per pair on this architecture).
 __device__ __forceinline__ uint64_t pair(float lo, float hi) {

@@ -25,9 +25,13 @@
 // the same pass took 60 us longer at B32 L16384 d128: 128 threads a block waiting for scratch.)
 // Rows: 16 without a probe. With one, rows 0-7 of the MMA are q and rows 8-15 the same rows' r:
 // the accumulator fragment gives a thread s and t of one row, p goes back as row i and p t as row
-// i + 8, and O1, O2 come out of one product, so the probe costs no extra matrix work.
-// Rounding: p and p t enter the second product as bf16 (the values are bf16 already; fp32 operands
-// have no matrix path at this rate); d1, d2 are fp32 sums of the unrounded weights.
+// i + 8, and O1, O2 come out of one product.
+// Rounding: p enters the second product as bf16 (the values are bf16 already; fp32 operands have no
+// matrix path at this rate); d1, an fp32 sum of the unrounded weights, goes into lse and divides softmax
+// attention's O. With a probe o is the difference of two sums that grow with the mean of t, so both are
+// taken with the same weights: the rounded ones in p t, d2 and a second d1, and p t as the sum of two
+// bf16 (16 bits), the lower parts by a product of their own. With p and p t rounded each for itself
+// the error grew with the mean of t (2e-3 of the output at 0.1, 5e-2 at 25; now 2e-3 at either).
 #include "lla_paged_rows.cuh"
 
 namespace lla {
@@ -73,7 +77,7 @@ __global__ void __launch_bounds__(NW * 32) attend_rows_kernel(Params p) {
   constexpr int CH = D / 8;                                 // 16-byte chunks per key
   extern __shared__ __align__(1024) uint8_t smem[];
   __shared__ float4 stats[NW][16];
-  __shared__ float4 fin_stats[16];  // the block's {m, d1, d2}
+  __shared__ float4 fin_stats[16];  // the block's sums
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   // the parts of a pair follow one another: clusters are made of neighbours
   const int pair = blockIdx.x / p.split, b = pair / p.Hkv, hk = pair % p.Hkv, part = blockIdx.x % p.split;
@@ -160,7 +164,7 @@ __global__ void __launch_bounds__(NW * 32) attend_rows_kernel(Params p) {
     pos[i] = r < nrows ? p0 + r / p.g : p1;  // rows past the end are not written
   }
   const float c2 = p.inv_h * kLog2e;
-  float m[NR], d1[NR], d2 = 0.f, o[D / 8][4];
+  float m[NR], d1[NR], d2 = 0.f, d1r = 0.f, o[D / 8][4];  // d1r: of the rounded weights (PROBE)
 #pragma unroll
   for (int i = 0; i < NR; ++i) { m[i] = -CUDART_INF_F; d1[i] = 0.f; }
 #pragma unroll
@@ -220,7 +224,7 @@ __global__ void __launch_bounds__(NW * 32) attend_rows_kernel(Params p) {
         }
       }
     }
-    uint32_t w[4];
+    uint32_t w[4], low[4] = {};  // weights; with a probe, the lower parts of p t as rows 8-15
     bool grew = false;
     float sc[NR];
 #pragma unroll
@@ -243,12 +247,17 @@ __global__ void __launch_bounds__(NW * 32) attend_rows_kernel(Params p) {
       w[i] = pack_bf16(e4[0], e4[1]);
       w[i + 2] = pack_bf16(e4[2], e4[3]);
       if (PROBE) {
+        const float pr[4] = {bf16_lo(w[0]), bf16_hi(w[0]), bf16_lo(w[2]), bf16_hi(w[2])};
         float z[4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) z[e] = x[0][e] == -CUDART_INF_F ? 0.f : e4[e] * t[e];
+        for (int e = 0; e < 4; ++e) z[e] = x[0][e] == -CUDART_INF_F ? 0.f : pr[e] * t[e];
+        d1r = fmaf(d1r, sc[0], (pr[0] + pr[1]) + (pr[2] + pr[3]));
         d2 = fmaf(d2, sc[0], (z[0] + z[1]) + (z[2] + z[3]));
-        w[1] = pack_bf16(z[0], z[1]);
-        w[3] = pack_bf16(z[2], z[3]);
+#pragma unroll
+        for (int e = 0; e < 4; e += 2) {
+          w[e + 1] = pack_bf16(z[e], z[e + 1]);
+          low[e + 1] = pack_bf16(z[e] - bf16_lo(w[e + 1]), z[e + 1] - bf16_hi(w[e + 1]));
+        }
       }
     }
     if (__any_sync(0xffffffffu, grew)) {
@@ -266,13 +275,17 @@ __global__ void __launch_bounds__(NW * 32) attend_rows_kernel(Params p) {
       ldmatrix4_t(f, vs_addr + v_row * (D * 2) + (((n * 2 + v_c) ^ (v_row & 7)) * 16));
       mma16816(o[2 * n], w, f[0], f[1]);
       mma16816(o[2 * n + 1], w, f[2], f[3]);
+      if (PROBE) {
+        mma16816(o[2 * n], low, f[0], f[1]);
+        mma16816(o[2 * n + 1], low, f[2], f[3]);
+      }
     }
     if (++stage == C::stages) stage = 0;
   }
   cp_async_wait<0>();
   __syncthreads();  // the rings are free
 
-  // Join of the four warps through shared memory: O [warp][16][D + 4], {m, d1, d2}.
+  // Join of the four warps through shared memory: O [warp][16][D + 4] and the sums.
   float* os = reinterpret_cast<float*>(smem);
   constexpr int OP = D + 4;
 #pragma unroll
@@ -282,9 +295,11 @@ __global__ void __launch_bounds__(NW * 32) attend_rows_kernel(Params p) {
   }
   d2 += __shfl_xor_sync(0xffffffffu, d2, 1);
   d2 += __shfl_xor_sync(0xffffffffu, d2, 2);
+  d1r += __shfl_xor_sync(0xffffffffu, d1r, 1);
+  d1r += __shfl_xor_sync(0xffffffffu, d1r, 2);
   if ((lane & 3) == 0) {
 #pragma unroll
-    for (int i = 0; i < NR; ++i) stats[warp][(lane >> 2) + 8 * i] = make_float4(m[i], d1[i], d2, 0.f);
+    for (int i = 0; i < NR; ++i) stats[warp][(lane >> 2) + 8 * i] = make_float4(m[i], d1[i], d2, d1r);
   }
 #pragma unroll
   for (int n = 0; n < D / 8; ++n) {
@@ -317,12 +332,12 @@ __global__ void __launch_bounds__(128) join_rows_kernel(Params p) {
   float top = -CUDART_INF_F;
   for (int s = 0; s < p.split; ++s) top = fmaxf(top, p.part_s[at(s)].x);
   const float ref = top == -CUDART_INF_F ? 0.f : top * c2;
-  float s1 = 0.f, s2 = 0.f, o1[VC] = {}, o2[VC] = {};
+  float4 sum = make_float4(top, 0.f, 0.f, 0.f);
+  float o1[VC] = {}, o2[VC] = {};
   for (int s = 0; s < p.split; ++s) {
     const float4 st = p.part_s[at(s)];
     const float f = ex2(fmaf(st.x, c2, -ref));
-    s1 = fmaf(st.y, f, s1);
-    s2 = fmaf(st.z, f, s2);
+    add_sums<PROBE>(sum, st, f);
     const float* src = p.part_o + at(s) * (PROBE ? 2 : 1) * D + lane * VC;
 #pragma unroll
     for (int c = 0; c < VC; ++c) {
@@ -330,7 +345,7 @@ __global__ void __launch_bounds__(128) join_rows_kernel(Params p) {
       if (PROBE) o2[c] = fmaf(src[D + c], f, o2[c]);
     }
   }
-  write_row<__nv_bfloat16, D, PROBE>(p, sq, b, Rows{sq.t0, sq.first, sq.len - 1, p.g, hk * p.g}, r, top, s1, s2, o1, o2);
+  write_row<__nv_bfloat16, D, PROBE>(p, sq, b, Rows{sq.t0, sq.first, sq.len - 1, p.g, hk * p.g}, r, sum, o1, o2);
 }
 
 // mass += the rows' weights, from the logits that the attention wrote (4 bytes a row and key,

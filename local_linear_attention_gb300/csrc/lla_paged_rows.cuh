@@ -24,15 +24,19 @@ struct Rows {
   int t0, p0, p1, width, h0;
 };
 
-// A finished row's sums, o1[c] and o2[c] its unnormalised columns lane * VC + c: writes out and lse.
+// A finished row's sums {m, d1, d2, d1 of the rounded weights} (the last one used where weights are
+// rounded and differences of sums taken: bf16 with a probe), o1[c] and o2[c] its unnormalised columns
+// lane * VC + c: writes out and lse.
+template <typename T, bool PROBE>
+constexpr bool kRoundedSum = PROBE && sizeof(T) == 2;
 template <typename T, int D, bool PROBE>
-__device__ __forceinline__ void write_row(const Params& p, const Seq& sq, int b, const Rows& rows, int r, float top,
-                                           float s1, float s2, const float (&o1)[D / 32],
-                                           const float (&o2)[D / 32]) {
+__device__ __forceinline__ void write_row(const Params& p, const Seq& sq, int b, const Rows& rows, int r, float4 st,
+                                           const float (&o1)[D / 32], const float (&o2)[D / 32]) {
   constexpr int VC = D / 32;
   const int lane = threadIdx.x & 31;
   const int token = rows.t0 + r / rows.width, head = rows.h0 + r % rows.width;
-  const float inv = s1 == 0.f ? 0.f : 1.f / s1, f1 = (1.f + s2 * inv) * inv;
+  const float s1 = st.y, norm = kRoundedSum<T, PROBE> ? st.w : s1;
+  const float inv = norm == 0.f ? 0.f : 1.f / norm, f1 = (1.f + st.z * inv) * inv;
   T* dst = static_cast<T*>(p.out) + ((long long)token * p.Hq + head) * p.dv + lane * VC;
   float bad = 0.f, y[VC];
 #pragma unroll
@@ -54,15 +58,22 @@ __device__ __forceinline__ void write_row(const Params& p, const Seq& sq, int b,
   }
   if (p.lse && lane == 0)
     p.lse[(long long)token * p.Hq + head] =
-        s1 == 0.f ? -CUDART_INF_F : (top * (p.inv_h * kLog2e) + log2f(s1)) * kLn2;
+        s1 == 0.f ? -CUDART_INF_F : (st.x * (p.inv_h * kLog2e) + log2f(s1)) * kLn2;
   if (__any_sync(0xffffffffu, !(bad == 0.f))) {
     repair_row<T, KT>(p, sq, b, rows.p0 + r / rows.width, rows.p0, rows.p1, token, head, s1);
   }
 }
 
+// Adds a part's sums, taken against another reference (factor f).
+template <bool ROUNDED>
+__device__ __forceinline__ void add_sums(float4& sum, const float4& st, float f) {
+  sum.y = fmaf(st.y, f, sum.y);
+  sum.z = fmaf(st.z, f, sum.z);
+  if (ROUNDED) sum.w = fmaf(st.w, f, sum.w);
+}
+
 // The join of a block's NW warps, and of the cluster's blocks where a pair's blocks are one
-// (CLUSTER): O [warp][OROWS][D + 4] in `os` (a row's O2 ROWS rows behind its O1), {m, d1, d2} in
-// `stats`; the block's own sums go to `fin` [OROWS][D] and `fin_stats`, to the scratch (more splits than
+// (CLUSTER): O [warp][OROWS][D + 4] in `os` (a row's O2 ROWS rows behind its O1), its sums in `stats`; the block's own sums go to `fin` [OROWS][D] and `fin_stats`, to the scratch (more splits than
 // a cluster has: row at(r), `cols` floats to a row's O), or finished to the output. All threads, behind a
 // barrier.
 template <typename T, int D, bool PROBE, bool CLUSTER, int NW, int ROWS, int OROWS, typename At>
@@ -77,13 +88,13 @@ __device__ __forceinline__ void join_block(const Params& p, const Seq& sq, int b
 #pragma unroll
     for (int i = 0; i < NW; ++i) top = fmaxf(top, stats[i][r].x);
     const float ref = top == -CUDART_INF_F ? 0.f : top * c2;
-    float s1 = 0.f, s2 = 0.f, o1[VC] = {}, o2[VC] = {};
+    float4 sum = make_float4(top, 0.f, 0.f, 0.f);
+    float o1[VC] = {}, o2[VC] = {};
 #pragma unroll
     for (int i = 0; i < NW; ++i) {
       const float4 st = stats[i][r];
       const float f = ex2(fmaf(st.x, c2, -ref));
-      s1 = fmaf(st.y, f, s1);
-      s2 = fmaf(st.z, f, s2);
+      add_sums<kRoundedSum<T, PROBE>>(sum, st, f);
 #pragma unroll
       for (int c = 0; c < VC; ++c) {
         o1[c] = fmaf(os[(i * OROWS + r) * OP + lane * VC + c], f, o1[c]);
@@ -91,7 +102,7 @@ __device__ __forceinline__ void join_block(const Params& p, const Seq& sq, int b
       }
     }
     if (CLUSTER) {
-      if (lane == 0) fin_stats[r] = make_float4(top, s1, s2, 0.f);
+      if (lane == 0) fin_stats[r] = sum;
       float* dst = fin + r * D + lane * VC;
 #pragma unroll
       for (int c = 0; c < VC; ++c) {
@@ -100,7 +111,7 @@ __device__ __forceinline__ void join_block(const Params& p, const Seq& sq, int b
       }
     } else if (p.split > 1) {
       const long long id = at(r);
-      if (lane == 0) p.part_s[id] = make_float4(top, s1, s2, 0.f);
+      if (lane == 0) p.part_s[id] = sum;
       if (lane * VC < cols) {
         float* dst = p.part_o + id * (PROBE ? 2 : 1) * cols + lane * VC;
 #pragma unroll
@@ -110,7 +121,7 @@ __device__ __forceinline__ void join_block(const Params& p, const Seq& sq, int b
         }
       }
     } else {
-      write_row<T, D, PROBE>(p, sq, b, rows, r, top, s1, s2, o1, o2);
+      write_row<T, D, PROBE>(p, sq, b, rows, r, sum, o1, o2);
     }
   }
   if constexpr (CLUSTER) {
@@ -127,13 +138,13 @@ __device__ __forceinline__ void join_block(const Params& p, const Seq& sq, int b
           top = fmaxf(top, st[i].x);
         }
       const float ref = top == -CUDART_INF_F ? 0.f : top * c2;
-      float s1 = 0.f, s2 = 0.f, o1[VC] = {}, o2[VC] = {};
+      float4 sum = make_float4(top, 0.f, 0.f, 0.f);
+      float o1[VC] = {}, o2[VC] = {};
 #pragma unroll
       for (int i = 0; i < kRowsCluster; ++i)
         if (i < p.split) {
           const float f = ex2(fmaf(st[i].x, c2, -ref));
-          s1 = fmaf(st[i].y, f, s1);
-          s2 = fmaf(st[i].z, f, s2);
+          add_sums<kRoundedSum<T, PROBE>>(sum, st[i], f);
           const float* src = cluster.map_shared_rank(fin, i) + r * D + lane * VC;
 #pragma unroll
           for (int c = 0; c < VC; ++c) {
@@ -141,7 +152,7 @@ __device__ __forceinline__ void join_block(const Params& p, const Seq& sq, int b
             if (PROBE) o2[c] = fmaf(src[ROWS * D + c], f, o2[c]);
           }
         }
-      write_row<T, D, PROBE>(p, sq, b, rows, r, top, s1, s2, o1, o2);
+      write_row<T, D, PROBE>(p, sq, b, rows, r, sum, o1, o2);
     }
     cluster.sync();  // this block's sums have been read
   }

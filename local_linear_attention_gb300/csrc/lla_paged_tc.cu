@@ -22,7 +22,11 @@
 // us on softmax prompts B4 T4096, 8 heads.)
 // The accumulators are rescaled only when a row's maximum outgrows its reference by more than 2^8;
 // after the first tiles this hardly happens.
-// Rounding: p and p t enter the value products as bf16, d1 and d2 sum the unrounded fp32 weights.
+// Rounding: p enters the value product as bf16; d1, the sum of the unrounded fp32 weights, goes into lse
+// and divides softmax attention's O. With a probe o is the difference of two sums that grow with the mean
+// of t, so both are taken with the same weights, the rounded ones (in p t, d2 and a second d1), and p t as
+// the sum of two bf16 (16 bits): P2 is a high and a low part, each with a value product. With p and p t
+// rounded each for itself the error grew with the mean of t (2e-3 of the output at 0.1, 5e-2 at 25).
 // What bounds it: at D = 128 the chain softmax - value product - next scores of a block, about 3,100
 // cycles a 128-key step against 2,048 of MMA for the two blocks (chunk of 2048 at 32768, 32 heads
 // over 8: 1.4 PFLOP/s); at D = 64 the N = 64 products (about 59 cycles for 32 of work) and the same chain.
@@ -64,16 +68,17 @@ struct Cfg {
   // own scores, which it has read.
   static constexpr int nc = kt / groups;
   static constexpr uint32_t p_col(int j) { return j / nc * nc + j % nc / 2; }
+  static constexpr uint32_t p_low = nc / 2;  // from there (in S, behind the weights): the lower part of p t
   static constexpr uint32_t cols = D == 64 ? 256 : 512;
   static_assert(t_o + ops * D <= cols, "tensor memory");
   // shared memory: operands [ops][D/64][128 rows][128 B], ring of key and value tiles
-  // [D/64][kt rows][128 B], barriers, row exchange [5 buffers][nsoft/4 groups][128], tile counts
+  // [D/64][kt rows][128 B], barriers, row exchange [6 buffers][nsoft/4 groups][128], tile counts
   static constexpr int op_bytes = BM * D * 2, tile = kt * D * 2, half = kt * 128;
   static constexpr int stages = D == 128 ? 4 : PROBE ? 8 : 5;
   static constexpr int sm_ring = ops * op_bytes;
   static constexpr int sm_bar = sm_ring + stages * tile;
   static constexpr int sm_x = sm_bar + 512;
-  static constexpr int sm_tiles = sm_x + 5 * (nsoft / 4) * BM * 4, tiles_bytes = 2048 * 4;
+  static constexpr int sm_tiles = sm_x + 6 * (nsoft / 4) * BM * 4, tiles_bytes = 2048 * 4;
   static constexpr int bytes = sm_tiles + tiles_bytes + 1024;  // 1024: aligning the base
   static_assert(ctas * (bytes + 1024) <= 227 * 1024, "shared memory");
 };
@@ -435,6 +440,9 @@ attend_tc_kernel(Params p, const __grid_constant__ CUtensorMap kmap, const __gri
             const int s = half * (KT / 32) + u;
             mma_ts(tbase + C::t_o + o * D, tbase + o * KT + C::p_col(s * 16),
                    v + (uint64_t)(s * (2048 >> 4)), id_o, (!first || s > 0) ? 1u : 0u);
+            if (PROBE && o == 1)
+              mma_ts(tbase + C::t_o + o * D, tbase + C::p_col(s * 16) + C::p_low,
+                     v + (uint64_t)(s * (2048 >> 4)), id_o, 1u);
           }
           if (half) mma_commit(&bar.pvdone[o]);
         }
@@ -607,7 +615,7 @@ attend_tc_kernel(Params p, const __grid_constant__ CUtensorMap kmap, const __gri
     const float c2 = p.inv_h * kLog2e, slack = 8.f / c2;
     const bool wide = (reinterpret_cast<uintptr_t>(p.out) & 31) == 0;
     // Exchange among the groups of a row: x[buffer][group][row], buffers 0 to 2 for the maxima of steps in
-    // turn, 3 and 4 for a piece's sums; between warps of the same rows.
+    // turn, 3 to 5 for a piece's sums; between warps of the same rows.
     float* const xm = reinterpret_cast<float*>(smem + C::sm_x);
     auto slot = [&](int buf, int g) -> float& { return xm[((buf * C::blocks + h) * NG + g) * BM + r]; };
     int xphase = 0;  // phases of rowx used so far
@@ -630,21 +638,22 @@ attend_tc_kernel(Params p, const __grid_constant__ CUtensorMap kmap, const __gri
       sq.first = w->first;
       return Tile(sq, w->tile, tokens);
     };
-    float m = -CUDART_INF_F, d1 = 0.f, d2 = 0.f, before = -CUDART_INF_F;
+    float m = -CUDART_INF_F, d1 = 0.f, d2 = 0.f, d1r = 0.f, before = -CUDART_INF_F;  // d1r: of the rounded weights (PROBE)
     for (int i = 0; i < n; ++i) {
       const int gi = base + i;
       ok = wait(&bar.sfull[h], gi & 1);
       if (PROBE) ok = ok && wait(&bar.sfull[1], gi & 1);
       if (!ok) break;
       tc_fence_after();
-      uint32_t s[NC / 32][32], tt[PROBE ? NC / 32 : 1][32];
+      // Probe scores come 16 at a time, the next ones under way while these are used: held all at once
+      // beside the scores they left too few registers to overlap anything (prompts B4 T4096, 8 heads of 64:
+      // 214 us, 186 so).
+      uint32_t s[NC / 32][32], tt[PROBE ? 2 : 1][16];
+      unsigned seen[NC / 32];
 #pragma unroll
       for (int c = 0; c < NC / 32; ++c) tmem_ld32(lanes + h * KT + sub * NC + c * 32, s[c]);
-      if constexpr (PROBE) {
-#pragma unroll
-        for (int c = 0; c < NC / 32; ++c) tmem_ld32(lanes + KT + sub * NC + c * 32, tt[c]);
-      }
       tmem_ld_wait();
+      if constexpr (PROBE) tmem_ld16(lanes + KT + sub * NC, tt[0]);
       const int info = uni(*(volatile int*)&step_s[gi & 7]), k0 = info & ~63, kb = k0 + sub * NC;
       const bool masked = (info >> h) & 1;
       if (masked) {
@@ -656,12 +665,9 @@ attend_tc_kernel(Params p, const __grid_constant__ CUtensorMap kmap, const __gri
         auto below = [](int x) { return x <= 0 ? 0u : x >= 32 ? 0xFFFFFFFFu : (1u << x) - 1u; };
 #pragma unroll
         for (int c = 0; c < NC / 32; ++c) {
-          const unsigned seen = below(hi + 1 - c * 32) & (~below(lo + 1 - c * 32) | below(first - c * 32));
+          seen[c] = below(hi + 1 - c * 32) & (~below(lo + 1 - c * 32) | below(first - c * 32));
 #pragma unroll
-          for (int e = 0; e < 32; ++e) {
-            s[c][e] = seen & (1u << e) ? s[c][e] : 0xFF800000u;
-            if constexpr (PROBE) tt[c][e] = seen & (1u << e) ? tt[c][e] : 0u;  // of a slot that may hold anything
-          }
+          for (int e = 0; e < 32; ++e) s[c][e] = seen[c] & (1u << e) ? s[c][e] : 0xFF800000u;
         }
       }
       auto own_max = [&]() {  // over this thread's keys
@@ -706,6 +712,7 @@ attend_tc_kernel(Params p, const __grid_constant__ CUtensorMap kmap, const __gri
           // beyond what the last step's weights could hold: the row is taken again at the end
           d1 = (top - m_old) * c2 > kTooFar && m_old != -CUDART_INF_F ? CUDART_INF_F : d1 * sc;
           d2 *= sc;
+          d1r *= sc;
         }
         if (i > 0) {
           // (the products that went into them precede this step's scores in the pipe)
@@ -747,45 +754,66 @@ attend_tc_kernel(Params p, const __grid_constant__ CUtensorMap kmap, const __gri
         fence_proxy_async_smem();
       }
       const float ref = m == -CUDART_INF_F ? 0.f : m * c2;
-      const uint64_t c22 = pair(c2, c2), ref2 = pair(-ref, -ref);
-      uint64_t sum[2] = {}, sumt[2] = {};  // pairs of partial sums
+      const uint64_t c22 = pair(c2, c2), ref2 = pair(-ref, -ref), minus = pair(-1.f, -1.f);
+      uint64_t sum[2] = {}, sumt = 0, sumr = 0;  // pairs of partial sums
+      constexpr int CW = PROBE ? 16 : 32;  // keys at once
 #pragma unroll
-      for (int c = 0; c < NC / 32; ++c) {
-        uint32_t wp[16], wt[PROBE ? 16 : 1];
+      for (int c = 0; c < NC; c += CW) {
+        uint32_t wp[CW / 2], wt[CW / 2], wl[CW / 2];
+        uint32_t(&t)[16] = tt[PROBE ? (c / CW) & 1 : 0];
+        if constexpr (PROBE) {
+          tmem_ld_wait();
+          if (c + CW < NC) tmem_ld16(lanes + KT + sub * NC + c + CW, tt[((c / CW) & 1) ^ 1]);
+          if (masked) {
 #pragma unroll
-        for (int e = 0; e < 32; e += 2) {
-          const uint64_t x = fma2(pair(__uint_as_float(s[c][e]), __uint_as_float(s[c][e + 1])), c22, ref2);
+            for (int e = 0; e < 16; ++e) t[e] = seen[c >> 5] & (1u << ((c & 31) + e)) ? t[e] : 0u;  // of a slot that may hold anything
+          }
+        }
+#pragma unroll
+        for (int e = 0; e < CW; e += 2) {
+          const uint32_t(&sc)[32] = s[(c + e) >> 5];
+          const int at = (c + e) & 31;
           float y0, y1;
-          unpair(x, y0, y1);
+          unpair(fma2(pair(__uint_as_float(sc[at]), __uint_as_float(sc[at + 1])), c22, ref2), y0, y1);
           y0 = ex2(y0);
           y1 = ex2(y1);
-          const uint64_t y = pair(y0, y1);
-          sum[(e >> 1) & 1] = add2(sum[(e >> 1) & 1], y);
+          sum[(e >> 1) & 1] = add2(sum[(e >> 1) & 1], pair(y0, y1));
           wp[e / 2] = pack_bf16(y0, y1);
           if constexpr (PROBE) {
-            const uint64_t z = mul2(y, pair(__uint_as_float(tt[c][e]), __uint_as_float(tt[c][e + 1])));
-            sumt[(e >> 1) & 1] = add2(sumt[(e >> 1) & 1], z);
+            const uint64_t yr = pair(bf16_lo(wp[e / 2]), bf16_hi(wp[e / 2]));
+            sumr = add2(sumr, yr);
+            const uint64_t z = mul2(yr, pair(__uint_as_float(t[e]), __uint_as_float(t[e + 1])));
+            sumt = add2(sumt, z);
             float z0, z1;
             unpair(z, z0, z1);
             wt[e / 2] = pack_bf16(z0, z1);
+            unpair(fma2(pair(bf16_lo(wt[e / 2]), bf16_hi(wt[e / 2])), minus, z), z0, z1);
+            wl[e / 2] = pack_bf16(z0, z1);
           }
         }
-        tmem_st16(lanes + h * KT + C::p_col(sub * NC) + c * 16, wp);
-        if constexpr (PROBE) tmem_st16(lanes + KT + C::p_col(sub * NC) + c * 16, wt);
+        if constexpr (PROBE) {
+          tmem_st8(lanes + C::p_col(sub * NC) + c / 2, wp);
+          tmem_st8(lanes + KT + C::p_col(sub * NC) + c / 2, wt);
+          tmem_st8(lanes + C::p_col(sub * NC) + C::p_low + c / 2, wl);
+        } else {
+          tmem_st16(lanes + h * KT + C::p_col(sub * NC) + c / 2, wp);
+        }
         // half of the step's weights are there: with this group's last, or, alone, halfway
-        if (c + 1 == NC / 32 || (NG == 1 && c + 1 == NC / 64)) {
+        if (c + CW == NC || (NG == 1 && c + CW == NC / 2)) {
           tmem_st_wait();
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive(&bar.pfull[h][NG == 1 ? c / (NC / 64) : sub]);
+          if (lane == 0) mbar_arrive(&bar.pfull[h][NG == 1 ? c / (NC / 2) : sub]);
         }
       }
       if (!ok) break;
       float a0, a1;
       unpair(add2(sum[0], sum[1]), a0, a1);
       d1 += a0 + a1;
-      unpair(add2(sumt[0], sumt[1]), a0, a1);
+      unpair(sumt, a0, a1);
       d2 += a0 + a1;
+      unpair(sumr, a0, a1);
+      d1r += a0 + a1;
       if (!exact) {
         tm = own_max();
         if (NG > 1) slot(gi % 3, sub) = tm;
@@ -794,15 +822,18 @@ attend_tc_kernel(Params p, const __grid_constant__ CUtensorMap kmap, const __gri
       if ((tm - m) * c2 > kTooFar) d1 = CUDART_INF_F;  // weights too large to go on with (see repair_row)
     }
 
+    if (PROBE) tmem_ld_wait();  // after a break: nothing may arrive in a register late
     if (NG > 1 && ok) {  // the groups' sums
       slot(3, sub) = d1;
       slot(4, sub) = d2;
+      slot(5, sub) = d1r;
       ok = exchange();
-      d1 = d2 = 0.f;
+      d1 = d2 = d1r = 0.f;
 #pragma unroll
       for (int g = 0; g < NG; ++g) {
         d1 += slot(3, g);
         d2 += slot(4, g);
+        d1r += slot(5, g);
       }
     }
     if (ok && n > 0) {
@@ -815,7 +846,8 @@ attend_tc_kernel(Params p, const __grid_constant__ CUtensorMap kmap, const __gri
     const Tile tile = tile_of();
     const int t0 = w->t0, hk = w->hk;
     const bool there = r_tok < tile.ntok, whole = w->whole;
-    const float inv = d1 == 0.f ? 0.f : 1.f / d1, f1 = (1.f + d2 * inv) * inv;
+    const float norm = PROBE ? d1r : d1;
+    const float inv = norm == 0.f ? 0.f : 1.f / norm, f1 = (1.f + d2 * inv) * inv;
     const long long id = (long long)(t0 + tile.tok0 + r_tok) * p.Hq + hk * p.g + r_head;
     // a piece of a tile: slot 0 when it begins inside the tile, else 1
     const int piece = blockIdx.x * 2 + (w->i0 == 0);
@@ -866,7 +898,7 @@ attend_tc_kernel(Params p, const __grid_constant__ CUtensorMap kmap, const __gri
     }
     tc_fence_before();  // these reads, before the arrivals that let the next piece's products go
     if (there && sub == 0) {
-      if (!whole) p.part_s[pid] = make_float4(m, d1, d2, 0.f);
+      if (!whole) p.part_s[pid] = make_float4(m, d1, d2, d1r);
       else if (p.lse) p.lse[id] = d1 == 0.f ? -CUDART_INF_F : (m * c2 + log2f(d1)) * kLn2;
     }
     if (!whole) {
@@ -940,13 +972,14 @@ __global__ void __launch_bounds__(256, 4) join_tc_kernel(Params p) {
 #pragma unroll
     for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
     const float ref = top == -CUDART_INF_F ? 0.f : top * c2;
-    float s1 = 0.f, s2 = 0.f, o1[VC] = {}, o2[VC] = {};
+    float s1 = 0.f, s2 = 0.f, s1r = 0.f, o1[VC] = {}, o2[VC] = {};
 #pragma unroll 4
     for (int i = 0; i < n; ++i) {
       const float4 st = p.part_s[at(i, row)];
       const float f = ex2(fmaf(st.x, c2, -ref));
       s1 = isinf(st.y) ? st.y : fmaf(st.y, f, s1);  // (infinite: see repair_row; times f it might be NaN)
       s2 = fmaf(st.z, f, s2);
+      s1r = fmaf(st.w, f, s1r);
       const float* src = p.part_o + at(i, row) * (PROBE ? 2 : 1) * D + lane * VC;
       if (lane * VC < p.dv) {
 #pragma unroll
@@ -957,7 +990,8 @@ __global__ void __launch_bounds__(256, 4) join_tc_kernel(Params p) {
       }
     }
     const int token = sq.t0 + tile.tok0 + t, head = hk * p.g + r % p.g;
-    const float inv = s1 == 0.f ? 0.f : 1.f / s1, f1 = (1.f + s2 * inv) * inv;
+    const float norm = PROBE ? s1r : s1;
+    const float inv = norm == 0.f ? 0.f : 1.f / norm, f1 = (1.f + s2 * inv) * inv;
     __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.out) + ((long long)token * p.Hq + head) * p.dv + lane * VC;
     float bad = (s1 + s2) * 0.f;
 #pragma unroll
