@@ -6,7 +6,6 @@ fallback: if the library is missing or the tensors are not on a CUDA device the 
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import os
 import struct
@@ -421,15 +420,32 @@ def _paged_starts(starts, cache):
 
 
 def _paged_stream(cache, stream):
-    """The raw stream of a call: `stream`, or the current one of the cache's device."""
-    if stream is None:
-        return torch._C._cuda_getCurrentRawStream(cache._index)
+    """The raw handle of a stream that a call was given."""
+    if getattr(stream, "device_index", cache._index) != cache._index:
+        raise ValueError(f"the stream must be one of {cache.device}, where the cache is")
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
-def _on_stream(stream):
+def _on_stream(cache, stream):
     """What a call on another stream than the current one allocates belongs to that stream."""
-    return torch.cuda.stream(stream) if isinstance(stream, torch.cuda.Stream) else contextlib.nullcontext()
+    if not isinstance(stream, torch.cuda.Stream):  # a raw handle; 0 is the default stream's
+        raw = _paged_stream(cache, stream)
+        stream = torch.cuda.ExternalStream(raw, device=cache.device) if raw else torch.cuda.default_stream(cache.device)
+    return torch.cuda.stream(stream)
+
+
+def _paged_call(fn, cache, stream, *args):
+    """Calls an entry point with the cache's device current: the library works on the current one, and the
+    default stream's handle is the same on all of them. (A decode step makes this call once per
+    layer: torch.cuda.current_device() would take a microsecond.)"""
+    raw = torch._C._cuda_getCurrentRawStream(cache._index) if stream is None else _paged_stream(cache, stream)
+    if torch._C._cuda_getDevice() == cache._index:
+        st = fn(*args, raw)
+    else:
+        with torch.cuda.device(cache._index):
+            st = fn(*args, raw)
+    if st:
+        raise LlaError(st, fn.__name__)
 
 
 def lla_paged_append(k, v, cache: PagedCache, starts, stream=None):
@@ -440,10 +456,7 @@ def lla_paged_append(k, v, cache: PagedCache, starts, stream=None):
     _paged_rows("k", k, cache, (tokens, cache.kv_heads, cache.d))
     _paged_rows("v", v, cache, (tokens, cache.kv_heads, cache.dv))
     _paged_starts(starts, cache)
-    st = _load().lla_paged_append(cache._packed, k.data_ptr(), v.data_ptr(), starts.data_ptr(), tokens,
-                                  _paged_stream(cache, stream))
-    if st:
-        raise LlaError(st, "lla_paged_append")
+    _paged_call(_load().lla_paged_append, cache, stream, cache._packed, k.data_ptr(), v.data_ptr(), starts.data_ptr(), tokens)
 
 
 def _paged_query(q, cache, starts, h, r, max_new, window, sinks, track_mass, out, lse, path):
@@ -483,15 +496,16 @@ def lla_paged_attention(q, cache: PagedCache, starts, h: float, r=None, max_new=
         if lse is None:
             lse = torch.empty(shape[:2], dtype=torch.float32, device=cache.device)
     else:
-        with _on_stream(stream):
+        with _on_stream(cache, stream):
             out = q.new_empty((*shape[:2], cache.dv)) if out is None else out
             lse = q.new_empty(shape[:2], dtype=torch.float32) if lse is None else lse
     query = _paged_query(q, cache, starts, h, r, max_new, window, sinks, track_mass, out, lse, path)
-    wp, wb = (0, 0) if workspace is None else (
-        workspace.data_ptr(), workspace.numel() * workspace.element_size())
-    st = _load().lla_paged_attention(cache._packed, query, wp, wb, _paged_stream(cache, stream))
-    if st:
-        raise LlaError(st, "lla_paged_attention")
+    wp = wb = 0
+    if workspace is not None:
+        if workspace.get_device() != cache._index or not workspace.is_contiguous():
+            raise ValueError("workspace must be a contiguous tensor on the cache's device")
+        wp, wb = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    _paged_call(_load().lla_paged_attention, cache, stream, cache._packed, query, wp, wb)
     return out, lse
 
 
@@ -517,15 +531,15 @@ def lla_paged_evict(cache: PagedCache, to: PagedCache, budget: int, sinks=0, rec
         raise ValueError("budget must be at least 1")
     shape = (cache.num_seqs, cache.kv_heads, budget)
     if kept is None:
-        with _on_stream(stream):
+        if stream is None:
             kept = torch.empty(shape, dtype=torch.int32, device=cache.device)
+        else:
+            with _on_stream(cache, stream):
+                kept = torch.empty(shape, dtype=torch.int32, device=cache.device)
     elif kept.shape != shape or kept.dtype != torch.int32 or kept.get_device() != cache._index \
             or not kept.is_contiguous():
         raise ValueError(f"kept must be a contiguous int32 tensor of shape {shape}")
-    st = _load().lla_paged_evict(cache._packed, to._packed, budget, sinks, recent, kept.data_ptr(),
-                                 _paged_stream(cache, stream))
-    if st:
-        raise LlaError(st, "lla_paged_evict")
+    _paged_call(_load().lla_paged_evict, cache, stream, cache._packed, to._packed, budget, sinks, recent, kept.data_ptr())
     return kept
 
 
