@@ -437,7 +437,7 @@ def _on_stream(cache, stream):
 def _paged_call(fn, cache, stream, *args):
     """Calls an entry point with the cache's device current: the library works on the current one, and the
     default stream's handle is the same on all of them. (A decode step makes this call once per
-    layer: torch.cuda.current_device() would take a microsecond.)"""
+    layer, so the current device is asked for without torch.cuda's own checks.)"""
     raw = torch._C._cuda_getCurrentRawStream(cache._index) if stream is None else _paged_stream(cache, stream)
     if torch._C._cuda_getDevice() == cache._index:
         st = fn(*args, raw)

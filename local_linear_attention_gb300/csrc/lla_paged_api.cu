@@ -95,6 +95,13 @@ int check_query(const lla_paged_cache* c, const lla_paged_query* a) {
 constexpr size_t kAlign = 256;
 size_t align_up(size_t x) { return (x + kAlign - 1) / kAlign * kAlign; }
 
+// The weights of sequences of few rows come from the logits that the attention leaves in scratch, sized
+// by the table's capacity. Above this much scratch they are computed again from q and k, as those of
+// longer sequences are. (32 sequences of 4k to 16k, 32 heads over 8 of 128: 249 us with a table as wide as
+// the longest, 289 with one of 262144 positions and 1 GiB of logits, 493 computed again; 16 of 2k to 4k in
+// fp32, 16 heads over 4: 53, 335 with a table of a million, 1224 computed again.)
+constexpr size_t kMostLogits = (size_t)1 << 31;
+
 // How one call runs: the kernels it takes, their splits and scratch (byte offsets).
 struct Plan {
   bool rows = false;   // the few-rows kernel takes the sequences of at most rows_limit rows
@@ -102,6 +109,8 @@ struct Plan {
   long long f32 = 0;   // fp32: one kernel's tiles; `rows` and `tiles` are the weight tracking's parts
   bool tc = false;
   bool join = false;   // tensor cores: tiles may be cut
+  bool logits_kept = false;  // weight tracking: of the sequences of at most row_cap rows from their logits
+  bool mass_tc = false;      // of the others (or all) on the tensor cores
   int D = 0;           // head size of the tensor-core kernels
   int rows_split = 1, tiles_split = 1;
   int row_cap = 0, keys_cap = 0;
@@ -173,16 +182,20 @@ Plan make_plan(const lla_paged_cache* c, const lla_paged_query* a) {
     }
     if (a->track_mass) {
       // The weights of sequences of up to kF32MassRows rows come from their logits, which cost 8 bytes
-      // of traffic each against 2 d flops to compute them again, where the scratch stays below 512 MB;
-      // those of longer ones from q and k.
+      // of traffic each against 2 d flops to compute them again; those of longer ones, or where the
+      // scratch would be too much, from q and k.
       pl.keys_cap = (int)((keys + 64 < cap ? keys + 64 : cap) + 15) / 16 * 16;
       const size_t row_bytes = (size_t)pairs * pl.keys_cap * sizeof(float);
-      if (rows <= kF32MassRows && rows * row_bytes <= (size_t)512 << 20) {
+      const long long few = rows < limit ? rows : limit;
+      if (rows <= kF32MassRows && rows * row_bytes <= kMostLogits) {
         pl.row_cap = (int)rows;
         pl.rows = true;
         pl.tiles = false;
-      } else if (pl.rows) {
-        pl.row_cap = (int)(rows < limit ? rows : limit);
+      } else if (pl.rows && few * row_bytes <= kMostLogits) {
+        pl.row_cap = (int)few;
+      } else {
+        pl.rows = false;
+        pl.tiles = true;
       }
       if (pl.rows) pl.logits = take(pl.row_cap * row_bytes);
     }
@@ -206,11 +219,14 @@ Plan make_plan(const lla_paged_cache* c, const lla_paged_query* a) {
     }
     if (a->track_mass) {
       pl.keys_cap = (int)((keys + 64 < cap ? keys + 64 : cap) + 15) / 16 * 16;
-      pl.logits = take((size_t)pairs * pl.row_cap * pl.keys_cap * sizeof(float));
+      const size_t bytes = (size_t)pairs * pl.row_cap * pl.keys_cap * sizeof(float);
+      pl.logits_kept = bytes <= kMostLogits;
+      if (pl.logits_kept) pl.logits = take(bytes);
     }
   }
+  const TcPlan t = tc ? plan_tc(pl.D, a->r != nullptr, a->tokens, c->num_seqs, c->kv_heads, g, keys) : TcPlan();
+  pl.mass_tc = t.ctas > 0;
   if (pl.tiles) {
-    const TcPlan t = tc ? plan_tc(pl.D, a->r != nullptr, a->tokens, c->num_seqs, c->kv_heads, g, keys) : TcPlan();
     pl.tc = t.ctas > 0;
     if (pl.tc) {
       pl.tiles_split = t.ctas;
@@ -300,7 +316,7 @@ int run_attention(const lla_paged_cache* c, const lla_paged_query* a, const Plan
       f.part_s = reinterpret_cast<float4*>(ws + pl.rows_s);
       f.part_o = reinterpret_cast<float*>(ws + pl.rows_o);
     }
-    if (a->track_mass) {
+    if (a->track_mass && pl.logits_kept) {
       f.keys_cap = pl.keys_cap;
       f.logits = reinterpret_cast<float*>(ws + pl.logits);
     }
@@ -310,7 +326,11 @@ int run_attention(const lla_paged_cache* c, const lla_paged_query* a, const Plan
     if (pl.tc ? pl.join && launch_join_tc(p, pl.D, s) != cudaSuccess
               : p.split > 1 && launch_join(p, c->dv, c->dtype, s) != cudaSuccess)
       return LLA_ERR_CUDA;
-    if (a->track_mass && (pl.tc ? launch_mass_tc(p, padded(c->d), s) : launch_mass_cc(p, c->d, c->dtype, s)) != cudaSuccess)
+  }
+  if (a->track_mass && (pl.tiles || !pl.logits_kept)) {
+    p.lo = pl.logits_kept ? pl.row_cap : 0;
+    if (!pl.tiles) p.hi = pl.row_cap;
+    if ((pl.mass_tc ? launch_mass_tc(p, padded(c->d), s) : launch_mass_cc(p, c->d, c->dtype, s)) != cudaSuccess)
       return LLA_ERR_CUDA;
   }
   return LLA_OK;
