@@ -254,6 +254,7 @@ Plan make_plan(const lla_paged_cache* c, const lla_paged_query* a) {
 
 int run_f32(const Params& p, const Plan& pl, int track_mass, char* ws, cudaStream_t s) {
   Params f = p;
+  f.hi = p.max_rows;
   f.split = pl.tiles_split;
   f.row_cap = pl.row_cap;
   f.keys_cap = pl.keys_cap;
@@ -270,7 +271,7 @@ int run_f32(const Params& p, const Plan& pl, int track_mass, char* ws, cudaStrea
   }
   if (track_mass && pl.tiles && err == cudaSuccess) {
     f.lo = pl.row_cap;
-    f.hi = p.hi;
+    f.hi = p.max_rows;
     err = launch_mass_cc(f, p.d, LLA_F32, s);
   }
   return err == cudaSuccess ? LLA_OK : LLA_ERR_CUDA;

@@ -378,13 +378,16 @@ __global__ void __launch_bounds__(NW * 32, 2) attend_f32_kernel(Params p) {
   const int index = blockIdx.x / p.split, part = blockIdx.x % p.split, hk = index % p.Hkv;
   const int per = max(1, kF32Rows / p.g), slices = (p.g + kF32Rows - 1) / kF32Rows;  // tokens a tile; tiles a token
   let_next();
+  // Sequences of more rows than p.hi (beyond max_new) have no tiles here, since the grid was not sized for
+  // them: they are reported.
+  if (blockIdx.x == 0)
+    for (int i = threadIdx.x; i < p.B; i += NW * 32) {
+      const int n = load_seq(p, i).n;
+      if (n > 0 && !mine(p, n)) atomicOr(p.status, kStatusBadIndex);
+    }
   int b, tile;
   if (!find_tile(p, per, index / p.Hkv / slices, &b, &tile)) return;
   const Seq sq = load_seq(p, b);
-  if (sq.n > p.max_rows / p.g) {  // beyond max_new: the grid may lack its tiles
-    if (threadIdx.x == 0) atomicOr(p.status, kStatusBadIndex);
-    return;
-  }
   const int u0 = index / p.Hkv % slices * kF32Rows, tok0 = tile * per, ntok = min(per, sq.n - tok0);
   const int p0 = sq.first + tok0;
   const Rows rows{sq.t0 + tok0, p0, p0 + ntok - 1, min(p.g - u0, kF32Rows), hk * p.g + u0};
