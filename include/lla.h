@@ -371,7 +371,8 @@ int lla_profile_collect(float* stage_ms, int max_stages, int* n_calls);
  * at most 65535, their product < 2^28 (LLA_ERR_UNSUPPORTED otherwise). What only the device can see is checked there: a
  * page index outside 0 .. num_pages-1, a length beyond the table, or starts that descend or pass
  * `tokens` are recorded in the status word (lla_stream_status: LLA_ERR_INVALID_ARG); nothing out of
- * range is read or written, and the outputs of that sequence are unspecified. Slots that no row
+ * range is read or written, and the outputs of that sequence are unspecified (with an impossible length or
+ * starts it is left out: nothing is appended, no weight is added, nothing is kept of it). Slots that no row
  * sees may hold anything, infinities and NaN included.
  */
 typedef struct lla_paged_cache {

@@ -60,18 +60,19 @@ struct Seq {
   int first;     // position of the first new token (negative when n > len)
 };
 
-// Sequence b with every field brought into range; a sequence with impossible starts or length is
-// treated as having no new tokens (or the nearest possible length) and reported once per reader.
+// Sequence b; one with impossible starts or length is treated as having no positions and no new tokens,
+// and reported once per reader. (Cut to the nearest possible length instead, it would write to whatever
+// its row of the table ends in.)
 __device__ __forceinline__ Seq load_seq(const Params& p, int b) {
   Seq s;
   const int t0 = p.starts[b], t1 = p.starts[b + 1];
   const int len = p.lens[b], cap = p.max_pages << p.page_shift;
-  const bool bad = t0 < 0 || t1 < t0 || t1 > p.tokens;
+  const bool bad = t0 < 0 || t1 < t0 || t1 > p.tokens || len < 0 || len > cap;
   s.t0 = bad ? 0 : t0;
   s.n = bad ? 0 : t1 - t0;
-  s.len = min(max(len, 0), cap);
+  s.len = bad ? 0 : len;
   s.first = s.len - s.n;
-  if (bad || s.len != len) atomicOr(p.status, kStatusBadIndex);
+  if (bad) atomicOr(p.status, kStatusBadIndex);
   return s;
 }
 

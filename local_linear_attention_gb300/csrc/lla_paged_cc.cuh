@@ -95,6 +95,7 @@ __global__ void __launch_bounds__(NT) attend_cc_kernel(Params p) {
   const int index = blockIdx.x / p.Hkv;
   if (!find_tile(p, per, index / slices, &b, &tile)) return;
   const Seq sq = load_seq(p, b);
+  if (sq.n == 0) return;                     // an impossible length (find_tile counts by the starts)
   const int u0 = (index % slices) * BM;      // first grouped head of this tile (g > BM)
   const int tok0 = tile * per, ntok = min(per, sq.n - tok0);
   const int width = min(p.g - u0, BM);                 // grouped heads per token in this tile

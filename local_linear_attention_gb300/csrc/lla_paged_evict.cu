@@ -85,7 +85,7 @@ __global__ void __launch_bounds__(NT) select_kernel(Params p, Evict e) {
   const int pair = blockIdx.x / C, b = pair / p.Hkv, hk = pair % p.Hkv;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int cap = p.max_pages << p.page_shift;
-  const int raw = p.lens[b], n = min(max(raw, 0), cap);
+  const int raw = p.lens[b], n = raw < 0 || raw > cap ? 0 : raw;  // impossible: nothing is kept
   if (raw != n && tid == 0) atomicOr(p.status, kStatusBadIndex);
   const int m = min(n, e.budget);
   // this CTA's positions c0 .. c1-1, and each warp's share of them (multiples of 32 and 128)

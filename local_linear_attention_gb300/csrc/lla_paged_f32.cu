@@ -388,6 +388,7 @@ __global__ void __launch_bounds__(NW * 32, 2) attend_f32_kernel(Params p) {
   int b, tile;
   if (!find_tile(p, per, index / p.Hkv / slices, &b, &tile)) return;
   const Seq sq = load_seq(p, b);
+  if (sq.n == 0) return;  // an impossible length (find_tile counts by the starts)
   const int u0 = index / p.Hkv % slices * kF32Rows, tok0 = tile * per, ntok = min(per, sq.n - tok0);
   const int p0 = sq.first + tok0;
   const Rows rows{sq.t0 + tok0, p0, p0 + ntok - 1, min(p.g - u0, kF32Rows), hk * p.g + u0};
