@@ -427,7 +427,8 @@ typedef struct lla_paged_query {
  * Attention of the new tokens over the cache (append them first). Per row, over its visible keys:
  * p = softmax(q.k / h), o = sum p v, or with a probe the Parallax output
  * o = sum p (1 + tbar - t) v with t = r.k and tbar = sum p t, as lla_parallax_forward computes it.
- * A row that sees nothing (a position below zero) gives o = 0, lse = -infinity. Sums are fp32.
+ * A row that sees nothing (a position below zero, or only keys whose logit is -infinity) gives o = 0,
+ * lse = -infinity and adds no weight. Sums are fp32.
  * `workspace` (256-byte aligned device memory of lla_paged_workspace_size bytes; its contents need
  * not be kept between calls) or NULL: scratch from the stream-ordered allocator.
  */

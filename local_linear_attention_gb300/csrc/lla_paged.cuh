@@ -147,6 +147,10 @@ __device__ __forceinline__ bool find_tile(const Params& p, int per, int x, int* 
   return false;
 }
 
+// What a weight exp(s - lse) of the finished row is taken with: a row without any weight (lse -infinity)
+// gives none either, not even to keys whose logit is -infinity as well.
+__device__ __forceinline__ float subtrahend(float lse) { return lse == -CUDART_INF_F ? CUDART_INF_F : lse; }
+
 // One row computed by one warp straight from the definition, skipping every key that the row does
 // not see (see repair_row). Slow, and off every ordinary path.
 template <typename T>

@@ -296,7 +296,7 @@ __global__ void __launch_bounds__(NT) mass_cc_kernel(Params p) {
     for (int i = 0; i < RM; ++i) {
       const int x = r0 + ty * RM + i;
       if (x >= rows) continue;
-      const float lse = p.lse[(long long)(sq.t0 + x / p.g) * p.Hq + hk * p.g + x % p.g];
+      const float lse = subtrahend(p.lse[(long long)(sq.t0 + x / p.g) * p.Hq + hk * p.g + x % p.g]);
       const int pos = sq.first + x / p.g;
 #pragma unroll
       for (int j = 0; j < 4; ++j)

@@ -425,7 +425,7 @@ __global__ void __launch_bounds__(256) mass_f32_kernel(Params p) {
   const int share = nrows > 4 ? 8 : nrows > 2 ? 4 : nrows, groups = 8 / share, span = groups * 128;
   if (blockIdx.y * span >= count) return;
   for (int r = threadIdx.x; r < nrows; r += 256)
-    lse[r] = p.lse[(long long)(sq.t0 + r / p.g) * p.Hq + hk * p.g + r % p.g] * kLog2e;
+    lse[r] = subtrahend(p.lse[(long long)(sq.t0 + r / p.g) * p.Hq + hk * p.g + r % p.g]) * kLog2e;
   __syncthreads();
   const float c2 = p.inv_h * kLog2e;
   for (int base = blockIdx.y * span; base < count; base += gridDim.y * span) {

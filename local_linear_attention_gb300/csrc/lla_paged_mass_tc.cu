@@ -100,6 +100,34 @@ __device__ __forceinline__ bool find_keys(const Params& p, int x, int* b_out, in
   return false;
 }
 
+// Whether key j, whose sum came out NaN, is not finite itself: its products with the zero rows past a
+// block's `width` are NaN then, whatever its weights are.
+__device__ __noinline__ bool infinite_key(const Params& p, int b, int hk, int j) {
+  const int pg = load_page(p, b, j >> p.page_shift);
+  bool finite = true;
+  const long long at = (((long long)pg * p.Hkv + hk) * p.page + (j & (p.page - 1))) * p.d;
+  for (int c = 0; c < p.d && pg >= 0; ++c) finite &= isfinite(ldf(static_cast<const __nv_bfloat16*>(p.k), at + c)) != 0;
+  return !finite;
+}
+// The sum of such a key over every second block of `per` tokens, from token tok0 to before tok1, row by row;
+// one warp.
+__device__ __noinline__ float key_again(const Params& p, const Seq& sq, int b, int hk, int j, int tok0, int tok1, int per) {
+  const int pg = load_page(p, b, j >> p.page_shift);
+  const __nv_bfloat16* k = static_cast<const __nv_bfloat16*>(p.k) + (((long long)pg * p.Hkv + hk) * p.page + (j & (p.page - 1))) * p.d;
+  float sum = 0.f;
+  for (; tok0 < tok1; tok0 += 2 * per)
+    for (int r = threadIdx.x & 31; r < min(per, tok1 - tok0) * p.g; r += 32) {
+      if (!visible(p, sq.first + tok0 + r / p.g, j)) continue;
+      const long long row = (long long)(sq.t0 + tok0 + r / p.g) * p.Hq + hk * p.g + r % p.g;
+      float s = 0.f;
+      for (int c = 0; c < p.d; ++c) s = fmaf(ldf(static_cast<const __nv_bfloat16*>(p.q), row * p.d + c), ldf(k, c), s);
+      sum += ex2((s * p.inv_h - subtrahend(p.lse[row])) * kLog2e);
+    }
+#pragma unroll
+  for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  return sum;
+}
+
 template <int D>
 __global__ void __launch_bounds__(NTHREADS, 2)
 mass_tc_kernel(Params p, const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap qmap) {
@@ -248,7 +276,7 @@ mass_tc_kernel(Params p, const __grid_constant__ CUtensorMap kmap, const __grid_
         for (int u = 0; u < 4; ++u) {
           const int t = (from + i) * per + lse_tok[u];
           ahead[u] = i < nblk && lse_tok[u] >= 0 && t < sq.n
-                         ? p.lse[(long long)(sq.t0 + t) * p.Hq + hk * p.g + lse_head[u]] * -kLog2e
+                         ? subtrahend(p.lse[(long long)(sq.t0 + t) * p.Hq + hk * p.g + lse_head[u]]) * -kLog2e
                          : -CUDART_INF_F;
         }
       };
@@ -262,7 +290,8 @@ mass_tc_kernel(Params p, const __grid_constant__ CUtensorMap kmap, const __grid_
         if (!warp_wait(&bar.sfull[grp], (c >> 1) & 1, status, TO, abort_p)) break;
         tc_fence_after();
         const int p0 = sq.first + tok0, p1 = p0 + per - 1;
-        // (the columns past `width` are zero scores with -lse = -infinity: nothing)
+        // (the columns past `width` are products with zero rows, with -lse = -infinity: nothing, unless the
+        // key is infinite, see key_again)
         const bool full = tok0 + per <= sq.n && all_visible(p, p0, p1, k0, k0 + KT);
         uint32_t s[2][32];
         tmem_ld32(lanes + grp * BR, s[0]);
@@ -310,6 +339,14 @@ mass_tc_kernel(Params p, const __grid_constant__ CUtensorMap kmap, const __grid_
             }
           }
           got += a[0] + a[1];
+        }
+      }
+      if (width < BR) {
+        unsigned again = __ballot_sync(0xffffffffu, got != got && j < sq.len && infinite_key(p, b, hk, j));
+        for (; again; again &= again - 1) {
+          const int l = __ffs(again) - 1, first = from + ((done ^ grp) & 1);
+          const float sum = key_again(p, sq, b, hk, j - lane + l, first * per, min(sq.n, (from + nblk) * per), per);
+          if (lane == l) got = sum;
         }
       }
       reinterpret_cast<float*>(smem + C::sm_sum)[((items & 1) * 2 + grp) * KT + r] = got;
