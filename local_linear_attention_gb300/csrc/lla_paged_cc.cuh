@@ -1,7 +1,8 @@
 // Attention of new tokens over a paged cache on the CUDA cores, head sizes 16, 32, 64, 128, keys and
 // values independent: the attention of bf16 where it is asked to (LLA_PATH_CUDA_CORE), with more than 128
-// heads to a key/value head, or for chunks of more than 2048 sequences at once; the join of splits and
-// the weight tracking of more than 16 rows, for fp32 too.
+// heads to a key/value head, or for chunks of more than 2048 sequences at once; the join of splits, for
+// fp32 too; the weight tracking that does not go by the attention's logits (fp32: more than 256 rows to a
+// sequence, or logits of more than 2 GiB; bf16 where the tensor cores do not take it).
 //
 // Mathematics, per row with visible keys j (logit s_j = q.k_j / h, probe t_j = r.k_j):
 //   m = max s, p_j = exp(s_j - m), d1 = sum p, O1 = sum p v, and with a probe d2 = sum p t,
