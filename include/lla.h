@@ -364,7 +364,11 @@ int lla_profile_collect(float* stage_ms, int max_stages, int* n_calls);
  *
  * New tokens of all sequences lie one after the other, as [tokens, heads, size] rows: sequence b's
  * are starts[b] .. starts[b+1]-1 (device memory, [num_seqs + 1], ascending, at most `tokens`), and
- * they are the sequence's last positions: lens already counts them.
+ * they are the sequence's last positions: lens already counts them. Rows that no sequence covers (before
+ * starts[0], from starts[num_seqs] on) take no part, and their outputs are not written.
+ *
+ * Attention over these caches is softmax attention or Parallax; the local linear attention of lla_forward
+ * and lla_decode reads contiguous keys and values only.
  *
  * Supported: d, dv in {16, 32, 64, 128}; page_size a power of two in 16 .. 1024; max_pages *
  * page_size < 2^30; tokens < 2^30, tokens * q_heads < 2^31, num_pages * kv_heads < 2^31, num_seqs and kv_heads

@@ -481,7 +481,8 @@ def lla_paged_attention(q, cache: PagedCache, starts, h: float, r=None, max_new=
     returns (out [tokens, q_heads, dv], lse [tokens, q_heads] float32). With a probe r (like q) the
     Parallax output, else softmax attention. The token at position i sees positions j <= i, all of
     them (window = 0) or the last `window` and the first `sinks`. track_mass adds the weights to
-    cache.mass. max_new: a bound of the tokens of one sequence (default: all); giving it lets a
+    cache.mass. Rows that no sequence covers are not written: in tensors that this call allocates they hold
+    anything. max_new: a bound of the tokens of one sequence (default: all); giving it lets a
     decode step run as one."""
     shape = q.shape
     if out is not None:
