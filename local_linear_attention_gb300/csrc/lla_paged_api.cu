@@ -1,28 +1,26 @@
 // C ABI of the paged-cache operators: argument validation, choice of kernels and splits, scratch.
 #include <cmath>
-#include <mutex>
 
 #include "lla_paged.cuh"
+#include "lla_smem_limits.h"
 
 namespace lla {
 namespace paged {
 
-// A kernel's limit is raised once per device and size: remembering it saves most of a microsecond
-// per launch. (Only a cache of what the driver already holds: a lost entry sets it again.)
 cudaError_t ensure_smem(const void* kern, size_t bytes) {
-  struct Entry { const void* kern; int dev; size_t bytes; };
-  constexpr int N = 256;
-  static std::mutex mu;
-  static Entry table[N];
+  static SmemLimits limits;
   int dev = 0;
-  cudaError_t err = cudaGetDevice(&dev);
+  const cudaError_t err = cudaGetDevice(&dev);
   if (err != cudaSuccess) return err;
-  Entry& e = table[(reinterpret_cast<uintptr_t>(kern) / 16 * 31 + dev) % N];
-  std::lock_guard<std::mutex> lk(mu);
-  if (e.kern == kern && e.dev == dev && e.bytes >= bytes) return cudaSuccess;
-  err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
-  if (err == cudaSuccess) e = {kern, dev, bytes};
-  return err;
+  return limits.ensure(
+      kern, dev, bytes,
+      [&](size_t* held) {
+        cudaFuncAttributes at;
+        const cudaError_t e = cudaFuncGetAttributes(&at, kern);
+        if (e == cudaSuccess) *held = (size_t)at.maxDynamicSharedSizeBytes;
+        return e;
+      },
+      [&](size_t most) { return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most); });
 }
 
 namespace {
