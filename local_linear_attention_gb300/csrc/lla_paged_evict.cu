@@ -290,6 +290,7 @@ cudaError_t launch_evict(const Params& p, void* k, void* v, float* mass, const i
   const int eb = dtype == LLA_F32 ? 4 : 2;
   const long long most = budget < cap ? budget : cap;
   const int blocks = (int)((most + 255) / 256);
+  if (blocks == 0) return cudaSuccess;  // tables without pages: nothing is kept
   if (pairs * blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
   return launch(gather_kernel, dim3((unsigned)(pairs * blocks)), 256, 0, 1, true, s, p, e, d * eb / 16, dv * eb / 16,
                 blocks);
