@@ -70,7 +70,8 @@ typedef enum { LLA_F32 = 0, LLA_BF16 = 1 } lla_dtype;
 /* Implementation choices (lla_options.path). */
 typedef enum {
   LLA_PATH_AUTO = 0,        /* tensor cores for bf16 (the forward: any d, zero-padded to 64 when
-                               d < 64; the other ops: d = dv = 64), CUDA cores otherwise */
+                               d < 64; the other ops: d = dv = 64; paged attention: every
+                               head size), CUDA cores otherwise */
   LLA_PATH_CUDA_CORE = 1,   /* CUDA cores always */
   LLA_PATH_TENSOR_CORE = 2, /* tensor cores wherever supported (currently the same as AUTO) */
   LLA_PATH_CG = 3           /* lla_forward*_ex only: matrix-free conjugate gradients for the ridge

@@ -119,9 +119,10 @@ struct Plan {
 // Blocks to a tile of the fp32 kernel: the number with the least time of a block (its keys in rounds of
 // 128, its start, and beyond a cluster the join through scratch) times the waves of blocks, in halves:
 // two blocks fit an SM and share its FMAs. Clusters stay within a GPC (19 SMs), whose slots their size
-// may not divide. Measured: 34 sequences of 10k, one tile each, 137 us with 20 blocks a tile, 177 with 8
-// (34 clusters where 32 fit); 42 sequences of 3.5k, window 1052, 2 heads, 21 us with 3, 27 with 2, 31 with 4;
-// 62 of 12k to 18k, 2 heads, 895 us with 10, 1099 with 2, 1154 with 64.
+// may not divide. Measured: 42 sequences of 3.5k, window 1052, 2 heads, 21 us with the 3 that it takes, 26
+// with 2, 30 with 4; 62 of 12k to 18k, 2 heads, 1.00 ms as it takes, 1.21 with 2, 1.29 with 64; 7 of 16k to
+// 24k, 96 us with 64, 184 with 16. It is not always the best: 34 of 10k, one tile each, with weights, 178 us,
+// 146 with 20; 10 of 11k to 23k with weights 224, 190 with 20.
 int f32_splits(long long tiles, long long keys, long long rows, int D, bool probe) {
   if (tiles <= 0) return 1;
   const double rate = 8.0 * 16 / (rows < 4 ? 4 : rows > 16 ? 16 : rows) * 128 / D * (probe ? 1 : 1.6);  // keys a us
@@ -203,10 +204,10 @@ Plan make_plan(const lla_paged_cache* c, const lla_paged_query* a) {
   }
   if (pl.rows) {
     pl.row_cap = (int)(rows < limit ? rows : limit);
-    // Two blocks per SM first, down to 128 keys each (one sequence, 8 heads of 64, L 1000: 5.0 us
-    // with 7 blocks a head, 7.6 with 2); then, so that uneven lengths level out, four waves of them,
-    // but no block under 1024 keys (48 sequences, 4 heads, window 1024: 30 us with 2 blocks a head,
-    // 47 with 7). More than a cluster of 8 only where its blocks would have over 1024 keys each:
+    // Two blocks per SM first, down to 128 keys each (one sequence, 8 heads of 64, L 1000: 6.4 us
+    // with 8 blocks a head, 8.8 with 2); then, so that uneven lengths level out, four waves of them,
+    // but no block under 1024 keys (48 sequences, 4 heads, window 1024: 19.5 us with 2 blocks a head,
+    // 37 with 7). More than a cluster of 8 only where its blocks would have over 1024 keys each:
     // below that, the launch that joins costs more than shorter blocks save.
     const int fill = splits(pairs, 304, 128), level = splits(pairs, pl.D == 128 ? 1216 : 1824, 1024);
     pl.rows_split = fill > level ? fill : level;

@@ -5,7 +5,7 @@
 // shuffles, no atomics, and a CTA that owns its keys adds its row blocks up in one fixed order.
 // What bounds it: the exponentials, one per (row, key) pair (32 a cycle and SM); the product is
 // half as long. Two CTAs a SM (two score buffers each) hide each other's waits.
-// Measured: prompts B4 T4096, 8 heads of 64, 60 us (268 M row-key pairs, 4.5 T a second; the limit of
+// Measured: prompts B4 T4096, 8 heads of 64, 68 us (268 M row-key pairs, 3.9 T a second; the limit of
 // the exponentials would be 27 us). Half a block's scores per buffer, so that the product refills one
 // while the other is read, was slower: its N = 64 products take about as long as N = 128 ones.
 // An item is a 128-key tile of one key/value head; CTAs take items in turn (their number depends on

@@ -6,9 +6,9 @@
 // and takes part in at most 32 row products per element, an order below the ridge point, so what
 // counts is bytes in flight: two steps of 8 KB a warp, 12 warps an SM at D = 128. Measured: 32
 // sequences of 4k to 16k, 32 heads over 8 of 128, 230 us for the attention, 6.2 TB/s (91 % of the
-// copy bandwidth); Parallax, 8 heads of 64, 2k to 16k, 99 us, 6.5 TB/s; one token of 8 heads at 1000
-// positions, 5 us, most of it the launch and the chain lengths - page - keys. Why not tcgen05: its M is 64 or 128 rows and a decode step has 1 to
-// 16, so the smaller mma.sync (m16n8k16) wastes less, keeps scores, weights and accumulators in
+// copy bandwidth); Parallax, 8 heads of 64, 2k to 16k, 103 us, 6.3 TB/s; one token of 8 heads at 1000
+// positions, 6.3 us, most of it the launch and the chain lengths - page - keys. Why not tcgen05: its M is
+// 64 or 128 rows and a decode step has 1 to 16, so the smaller mma.sync (m16n8k16) wastes less, keeps scores, weights and accumulators in
 // registers (no tensor-memory round trip between the two products of a 16-key step), and lets
 // every warp run by itself.
 //

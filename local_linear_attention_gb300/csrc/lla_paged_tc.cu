@@ -5,8 +5,8 @@
 // One pass over the keys. Per tile of KT keys and block of 128 rows (tokens x grouped heads of one
 // key/value head): S = Q K^T, P = exp(S - m), O += P V; with a probe also T = R K^T, P2 = P .* T,
 // O2 += P2 V. "Operand" below: Q of a block, or R.
-//   D = 128: one CTA per SM with two operands (512 tensor-memory columns: two S, two O). Softmax
-//     attention takes two row blocks, whose softmax and matrix products alternate: while one
+//   D = 128: one CTA per SM with two operands (512 tensor-memory columns: two S, two O; with a probe S and
+//     T, O and O2). Softmax attention takes two row blocks, whose softmax and matrix products alternate: while one
 //     block's weights are computed the tensor core works for the other, and both read one key tile.
 //   D = 64: two CTAs per SM of 256 columns each, which alternate by themselves: one row block with
 //     128-key tiles, or with a probe Q and R with 64-key tiles.
@@ -17,8 +17,8 @@
 // 75 cycles of operand moves against 64 of tensor pipe, and that was the bound (chunk of 2048 at
 // 32768, D = 128: 1.06 -> 0.85 ms). One issuer serves both blocks in turn; with an issuer each, their
 // products interleave, finish together and the two softmax phases run in step instead of alternating.
-// bf16 P overwrites its S, and the next score product is issued behind the value product that reads
-// P (MMAs run in order). (At D = 64 there is room for P beside S; using it measured 108 against 106
+// bf16 P overwrites its S (P2 its T, its lower part S behind P), and the next score product is issued behind
+// the value product that reads P (MMAs run in order). (At D = 64 there is room for P beside S; using it measured 108 against 106
 // us on softmax prompts B4 T4096, 8 heads.)
 // The accumulators are rescaled only when a row's maximum outgrows its reference by more than 2^8;
 // after the first tiles this hardly happens.
@@ -29,7 +29,9 @@
 // rounded each for itself the error grew with the mean of t (2e-3 of the output at 0.1, 5e-2 at 25).
 // What bounds it: at D = 128 the chain softmax - value product - next scores of a block, about 3,100
 // cycles a 128-key step against 2,048 of MMA for the two blocks (chunk of 2048 at 32768, 32 heads
-// over 8: 1.4 PFLOP/s); at D = 64 the N = 64 products (about 59 cycles for 32 of work) and the same chain.
+// over 8: 1.4 PFLOP/s in a row of calls); at D = 64 the N = 64 products (about 59 cycles for 32 of work) and
+// the same chain, which is longer with a probe (prompts B4 T4096, 8 heads of 64: 99 us, with a probe 186); at
+// D = 128 with a probe the chain of the one block a CTA has (8 heads of 128: 361 us, tensor pipe 42 % active).
 // All mbarrier waits are bounded.
 #include <type_traits>
 
@@ -54,9 +56,9 @@ struct Cfg {
   static constexpr int ops = blocks * (PROBE ? 2 : 1);         // operands: Q of each block, or Q and R
   // Groups of four warps per row block. One, a thread taking a whole row of the tile, where the
   // registers allow it: nothing is exchanged then (chunk of 2048 at 32768, D = 128: 779 us with two,
-  // 729 with one; prompts B4 T4096 D = 64: 121 and 108, with a probe 205 and 168). At D = 128 with a
-  // probe a row's scores and probe scores are 256 values: two groups (280 us with four, 269 with two
-  // on five prompts of 500 to 1800 tokens, 40 heads over 8).
+  // 729 with one; prompts B4 T4096 D = 64: 121 and 108, with a probe 462 and 186, the threads of two short of
+  // registers). At D = 128 with a probe a step's weights are a long way for one: two (chunk of 2048 at
+  // 8192, 32 heads over 8: 675 us with one, 590 with two).
   static constexpr int groups = D == 128 && PROBE ? 2 : 1;
   static_assert(groups <= 2, "a group's weights are one half of a step's, or all");
   static constexpr int nsoft = blocks * groups * 4;            // softmax warps
