@@ -442,6 +442,25 @@ int lla_paged_attention(const lla_paged_cache* cache, const lla_paged_query* que
                         size_t workspace_bytes, void* stream);
 
 /*
+ * Attention of trees of drafted tokens over the cache (append them first): a sequence's new tokens are the
+ * nodes of a tree (or of several) that goes on where the sequence's other positions end. parents [tokens]
+ * (device memory) holds of each node its parent's index among the sequence's new tokens, which comes before
+ * the node's own, or -1: a child of the last position before the nodes. Node i lies in slot first + i,
+ * first = lens - (number of nodes), and is at position first + depth(i), depth 0 being a child of -1. It sees
+ * itself, its ancestors, and the positions before the nodes; with a window those of them whose position is
+ * within the last `window` up to its own or among the first `sinks`. Otherwise as lla_paged_attention, for
+ * the same caches and queries: parents[i] = i - 1 gives its results. A drafted node's weight is not
+ * counted: track_mass has to be 0.
+ *
+ * At most 1024 nodes to a sequence (LLA_ERR_UNSUPPORTED where max_new and tokens are both larger). Reported
+ * in the status word, the sequence's outputs unspecified: a parent that does not come before its child,
+ * more nodes than max_new or than positions.
+ */
+size_t lla_paged_tree_workspace_size(const lla_paged_cache* cache, const lla_paged_query* query);
+int lla_paged_tree_attention(const lla_paged_cache* cache, const lla_paged_query* query, const int* parents,
+                             void* workspace, size_t workspace_bytes, void* stream);
+
+/*
  * Eviction: for every sequence of `from` and key/value head, min(lens, budget) positions are kept:
  * the first `sinks`, the last `recent` (sinks + recent <= budget), and of the others those with the
  * largest mass (ties: the lower position; NaN counts as the lowest), in their order. Their keys,

@@ -12,7 +12,7 @@ _BINDING = {
     "launch_count", "profile_enable", "profile_collect", "lla_forward_noalloc",
     "lla_parallax_forward", "lla_decode", "lla_parallax_decode", "lla_parallax_backward",
     "Options", "PagedCache", "lla_paged_append", "lla_paged_attention", "lla_paged_workspace_size",
-    "lla_paged_evict",
+    "lla_paged_evict", "lla_paged_tree_attention", "lla_paged_tree_workspace_size",
 }
 
 

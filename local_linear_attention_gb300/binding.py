@@ -20,7 +20,7 @@ __all__ = [
     "PATH_TENSOR_CORE", "PATH_CG", "lla_parallax_forward", "lla_decode", "lla_parallax_decode",
     "FORM_CENTRED", "FORM_PAGE", "FAULT_WITHHOLD_KEYS", "lla_parallax_backward", "Options",
     "PagedCache", "lla_paged_append", "lla_paged_attention", "lla_paged_workspace_size",
-    "lla_paged_evict",
+    "lla_paged_evict", "lla_paged_tree_attention", "lla_paged_tree_workspace_size",
 ]
 
 LLA_OK = 0
@@ -36,7 +36,7 @@ EXPORTED_SYMBOLS = (
     "lla_parallax_decode", "lla_parallax_forward", "lla_parallax_backward", "lla_forward_ex",
     "lla_parallax_forward_ex", "lla_decode_ex", "lla_parallax_decode_ex",
     "lla_parallax_backward_ex", "lla_paged_append", "lla_paged_workspace_size",
-    "lla_paged_attention", "lla_paged_evict",
+    "lla_paged_attention", "lla_paged_evict", "lla_paged_tree_workspace_size", "lla_paged_tree_attention",
 )
 
 # LLA_NOALLOC_SCRATCH_BYTES in include/lla.h: the fixed scratch of lla_forward_noalloc.
@@ -122,6 +122,8 @@ def _load():
         "lla_paged_workspace_size": (sz, [vp, vp]),
         "lla_paged_attention": (i, [vp, vp, vp, sz, vp]),
         "lla_paged_evict": (i, [vp, vp, i, i, i, vp, vp]),
+        "lla_paged_tree_workspace_size": (sz, [vp, vp]),
+        "lla_paged_tree_attention": (i, [vp, vp, vp, vp, sz, vp]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -474,16 +476,8 @@ def _paged_query(q, cache, starts, h, r, max_new, window, sinks, track_mass, out
                        1 if track_mass else 0, path, 0, 0)
 
 
-def lla_paged_attention(q, cache: PagedCache, starts, h: float, r=None, max_new=None, window=0,
-                        sinks=0, track_mass=False, out=None, lse=None, workspace=None, stream=None,
-                        *, path=0):
-    """Attention of the new tokens q [tokens, q_heads, d] over the cache that they were appended to;
-    returns (out [tokens, q_heads, dv], lse [tokens, q_heads] float32). With a probe r (like q) the
-    Parallax output, else softmax attention. The token at position i sees positions j <= i, all of
-    them (window = 0) or the last `window` and the first `sinks`. track_mass adds the weights to
-    cache.mass. Rows that no sequence covers are not written: in tensors that this call allocates they hold
-    anything. max_new: a bound of the tokens of one sequence (default: all); giving it lets a
-    decode step run as one."""
+def _paged_attend(fn, parents, q, cache, starts, h, r, max_new, window, sinks, track_mass, out, lse, workspace, stream,
+                  path):
     shape = q.shape
     if out is not None:
         _paged_rows("out", out, cache, (*shape[:2], cache.dv))
@@ -506,8 +500,22 @@ def lla_paged_attention(q, cache: PagedCache, starts, h: float, r=None, max_new=
         if workspace.get_device() != cache._index or not workspace.is_contiguous():
             raise ValueError("workspace must be a contiguous tensor on the cache's device")
         wp, wb = workspace.data_ptr(), workspace.numel() * workspace.element_size()
-    _paged_call(_load().lla_paged_attention, cache, stream, cache._packed, query, wp, wb)
+    _paged_call(fn, cache, stream, cache._packed, query, *parents, wp, wb)
     return out, lse
+
+
+def lla_paged_attention(q, cache: PagedCache, starts, h: float, r=None, max_new=None, window=0,
+                        sinks=0, track_mass=False, out=None, lse=None, workspace=None, stream=None,
+                        *, path=0):
+    """Attention of the new tokens q [tokens, q_heads, d] over the cache that they were appended to;
+    returns (out [tokens, q_heads, dv], lse [tokens, q_heads] float32). With a probe r (like q) the
+    Parallax output, else softmax attention. The token at position i sees positions j <= i, all of
+    them (window = 0) or the last `window` and the first `sinks`. track_mass adds the weights to
+    cache.mass. Rows that no sequence covers are not written: in tensors that this call allocates they hold
+    anything. max_new: a bound of the tokens of one sequence (default: all); giving it lets a
+    decode step run as one."""
+    return _paged_attend(_load().lla_paged_attention, (), q, cache, starts, h, r, max_new, window, sinks, track_mass, out,
+                         lse, workspace, stream, path)
 
 
 def lla_paged_workspace_size(q, cache: PagedCache, starts, h: float, r=None, max_new=None, window=0,
@@ -516,6 +524,37 @@ def lla_paged_workspace_size(q, cache: PagedCache, starts, h: float, r=None, max
     or from the stream-ordered allocator)."""
     query = _paged_query(q, cache, starts, h, r, max_new, window, sinks, track_mass, None, lse, path)
     return int(_load().lla_paged_workspace_size(cache._packed, query))
+
+
+MAX_NODES = 1024  # of a sequence's tree
+
+
+def _paged_parents(parents, cache, tokens):
+    if parents.dtype != torch.int32 or parents.shape != (tokens,) or parents.get_device() != cache._index or \
+            not parents.is_contiguous():
+        raise ValueError("parents must be a contiguous int32 [tokens] tensor on the cache's device")
+
+
+def lla_paged_tree_attention(q, cache: PagedCache, starts, parents, h: float, r=None, max_new=None, window=0, sinks=0,
+                             out=None, lse=None, workspace=None, stream=None, *, path=0):
+    """Attention of trees of drafted tokens over the cache that they were appended to: sequence b's new
+    tokens are nodes, parents [tokens] int32 holds of each its parent's index among them (below its
+    own) or -1. A node sees the positions before the nodes, its ancestors and itself; its position is
+    that of the first node's slot plus its depth. Otherwise as lla_paged_attention. max_new: a bound of the nodes
+    of one sequence (default: all tokens, at most 1024)."""
+    tokens = q.shape[0]
+    _paged_parents(parents, cache, tokens)
+    max_new = min(tokens, MAX_NODES) if max_new is None else max_new
+    return _paged_attend(_load().lla_paged_tree_attention, (parents.data_ptr(),), q, cache, starts, h, r, max_new, window,
+                         sinks, False, out, lse, workspace, stream, path)
+
+
+def lla_paged_tree_workspace_size(q, cache: PagedCache, starts, h: float, r=None, max_new=None, window=0, sinks=0,
+                                  lse=None, *, path=0) -> int:
+    """Bytes of device scratch that lla_paged_tree_attention takes for these arguments."""
+    max_new = min(q.shape[0], MAX_NODES) if max_new is None else max_new
+    query = _paged_query(q, cache, starts, h, r, max_new, window, sinks, False, None, lse, path)
+    return int(_load().lla_paged_tree_workspace_size(cache._packed, query))
 
 
 def lla_paged_evict(cache: PagedCache, to: PagedCache, budget: int, sinks=0, recent=0, kept=None,

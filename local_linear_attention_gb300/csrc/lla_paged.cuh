@@ -52,6 +52,11 @@ struct Params {
   float* logits;     // [B * Hkv][row_cap][keys_cap]  raw q.k of the few-rows kernel, by the key's
                      // place among the visible 16-key steps (weight tracking)
   int row_cap, keys_cap;
+  // Trees of drafted tokens (lla_paged_tree.cu): the new tokens of a sequence are nodes.
+  const int* parents;    // [tokens]: a node's parent, an index among its sequence's new tokens or -1; nullptr: no trees
+  const uint32_t* bits;  // [tokens][words]: which nodes a node sees
+  const int* depth;      // [tokens]
+  int words;
 };
 
 struct Seq {
@@ -67,7 +72,8 @@ __device__ __forceinline__ Seq load_seq(const Params& p, int b) {
   Seq s;
   const int t0 = p.starts[b], t1 = p.starts[b + 1];
   const int len = p.lens[b], cap = p.max_pages << p.page_shift;
-  const bool bad = t0 < 0 || t1 < t0 || t1 > p.tokens || len < 0 || len > cap;
+  // (A node's key has to be in the cache: more nodes than positions are impossible too.)
+  const bool bad = t0 < 0 || t1 < t0 || t1 > p.tokens || len < 0 || len > cap || (p.parents && t1 - t0 > len);
   s.t0 = bad ? 0 : t0;
   s.n = bad ? 0 : t1 - t0;
   s.len = bad ? 0 : len;
@@ -108,6 +114,59 @@ struct TileRange {
 __device__ __forceinline__ bool all_visible(const Params& p, int p0, int p1, int k0, int k1) {
   return k1 - 1 <= p0 && (k0 > p1 - p.window || k1 <= p.sinks);
 }
+
+// Trees. Node i of a sequence (its new token i, in slot first + i) is at position first + depth(i). Of the
+// positions before the nodes it sees what a token at that position does, of the nodes itself and its ancestors
+// within the window or the first tokens.
+//
+// The same for rows of nodes whose indices are at most p1 - first: depths are between 0 and the index, so the
+// key tiles are TileRange(p, first, p1)'s.
+__device__ __forceinline__ bool tree_all_visible(const Params& p, int first, int p1, int k0, int k1) {
+  return k1 <= first && (k0 > p1 - p.window || k1 <= p.sinks);
+}
+// A parent as the kernels take it: one that does not come before its child (reported by whoever reads the
+// tree first) is none. Walks up a tree end, since indices fall.
+__device__ __forceinline__ int load_parent(const Params& p, const Seq& sq, int i) {
+  const int a = __ldg(p.parents + sq.t0 + i);
+  return a >= -1 && a < i ? a : -1;
+}
+// The words of a node's bits from node `at` on (a multiple of 32 or not, negative too), as 32 bits.
+__device__ __forceinline__ uint32_t node_bits(const Params& p, int token, int at) {
+  const uint32_t* w = p.bits + (long long)token * p.words;
+  const int i = at >> 5;
+  const uint32_t lo = i >= 0 && i < p.words ? w[i] : 0u, hi = i >= -1 && i + 1 < p.words ? w[i + 1] : 0u;
+  return __funnelshift_r(lo, hi, at & 31);
+}
+// Whether the node of row `token` (position pos) sees position j (slot), from its bits.
+__device__ __forceinline__ bool node_sees(const Params& p, int first, int token, int pos, int j) {
+  if (j < first) return j > pos - p.window || j < p.sinks;
+  const int a = j - first;
+  return a < 32 * p.words && ((p.bits[(long long)token * p.words + (a >> 5)] >> (a & 31)) & 1u);
+}
+
+// A row of the slow paths below: new token i of its sequence at position pos. `sees` goes up the tree.
+struct RowAt {
+  int i, pos;
+  __device__ __forceinline__ RowAt(const Params& p, const Seq& sq, int i_) : i(i_), pos(sq.first + i_) {
+    if (!p.parents) return;
+    pos = sq.first;
+    for (int a = load_parent(p, sq, i); a >= 0; a = load_parent(p, sq, a)) ++pos;
+  }
+  __device__ __forceinline__ bool sees(const Params& p, const Seq& sq, int j) const {
+    if (!p.parents) return visible(p, pos, j);
+    if (j < sq.first) return j > pos - p.window || j < p.sinks;
+    int a = i, up = 0;
+    for (; a > j - sq.first; ++up) a = load_parent(p, sq, a);
+    return a == j - sq.first && (up < p.window || pos - up < p.sinks);
+  }
+  template <int KT>
+  __device__ __forceinline__ TileRange<KT> range(const Params& p, const Seq& sq) const {
+    return TileRange<KT>(p, p.parents ? sq.first : pos, sq.first + i);
+  }
+  __device__ __forceinline__ bool sees_all(const Params& p, const Seq& sq, int k0, int k1) const {
+    return p.parents ? tree_all_visible(p, sq.first, pos, k0, k1) : all_visible(p, pos, pos, k0, k1);
+  }
+};
 
 // Whether sequence rows `n` x g are this launch's.
 __device__ __forceinline__ bool mine(const Params& p, int n) {
@@ -154,7 +213,8 @@ __device__ __forceinline__ float subtrahend(float lse) { return lse == -CUDART_I
 // One row computed by one warp straight from the definition, skipping every key that the row does
 // not see (see repair_row). Slow, and off every ordinary path.
 template <typename T>
-__device__ __noinline__ void exact_row(const Params& p, int b, int pos, int token, int head) {
+__device__ __noinline__ void exact_row(const Params& p, Seq sq, int b, int token, int head) {
+  const RowAt row(p, sq, token - sq.t0);
   const int d = p.d, dv = p.dv;
   const int lane = threadIdx.x & 31, hk = head / p.g;
   const T* q = static_cast<const T*>(p.q) + ((long long)token * p.Hq + head) * d;
@@ -162,10 +222,10 @@ __device__ __noinline__ void exact_row(const Params& p, int b, int pos, int toke
   const T* kp = static_cast<const T*>(p.k);
   const T* vp = static_cast<const T*>(p.v);
   float m = -CUDART_INF_F, d1 = 0.f, d2 = 0.f, o1[4] = {}, o2[4] = {};
-  const TileRange<32> range(p, pos, pos);
+  const TileRange<32> range = row.range<32>(p, sq);
   for (int i = 0; i < range.count; ++i) {
     const int j = range.tile(i) * 32 + lane;
-    const bool see = visible(p, pos, j);
+    const bool see = row.sees(p, sq, j);
     float s = -CUDART_INF_F, t = 0.f;
     long long slot = -1;
     if (see) {
@@ -220,22 +280,23 @@ __device__ __noinline__ void exact_row(const Params& p, int b, int pos, int toke
     p.lse[(long long)token * p.Hq + head] = d1 == 0.f ? -CUDART_INF_F : m + logf(d1);
 }
 
-// Whether a key that the row at position `pos` does not see, in the KT-key tiles that its row block
+// Whether a key that the row of `token` does not see, in the KT-key tiles that its row block
 // (positions p0 .. p1) goes over, has a value that is not finite. One warp.
 template <typename T, int KT>
-__device__ __noinline__ bool hides_bad(const Params& p, const Seq& sq, int b, int hk, int pos, int p0, int p1) {
+__device__ __noinline__ bool hides_bad(const Params& p, Seq sq, int b, int hk, int token, int p0, int p1) {
+  const RowAt row(p, sq, token - sq.t0);
   const int lane = threadIdx.x & 31;
   const TileRange<KT> range(p, p0, p1);
   const T* vp = static_cast<const T*>(p.v);
   for (int base = 0; base < range.count; base += 32) {
     const int k0 = base + lane < range.count ? range.tile(base + lane) * KT : 0;
-    unsigned masked = __ballot_sync(0xffffffffu, base + lane < range.count && !all_visible(p, pos, pos, k0, k0 + KT));
+    unsigned masked = __ballot_sync(0xffffffffu, base + lane < range.count && !row.sees_all(p, sq, k0, k0 + KT));
     while (masked) {
       const int t0 = __shfl_sync(0xffffffffu, k0, __ffs(masked) - 1);
       masked &= masked - 1;
       bool bad = false;
       for (int j = t0; j < min(t0 + KT, sq.len); ++j) {
-        if (visible(p, pos, j)) continue;
+        if (row.sees(p, sq, j)) continue;
         const int pg = load_page(p, b, j >> p.page_shift);
         if (pg < 0) continue;
         const long long slot = ((long long)pg * p.Hkv + hk) * p.page + (j & (p.page - 1));
@@ -254,11 +315,11 @@ __device__ __noinline__ bool hides_bad(const Params& p, const Seq& sq, int b, in
 // weights comes from a key that the row sees, and so does everything else that is not finite: those
 // rows stay as they are.
 template <typename T, int KT>
-__device__ __forceinline__ void repair_row(const Params& p, const Seq& sq, int b, int pos, int p0, int p1, int token,
-                                           int head, float d1) {
+__device__ __forceinline__ void repair_row(const Params& p, const Seq& sq, int b, int p0, int p1, int token, int head,
+                                           float d1) {
   __syncwarp();
   if (isnan(d1)) return;
-  if (isinf(d1) || hides_bad<T, KT>(p, sq, b, head / p.g, pos, p0, p1)) exact_row<T>(p, b, pos, token, head);
+  if (isinf(d1) || hides_bad<T, KT>(p, sq, b, head / p.g, token, p0, p1)) exact_row<T>(p, sq, b, token, head);
 }
 
 // ------------------------------------------------------------------------------------- arithmetic
@@ -389,6 +450,9 @@ cudaError_t launch_join_tc(const Params& p, int D, cudaStream_t s);
 cudaError_t launch_mass_tc(const Params& p, int D, cudaStream_t s);
 cudaError_t encode_query_map(const Params& p, const void* q, CUtensorMap* map);
 cudaError_t encode_page_map(const Params& p, void* pages, int d, int kt, CUtensorMap* map);
+// The nodes' bits and depths (p.bits, p.depth point there), for sequences of at most max_nodes <= kMaxNodes.
+constexpr int kMaxNodes = 1024;
+cudaError_t launch_tree(const Params& p, uint32_t* bits, int* depth, int max_nodes, cudaStream_t s);
 cudaError_t launch_append(const Params& p, const void* k_new, const void* v_new, int d, int dv,
                           int dtype, cudaStream_t s);
 // `p` is the source cache; the other arguments the destination and the choice.

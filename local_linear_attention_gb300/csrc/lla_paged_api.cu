@@ -113,6 +113,9 @@ struct Plan {
   int rows_split = 1, tiles_split = 1;
   int row_cap = 0, keys_cap = 0;
   size_t rows_s = 0, rows_o = 0, logits = 0, pieces = 0, tiles_s = 0, tiles_o = 0, lse = 0;
+  bool tree = false;         // a launch finds the nodes' bits and depths first
+  int words = 0;
+  size_t bits = 0, depth = 0;
   size_t bytes = 0;
 };
 
@@ -145,7 +148,7 @@ int f32_splits(long long tiles, long long keys, long long rows, int D, bool prob
   return best;
 }
 
-Plan make_plan(const lla_paged_cache* c, const lla_paged_query* a) {
+Plan make_plan(const lla_paged_cache* c, const lla_paged_query* a, bool tree) {
   Plan pl;
   const int g = a->q_heads / c->kv_heads;
   const long long cap = (long long)c->max_pages * c->page_size;
@@ -169,6 +172,12 @@ Plan make_plan(const lla_paged_cache* c, const lla_paged_query* a) {
     if (n > keys / least) n = keys / least;
     return n < 1 ? 1 : n > 512 ? 512 : (int)n;
   };
+  pl.tree = tree && (c->dtype == LLA_F32 || pl.tiles);
+  if (pl.tree) {
+    pl.words = (int)((max_new + 31) / 32);
+    pl.bits = take((size_t)a->tokens * pl.words * sizeof(uint32_t));
+    pl.depth = take((size_t)a->tokens * sizeof(int));
+  }
   if (c->dtype == LLA_F32) {
     pl.f32 = f32_tiles(a->tokens, max_new, c->num_seqs, g);
     // (the bound counts a part tile for every sequence: as likely as not there is one)
@@ -276,7 +285,7 @@ int run_f32(const Params& p, const Plan& pl, int track_mass, char* ws, cudaStrea
   return err == cudaSuccess ? LLA_OK : LLA_ERR_CUDA;
 }
 
-int run_attention(const lla_paged_cache* c, const lla_paged_query* a, const Plan& pl, char* ws,
+int run_attention(const lla_paged_cache* c, const lla_paged_query* a, const int* parents, const Plan& pl, char* ws,
                   cudaStream_t s) {
   Params p = cache_params(c);
   if (device_status(&p.status) != cudaSuccess) return LLA_ERR_CUDA;
@@ -294,6 +303,16 @@ int run_attention(const lla_paged_cache* c, const lla_paged_query* a, const Plan
   const long long rows = (long long)a->max_new * p.g;
   p.max_rows = rows < 0x7fffffffLL ? (int)rows : 0x7fffffff;
   if (a->track_mass && !a->lse) p.lse = reinterpret_cast<float*>(ws + pl.lse);
+  p.parents = parents;
+  if (parents) p.hi = p.max_rows;  // the bits have room for max_new nodes
+  if (pl.tree) {
+    p.words = pl.words;
+    p.bits = reinterpret_cast<uint32_t*>(ws + pl.bits);
+    p.depth = reinterpret_cast<int*>(ws + pl.depth);
+    if (launch_tree(p, reinterpret_cast<uint32_t*>(ws + pl.bits), reinterpret_cast<int*>(ws + pl.depth),
+                    a->max_new < a->tokens ? a->max_new : a->tokens, s) != cudaSuccess)
+      return LLA_ERR_CUDA;
+  }
   if (c->dtype == LLA_F32) return run_f32(p, pl, a->track_mass, ws, s);
   Params f = p;  // the few-rows kernel's
   p.lo = pl.rows ? pl.row_cap : 0;
@@ -336,6 +355,38 @@ int run_attention(const lla_paged_cache* c, const lla_paged_query* a, const Plan
   return LLA_OK;
 }
 
+// A tree's nodes are new tokens of which most will not stay, so their weights are not counted.
+int check_tree_query(const lla_paged_cache* c, const lla_paged_query* a) {
+  const int st = check_query(c, a);
+  if (st != LLA_OK) return st;
+  if (a->track_mass) return LLA_ERR_INVALID_ARG;
+  return (a->max_new < a->tokens ? a->max_new : a->tokens) > kMaxNodes ? LLA_ERR_UNSUPPORTED : LLA_OK;
+}
+
+// The attention of checked queries, of trees where there are parents.
+int attend(const lla_paged_cache* cache, const lla_paged_query* query, const int* parents, void* workspace,
+           size_t workspace_bytes, cudaStream_t s) {
+  if (query->tokens == 0 || cache->num_seqs == 0) return LLA_OK;
+  if (query->max_new == 0) return LLA_ERR_INVALID_ARG;
+  int st = check_cache_pointers(cache, query->track_mass != 0);
+  if (st != LLA_OK) return st;
+  if (!query->q || !query->out || !query->starts || !aligned16(query->q) || !aligned16(query->out) ||
+      (query->r && !aligned16(query->r)))
+    return LLA_ERR_INVALID_ARG;
+  const Plan pl = make_plan(cache, query, parents != nullptr);
+  if (workspace || pl.bytes == 0) {
+    if (workspace && ((reinterpret_cast<uintptr_t>(workspace) % 256) != 0 || workspace_bytes < pl.bytes))
+      return LLA_ERR_INVALID_ARG;
+    return run_attention(cache, query, parents, pl, static_cast<char*>(workspace), s);
+  }
+  if (ensure_pool() != cudaSuccess) return LLA_ERR_CUDA;
+  void* ws = nullptr;
+  if (cudaMallocAsync(&ws, pl.bytes, s) != cudaSuccess) return LLA_ERR_CUDA;
+  st = run_attention(cache, query, parents, pl, static_cast<char*>(ws), s);
+  if (cudaFreeAsync(ws, s) != cudaSuccess && st == LLA_OK) st = LLA_ERR_CUDA;
+  return st;
+}
+
 }  // namespace
 }  // namespace paged
 }  // namespace lla
@@ -369,33 +420,27 @@ int lla_paged_append(const lla_paged_cache* cache, const void* k_new, const void
 size_t lla_paged_workspace_size(const lla_paged_cache* cache, const lla_paged_query* query) {
   if (check_query(cache, query) != LLA_OK) return 0;
   if (query->tokens == 0 || cache->num_seqs == 0) return 0;
-  return make_plan(cache, query).bytes;
+  return make_plan(cache, query, false).bytes;
 }
 
 int lla_paged_attention(const lla_paged_cache* cache, const lla_paged_query* query, void* workspace,
                         size_t workspace_bytes, void* stream) {
-  int st = check_query(cache, query);
+  const int st = check_query(cache, query);
+  return st != LLA_OK ? st : attend(cache, query, nullptr, workspace, workspace_bytes, static_cast<cudaStream_t>(stream));
+}
+
+size_t lla_paged_tree_workspace_size(const lla_paged_cache* cache, const lla_paged_query* query) {
+  if (check_tree_query(cache, query) != LLA_OK) return 0;
+  if (query->tokens == 0 || cache->num_seqs == 0) return 0;
+  return make_plan(cache, query, true).bytes;
+}
+
+int lla_paged_tree_attention(const lla_paged_cache* cache, const lla_paged_query* query, const int* parents,
+                             void* workspace, size_t workspace_bytes, void* stream) {
+  const int st = check_tree_query(cache, query);
   if (st != LLA_OK) return st;
-  if (query->tokens == 0 || cache->num_seqs == 0) return LLA_OK;
-  if (query->max_new == 0) return LLA_ERR_INVALID_ARG;
-  st = check_cache_pointers(cache, query->track_mass != 0);
-  if (st != LLA_OK) return st;
-  if (!query->q || !query->out || !query->starts || !aligned16(query->q) || !aligned16(query->out) ||
-      (query->r && !aligned16(query->r)))
-    return LLA_ERR_INVALID_ARG;
-  const Plan pl = make_plan(cache, query);
-  cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (workspace || pl.bytes == 0) {
-    if (workspace && ((reinterpret_cast<uintptr_t>(workspace) % 256) != 0 || workspace_bytes < pl.bytes))
-      return LLA_ERR_INVALID_ARG;
-    return run_attention(cache, query, pl, static_cast<char*>(workspace), s);
-  }
-  if (ensure_pool() != cudaSuccess) return LLA_ERR_CUDA;
-  void* ws = nullptr;
-  if (cudaMallocAsync(&ws, pl.bytes, s) != cudaSuccess) return LLA_ERR_CUDA;
-  st = run_attention(cache, query, pl, static_cast<char*>(ws), s);
-  if (cudaFreeAsync(ws, s) != cudaSuccess && st == LLA_OK) st = LLA_ERR_CUDA;
-  return st;
+  if (query->tokens > 0 && cache->num_seqs > 0 && !parents) return LLA_ERR_INVALID_ARG;
+  return attend(cache, query, parents, workspace, workspace_bytes, static_cast<cudaStream_t>(stream));
 }
 
 int lla_paged_evict(const lla_paged_cache* from, const lla_paged_cache* to, int budget, int sinks,

@@ -112,7 +112,8 @@ __global__ void __launch_bounds__(NT) attend_cc_kernel(Params p) {
   if (PROBE)
     stage<D, S::QP, BM, T>(sm + S::r, [&](int row) { return row < nrows ? rg + rowid(row) * D : (const T*)nullptr; });
 
-  const int p0 = sq.first + tok0, p1 = p0 + ntok - 1;
+  // (With trees the rows' positions lie between the first node's and this, and `visible` goes by their bits.)
+  const int p0 = p.parents ? sq.first : sq.first + tok0, p1 = sq.first + tok0 + ntok - 1;
   const TileRange<KT> range(p, p0, p1);
   const int chunk = (range.count + p.split - 1) / p.split;
   const int i0 = part * chunk, i1 = min(range.count, i0 + chunk);
@@ -122,7 +123,12 @@ __global__ void __launch_bounds__(NT) attend_cc_kernel(Params p) {
   for (int i = 0; i < RM; ++i) {
     const int row = ty * RM + i;
     pos[i] = row < nrows ? p0 + row / width : -1;      // a row past the end sees nothing
+    if (p.parents && row < nrows) pos[i] = sq.first + p.depth[sq.t0 + tok0 + row / width];
   }
+  auto see = [&](int i, int j) {
+    if (!p.parents || pos[i] < 0) return visible(p, pos[i], j);
+    return j < sq.len && node_sees(p, sq.first, sq.t0 + tok0 + (ty * RM + i) / width, pos[i], j);
+  };
   float m[RM], d1[RM], d2[RM], o1[RM][VC], o2[PROBE ? RM : 1][VC];
 #pragma unroll
   for (int i = 0; i < RM; ++i) {
@@ -155,7 +161,7 @@ __global__ void __launch_bounds__(NT) attend_cc_kernel(Params p) {
       float tm = -CUDART_INF_F;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        s[i][j] = visible(p, pos[i], k0 + tx + 16 * j) ? s[i][j] : -CUDART_INF_F;
+        s[i][j] = see(i, k0 + tx + 16 * j) ? s[i][j] : -CUDART_INF_F;
         tm = fmaxf(tm, s[i][j]);
       }
 #pragma unroll
@@ -258,7 +264,7 @@ __global__ void __launch_bounds__(NT) attend_cc_kernel(Params p) {
       if (u == i) sum = d1[u];
     sum = __shfl_sync(0xffffffffu, sum, bit & 16);
     const long long id = rowid(row);
-    repair_row<T, KT>(p, sq, b, p0 + row / width, p0, p1, (int)(id / p.Hq), (int)(id % p.Hq), sum);
+    repair_row<T, KT>(p, sq, b, p0, p1, (int)(id / p.Hq), (int)(id % p.Hq), sum);
   }
 }
 
@@ -371,8 +377,8 @@ __global__ void __launch_bounds__(128) join_kernel(Params p) {
   if (p.lse && lane == 0) p.lse[id] = d1 == 0.f ? -CUDART_INF_F : m * p.inv_h + logf(d1);
   if (__any_sync(0xffffffffu, !(bad == 0.f))) {
     const int first = sq.first + (token - sq.t0) / 64 * 64;  // (a block's rows are at most 64 tokens)
-    repair_row<T, KT>(p, sq, b, sq.first + token - sq.t0, max(first - 64, sq.first), min(first + 127, sq.len - 1),
-                      token, (int)(id % p.Hq), d1);
+    repair_row<T, KT>(p, sq, b, p.parents ? sq.first : max(first - 64, sq.first), min(first + 127, sq.len - 1), token,
+                      (int)(id % p.Hq), d1);
   }
 }
 

@@ -55,8 +55,9 @@ __device__ __forceinline__ void load2(const void* at, uint64_t& a, uint64_t& b) 
   b = x.y;
 }
 
-// A tile of nrows <= RT rows over this block's part of its keys: leaves the warps' sums for the join.
-template <int D, int RT, bool PROBE>
+// A tile of nrows <= RT rows over this block's part of its keys: leaves the warps' sums for the join. TREE: the
+// new tokens are a tree's nodes, whose bits and depths the launch before this one writes.
+template <int D, int RT, bool PROBE, bool TREE>
 __device__ __forceinline__ void attend_tile(const Params& p, const Seq& sq, const Rows& rows, int nrows, int b, int hk,
                                             int part, uint8_t* smem, float4 (&stats)[NW][16]) {
   using C = Cfg<D, RT, PROBE>;
@@ -149,11 +150,16 @@ __device__ __forceinline__ void attend_tile(const Params& p, const Seq& sq, cons
   // Rows i * RG + rg of this lane, keys kl + KL kk of a step. The weights of a key lie as
   // [rg][i], so slot rg * 4 + i of the second product is row i * RG + rg.
   const int rg = lane / KL, kl = lane % KL;
-  int pos[4];
+  int pos[4], token[4];
+  if (TREE) wait_previous();
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const int r = i * RG + rg;
     pos[i] = r < nrows ? p0 + r / rows.width : p1;  // rows past the end are not written
+    if constexpr (TREE) {
+      token[i] = rows.t0 + min(r, nrows - 1) / rows.width;
+      pos[i] = p0 + p.depth[token[i]];
+    }
   }
   const float c2 = p.inv_h * kLog2e, slack = fminf(8.f / c2, 1e38f);
   float m[4], ref[4], d1[4], d2[4];
@@ -223,7 +229,10 @@ __device__ __forceinline__ void attend_tile(const Params& p, const Seq& sq, cons
       }
     }
     float x[4][RG];
-    const bool full = all_visible(p, p0, p1, cur.j[0], cur.j[0] + KT) && all_visible(p, p0, p1, cur.j[1], cur.j[1] + KT);
+    const bool full = TREE ? tree_all_visible(p, p0, p1, cur.j[0], cur.j[0] + KT) &&
+                                 tree_all_visible(p, p0, p1, cur.j[1], cur.j[1] + KT)
+                           : all_visible(p, p0, p1, cur.j[0], cur.j[0] + KT) &&
+                                 all_visible(p, p0, p1, cur.j[1], cur.j[1] + KT);
     bool grew = false;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -234,7 +243,7 @@ __device__ __forceinline__ void attend_tile(const Params& p, const Seq& sq, cons
         unpair(s2[i][k], lo, hi);
         x[i][k] = lo + hi;
         const int key = kl + KL * k, j = (key < KT ? cur.j[0] : cur.j[1]) + (key & (KT - 1));
-        if (!full && !visible(p, pos[i], j)) x[i][k] = -CUDART_INF_F;
+        if (!full && !(TREE ? node_sees(p, p0, token[i], pos[i], j) : visible(p, pos[i], j))) x[i][k] = -CUDART_INF_F;
         top = fmaxf(top, x[i][k]);
       }
       grew |= top > m[i] + slack;
@@ -369,7 +378,7 @@ __device__ __forceinline__ void attend_tile(const Params& p, const Seq& sq, cons
   }
 }
 
-template <int D, bool PROBE>
+template <int D, bool PROBE, bool TREE>
 __global__ void __launch_bounds__(NW * 32, 2) attend_f32_kernel(Params p) {
   extern __shared__ __align__(1024) uint8_t smem[];
   __shared__ float4 stats[NW][16];
@@ -380,6 +389,7 @@ __global__ void __launch_bounds__(NW * 32, 2) attend_f32_kernel(Params p) {
   let_next();
   // Sequences of more rows than p.hi (beyond max_new) have no tiles here, since the grid was not sized for
   // them: they are reported.
+  if (TREE && blockIdx.x == 0) wait_previous();  // the end of this grid is the end of both, whatever the others do
   if (blockIdx.x == 0)
     for (int i = threadIdx.x; i < p.B; i += NW * 32) {
       const int n = load_seq(p, i).n;
@@ -391,11 +401,11 @@ __global__ void __launch_bounds__(NW * 32, 2) attend_f32_kernel(Params p) {
   if (sq.n == 0) return;  // an impossible length (find_tile counts by the starts)
   const int u0 = index / p.Hkv % slices * kF32Rows, tok0 = tile * per, ntok = min(per, sq.n - tok0);
   const int p0 = sq.first + tok0;
-  const Rows rows{sq.t0 + tok0, p0, p0 + ntok - 1, min(p.g - u0, kF32Rows), hk * p.g + u0};
+  const Rows rows{sq.t0 + tok0, TREE ? sq.first : p0, p0 + ntok - 1, min(p.g - u0, kF32Rows), hk * p.g + u0};
   const int nrows = ntok * rows.width;
-  if (nrows <= 4) attend_tile<D, 4, PROBE>(p, sq, rows, nrows, b, hk, part, smem, stats);
-  else if (nrows <= 8) attend_tile<D, 8, PROBE>(p, sq, rows, nrows, b, hk, part, smem, stats);
-  else attend_tile<D, 16, PROBE>(p, sq, rows, nrows, b, hk, part, smem, stats);
+  if (nrows <= 4) attend_tile<D, 4, PROBE, TREE>(p, sq, rows, nrows, b, hk, part, smem, stats);
+  else if (nrows <= 8) attend_tile<D, 8, PROBE, TREE>(p, sq, rows, nrows, b, hk, part, smem, stats);
+  else attend_tile<D, 16, PROBE, TREE>(p, sq, rows, nrows, b, hk, part, smem, stats);
   __syncthreads();
   using C = Cfg<D, kF32Rows, PROBE>;
   const float* os = reinterpret_cast<const float*>(smem);
@@ -463,13 +473,13 @@ __global__ void __launch_bounds__(256) mass_f32_kernel(Params p) {
   }
 }
 
-template <int D, bool PROBE>
+template <int D, bool PROBE, bool TREE>
 cudaError_t launch_t(const Params& p, long long tiles, cudaStream_t s) {
   const long long blocks = tiles * p.Hkv * p.split;
   if (blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
   const bool cluster = p.split > 1 && p.split <= kRowsCluster;
-  return launch(attend_f32_kernel<D, PROBE>, dim3((unsigned)blocks), NW * 32, Cfg<D, kF32Rows, PROBE>::bytes,
-                cluster ? p.split : 1, false, s, p);
+  return launch(attend_f32_kernel<D, PROBE, TREE>, dim3((unsigned)blocks), NW * 32, Cfg<D, kF32Rows, PROBE>::bytes,
+                cluster ? p.split : 1, TREE, s, p);
 }
 
 }  // namespace
@@ -480,9 +490,13 @@ long long f32_tiles(long long tokens, long long max_new, int B, int g) {
   return (by_tokens < by_seqs ? by_tokens : by_seqs) * slices;
 }
 
+template <bool TREE>
+static cudaError_t pick(const Params& p, long long tiles, int D, cudaStream_t s) {
+  if (D == 128) return p.r ? launch_t<128, true, TREE>(p, tiles, s) : launch_t<128, false, TREE>(p, tiles, s);
+  return p.r ? launch_t<64, true, TREE>(p, tiles, s) : launch_t<64, false, TREE>(p, tiles, s);
+}
 cudaError_t launch_attend_f32(const Params& p, long long tiles, int D, cudaStream_t s) {
-  if (D == 128) return p.r ? launch_t<128, true>(p, tiles, s) : launch_t<128, false>(p, tiles, s);
-  return p.r ? launch_t<64, true>(p, tiles, s) : launch_t<64, false>(p, tiles, s);
+  return p.parents ? pick<true>(p, tiles, D, s) : pick<false>(p, tiles, D, s);
 }
 cudaError_t launch_mass_f32(const Params& p, cudaStream_t s) {
   const int blocks = (p.keys_cap + 127) / 128;

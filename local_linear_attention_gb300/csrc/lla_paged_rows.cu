@@ -69,8 +69,39 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-// CLUSTER: the blocks of a pair are one cluster and join there.
-template <int D, bool PROBE, bool LOGITS, bool CLUSTER>
+// The nodes of a sequence of at most 16, one per lane: a node's parent's, grandparent's, .. bits (among the
+// nodes) and its own where it sees them, and its depth. Parents go from lane to lane, so the tree costs one
+// load and no launch before this one's.
+__device__ __forceinline__ void small_tree(const Params& p, const Seq& sq, uint32_t* bits, int* depth) {
+  const int lane = threadIdx.x & 31, n = min(sq.n, 32);
+  const int stated = lane < n ? __ldg(p.parents + sq.t0 + lane) : -1;
+  if (stated < -1 || stated >= lane) atomicOr(p.status, kStatusBadIndex);
+  const int parent = stated < lane ? max(stated, -1) : -1;
+  uint32_t up = 1u << lane;
+  int d = 0;
+  for (int a = parent; __any_sync(0xffffffffu, a >= 0);) {
+    const int next = __shfl_sync(0xffffffffu, parent, max(a, 0));
+    if (a >= 0) {
+      up |= 1u << a;
+      ++d;
+      a = next;
+    }
+  }
+  if (p.window < n) {  // ancestors that fell out of the window
+    int steps = 1;
+    for (int a = parent; __any_sync(0xffffffffu, a >= 0); ++steps) {
+      const int next = __shfl_sync(0xffffffffu, parent, max(a, 0));
+      if (a >= 0) {
+        if (steps >= p.window && sq.first + d - steps >= p.sinks) up &= ~(1u << a);
+        a = next;
+      }
+    }
+  }
+  *bits = up;
+  *depth = d;
+}
+// CLUSTER: the blocks of a pair are one cluster and join there. TREE: the new tokens are a tree's nodes.
+template <int D, bool PROBE, bool LOGITS, bool CLUSTER, bool TREE>
 __global__ void __launch_bounds__(NW * 32) attend_rows_kernel(Params p) {
   using C = Cfg<D>;
   constexpr int ROWS = PROBE ? 8 : 16, NR = PROBE ? 1 : 2;  // rows; rows per thread
@@ -92,7 +123,7 @@ __global__ void __launch_bounds__(NW * 32) attend_rows_kernel(Params p) {
   }
   const int nrows = sq.n * p.g;
   const int p0 = sq.first, p1 = sq.len - 1;
-  const TileRange<KT> range(p, p0, p1);
+  const TileRange<KT> range(p, p0, p1);  // (a tree's too)
   const int chunk = (range.count + p.split - 1) / p.split;
   const int i0 = min(range.count, part * chunk), i1 = min(range.count, i0 + chunk);
   const __nv_bfloat16* kg = static_cast<const __nv_bfloat16*>(p.k);
@@ -158,10 +189,19 @@ __global__ void __launch_bounds__(NW * 32) attend_rows_kernel(Params p) {
     }
   }
   int pos[NR];
+  uint32_t up[NR] = {};  // TREE: the nodes that a row sees
+  uint32_t tree_bits = 0;
+  int tree_depth = 0;
+  if constexpr (TREE) small_tree(p, sq, &tree_bits, &tree_depth);
 #pragma unroll
   for (int i = 0; i < NR; ++i) {
     const int r = (lane >> 2) + 8 * i;
     pos[i] = r < nrows ? p0 + r / p.g : p1;  // rows past the end are not written
+    if constexpr (TREE) {
+      const int node = min(r / p.g, sq.n - 1);
+      up[i] = __shfl_sync(0xffffffffu, tree_bits, node);
+      pos[i] = p0 + __shfl_sync(0xffffffffu, tree_depth, node);
+    }
   }
   const float c2 = p.inv_h * kLog2e;
   float m[NR], d1[NR], d2 = 0.f, d1r = 0.f, o[D / 8][4];  // d1r: of the rounded weights (PROBE)
@@ -195,7 +235,8 @@ __global__ void __launch_bounds__(NW * 32) attend_rows_kernel(Params p) {
       mma16816(s[1][ks & 1], a[ks], f[2], f[3]);
     }
     const int j0 = range.tile(it) * KT + (lane & 3) * 2;
-    const bool full = all_visible(p, p0, p1, j0 & ~15, (j0 & ~15) + KT);
+    const bool full = TREE ? tree_all_visible(p, p0, p1, j0 & ~15, (j0 & ~15) + KT)
+                           : all_visible(p, p0, p1, j0 & ~15, (j0 & ~15) + KT);
     float x[NR][4], t[4];  // logits q.k of this thread's rows and 4 keys (t: probe scores)
 #pragma unroll
     for (int n = 0; n < 2; ++n)
@@ -210,8 +251,11 @@ __global__ void __launch_bounds__(NW * 32) attend_rows_kernel(Params p) {
 #pragma unroll
       for (int i = 0; i < NR; ++i)
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-          if (!visible(p, pos[i], j0 + (e >> 1) * 8 + (e & 1))) x[i][e] = -CUDART_INF_F;
+        for (int e = 0; e < 4; ++e) {
+          const int j = j0 + (e >> 1) * 8 + (e & 1);
+          const bool see = TREE && j >= p0 ? (up[i] >> min(j - p0, 31)) & 1u : visible(p, pos[i], j);
+          if (!see) x[i][e] = -CUDART_INF_F;
+        }
     }
     if (LOGITS) {
 #pragma unroll
@@ -387,12 +431,12 @@ __global__ void __launch_bounds__(256) mass_rows_kernel(Params p) {
   }
 }
 
-template <int D, bool PROBE, bool LOGITS>
+template <int D, bool PROBE, bool LOGITS, bool TREE = false>
 cudaError_t launch_rows_t(const Params& p, cudaStream_t s) {
   const unsigned pairs = (unsigned)p.B * p.Hkv;
   if ((long long)pairs * p.split > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
   const bool cluster = p.split > 1 && p.split <= kRowsCluster;
-  auto kern = cluster ? attend_rows_kernel<D, PROBE, LOGITS, true> : attend_rows_kernel<D, PROBE, LOGITS, false>;
+  auto kern = cluster ? attend_rows_kernel<D, PROBE, LOGITS, true, TREE> : attend_rows_kernel<D, PROBE, LOGITS, false, TREE>;
   cudaError_t err = launch(kern, dim3(pairs * p.split), NW * 32, Cfg<D>::bytes, cluster ? p.split : 1, p.beside != 0, s, p);
   if (err == cudaSuccess && !cluster && p.split > 1) {
     const long long rows = (long long)pairs * p.row_cap;
@@ -407,6 +451,7 @@ cudaError_t launch_rows_t(const Params& p, cudaStream_t s) {
 
 template <int D>
 cudaError_t pick(const Params& p, cudaStream_t s) {
+  if (p.parents) return p.r ? launch_rows_t<D, true, false, true>(p, s) : launch_rows_t<D, false, false, true>(p, s);
   if (p.r) return p.logits ? launch_rows_t<D, true, true>(p, s) : launch_rows_t<D, true, false>(p, s);
   return p.logits ? launch_rows_t<D, false, true>(p, s) : launch_rows_t<D, false, false>(p, s);
 }

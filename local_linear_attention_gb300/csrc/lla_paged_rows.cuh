@@ -60,7 +60,7 @@ __device__ __forceinline__ void write_row(const Params& p, const Seq& sq, int b,
     p.lse[(long long)token * p.Hq + head] =
         s1 == 0.f ? -CUDART_INF_F : (st.x * (p.inv_h * kLog2e) + log2f(s1)) * kLn2;
   if (__any_sync(0xffffffffu, !(bad == 0.f))) {
-    repair_row<T, KT>(p, sq, b, rows.p0 + r / rows.width, rows.p0, rows.p1, token, head, s1);
+    repair_row<T, KT>(p, sq, b, rows.p0, rows.p1, token, head, s1);
   }
 }
 

@@ -132,14 +132,16 @@ struct Sched {
 struct Place {  // step s of a tile; b = number of sequences: the end
   int b, tile, hk, s;
 };
+// TREE: the positions of a tile's nodes lie between the first node's and p1.
 struct Tile {
   int tok0, ntok, p0, p1;
-  __device__ __forceinline__ Tile(const Seq& sq, int tile, int tokens)
-      : tok0(tile * tokens), ntok(min(tokens, sq.n - tok0)), p0(sq.first + tok0), p1(p0 + ntok - 1) {}
+  __device__ __forceinline__ Tile(const Seq& sq, int tile, int tokens, bool tree)
+      : tok0(tile * tokens), ntok(min(tokens, sq.n - tok0)), p0(tree ? sq.first : sq.first + tok0),
+        p1(sq.first + tok0 + ntok - 1) {}
 };
 // Steps of sequence b's tiles (one head), kStart included, and the shortest's; all lanes of the warp
 // return them.
-template <int D, bool PROBE>
+template <int D, bool PROBE, bool TREE>
 __device__ __forceinline__ long long seq_cost(const Params& p, int b, int tokens, int* tiles, int* shortest) {
   using S = Sched<D, PROBE>;
   const Seq sq = load_seq(p, b);
@@ -148,7 +150,7 @@ __device__ __forceinline__ long long seq_cost(const Params& p, int b, int tokens
   if (mine(p, sq.n)) {
     nt = (sq.n + tokens - 1) / tokens;
     for (int t = threadIdx.x & 31; t < nt; t += 32) {
-      const Tile x(sq, t, tokens);
+      const Tile x(sq, t, tokens, TREE);
       const int n = TileRange<S::C::kt>(p, x.p0, x.p1).count + S::kStart;
       c += n;
       least = min(least, n);
@@ -172,7 +174,7 @@ __device__ __forceinline__ long long scan_incl(long long x) {
   return x;
 }
 // The place at step u of the line, from the sequences' costs (a whole warp calls and agrees).
-template <int D, bool PROBE>
+template <int D, bool PROBE, bool TREE>
 __device__ __forceinline__ Place locate(const Params& p, const long long* cost, long long u, int tokens) {
   using S = Sched<D, PROBE>;
   const int lane = threadIdx.x & 31;
@@ -192,7 +194,7 @@ __device__ __forceinline__ Place locate(const Params& p, const long long* cost, 
       int count = 0;
       long long tc = 0;
       if (tb + lane < nt) {
-        const Tile x(sq, tb + lane, tokens);
+        const Tile x(sq, tb + lane, tokens, TREE);
         count = TileRange<S::C::kt>(p, x.p0, x.p1).count;
         tc = (long long)(count + S::kStart) * p.Hkv;
       }
@@ -269,7 +271,8 @@ __device__ __forceinline__ int next_seq(const Params& p, int b) {
   return p.B;
 }
 
-template <int D, bool PROBE>
+// TREE: the new tokens are nodes of trees, whose bits and depths the launch before this one writes.
+template <int D, bool PROBE, bool TREE>
 __global__ void __launch_bounds__((Cfg<D, PROBE>::threads), (Cfg<D, PROBE>::ctas))
 attend_tc_kernel(Params p, const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
                  const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap rmap) {
@@ -331,7 +334,7 @@ attend_tc_kernel(Params p, const __grid_constant__ CUtensorMap kmap, const __gri
     static_assert(kMaxSeqs * 12 <= C::stages * C::tile && kMaxSeqs * 4 <= C::tiles_bytes, "the sequences' costs");
     for (int i = warp; i < p.B; i += C::threads / 32) {
       int nt, least;
-      const long long c = seq_cost<D, PROBE>(p, i, tokens, &nt, &least);
+      const long long c = seq_cost<D, PROBE, TREE>(p, i, tokens, &nt, &least);
       if (lane == 0) {
         cost[i] = c;
         shortest[i] = least;
@@ -365,7 +368,7 @@ attend_tc_kernel(Params p, const __grid_constant__ CUtensorMap kmap, const __gri
         if (lane == 0) bounds[warp] = {p.B, 0, 0, 0};
       } else {
         const long long share = max((w + gridDim.x - 1) / gridDim.x, (long long)(Sched<D, PROBE>::kPiece));
-        const Place x = locate<D, PROBE>(p, cost, (blockIdx.x + warp) * share, tokens);
+        const Place x = locate<D, PROBE, TREE>(p, cost, (blockIdx.x + warp) * share, tokens);
         if (lane == 0) bounds[warp] = x;
         if (tid == 0) whole_s = 0;
       }
@@ -511,14 +514,14 @@ attend_tc_kernel(Params p, const __grid_constant__ CUtensorMap kmap, const __gri
         const Place t = at < ntiles ? by_rank(p, tiles_s, most, (unsigned)at) : Place{p.B, 0, 0, 0};
         if (t.b < p.B) {
           const Seq sq = load_seq(p, t.b);
-          const Tile x(sq, t.tile, tokens);
+          const Tile x(sq, t.tile, tokens, TREE);
           const TileRange<KT> range(p, x.p0, x.p1);
           w = {t.b, t.tile, t.hk, 0, range.count, 1, 0, sq.t0, sq.n, sq.len, sq.first, range.n1, range.w0};
         }
       }
       while (most == 0 && !over && cur.b < p.B) {
         const Seq sq = load_seq(p, cur.b);
-        const Tile x(sq, cur.tile, tokens);
+        const Tile x(sq, cur.tile, tokens, TREE);
         const TileRange<KT> range(p, x.p0, x.p1);
         const int count = range.count;
         over = cur.b == end.b && cur.tile == end.tile && cur.hk == end.hk;
@@ -545,7 +548,7 @@ attend_tc_kernel(Params p, const __grid_constant__ CUtensorMap kmap, const __gri
       __syncwarp();
       if (w.none) break;
       if (w.n == 0) continue;
-      const Tile x(Seq{w.t0, w.seq_n, w.len, w.first}, w.tile, tokens);
+      const Tile x(Seq{w.t0, w.seq_n, w.len, w.first}, w.tile, tokens, TREE);
       // Step i's first key, and this lane's page fragment of it: the page number is read a step ahead.
       auto first_key = [&](int i) {
         const int it = w.i0 + i;
@@ -574,8 +577,10 @@ attend_tc_kernel(Params p, const __grid_constant__ CUtensorMap kmap, const __gri
         int info = k0 | (k0 + KT > w.len ? 4 : 0);
 #pragma unroll
         for (int h = 0; h < C::blocks; ++h) {
-          const int q0 = min(x.p0 + h * per, x.p1);
-          if (!all_visible(p, q0, min(q0 + per - 1, x.p1), k0, k0 + KT)) info |= 1 << h;
+          const int q0 = TREE ? x.p0 : min(x.p0 + h * per, x.p1);
+          if (TREE ? !tree_all_visible(p, x.p0, x.p1, k0, k0 + KT)
+                   : !all_visible(p, q0, min(q0 + per - 1, x.p1), k0, k0 + KT))
+            info |= 1 << h;
         }
         for (int kv = 0; kv < 2 && ok; ++kv) {
           const int y = 2 * (base + i) + kv, st = y % C::stages;
@@ -638,7 +643,7 @@ attend_tc_kernel(Params p, const __grid_constant__ CUtensorMap kmap, const __gri
       Seq sq;
       sq.n = w->seq_n;
       sq.first = w->first;
-      return Tile(sq, w->tile, tokens);
+      return Tile(sq, w->tile, tokens, TREE);
     };
     float m = -CUDART_INF_F, d1 = 0.f, d2 = 0.f, d1r = 0.f, before = -CUDART_INF_F;  // d1r: of the rounded weights (PROBE)
     for (int i = 0; i < n; ++i) {
@@ -660,14 +665,22 @@ attend_tc_kernel(Params p, const __grid_constant__ CUtensorMap kmap, const __gri
       const bool masked = (info >> h) & 1;
       if (masked) {
         const Tile tile = tile_of();
-        const int pos = r_tok < tile.ntok ? tile.p0 + r_tok : tile.p1;  // rows that do not exist are not written
-        // column c is visible when c <= hi and (c > lo or c < first): as bits, then a select each (a
-        // branch per column made such a tile five times as long as a full one)
-        const int hi = pos - kb, lo = pos - p.window - kb, first = p.sinks - kb;
+        int pos = r_tok < tile.ntok ? tile.p0 + r_tok : tile.p1;  // rows that do not exist are not written
+        int past = pos + 1, token = 0;
+        if constexpr (TREE) {
+          wait_previous();  // (at once but the first time)
+          token = w->t0 + tile.tok0 + min(r_tok, tile.ntok - 1);
+          past = w->first;
+          pos = past + p.depth[token];
+        }
+        // column c is visible when c < past and (c > lo or c < first), a node's by its bit: as bits, then a
+        // select each (a branch per column made such a tile five times as long as a full one)
+        const int hi = past - kb, lo = pos - p.window - kb, first = p.sinks - kb;
         auto below = [](int x) { return x <= 0 ? 0u : x >= 32 ? 0xFFFFFFFFu : (1u << x) - 1u; };
 #pragma unroll
         for (int c = 0; c < NC / 32; ++c) {
-          seen[c] = below(hi + 1 - c * 32) & (~below(lo + 1 - c * 32) | below(first - c * 32));
+          seen[c] = below(hi - c * 32) & (~below(lo + 1 - c * 32) | below(first - c * 32));
+          if (TREE && hi < (c + 1) * 32) seen[c] |= node_bits(p, token, c * 32 - hi);
 #pragma unroll
           for (int e = 0; e < 32; ++e) s[c][e] = seen[c] & (1u << e) ? s[c][e] : 0xFF800000u;
         }
@@ -925,7 +938,7 @@ attend_tc_kernel(Params p, const __grid_constant__ CUtensorMap kmap, const __gri
       const int l = __ffs(again) - 1, row = (warp & 3) * 32 + l, tk = h * per + row / p.g;
       again &= again - 1;
       const Seq sq{t0, w->seq_n, w->len, w->first};
-      repair_row<__nv_bfloat16, KT>(p, sq, w->b, tile.p0 + tk, tile.p0, tile.p1, t0 + tile.tok0 + tk, hk * p.g + row % p.g,
+      repair_row<__nv_bfloat16, KT>(p, sq, w->b, tile.p0, tile.p1, t0 + tile.tok0 + tk, hk * p.g + row % p.g,
                                     __shfl_sync(0xffffffffu, d1, l));
     }
     give_back(k);
@@ -933,6 +946,7 @@ attend_tc_kernel(Params p, const __grid_constant__ CUtensorMap kmap, const __gri
     }
   }
 
+  if (TREE && tid == 0) wait_previous();  // the end of this grid is the end of both, whatever it had to do
   tc_fence_before();
   __syncthreads();
   if (warp == C::nsoft + 1) {
@@ -963,7 +977,7 @@ __global__ void __launch_bounds__(256, 4) join_tc_kernel(Params p) {
   }
   const int per = BM / p.g, tokens = C::blocks * per, b = first.x, hk = first.z;
   const Seq sq = load_seq(p, b);
-  const Tile tile(sq, first.y, tokens);
+  const Tile tile(sq, first.y, tokens, p.parents != nullptr);
   const float c2 = p.inv_h * kLog2e;
   auto at = [&](int i, int row) { return (long long)((blockIdx.x + i) * 2 + (i == 0)) * ROWS + row; };
   for (int row = blockIdx.y * 8 + (threadIdx.x >> 5); row < ROWS; row += gridDim.y * 8) {
@@ -1006,12 +1020,12 @@ __global__ void __launch_bounds__(256, 4) join_tc_kernel(Params p) {
     if (p.lse && lane == 0)
       p.lse[(long long)token * p.Hq + head] = s1 == 0.f ? -CUDART_INF_F : (top * c2 + log2f(s1)) * kLn2;
     if (__any_sync(0xffffffffu, !(bad == 0.f))) {
-      repair_row<__nv_bfloat16, C::kt>(p, sq, b, tile.p0 + t, tile.p0, tile.p1, token, head, s1);
+      repair_row<__nv_bfloat16, C::kt>(p, sq, b, tile.p0, tile.p1, token, head, s1);
     }
   }
 }
 
-template <int D, bool PROBE>
+template <int D, bool PROBE, bool TREE>
 cudaError_t launch_tc_t(const Params& p, cudaStream_t s) {
   using C = Cfg<D, PROBE>;
   CUtensorMap kmap, vmap, qmap, rmap;
@@ -1020,8 +1034,8 @@ cudaError_t launch_tc_t(const Params& p, cudaStream_t s) {
   if (err == cudaSuccess) err = encode_query_map(p, p.q, &qmap);
   if (err == cudaSuccess) err = encode_query_map(p, PROBE ? p.r : p.q, &rmap);
   if (err != cudaSuccess) return err;
-  return launch(attend_tc_kernel<D, PROBE>, dim3((unsigned)p.split), C::threads, C::bytes, 1, false, s, p, kmap, vmap,
-                qmap, rmap);
+  return launch(attend_tc_kernel<D, PROBE, TREE>, dim3((unsigned)p.split), C::threads, C::bytes, 1, TREE, s, p, kmap,
+                vmap, qmap, rmap);
 }
 
 template <int D, bool PROBE>
@@ -1080,9 +1094,13 @@ TcPlan plan_tc(int D, bool probe, long long tokens, int B, int Hkv, int g, long 
   return D == 128 ? plan_t<128, false>(tokens, B, Hkv, g, keys) : plan_t<64, false>(tokens, B, Hkv, g, keys);
 }
 
+template <bool TREE>
+static cudaError_t pick(const Params& p, int D, cudaStream_t s) {
+  if (p.r) return D == 128 ? launch_tc_t<128, true, TREE>(p, s) : launch_tc_t<64, true, TREE>(p, s);
+  return D == 128 ? launch_tc_t<128, false, TREE>(p, s) : launch_tc_t<64, false, TREE>(p, s);
+}
 cudaError_t launch_attend_tc(const Params& p, int D, cudaStream_t s) {
-  if (p.r) return D == 128 ? launch_tc_t<128, true>(p, s) : launch_tc_t<64, true>(p, s);
-  return D == 128 ? launch_tc_t<128, false>(p, s) : launch_tc_t<64, false>(p, s);
+  return p.parents ? pick<true>(p, D, s) : pick<false>(p, D, s);
 }
 
 cudaError_t launch_join_tc(const Params& p, int D, cudaStream_t s) {
