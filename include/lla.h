@@ -261,6 +261,52 @@ int lla_parallax_forward_ex(const void* q, const void* k, const void* v, const v
                             const lla_options* opts, void* stream);
 
 /*
+ * Rotary positions. A spec says how far a position turns each of rot/2 pairs of a head's first `rot`
+ * features: pair i is (i, i + rot/2) (LLA_ROTARY_HALVES) or (2i, 2i + 1) (LLA_ROTARY_INTERLEAVED) and at
+ * position pos becomes scale * (x0 cos a - x1 sin a, x0 sin a + x1 cos a), a = pos * freq[i]. The other
+ * features are copied. (The probe of Parallax meets the keys like a query and is rotated like one.) Angles are exact: pos * freq[i] is
+ * taken modulo a turn before it is rounded, so far positions lose nothing. rot is even, 2 .. d; |freq| <=
+ * 2^20; specs are host memory, read during the call.
+ */
+typedef enum { LLA_ROTARY_HALVES = 0, LLA_ROTARY_INTERLEAVED = 1 } lla_rotary_layout;
+typedef struct lla_rotary_spec {
+  double freq[64];  /* radians per position of pair i */
+  float scale;      /* on the rotated features */
+  int rot;
+  int layout;       /* lla_rotary_layout */
+  int reserved[3];  /* must be zero */
+} lla_rotary_spec;
+
+/*
+ * Fills a spec: freq[i] = base^(-2i/rot) (base >= 1), scale 1, stretched for contexts `factor` (>= 1) times longer by
+ *   LLA_STRETCH_POSITIONS    freq / factor (positions interpolated),
+ *   LLA_STRETCH_BASE         base * factor^(rot / (rot - 2)): the slowest pair as above, the fastest as it was,
+ *   LLA_STRETCH_WAVELENGTHS  by the turns n that a pair makes over the `context` positions of training: with
+ *                            keep = clamp((n - slow) / (fast - slow), 0, 1), freq * (keep + (1 - keep) / factor),
+ *                            and scale = 0.1 ln(factor) + 1,
+ * or not at all (LLA_STRETCH_NONE; factor is not used). Any other table of frequencies goes into the struct
+ * directly. Host only; LLA_ERR_INVALID_ARG leaves the spec as it was.
+ */
+typedef enum {
+  LLA_STRETCH_NONE = 0,
+  LLA_STRETCH_POSITIONS = 1,
+  LLA_STRETCH_BASE = 2,
+  LLA_STRETCH_WAVELENGTHS = 3
+} lla_rotary_stretch;
+int lla_rotary_frequencies(lla_rotary_spec* spec, int rot, int layout, double base, int stretch, double factor,
+                           int context, double slow, double fast);
+
+/*
+ * Rotates `count` (1 .. 3) tensors that share their positions, such as q, k and r of an attention: x[i] is
+ * [B, heads[i], T, d], y[i] the same (x[i] == y[i]: in place; otherwise none may overlap another), x, y and
+ * heads host arrays. positions [B, T] (device) or NULL: 0 .. T-1. backward nonzero: the gradient with respect
+ * to the input from that with respect to the output, which is the transposed rotation times scale. d in {16, 32, 64,
+ * 128}; fewer than 2^31 rows in all. One launch, asynchronous, allocates nothing; fp32 arithmetic, one rounding.
+ */
+int lla_rotary(const lla_rotary_spec* spec, const void* const* x, void* const* y, const int* heads, int count,
+               const int* positions, int B, int T, int d, int backward, int dtype, void* stream);
+
+/*
  * Decode: one query per head against a key/value cache of L positions that the query attends to
  * in full (it is the newest token; its own key and value are already appended). The output is
  * what lla_forward returns for its last row, o = vbar + C_vk (C_kk + lambda I)^-1 (q - kbar) with
@@ -400,6 +446,17 @@ int lla_paged_append(const lla_paged_cache* cache, const void* k_new, const void
                      const int* starts, int tokens, void* stream);
 
 /*
+ * lla_paged_append with rotary positions: k_new is written rotated, and the same tokens' queries q and probe r
+ * ([tokens, q_heads, d] or NULL; r needs q) come out rotated in q_out and r_out (which may be q and r; no other overlap). The
+ * token's position is that of its sequence's first new token's slot plus offsets[token] (device memory,
+ * [tokens]; NULL: its index among the sequence's new tokens, so its own slot's): the depth of a drafted
+ * node, and, where eviction has dropped positions, their number besides. Rows of q_out and r_out that no sequence covers are not written.
+ */
+int lla_paged_append_rotary(const lla_paged_cache* cache, const lla_rotary_spec* spec, const void* k_new,
+                            const void* v_new, const void* q, const void* r, void* q_out, void* r_out, int q_heads,
+                            const int* offsets, const int* starts, int tokens, void* stream);
+
+/*
  * The queries of one lla_paged_attention call.
  *   q, r, out   [tokens, q_heads, d], the same (NULL: softmax attention), [tokens, q_heads, dv],
  *               of the cache's type. q_heads is a multiple of kv_heads: query heads hk*g ..
@@ -471,6 +528,62 @@ int lla_paged_tree_attention(const lla_paged_cache* cache, const lla_paged_query
  */
 int lla_paged_evict(const lla_paged_cache* from, const lla_paged_cache* to, int budget, int sinks,
                     int recent, int* kept, void* stream);
+
+/*
+ * Sharing, growing and releasing pages. refs [num_pages] (device memory, 16-byte aligned, the caller's, zero at
+ * first) counts the table entries that hold each page: sequence b holds the first ceil(lens[b] / page_size)
+ * entries of its row, and a page is free while refs is 0. Sequences that fork share all their pages; one
+ * that grows takes its own copy of a last page that it would write to while others hold it. Fork, free and
+ * grow touch tables, lens and refs alone, which the caches of a model's layers share: they are called once,
+ * lla_paged_copy and lla_paged_compact once per layer. None of them allocates or synchronises, and all give
+ * the same pages whatever the scheduling. Impossible lengths, page numbers, parents and paths are reported in the
+ * status word (LLA_ERR_INVALID_ARG); that sequence or pair is left as it is.
+ *
+ * lla_paged_fork: sequence c of `to` becomes a copy of sequence parents[c] of `from` (-1: an empty one): its table
+ * entries and length, the pages' refs one more each. `to` is another table and lens over the same pages (what
+ * it held before is not released), with room for the lengths. A parent out of range, or one that does not
+ * fit, gives an empty sequence.
+ */
+int lla_paged_fork(const lla_paged_cache* from, const lla_paged_cache* to, const int* parents, int* refs, void* stream);
+
+/*
+ * Shortens each sequence to its first keep[b] positions (keep NULL or negative: to none; more than it has: as
+ * it is) and gives up the pages behind them: refs one less each. A page that nobody held is reported.
+ */
+int lla_paged_free(const lla_paged_cache* cache, const int* keep, int* refs, void* stream);
+
+/*
+ * Makes room for the new tokens of `starts` (as in lla_paged_append, which may follow): lens[b] grows by
+ * starts[b+1] - starts[b], and the table gets the pages for that, the lowest free ones first, in the order of
+ * the sequences. Where the first new position falls into a page that others hold too, the lowest free page
+ * takes that page's place in the table before any other, and copies[b] = (old page, new page) is to be made by
+ * lla_paged_copy for each layer; elsewhere copies[b] = (-1, -1). Among sequences that share such a page and
+ * all grow, the last keeps it if nobody else holds it. copies: [num_seqs][2], 8-byte aligned.
+ * *left (device memory): free pages afterwards. Negative: so many were missing, and nothing has changed but
+ * copies, which is all -1; lens then does not count the new tokens, so they may not be appended.
+ * At most 4096 sequences (LLA_ERR_UNSUPPORTED).
+ */
+int lla_paged_grow(const lla_paged_cache* cache, const int* starts, int* refs, int* copies, int* left, void* stream);
+
+/*
+ * Copies whole pages, keys, values and (where both caches have it) mass: page pairs[i][0] of `from` to page
+ * pairs[i][1] of `to`, count pairs in device memory, 8-byte aligned; a pair with a negative number is skipped. The caches (which may be
+ * one) agree in kv_heads, page_size, d, dv and type; tables and lens are not used. No page may be written
+ * twice, or written and read, in one call.
+ */
+int lla_paged_copy(const lla_paged_cache* from, const lla_paged_cache* to, const int* pairs, int count, void* stream);
+
+/*
+ * Keeps one path of each drafted tree (or any selection of new tokens): path[b][0 ..] are the indices, rising, of the
+ * kept ones among sequence b's new tokens, ended by -1 where there are fewer than max_path. Their keys,
+ * values and mass move to the slots first, first + 1, .. (first = lens[b] - number of new tokens), and keep[b] =
+ * first + their number is what lla_paged_free is then given, once all layers are done: lens and table stay as
+ * they are here. A path that does not rise or leaves the new tokens is reported and nothing of it kept. The
+ * moved positions' pages must be the sequence's own (as after lla_paged_grow). tokens: of the batch, as in
+ * lla_paged_append.
+ */
+int lla_paged_compact(const lla_paged_cache* cache, const int* starts, int tokens, const int* path, int max_path, int* keep,
+                      void* stream);
 
 #ifdef __cplusplus
 }

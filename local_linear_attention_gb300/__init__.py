@@ -13,6 +13,9 @@ _BINDING = {
     "lla_parallax_forward", "lla_decode", "lla_parallax_decode", "lla_parallax_backward",
     "Options", "PagedCache", "lla_paged_append", "lla_paged_attention", "lla_paged_workspace_size",
     "lla_paged_evict", "lla_paged_tree_attention", "lla_paged_tree_workspace_size",
+    "RotarySpec", "ROTARY_HALVES", "ROTARY_INTERLEAVED", "STRETCH_NONE", "STRETCH_POSITIONS", "STRETCH_BASE",
+    "STRETCH_WAVELENGTHS", "lla_rotary", "lla_paged_append_rotary", "lla_paged_fork", "lla_paged_free", "lla_paged_grow",
+    "lla_paged_copy", "lla_paged_compact",
 }
 
 

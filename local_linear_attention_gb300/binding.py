@@ -6,6 +6,7 @@ fallback: if the library is missing or the tensors are not on a CUDA device the 
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import struct
@@ -21,6 +22,9 @@ __all__ = [
     "FORM_CENTRED", "FORM_PAGE", "FAULT_WITHHOLD_KEYS", "lla_parallax_backward", "Options",
     "PagedCache", "lla_paged_append", "lla_paged_attention", "lla_paged_workspace_size",
     "lla_paged_evict", "lla_paged_tree_attention", "lla_paged_tree_workspace_size",
+    "RotarySpec", "ROTARY_HALVES", "ROTARY_INTERLEAVED", "STRETCH_NONE", "STRETCH_POSITIONS", "STRETCH_BASE",
+    "STRETCH_WAVELENGTHS", "lla_rotary", "lla_paged_append_rotary", "lla_paged_fork", "lla_paged_free", "lla_paged_grow",
+    "lla_paged_copy", "lla_paged_compact",
 ]
 
 LLA_OK = 0
@@ -37,6 +41,8 @@ EXPORTED_SYMBOLS = (
     "lla_parallax_forward_ex", "lla_decode_ex", "lla_parallax_decode_ex",
     "lla_parallax_backward_ex", "lla_paged_append", "lla_paged_workspace_size",
     "lla_paged_attention", "lla_paged_evict", "lla_paged_tree_workspace_size", "lla_paged_tree_attention",
+    "lla_rotary_frequencies", "lla_rotary", "lla_paged_append_rotary", "lla_paged_fork", "lla_paged_free", "lla_paged_grow",
+    "lla_paged_copy", "lla_paged_compact",
 )
 
 # LLA_NOALLOC_SCRATCH_BYTES in include/lla.h: the fixed scratch of lla_forward_noalloc.
@@ -47,6 +53,8 @@ _lib = None
 PATH_AUTO, PATH_CUDA_CORE, PATH_TENSOR_CORE, PATH_CG = 0, 1, 2, 3
 FORM_CENTRED, FORM_PAGE = 0, 1
 FAULT_WITHHOLD_KEYS = 1
+ROTARY_HALVES, ROTARY_INTERLEAVED = 0, 1
+STRETCH_NONE, STRETCH_POSITIONS, STRETCH_BASE, STRETCH_WAVELENGTHS = 0, 1, 2, 3
 
 
 class Options(ctypes.Structure):
@@ -60,6 +68,7 @@ class Options(ctypes.Structure):
 # once per layer, and struct.pack takes a third of the time of a ctypes.Structure.
 _CACHE = struct.Struct("@5P10i")
 _QUERY = struct.Struct("@5P3if6i")
+_SPEC = struct.Struct("@64df5i")  # lla_rotary_spec
 
 
 def _options(path=0, form=0, cg=None, test_fault=0):
@@ -94,6 +103,7 @@ def _load():
                           "`python -m local_linear_attention_gb300.build`")
     lib = ctypes.CDLL(path)
     vp, i, f, sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_size_t
+    dbl = ctypes.c_double
     fp = ctypes.POINTER(ctypes.c_float)
     op = ctypes.POINTER(Options)
     sig = {
@@ -124,6 +134,14 @@ def _load():
         "lla_paged_evict": (i, [vp, vp, i, i, i, vp, vp]),
         "lla_paged_tree_workspace_size": (sz, [vp, vp]),
         "lla_paged_tree_attention": (i, [vp, vp, vp, vp, sz, vp]),
+        "lla_rotary_frequencies": (i, [vp, i, i, dbl, i, dbl, i, dbl, dbl]),
+        "lla_rotary": (i, [vp, vp, vp, vp, i, vp, i, i, i, i, i, vp]),
+        "lla_paged_append_rotary": (i, [vp] * 8 + [i, vp, vp, i, vp]),
+        "lla_paged_fork": (i, [vp, vp, vp, vp, vp]),
+        "lla_paged_free": (i, [vp, vp, vp, vp]),
+        "lla_paged_grow": (i, [vp, vp, vp, vp, vp, vp]),
+        "lla_paged_copy": (i, [vp, vp, vp, i, vp]),
+        "lla_paged_compact": (i, [vp, vp, i, vp, i, vp, vp]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -366,6 +384,89 @@ def lla_moments(q, k, v, idx, h: float, stream=None):
     return res
 
 
+class RotarySpec:
+    """How positions rotate the first `rot` features of a head (lla_rotary_spec): pairs (i, i + rot/2)
+    (ROTARY_HALVES) or (2i, 2i + 1) (ROTARY_INTERLEAVED) by pos * freq[i] radians, times scale. freq is
+    base^(-2i/rot), stretched for contexts `factor` times longer as lla_rotary_frequencies describes
+    (STRETCH_*; `context`, `slow` and `fast` belong to STRETCH_WAVELENGTHS), or given, rot/2 numbers."""
+
+    __slots__ = ("rot", "layout", "scale", "freq", "_packed")
+
+    def __init__(self, rot, layout=ROTARY_HALVES, base=10000.0, stretch=STRETCH_NONE, factor=1.0, context=0, slow=1.0,
+                 fast=32.0, scale=None, freq=None):
+        if freq is None:
+            buf = ctypes.create_string_buffer(_SPEC.size)
+            _check(_load().lla_rotary_frequencies(buf, rot, layout, base, stretch, factor, context, slow, fast),
+                   "lla_rotary_frequencies")
+            values = _SPEC.unpack(buf.raw)
+            freq, scale = values[:rot // 2], values[64] if scale is None else scale
+        else:
+            freq, scale = tuple(float(x) for x in freq), 1.0 if scale is None else scale
+            if len(freq) != rot // 2 or len(freq) > 64:
+                raise ValueError("freq must have rot/2 numbers, at most 64")
+        self.rot, self.layout, self.freq, self.scale = rot, layout, tuple(freq), float(scale)
+        self._packed = _SPEC.pack(*freq, *[0.0] * (64 - len(freq)), scale, rot, layout, 0, 0, 0)
+
+
+def _stream_on(index, device, stream):
+    """The raw handle of a call's stream (None: the current one) and what to allocate its outputs under."""
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(index), contextlib.nullcontext()
+    if getattr(stream, "device_index", index) != index:
+        raise ValueError(f"the stream must be one of {device}, where the tensors are")
+    raw = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(raw, device=device) if raw else torch.cuda.default_stream(device)
+    return raw, torch.cuda.stream(stream)
+
+
+def lla_rotary(x, spec: RotarySpec, positions=None, backward=False, out=None, stream=None):
+    """Rotates x, a tensor [B, H, T, d] or up to three of them that share B, T and d (q, k and the probe of an
+    attention, with any numbers of heads), by their positions [B, T] int32 (None: 0 .. T-1); returns the
+    same. backward: the gradients with respect to x from those with respect to the result. out may be x."""
+    single = isinstance(x, torch.Tensor)
+    xs = (x,) if single else tuple(x)
+    if not 1 <= len(xs) <= 3:
+        raise ValueError("one to three tensors")
+    first = xs[0]
+    index = first.get_device()
+    if index < 0:
+        raise ValueError("liblla runs on CUDA tensors only")
+    code = DTYPE_CODES.get(first.dtype)
+    if code is None:
+        raise ValueError("dtype must be float32 or bfloat16")
+    if len(first.shape) != 4:
+        raise ValueError("expected x [B, H, T, d]")
+    B, _, T, d = first.shape
+    heads = []
+    for t in xs:
+        s = t.shape
+        if len(s) != 4 or (s[0], s[2], s[3]) != (B, T, d) or t.dtype != first.dtype or t.get_device() != index or \
+                not t.is_contiguous():
+            raise ValueError("the tensors must be contiguous [B, H, T, d] of one dtype, on one device, alike but for H")
+        heads.append(s[1])
+    if positions is not None and (positions.dtype != torch.int32 or positions.shape != (B, T) or
+                                  positions.get_device() != index or not positions.is_contiguous()):
+        raise ValueError("positions must be a contiguous int32 [B, T] tensor on the device of x")
+    raw, on = _stream_on(index, first.device, stream)
+    if out is None:
+        with on:
+            outs = tuple(torch.empty_like(t) for t in xs)
+    else:
+        outs = (out,) if isinstance(out, torch.Tensor) else tuple(out)
+        if len(outs) != len(xs) or any(o.shape != t.shape or o.dtype != t.dtype or o.get_device() != index or
+                                       not o.is_contiguous() for o, t in zip(outs, xs)):
+            raise ValueError("out must be like x")
+    n = len(xs)
+    args = (spec._packed, struct.pack(f"@{n}P", *[t.data_ptr() for t in xs]),
+            struct.pack(f"@{n}P", *[t.data_ptr() for t in outs]), struct.pack(f"@{n}i", *heads), n,
+            None if positions is None else positions.data_ptr(), B, T, d, 1 if backward else 0, code, raw)
+    with torch.cuda.device(index):
+        st = _load().lla_rotary(*args)
+    _check(st, "lla_rotary")
+    return outs[0] if single else list(outs)
+
+
 class PagedCache:
     """A paged key/value cache (lla_paged_cache): k_pages [num_pages, kv_heads, page_size, d],
     v_pages [num_pages, kv_heads, page_size, dv], page_table [num_seqs, max_pages] int32, lens
@@ -459,6 +560,42 @@ def lla_paged_append(k, v, cache: PagedCache, starts, stream=None):
     _paged_rows("v", v, cache, (tokens, cache.kv_heads, cache.dv))
     _paged_starts(starts, cache)
     _paged_call(_load().lla_paged_append, cache, stream, cache._packed, k.data_ptr(), v.data_ptr(), starts.data_ptr(), tokens)
+
+
+def lla_paged_append_rotary(k, v, cache: PagedCache, starts, spec: RotarySpec, q=None, r=None, offsets=None, q_out=None,
+                            r_out=None, stream=None):
+    """lla_paged_append with the keys rotated, and the queries q [tokens, q_heads, d] and probe r (like q) of
+    the same tokens; returns (q_out, r_out), None where there is none. A token's position is that of its
+    sequence's first new token's slot plus offsets [tokens] int32 (None: its own slot's). q_out may be q."""
+    tokens = k.shape[0]
+    _paged_rows("k", k, cache, (tokens, cache.kv_heads, cache.d))
+    _paged_rows("v", v, cache, (tokens, cache.kv_heads, cache.dv))
+    _paged_starts(starts, cache)
+    if offsets is not None and (offsets.dtype != torch.int32 or offsets.shape != (tokens,) or
+                                offsets.get_device() != cache._index or not offsets.is_contiguous()):
+        raise ValueError("offsets must be a contiguous int32 [tokens] tensor on the cache's device")
+    if q is None and (r is not None or q_out is not None) or r is None and r_out is not None:
+        raise ValueError("r comes with q, and outputs with their inputs")
+    outs = []
+    for name, x, y in (("q", q, q_out), ("r", r, r_out)):
+        if x is not None:
+            if len(q.shape) != 3:
+                raise ValueError("expected q [tokens, q_heads, d]")
+            _paged_rows(name, x, cache, (tokens, q.shape[1], cache.d))
+            if y is None:
+                if stream is None:
+                    y = torch.empty_like(x)
+                else:
+                    with _on_stream(cache, stream):
+                        y = x.new_empty(x.shape)
+            else:
+                _paged_rows(name + "_out", y, cache, x.shape)
+        outs.append(y)
+    ptr = lambda x: None if x is None else x.data_ptr()  # noqa: E731
+    _paged_call(_load().lla_paged_append_rotary, cache, stream, cache._packed, spec._packed, k.data_ptr(), v.data_ptr(),
+                ptr(q), ptr(r), ptr(outs[0]), ptr(outs[1]), 0 if q is None else q.shape[1], ptr(offsets),
+                starts.data_ptr(), tokens)
+    return tuple(outs)
 
 
 def _paged_query(q, cache, starts, h, r, max_new, window, sinks, track_mass, out, lse, path):
@@ -581,6 +718,88 @@ def lla_paged_evict(cache: PagedCache, to: PagedCache, budget: int, sinks=0, rec
         raise ValueError(f"kept must be a contiguous int32 tensor of shape {shape}")
     _paged_call(_load().lla_paged_evict, cache, stream, cache._packed, to._packed, budget, sinks, recent, kept.data_ptr())
     return kept
+
+
+def _paged_ints(name, x, cache, shape):
+    if x.dtype != torch.int32 or x.shape != shape or x.get_device() != cache._index or not x.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous int32 tensor of shape {tuple(shape)} on the cache's device")
+
+
+def _paged_new(cache, stream, *shapes):
+    """Integer outputs that a call allocates, which belong to its stream."""
+    if stream is None:
+        return [torch.empty(s, dtype=torch.int32, device=cache.device) for s in shapes]
+    with _on_stream(cache, stream):
+        return [torch.empty(s, dtype=torch.int32, device=cache.device) for s in shapes]
+
+
+def lla_paged_fork(cache: PagedCache, to: PagedCache, parents, refs, stream=None):
+    """Sequence c of `to` (another table and lens over the same pages) becomes a copy of sequence parents[c] of
+    `cache` (int32; -1: an empty one) that shares its pages; refs [num_pages] int32 counts the table entries that
+    hold each page."""
+    if cache._index != to._index:
+        raise ValueError("the caches must be on one device")
+    _paged_ints("parents", parents, to, (to.num_seqs,))
+    _paged_ints("refs", refs, cache, cache.k_pages.shape[:1])
+    _paged_call(_load().lla_paged_fork, cache, stream, cache._packed, to._packed, parents.data_ptr(), refs.data_ptr())
+
+
+def lla_paged_free(cache: PagedCache, refs, keep=None, stream=None):
+    """Shortens every sequence to its first keep[b] positions (int32; None: to none) and releases the pages
+    behind them."""
+    _paged_ints("refs", refs, cache, cache.k_pages.shape[:1])
+    if keep is not None:
+        _paged_ints("keep", keep, cache, (cache.num_seqs,))
+    _paged_call(_load().lla_paged_free, cache, stream, cache._packed, None if keep is None else keep.data_ptr(),
+                refs.data_ptr())
+
+
+def lla_paged_grow(cache: PagedCache, starts, refs, copies=None, left=None, stream=None):
+    """Room for the new tokens of `starts`: cache.lens grows by them and the table gets the lowest free pages.
+    Returns (copies [num_seqs, 2], left [1]), int32: the pages (old, new) that lla_paged_copy has to copy in
+    each layer because others hold the old one too (-1: none), and how many pages are free afterwards. left
+    below zero: so many were missing and nothing has changed."""
+    _paged_starts(starts, cache)
+    _paged_ints("refs", refs, cache, cache.k_pages.shape[:1])
+    if copies is not None:
+        _paged_ints("copies", copies, cache, (cache.num_seqs, 2))
+    if left is not None:
+        _paged_ints("left", left, cache, (1,))
+    if copies is None:
+        copies, = _paged_new(cache, stream, (cache.num_seqs, 2))
+    if left is None:
+        left, = _paged_new(cache, stream, (1,))
+    _paged_call(_load().lla_paged_grow, cache, stream, cache._packed, starts.data_ptr(), refs.data_ptr(),
+                copies.data_ptr(), left.data_ptr())
+    return copies, left
+
+
+def lla_paged_copy(cache: PagedCache, to: PagedCache, pairs, stream=None):
+    """Copies page pairs[i, 0] of `cache` to page pairs[i, 1] of `to` (keys, values, and mass where both have
+    it); pairs [n, 2] int32, negative numbers: skipped. Both may be one cache."""
+    if cache._index != to._index:
+        raise ValueError("the caches must be on one device")
+    count = pairs.shape[0]
+    _paged_ints("pairs", pairs, cache, (count, 2))
+    _paged_call(_load().lla_paged_copy, cache, stream, cache._packed, to._packed, pairs.data_ptr(), count)
+
+
+def lla_paged_compact(cache: PagedCache, starts, path, tokens=None, keep=None, stream=None):
+    """Keeps one path of each sequence's new tokens: path [num_seqs, max_path] int32, rising indices among
+    them, -1 past the last. They move to the front of the new tokens' slots; returns keep [num_seqs]
+    int32, the lengths to give to lla_paged_free once all layers are done. tokens: a bound of the batch's
+    (default: none)."""
+    _paged_starts(starts, cache)
+    if len(path.shape) != 2:
+        raise ValueError("path must be [num_seqs, max_path]")
+    _paged_ints("path", path, cache, (cache.num_seqs, path.shape[1]))
+    if keep is not None:
+        _paged_ints("keep", keep, cache, (cache.num_seqs,))
+    else:
+        keep, = _paged_new(cache, stream, (cache.num_seqs,))
+    _paged_call(_load().lla_paged_compact, cache, stream, cache._packed, starts.data_ptr(),
+                (1 << 30) - 1 if tokens is None else tokens, path.data_ptr(), path.shape[1], keep.data_ptr())
+    return keep
 
 
 def lla_stream_status(stream=None) -> int:

@@ -14,6 +14,9 @@
 #include "lla_internal.cuh"
 
 namespace lla {
+namespace rotary {
+struct Turn;
+}
 namespace paged {
 
 constexpr int kNoWindow = 1 << 30;  // lengths stay below this (checked on the host)
@@ -455,6 +458,17 @@ constexpr int kMaxNodes = 1024;
 cudaError_t launch_tree(const Params& p, uint32_t* bits, int* depth, int max_nodes, cudaStream_t s);
 cudaError_t launch_append(const Params& p, const void* k_new, const void* v_new, int d, int dv,
                           int dtype, cudaStream_t s);
+cudaError_t launch_append_rotary(const Params& p, const rotary::Turn& turn, int layout, const void* k, const void* v,
+                                 const void* q, const void* r, void* q_out, void* r_out, int q_heads,
+                                 const int* offsets, int dtype, cudaStream_t s);
+// `p` is the cache forked from; table, lens, num_seqs and max_pages the new sequences'.
+cudaError_t launch_fork(const Params& p, const int* parents, int* table, int* lens, int num_seqs, int max_pages, int* refs,
+                        cudaStream_t s);
+cudaError_t launch_free(const Params& p, const int* keep, int* lens, int* refs, cudaStream_t s);
+constexpr int kMaxGrow = 4096;  // sequences that grow in one call
+cudaError_t launch_grow(const Params& p, int* table, int* lens, int* refs, int* copies, int* left, cudaStream_t s);
+cudaError_t launch_copy(const Params& from, const Params& to, const int* pairs, int count, int dtype, cudaStream_t s);
+cudaError_t launch_compact(const Params& p, const int* path, int max_path, int* keep, int dtype, cudaStream_t s);
 // `p` is the source cache; the other arguments the destination and the choice.
 cudaError_t launch_evict(const Params& p, void* k, void* v, float* mass, const int* table, int* lens,
                          int max_pages, int num_pages, int budget, int sinks, int recent, int* kept,

@@ -2,6 +2,7 @@
 #include <cmath>
 
 #include "lla_paged.cuh"
+#include "lla_rotary.cuh"
 #include "lla_smem_limits.h"
 
 namespace lla {
@@ -355,6 +356,12 @@ int run_attention(const lla_paged_cache* c, const lla_paged_query* a, const int*
   return LLA_OK;
 }
 
+// Whether pages of one cache fit the other.
+bool same_pages(const lla_paged_cache* a, const lla_paged_cache* b) {
+  return a->kv_heads == b->kv_heads && a->page_size == b->page_size && a->d == b->d && a->dv == b->dv &&
+         a->dtype == b->dtype;
+}
+
 // A tree's nodes are new tokens of which most will not stay, so their weights are not counted.
 int check_tree_query(const lla_paged_cache* c, const lla_paged_query* a) {
   const int st = check_query(c, a);
@@ -417,6 +424,35 @@ int lla_paged_append(const lla_paged_cache* cache, const void* k_new, const void
              : LLA_ERR_CUDA;
 }
 
+int lla_paged_append_rotary(const lla_paged_cache* cache, const lla_rotary_spec* spec, const void* k_new,
+                            const void* v_new, const void* q, const void* r, void* q_out, void* r_out, int q_heads,
+                            const int* offsets, const int* starts, int tokens, void* stream) {
+  int st = check_cache_shape(cache);
+  if (st != LLA_OK) return st;
+  rotary::Turn turn;
+  st = rotary::make_turn(spec, cache->d, false, &turn);
+  if (st != LLA_OK) return st;
+  if (tokens < 0 || (r && !q) || (q && q_heads <= 0)) return LLA_ERR_INVALID_ARG;
+  if ((long long)tokens * cache->kv_heads >= (1LL << 31) || tokens >= kNoWindow ||
+      (q && (long long)tokens * q_heads >= (1LL << 31)))
+    return LLA_ERR_UNSUPPORTED;
+  if (tokens == 0 || cache->num_seqs == 0) return LLA_OK;
+  st = check_cache_pointers(cache, false);
+  if (st != LLA_OK) return st;
+  if (!k_new || !v_new || !starts || !aligned16(k_new) || !aligned16(v_new) || !aligned16(q) || !aligned16(r))
+    return LLA_ERR_INVALID_ARG;
+  if ((q && (!q_out || !aligned16(q_out))) || (r && (!r_out || !aligned16(r_out)))) return LLA_ERR_INVALID_ARG;
+  if (r && (q_out == r_out || q_out == r || r_out == q)) return LLA_ERR_INVALID_ARG;
+  Params p = cache_params(cache);
+  if (device_status(&p.status) != cudaSuccess) return LLA_ERR_CUDA;
+  p.starts = starts;
+  p.tokens = tokens;
+  return launch_append_rotary(p, turn, spec->layout, k_new, v_new, q, r, q_out, r_out, q_heads, offsets, cache->dtype,
+                              static_cast<cudaStream_t>(stream)) == cudaSuccess
+             ? LLA_OK
+             : LLA_ERR_CUDA;
+}
+
 size_t lla_paged_workspace_size(const lla_paged_cache* cache, const lla_paged_query* query) {
   if (check_query(cache, query) != LLA_OK) return 0;
   if (query->tokens == 0 || cache->num_seqs == 0) return 0;
@@ -468,6 +504,91 @@ int lla_paged_evict(const lla_paged_cache* from, const lla_paged_cache* to, int 
   return launch_evict(p, to->k_pages, to->v_pages, to->mass, to->page_table, to->lens, to->max_pages,
                       to->num_pages, budget, sinks, recent, kept, from->d, from->dv, from->dtype,
                       static_cast<cudaStream_t>(stream)) == cudaSuccess
+             ? LLA_OK
+             : LLA_ERR_CUDA;
+}
+
+int lla_paged_fork(const lla_paged_cache* from, const lla_paged_cache* to, const int* parents, int* refs, void* stream) {
+  int st = check_cache_shape(from);
+  if (st == LLA_OK) st = check_cache_shape(to);
+  if (st != LLA_OK) return st;
+  if (!same_pages(from, to) || to->k_pages != from->k_pages || to->v_pages != from->v_pages ||
+      to->num_pages != from->num_pages)
+    return LLA_ERR_INVALID_ARG;
+  if (to->num_seqs == 0) return LLA_OK;
+  st = check_cache_pointers(to, false);
+  if (st == LLA_OK && from->num_seqs > 0) st = check_cache_pointers(from, false);
+  if (st != LLA_OK) return st;
+  if (!parents || !refs || !aligned16(refs) || from->lens == to->lens || from->page_table == to->page_table)
+    return LLA_ERR_INVALID_ARG;
+  Params p = cache_params(from);
+  if (device_status(&p.status) != cudaSuccess) return LLA_ERR_CUDA;
+  return launch_fork(p, parents, const_cast<int*>(to->page_table), to->lens, to->num_seqs, to->max_pages, refs,
+                     static_cast<cudaStream_t>(stream)) == cudaSuccess
+             ? LLA_OK
+             : LLA_ERR_CUDA;
+}
+
+int lla_paged_free(const lla_paged_cache* cache, const int* keep, int* refs, void* stream) {
+  int st = check_cache_shape(cache);
+  if (st != LLA_OK) return st;
+  if (cache->num_seqs == 0) return LLA_OK;
+  st = check_cache_pointers(cache, false);
+  if (st != LLA_OK) return st;
+  if (!refs || !aligned16(refs)) return LLA_ERR_INVALID_ARG;
+  Params p = cache_params(cache);
+  if (device_status(&p.status) != cudaSuccess) return LLA_ERR_CUDA;
+  return launch_free(p, keep, cache->lens, refs, static_cast<cudaStream_t>(stream)) == cudaSuccess ? LLA_OK : LLA_ERR_CUDA;
+}
+
+int lla_paged_grow(const lla_paged_cache* cache, const int* starts, int* refs, int* copies, int* left, void* stream) {
+  int st = check_cache_shape(cache);
+  if (st != LLA_OK) return st;
+  if (cache->num_seqs > kMaxGrow) return LLA_ERR_UNSUPPORTED;
+  if (cache->num_seqs > 0) st = check_cache_pointers(cache, false);
+  if (st != LLA_OK) return st;
+  if (!refs || !aligned16(refs) || !left) return LLA_ERR_INVALID_ARG;
+  if (cache->num_seqs > 0 && (!starts || !copies || (reinterpret_cast<uintptr_t>(copies) & 7u))) return LLA_ERR_INVALID_ARG;
+  Params p = cache_params(cache);
+  if (device_status(&p.status) != cudaSuccess) return LLA_ERR_CUDA;
+  p.starts = starts;
+  return launch_grow(p, const_cast<int*>(cache->page_table), cache->lens, refs, copies, left,
+                     static_cast<cudaStream_t>(stream)) == cudaSuccess
+             ? LLA_OK
+             : LLA_ERR_CUDA;
+}
+
+int lla_paged_copy(const lla_paged_cache* from, const lla_paged_cache* to, const int* pairs, int count, void* stream) {
+  int st = check_cache_shape(from);
+  if (st == LLA_OK) st = check_cache_shape(to);
+  if (st != LLA_OK) return st;
+  if (!same_pages(from, to) || count < 0) return LLA_ERR_INVALID_ARG;
+  if (count == 0) return LLA_OK;
+  if (!from->k_pages || !from->v_pages || !to->k_pages || !to->v_pages || !aligned16(from->k_pages) ||
+      !aligned16(from->v_pages) || !aligned16(to->k_pages) || !aligned16(to->v_pages) || !aligned16(from->mass) ||
+      !aligned16(to->mass) || !pairs || (reinterpret_cast<uintptr_t>(pairs) & 7u))
+    return LLA_ERR_INVALID_ARG;
+  Params p = cache_params(from), t = cache_params(to);
+  if (device_status(&p.status) != cudaSuccess) return LLA_ERR_CUDA;
+  return launch_copy(p, t, pairs, count, from->dtype, static_cast<cudaStream_t>(stream)) == cudaSuccess ? LLA_OK
+                                                                                                       : LLA_ERR_CUDA;
+}
+
+int lla_paged_compact(const lla_paged_cache* cache, const int* starts, int tokens, const int* path, int max_path, int* keep,
+                      void* stream) {
+  int st = check_cache_shape(cache);
+  if (st != LLA_OK) return st;
+  if (tokens < 0 || max_path < 0) return LLA_ERR_INVALID_ARG;
+  if (tokens >= kNoWindow) return LLA_ERR_UNSUPPORTED;
+  if (cache->num_seqs == 0) return LLA_OK;
+  st = check_cache_pointers(cache, false);
+  if (st != LLA_OK) return st;
+  if (!aligned16(cache->mass) || !starts || !keep || (max_path > 0 && !path)) return LLA_ERR_INVALID_ARG;
+  Params p = cache_params(cache);
+  if (device_status(&p.status) != cudaSuccess) return LLA_ERR_CUDA;
+  p.starts = starts;
+  p.tokens = tokens;
+  return launch_compact(p, path, max_path, keep, cache->dtype, static_cast<cudaStream_t>(stream)) == cudaSuccess
              ? LLA_OK
              : LLA_ERR_CUDA;
 }
