@@ -60,6 +60,7 @@ struct Params {
   const uint32_t* bits;  // [tokens][words]: which nodes a node sees
   const int* depth;      // [tokens]
   int words;
+  int row_tiles;         // few rows: tiles of a sequence's rows
 };
 
 struct Seq {
@@ -433,6 +434,7 @@ inline int padded(int d) { return d > 64 ? 128 : 64; }
 constexpr int kRowsCluster = 8;  // splits that join within a cluster (the portable size)
 inline int rows_limit(bool probe) { return probe ? 8 : 16; }
 cudaError_t launch_attend_rows(const Params& p, int D, cudaStream_t s);
+constexpr int kRowsNodes = 64;  // of a tree, whose rows may be several tiles of rows_limit
 // fp32: the attention of every sequence in tiles of kF32Rows rows, at most f32_tiles a key/value head;
 // the weight tracking of the sequences of at most p.row_cap rows, whose logits are in p.logits.
 constexpr int kF32Rows = 16, kF32MassRows = 256;

@@ -159,7 +159,16 @@ Plan make_plan(const lla_paged_cache* c, const lla_paged_query* a, bool tree) {
   const long long rows = max_new * g, pairs = (long long)c->num_seqs * c->kv_heads;
   const bool tc = c->dtype == LLA_BF16 && a->path != LLA_PATH_CUDA_CORE;
   pl.D = padded(c->d > c->dv ? c->d : c->dv);
-  const int limit = c->dtype == LLA_F32 ? kF32Rows : rows_limit(a->r != nullptr);
+  int limit = c->dtype == LLA_F32 ? kF32Rows : rows_limit(a->r != nullptr);
+  const long long pairs_keys = pairs * keys;
+  if (tree && tc) {
+    // The few-rows kernel goes over the keys again for every 16 rows (8 with a probe) and the tiled one once for
+    // 128, but starts up in 7 to 10 us against 20 to 35. 8 heads, rows: few-rows / tiled us. 64, 24: 7.5 / 21 at
+    // 1000 positions, 18 / 25 at 16000, 88 / 77 at 16 x 8000; 64 rows: 8 / 21, 31 / 27, 138 / 82. Probe, 24: 8 / 32,
+    // 25 / 40, 119 / 126. 128, 24: 10 / 24, 25 / 33, 123 / 115; 64 rows: 11 / 24, 48 / 34, 230 / 116.
+    limit *= pairs_keys <= 1 << 16 ? 8 : a->r ? 3 : 2;
+    if (limit > kRowsNodes) limit = kRowsNodes;
+  }
   const int branches = a->r ? 2 : 1;
   // The few-rows kernel, unless the counts leave no sequence for it: a sequence of at most limit / g
   // new tokens falls short of max_new by more than all sequences together do.
@@ -219,7 +228,9 @@ Plan make_plan(const lla_paged_cache* c, const lla_paged_query* a, bool tree) {
     // but no block under 1024 keys (48 sequences, 4 heads, window 1024: 19.5 us with 2 blocks a head,
     // 37 with 7). More than a cluster of 8 only where its blocks would have over 1024 keys each:
     // below that, the launch that joins costs more than shorter blocks save.
-    const int fill = splits(pairs, 304, 128), level = splits(pairs, pl.D == 128 ? 1216 : 1824, 1024);
+    const int tile = rows_limit(a->r != nullptr);
+    const long long blocks = tree ? pairs * ((pl.row_cap + tile - 1) / tile) : pairs;
+    const int fill = splits(blocks, 304, 128), level = splits(blocks, pl.D == 128 ? 1216 : 1824, 1024);
     pl.rows_split = fill > level ? fill : level;
     if (pl.rows_split > kRowsCluster && keys <= kRowsCluster * 1024) pl.rows_split = kRowsCluster;
     if (pl.rows_split > kRowsCluster) {

@@ -54,53 +54,47 @@ struct Cfg {
   static_assert(fin + 16 * D * 4 <= bytes, "join regions");
 };
 
-__device__ __forceinline__ void ldmatrix4(uint32_t (&r)[4], uint32_t addr) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
-}
-__device__ __forceinline__ void ldmatrix4_t(uint32_t (&r)[4], uint32_t addr) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
-}
-__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
-      "{%8, %9}, {%0, %1, %2, %3};"
-      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-// The nodes of a sequence of at most 16, one per lane: a node's parent's, grandparent's, .. bits (among the
-// nodes) and its own where it sees them, and its depth. Parents go from lane to lane, so the tree costs one
-// load and no launch before this one's.
-__device__ __forceinline__ void small_tree(const Params& p, const Seq& sq, uint32_t* bits, int* depth) {
-  const int lane = threadIdx.x & 31, n = min(sq.n, 32);
-  const int stated = lane < n ? __ldg(p.parents + sq.t0 + lane) : -1;
-  if (stated < -1 || stated >= lane) atomicOr(p.status, kStatusBadIndex);
-  const int parent = stated < lane ? max(stated, -1) : -1;
-  uint32_t up = 1u << lane;
-  int d = 0;
-  for (int a = parent; __any_sync(0xffffffffu, a >= 0);) {
-    const int next = __shfl_sync(0xffffffffu, parent, max(a, 0));
-    if (a >= 0) {
-      up |= 1u << a;
-      ++d;
-      a = next;
-    }
+// The nodes of a sequence of at most 64: of each the nodes that it sees (its parent, its parent's, .. and itself,
+// less those that fell out of the window) as bits, and its position. One warp, lane l has nodes l and l + 32;
+// parents come from the other lanes, so a tree costs one load and no launch before this one's.
+__device__ __forceinline__ void small_tree(const Params& p, const Seq& sq, uint64_t* bits_of, int* pos_of) {
+  const int lane = threadIdx.x & 31, n = min(sq.n, 64);
+  int parent[2];
+  bool bad = false;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int i = lane + 32 * h, a = i < n ? __ldg(p.parents + sq.t0 + i) : -1;
+    bad |= a < -1 || a >= i;
+    parent[h] = a < i ? max(a, -1) : -1;
   }
-  if (p.window < n) {  // ancestors that fell out of the window
-    int steps = 1;
-    for (int a = parent; __any_sync(0xffffffffu, a >= 0); ++steps) {
-      const int next = __shfl_sync(0xffffffffu, parent, max(a, 0));
+  if (bad) atomicOr(p.status, kStatusBadIndex);
+  auto up = [&](int a) {  // whole warps call
+    const int x = __shfl_sync(0xffffffffu, parent[0], a & 31), y = __shfl_sync(0xffffffffu, parent[1], a & 31);
+    return a < 0 ? -1 : a < 32 ? x : y;
+  };
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int i = lane + 32 * h;
+    uint64_t bits = 1ull << i;
+    int d = 0;
+    for (int a = parent[h]; __any_sync(0xffffffffu, a >= 0); a = up(a)) {
       if (a >= 0) {
-        if (steps >= p.window && sq.first + d - steps >= p.sinks) up &= ~(1u << a);
-        a = next;
+        bits |= 1ull << a;
+        ++d;
       }
     }
+    if (p.window < n) {
+      int steps = 1;
+      for (int a = parent[h]; __any_sync(0xffffffffu, a >= 0); a = up(a), ++steps)
+        if (a >= 0 && steps >= p.window && sq.first + d - steps >= p.sinks) bits &= ~(1ull << a);
+    }
+    bits_of[i] = bits;
+    pos_of[i] = sq.first + d;
   }
-  *bits = up;
-  *depth = d;
 }
-// CLUSTER: the blocks of a pair are one cluster and join there. TREE: the new tokens are a tree's nodes.
+
+// CLUSTER: the blocks of a pair (and tile) are one cluster and join there.
+// TREE: the new tokens are a tree's nodes (64 at most), their rows in tiles of a block's, which find the keys again in L2.
 template <int D, bool PROBE, bool LOGITS, bool CLUSTER, bool TREE>
 __global__ void __launch_bounds__(NW * 32) attend_rows_kernel(Params p) {
   using C = Cfg<D>;
@@ -110,8 +104,11 @@ __global__ void __launch_bounds__(NW * 32) attend_rows_kernel(Params p) {
   __shared__ float4 stats[NW][16];
   __shared__ float4 fin_stats[16];  // the block's sums
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  // the parts of a pair follow one another: clusters are made of neighbours
-  const int pair = blockIdx.x / p.split, b = pair / p.Hkv, hk = pair % p.Hkv, part = blockIdx.x % p.split;
+  __shared__ uint64_t node_bits_s[TREE ? kRowsNodes : 1];
+  __shared__ int node_pos_s[TREE ? kRowsNodes : 1];
+  // the parts of a pair (and tile) follow one another: clusters are made of neighbours
+  const int part = blockIdx.x % p.split, index = blockIdx.x / p.split, pair = TREE ? index / p.row_tiles : index;
+  const int b = pair / p.Hkv, hk = pair % p.Hkv;
   let_next();
   // Set up behind the tiled kernel of the same call, this one may run beside its last blocks (they
   // share no output); one thread's wait makes the end of this grid the end of both.
@@ -121,9 +118,10 @@ __global__ void __launch_bounds__(NW * 32) attend_rows_kernel(Params p) {
     if (sq.n > 0 && sq.n * p.g > p.max_rows) atomicOr(p.status, kStatusBadIndex);  // beyond max_new
     return;
   }
-  const int nrows = sq.n * p.g;
-  const int p0 = sq.first, p1 = sq.len - 1;
-  const TileRange<KT> range(p, p0, p1);  // (a tree's too)
+  const int r0 = TREE ? index % p.row_tiles * ROWS : 0, nrows = TREE ? min(ROWS, sq.n * p.g - r0) : sq.n * p.g;
+  if (TREE && nrows <= 0) return;
+  const int p0 = sq.first, p1 = TREE ? p0 + (r0 + nrows - 1) / p.g : sq.len - 1;
+  const TileRange<KT> range(p, p0, p1);
   const int chunk = (range.count + p.split - 1) / p.split;
   const int i0 = min(range.count, part * chunk), i1 = min(range.count, i0 + chunk);
   const __nv_bfloat16* kg = static_cast<const __nv_bfloat16*>(p.k);
@@ -171,14 +169,15 @@ __global__ void __launch_bounds__(NW * 32) attend_rows_kernel(Params p) {
   // A operand of the first product: rows of q (and r) of this thread.
   uint32_t a[D / 16][4];
   {
-    const int r0 = lane >> 2, cc = (lane & 3) * 2;
+    const int i = lane >> 2, cc = (lane & 3) * 2;
     auto row = [&](const void* base, int r) -> const uint32_t* {
+      r += r0;
       return reinterpret_cast<const uint32_t*>(static_cast<const __nv_bfloat16*>(base) +
              ((long long)(sq.t0 + r / p.g) * p.Hq + hk * p.g + r % p.g) * p.d + cc);
     };
-    const uint32_t* x = r0 < nrows ? row(p.q, r0) : nullptr;
-    const uint32_t* y = PROBE ? (r0 < nrows ? row(p.r, r0) : nullptr)
-                              : (r0 + 8 < nrows ? row(p.q, r0 + 8) : nullptr);
+    const uint32_t* x = i < nrows ? row(p.q, i) : nullptr;
+    const uint32_t* y = PROBE ? (i < nrows ? row(p.r, i) : nullptr)
+                              : (i + 8 < nrows ? row(p.q, i + 8) : nullptr);
 #pragma unroll
     for (int ks = 0; ks < D / 16; ++ks) {
       const bool in = ks * 16 < p.d;
@@ -189,19 +188,14 @@ __global__ void __launch_bounds__(NW * 32) attend_rows_kernel(Params p) {
     }
   }
   int pos[NR];
-  uint32_t up[NR] = {};  // TREE: the nodes that a row sees
-  uint32_t tree_bits = 0;
-  int tree_depth = 0;
-  if constexpr (TREE) small_tree(p, sq, &tree_bits, &tree_depth);
 #pragma unroll
   for (int i = 0; i < NR; ++i) {
     const int r = (lane >> 2) + 8 * i;
     pos[i] = r < nrows ? p0 + r / p.g : p1;  // rows past the end are not written
-    if constexpr (TREE) {
-      const int node = min(r / p.g, sq.n - 1);
-      up[i] = __shfl_sync(0xffffffffu, tree_bits, node);
-      pos[i] = p0 + __shfl_sync(0xffffffffu, tree_depth, node);
-    }
+  }
+  if constexpr (TREE) {
+    if (warp == 0) small_tree(p, sq, node_bits_s, node_pos_s);
+    __syncthreads();
   }
   const float c2 = p.inv_h * kLog2e;
   float m[NR], d1[NR], d2 = 0.f, d1r = 0.f, o[D / 8][4];  // d1r: of the rounded weights (PROBE)
@@ -249,13 +243,17 @@ __global__ void __launch_bounds__(NW * 32) attend_rows_kernel(Params p) {
       }
     if (!full) {
 #pragma unroll
-      for (int i = 0; i < NR; ++i)
+      for (int i = 0; i < NR; ++i) {
+        const int node = TREE ? (r0 + min((lane >> 2) + 8 * i, nrows - 1)) / p.g : 0, at = TREE ? node_pos_s[node] : pos[i];
+        const uint64_t bits = TREE ? node_bits_s[node] : 0;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const int j = j0 + (e >> 1) * 8 + (e & 1);
-          const bool see = TREE && j >= p0 ? (up[i] >> min(j - p0, 31)) & 1u : visible(p, pos[i], j);
+          const bool see = !TREE ? visible(p, at, j)
+                           : j < p0 ? j > at - p.window || j < p.sinks : j - p0 < kRowsNodes && (bits >> (j - p0) & 1u);
           if (!see) x[i][e] = -CUDART_INF_F;
         }
+      }
     }
     if (LOGITS) {
 #pragma unroll
@@ -352,8 +350,8 @@ __global__ void __launch_bounds__(NW * 32) attend_rows_kernel(Params p) {
     *reinterpret_cast<float2*>(dst + 8 * OP) = make_float2(o[n][2], o[n][3]);
   }
   __syncthreads();
-  const Rows rows{sq.t0, p0, p1, p.g, hk * p.g};
-  auto at = [&](int r) { return ((long long)part * p.B * p.Hkv + pair) * p.row_cap + r; };
+  const Rows rows{sq.t0, p0, p1, p.g, hk * p.g, r0};
+  auto at = [&](int r) { return ((long long)part * p.B * p.Hkv + pair) * p.row_cap + r0 + r; };
   join_block<__nv_bfloat16, D, PROBE, CLUSTER, NW, ROWS, 16>(p, sq, b, rows, part, nrows, at, D, os, stats,
                                                              reinterpret_cast<float*>(smem + C::fin), fin_stats);
 }
@@ -432,12 +430,14 @@ __global__ void __launch_bounds__(256) mass_rows_kernel(Params p) {
 }
 
 template <int D, bool PROBE, bool LOGITS, bool TREE = false>
-cudaError_t launch_rows_t(const Params& p, cudaStream_t s) {
+cudaError_t launch_rows_t(Params p, cudaStream_t s) {
   const unsigned pairs = (unsigned)p.B * p.Hkv;
-  if ((long long)pairs * p.split > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+  p.row_tiles = TREE ? (p.row_cap + rows_limit(PROBE) - 1) / rows_limit(PROBE) : 1;
+  const long long blocks = (long long)pairs * p.row_tiles * p.split;
+  if (blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
   const bool cluster = p.split > 1 && p.split <= kRowsCluster;
   auto kern = cluster ? attend_rows_kernel<D, PROBE, LOGITS, true, TREE> : attend_rows_kernel<D, PROBE, LOGITS, false, TREE>;
-  cudaError_t err = launch(kern, dim3(pairs * p.split), NW * 32, Cfg<D>::bytes, cluster ? p.split : 1, p.beside != 0, s, p);
+  cudaError_t err = launch(kern, dim3((unsigned)blocks), NW * 32, Cfg<D>::bytes, cluster ? p.split : 1, p.beside != 0, s, p);
   if (err == cudaSuccess && !cluster && p.split > 1) {
     const long long rows = (long long)pairs * p.row_cap;
     err = launch(join_rows_kernel<D, PROBE>, dim3((unsigned)((rows + 3) / 4)), 128, 0, 1, true, s, p);

@@ -19,11 +19,26 @@ using tc::smem_u32;
 constexpr int KT = 16;  // keys per tile: within one page, since pages hold a multiple of 16
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
-// The rows of a block: row r is token t0 + r / width (positions from p0 on) and head h0 + r % width.
+// The rows of a block: row r is token t0 + (r0 + r) / width (positions from p0 on) and head h0 + (r0 + r) % width.
 struct Rows {
-  int t0, p0, p1, width, h0;
+  int t0, p0, p1, width, h0, r0 = 0;
 };
 
+__device__ __forceinline__ void ldmatrix4(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ void ldmatrix4_t(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+      "{%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
 // A finished row's sums {m, d1, d2, d1 of the rounded weights} (the last one used where weights are
 // rounded and differences of sums taken: bf16 with a probe), o1[c] and o2[c] its unnormalised columns
 // lane * VC + c: writes out and lse.
@@ -34,7 +49,7 @@ __device__ __forceinline__ void write_row(const Params& p, const Seq& sq, int b,
                                            const float (&o1)[D / 32], const float (&o2)[D / 32]) {
   constexpr int VC = D / 32;
   const int lane = threadIdx.x & 31;
-  const int token = rows.t0 + r / rows.width, head = rows.h0 + r % rows.width;
+  const int token = rows.t0 + (rows.r0 + r) / rows.width, head = rows.h0 + (rows.r0 + r) % rows.width;
   const float s1 = st.y, norm = kRoundedSum<T, PROBE> ? st.w : s1;
   const float inv = norm == 0.f ? 0.f : 1.f / norm, f1 = (1.f + st.z * inv) * inv;
   T* dst = static_cast<T*>(p.out) + ((long long)token * p.Hq + head) * p.dv + lane * VC;

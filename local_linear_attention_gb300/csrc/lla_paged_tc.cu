@@ -343,11 +343,12 @@ attend_tc_kernel(Params p, const __grid_constant__ CUtensorMap kmap, const __gri
     }
     __syncthreads();
     if (warp < 2) {
-      long long w = 0, nt = 0;
+      long long w = 0, nt = 0, longest = 0;
       int least = 0x7fffffff, most = 0;
       for (int i = lane; i < p.B; i += 32) {
         w += cost[i];
         nt += tiles_s[i];
+        if (TREE && tiles_s[i] > 0) longest = max(longest, cost[i] / tiles_s[i]);  // (alike but for a few nodes)
         least = min(least, shortest[i]);
         most = max(most, tiles_s[i]);
       }
@@ -357,12 +358,16 @@ attend_tc_kernel(Params p, const __grid_constant__ CUtensorMap kmap, const __gri
         nt += __shfl_xor_sync(0xffffffffu, nt, o);
         least = min(least, __shfl_xor_sync(0xffffffffu, least, o));
         most = max(most, __shfl_xor_sync(0xffffffffu, most, o));
+        if (TREE) longest = max(longest, __shfl_xor_sync(0xffffffffu, longest, o));
       }
       w *= p.Hkv;
       nt *= p.Hkv;
       // Whole tiles: the CTAs that the last row leaves out wait for about the shortest tile.
       const long long rows = (nt + gridDim.x - 1) / gridDim.x;
-      const bool whole = (rows * gridDim.x - nt) * least <= (long long)Sched<D, PROBE>::kCut * gridDim.x;
+      // (Trees: a sequence's tiles all see its whole prefix, so few sequences of unlike lengths leave CTAs idle
+      // behind the longest. 16 of 4k to 16k, 8 heads of 128, a tile each: 201 us whole, 163 cut.)
+      const bool whole = TREE ? (rows * longest - Sched<D, PROBE>::kCut) * gridDim.x <= w
+                              : (rows * gridDim.x - nt) * least <= (long long)Sched<D, PROBE>::kCut * gridDim.x;
       if (whole) {
         if (tid == 0) whole_s = most;
         if (lane == 0) bounds[warp] = {p.B, 0, 0, 0};
@@ -1106,7 +1111,9 @@ cudaError_t launch_attend_tc(const Params& p, int D, cudaStream_t s) {
 cudaError_t launch_join_tc(const Params& p, int D, cudaStream_t s) {
   auto kern = p.r ? (D == 128 ? join_tc_kernel<128, true> : join_tc_kernel<64, true>)
                   : (D == 128 ? join_tc_kernel<128, false> : join_tc_kernel<64, false>);
-  return launch(kern, dim3((unsigned)p.split, 8), 256, 0, 1, true, s, p);
+  // Blocks to a cut tile: with few rows to a warp its loads' latencies do not add up (256 nodes at 32768, 8
+  // heads, ends from a cold L2: 18 us with 8 blocks, 14 with 32).
+  return launch(kern, dim3((unsigned)p.split, 32), 256, 0, 1, true, s, p);
 }
 
 }  // namespace paged
