@@ -6,7 +6,6 @@ fallback: if the library is missing or the tensors are not on a CUDA device the 
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import os
 import struct
@@ -69,6 +68,7 @@ class Options(ctypes.Structure):
 _CACHE = struct.Struct("@5P10i")
 _QUERY = struct.Struct("@5P3if6i")
 _SPEC = struct.Struct("@64df5i")  # lla_rotary_spec
+_POINTERS, _INTS = [struct.Struct(f"@{n}P") for n in range(4)], [struct.Struct(f"@{n}i") for n in range(4)]
 
 
 def _options(path=0, form=0, cg=None, test_fault=0):
@@ -408,18 +408,6 @@ class RotarySpec:
         self._packed = _SPEC.pack(*freq, *[0.0] * (64 - len(freq)), scale, rot, layout, 0, 0, 0)
 
 
-def _stream_on(index, device, stream):
-    """The raw handle of a call's stream (None: the current one) and what to allocate its outputs under."""
-    if stream is None:
-        return torch._C._cuda_getCurrentRawStream(index), contextlib.nullcontext()
-    if getattr(stream, "device_index", index) != index:
-        raise ValueError(f"the stream must be one of {device}, where the tensors are")
-    raw = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
-    if not isinstance(stream, torch.cuda.Stream):
-        stream = torch.cuda.ExternalStream(raw, device=device) if raw else torch.cuda.default_stream(device)
-    return raw, torch.cuda.stream(stream)
-
-
 def lla_rotary(x, spec: RotarySpec, positions=None, backward=False, out=None, stream=None):
     """Rotates x, a tensor [B, H, T, d] or up to three of them that share B, T and d (q, k and the probe of an
     attention, with any numbers of heads), by their positions [B, T] int32 (None: 0 .. T-1); returns the
@@ -448,21 +436,33 @@ def lla_rotary(x, spec: RotarySpec, positions=None, backward=False, out=None, st
     if positions is not None and (positions.dtype != torch.int32 or positions.shape != (B, T) or
                                   positions.get_device() != index or not positions.is_contiguous()):
         raise ValueError("positions must be a contiguous int32 [B, T] tensor on the device of x")
-    raw, on = _stream_on(index, first.device, stream)
-    if out is None:
-        with on:
-            outs = tuple(torch.empty_like(t) for t in xs)
+    if stream is None:
+        raw = torch._C._cuda_getCurrentRawStream(index)
+    elif getattr(stream, "device_index", index) != index:
+        raise ValueError(f"the stream must be one of {first.device}, where the tensors are")
     else:
+        raw = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+    if out is not None:
         outs = (out,) if isinstance(out, torch.Tensor) else tuple(out)
         if len(outs) != len(xs) or any(o.shape != t.shape or o.dtype != t.dtype or o.get_device() != index or
                                        not o.is_contiguous() for o, t in zip(outs, xs)):
             raise ValueError("out must be like x")
+    elif stream is None:
+        outs = [torch.empty_like(t) for t in xs]
+    else:  # what the call allocates belongs to its stream
+        if not isinstance(stream, torch.cuda.Stream):
+            stream = torch.cuda.ExternalStream(raw, device=first.device) if raw else torch.cuda.default_stream(first.device)
+        with torch.cuda.stream(stream):
+            outs = [torch.empty_like(t) for t in xs]
     n = len(xs)
-    args = (spec._packed, struct.pack(f"@{n}P", *[t.data_ptr() for t in xs]),
-            struct.pack(f"@{n}P", *[t.data_ptr() for t in outs]), struct.pack(f"@{n}i", *heads), n,
-            None if positions is None else positions.data_ptr(), B, T, d, 1 if backward else 0, code, raw)
-    with torch.cuda.device(index):
+    args = (spec._packed, _POINTERS[n].pack(*[t.data_ptr() for t in xs]), _POINTERS[n].pack(*[t.data_ptr() for t in outs]),
+            _INTS[n].pack(*heads), n, None if positions is None else positions.data_ptr(), B, T, d, 1 if backward else 0,
+            code, raw)
+    if torch._C._cuda_getDevice() == index:
         st = _load().lla_rotary(*args)
+    else:
+        with torch.cuda.device(index):
+            st = _load().lla_rotary(*args)
     _check(st, "lla_rotary")
     return outs[0] if single else list(outs)
 

@@ -61,6 +61,7 @@ struct Params {
   const int* depth;      // [tokens]
   int words;
   int row_tiles;         // few rows: tiles of a sequence's rows
+  int streams;           // tensor cores: a CTA takes two key tiles at a time instead of two row blocks
 };
 
 struct Seq {
@@ -449,7 +450,8 @@ struct TcPlan {
   int row_floats = 0;
   bool cuts = false;       // whether a tile may have enough steps to be cut
 };
-TcPlan plan_tc(int D, bool probe, long long tokens, int B, int Hkv, int g, long long keys);
+// streams: for trees of at most 128 rows, softmax attention at D = 128.
+TcPlan plan_tc(int D, bool probe, bool streams, long long tokens, int B, int Hkv, int g, long long keys);
 cudaError_t launch_attend_tc(const Params& p, int D, cudaStream_t s);
 cudaError_t launch_join_tc(const Params& p, int D, cudaStream_t s);
 cudaError_t launch_mass_tc(const Params& p, int D, cudaStream_t s);

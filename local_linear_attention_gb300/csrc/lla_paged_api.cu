@@ -114,6 +114,7 @@ struct Plan {
   int rows_split = 1, tiles_split = 1;
   int row_cap = 0, keys_cap = 0;
   size_t rows_s = 0, rows_o = 0, logits = 0, pieces = 0, tiles_s = 0, tiles_o = 0, lse = 0;
+  bool streams = false;      // tensor cores: two key tiles at a time
   bool tree = false;         // a launch finds the nodes' bits and depths first
   int words = 0;
   size_t bits = 0, depth = 0;
@@ -244,7 +245,8 @@ Plan make_plan(const lla_paged_cache* c, const lla_paged_query* a, bool tree) {
       if (pl.logits_kept) pl.logits = take(bytes);
     }
   }
-  const TcPlan t = tc ? plan_tc(pl.D, a->r != nullptr, a->tokens, c->num_seqs, c->kv_heads, g, keys) : TcPlan();
+  pl.streams = tree && pl.D == 128 && !a->r && rows <= 128;
+  const TcPlan t = tc ? plan_tc(pl.D, a->r != nullptr, pl.streams, a->tokens, c->num_seqs, c->kv_heads, g, keys) : TcPlan();
   pl.mass_tc = t.ctas > 0;
   if (pl.tiles) {
     pl.tc = t.ctas > 0;
@@ -316,6 +318,7 @@ int run_attention(const lla_paged_cache* c, const lla_paged_query* a, const int*
   p.max_rows = rows < 0x7fffffffLL ? (int)rows : 0x7fffffff;
   if (a->track_mass && !a->lse) p.lse = reinterpret_cast<float*>(ws + pl.lse);
   p.parents = parents;
+  p.streams = pl.streams;
   if (parents) p.hi = p.max_rows;  // the bits have room for max_new nodes
   if (pl.tree) {
     p.words = pl.words;

@@ -49,11 +49,17 @@ constexpr int BM = 128;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kTooFar = 100.f;  // a weight of 2^100: its products and sums may leave fp32
 
-template <int D, bool PROBE>
+// STREAMS: a CTA has one row block and takes its key tiles two at a time, each with scores, weights and an
+// accumulator of its own, which alternate like two row blocks; they are joined at a piece's end. For trees of at
+// most 128 rows, which would leave a second row block empty (softmax attention at D = 128).
+template <int D, bool PROBE, bool STREAMS>
 struct Cfg {
+  static_assert(!STREAMS || (D == 128 && !PROBE), "streams");
   static constexpr int kt = D == 64 && PROBE ? 64 : 128;       // keys per tile
-  static constexpr int blocks = D == 128 && !PROBE ? 2 : 1;    // row blocks
-  static constexpr int ops = blocks * (PROBE ? 2 : 1);         // operands: Q of each block, or Q and R
+  static constexpr int blocks = D == 128 && !PROBE && !STREAMS ? 2 : 1;  // row blocks
+  static constexpr int halves = STREAMS ? 2 : blocks;          // row blocks or streams, with softmax warps of their own
+  static constexpr int ops = halves * (PROBE ? 2 : 1);         // scores at once: of Q of each half, or of Q and R
+  static constexpr int operands = STREAMS ? 1 : ops;           // of these in shared memory
   // Groups of four warps per row block. One, a thread taking a whole row of the tile, where the
   // registers allow it: nothing is exchanged then (chunk of 2048 at 32768, D = 128: 779 us with two,
   // 729 with one; prompts B4 T4096 D = 64: 121 and 108, with a probe 462 and 186, the threads of two short of
@@ -61,7 +67,7 @@ struct Cfg {
   // 8192, 32 heads over 8: 675 us with one, 590 with two).
   static constexpr int groups = D == 128 && PROBE ? 2 : 1;
   static_assert(groups <= 2, "a group's weights are one half of a step's, or all");
-  static constexpr int nsoft = blocks * groups * 4;            // softmax warps
+  static constexpr int nsoft = halves * groups * 4;            // softmax warps
   static constexpr int ctas = D == 64 ? 2 : 1;                 // per SM
   static constexpr int threads = (nsoft + 2) * 32;
   // tensor memory: S [ops][kt] with P in it, O [ops][D]
@@ -76,8 +82,9 @@ struct Cfg {
   // shared memory: operands [ops][D/64][128 rows][128 B], ring of key and value tiles
   // [D/64][kt rows][128 B], barriers, row exchange [6 buffers][nsoft/4 groups][128], tile counts
   static constexpr int op_bytes = BM * D * 2, tile = kt * D * 2, half = kt * 128;
-  static constexpr int stages = D == 128 ? 4 : PROBE ? 8 : 5;
-  static constexpr int sm_ring = ops * op_bytes;
+  static constexpr int stages = STREAMS ? 5 : D == 128 ? 4 : PROBE ? 8 : 5;
+  static constexpr int items = STREAMS ? 4 : 2;                // ring stages of a step
+  static constexpr int sm_ring = operands * op_bytes;
   static constexpr int sm_bar = sm_ring + stages * tile;
   static constexpr int sm_x = sm_bar + 512;
   static constexpr int sm_tiles = sm_x + 6 * (nsoft / 4) * BM * 4, tiles_bytes = 2048 * 4;
@@ -123,10 +130,11 @@ __device__ __forceinline__ void store32(void* dst, const uint32_t (&x)[8], bool 
 // prompt are the longest, its first the shortest), each CTA takes whole tiles instead: longest
 // first, in rows of one per CTA that run back and forth, which levels out a steady decline.
 constexpr int kMaxSeqs = 2048;  // their costs wait in the ring's shared memory (larger batches: CUDA cores)
-template <int D, bool PROBE>
+template <int D, bool PROBE, bool STREAMS>
 struct Sched {
-  using C = Cfg<D, PROBE>;
-  static constexpr int kStart = C::kt == 64 ? 4 : 3, kPiece = C::kt == 64 ? 8 : 4, kCut = C::kt == 64 ? 18 : 12;
+  using C = Cfg<D, PROBE, STREAMS>;
+  static constexpr int kStart = STREAMS ? 6 : C::kt == 64 ? 4 : 3, kPiece = C::kt == 64 ? 8 : 4;
+  static constexpr int kCut = C::kt == 64 || STREAMS ? 18 : 12;
   static constexpr int rows = C::blocks * BM;
 };
 struct Place {  // step s of a tile; b = number of sequences: the end
@@ -141,9 +149,9 @@ struct Tile {
 };
 // Steps of sequence b's tiles (one head), kStart included, and the shortest's; all lanes of the warp
 // return them.
-template <int D, bool PROBE, bool TREE>
+template <int D, bool PROBE, bool TREE, bool STREAMS>
 __device__ __forceinline__ long long seq_cost(const Params& p, int b, int tokens, int* tiles, int* shortest) {
-  using S = Sched<D, PROBE>;
+  using S = Sched<D, PROBE, STREAMS>;
   const Seq sq = load_seq(p, b);
   long long c = 0;
   int least = 0x7fffffff, nt = 0;
@@ -174,9 +182,9 @@ __device__ __forceinline__ long long scan_incl(long long x) {
   return x;
 }
 // The place at step u of the line, from the sequences' costs (a whole warp calls and agrees).
-template <int D, bool PROBE, bool TREE>
+template <int D, bool PROBE, bool TREE, bool STREAMS>
 __device__ __forceinline__ Place locate(const Params& p, const long long* cost, long long u, int tokens) {
-  using S = Sched<D, PROBE>;
+  using S = Sched<D, PROBE, STREAMS>;
   const int lane = threadIdx.x & 31;
   for (int base = 0; base < p.B; base += 32) {
     const long long c = base + lane < p.B ? cost[base + lane] * p.Hkv : 0;
@@ -272,11 +280,11 @@ __device__ __forceinline__ int next_seq(const Params& p, int b) {
 }
 
 // TREE: the new tokens are nodes of trees, whose bits and depths the launch before this one writes.
-template <int D, bool PROBE, bool TREE>
-__global__ void __launch_bounds__((Cfg<D, PROBE>::threads), (Cfg<D, PROBE>::ctas))
+template <int D, bool PROBE, bool TREE, bool STREAMS>
+__global__ void __launch_bounds__((Cfg<D, PROBE, STREAMS>::threads), (Cfg<D, PROBE, STREAMS>::ctas))
 attend_tc_kernel(Params p, const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
                  const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap rmap) {
-  using C = Cfg<D, PROBE>;
+  using C = Cfg<D, PROBE, STREAMS>;
   constexpr int KT = C::kt;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
@@ -289,8 +297,9 @@ attend_tc_kernel(Params p, const __grid_constant__ CUtensorMap kmap, const __gri
   int* const tiles_s = reinterpret_cast<int*>(smem + C::sm_tiles);  // [B] tiles of each sequence
   __shared__ Work work_s[2];
   // Of each step, by the loader: its first key, and in the low bits (it is a multiple of 64) whether
-  // row blocks 0 and 1 need a mask and whether the sequence ends inside it.
-  __shared__ int step_s[8];
+  // row blocks 0 and 1 need a mask and whether the sequence ends inside it; with streams of each of a
+  // step's tiles, and whether there is none.
+  __shared__ int step_s[4 * C::items];
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   let_next();  // the few-rows kernel of the same call, which does not depend on this one
   const int per = BM / p.g, width = per * p.g;  // tokens and rows of a row block
@@ -303,7 +312,7 @@ attend_tc_kernel(Params p, const __grid_constant__ CUtensorMap kmap, const __gri
       mbar_init(&bar.pfull[s][0], C::groups * 4);  // (with two groups the second's rescaling too, see there)
       mbar_init(&bar.pfull[s][1], 4);
       mbar_init(&bar.pvdone[s], 1);
-      for (int q = 0; q < 4; ++q) mbar_init(&bar.rowx[s][q], C::groups);
+      for (int q = 0; q < 4; ++q) mbar_init(&bar.rowx[s][q], STREAMS ? 2 : C::groups);
       mbar_init(&bar.workfull[s], 1);
       mbar_init(&bar.workempty[s], C::nsoft + 1);
     }
@@ -318,7 +327,7 @@ attend_tc_kernel(Params p, const __grid_constant__ CUtensorMap kmap, const __gri
     tmem_relinquish();
   }
   // The operands' rows past `width` are never loaded: zeros.
-  for (int e = tid; e < C::ops * (D / 64) * (BM - width) * 8; e += C::threads) {
+  for (int e = tid; e < C::operands * (D / 64) * (BM - width) * 8; e += C::threads) {
     const int c = e & 7, row = width + (e >> 3) % (BM - width), half = (e >> 3) / (BM - width);
     *reinterpret_cast<uint4*>(smem + half * 16384 + row * 128 + c * 16) = make_uint4(0u, 0u, 0u, 0u);
   }
@@ -334,7 +343,7 @@ attend_tc_kernel(Params p, const __grid_constant__ CUtensorMap kmap, const __gri
     static_assert(kMaxSeqs * 12 <= C::stages * C::tile && kMaxSeqs * 4 <= C::tiles_bytes, "the sequences' costs");
     for (int i = warp; i < p.B; i += C::threads / 32) {
       int nt, least;
-      const long long c = seq_cost<D, PROBE, TREE>(p, i, tokens, &nt, &least);
+      const long long c = seq_cost<D, PROBE, TREE, STREAMS>(p, i, tokens, &nt, &least);
       if (lane == 0) {
         cost[i] = c;
         shortest[i] = least;
@@ -366,14 +375,14 @@ attend_tc_kernel(Params p, const __grid_constant__ CUtensorMap kmap, const __gri
       const long long rows = (nt + gridDim.x - 1) / gridDim.x;
       // (Trees: a sequence's tiles all see its whole prefix, so few sequences of unlike lengths leave CTAs idle
       // behind the longest. 16 of 4k to 16k, 8 heads of 128, a tile each: 201 us whole, 163 cut.)
-      const bool whole = TREE ? (rows * longest - Sched<D, PROBE>::kCut) * gridDim.x <= w
-                              : (rows * gridDim.x - nt) * least <= (long long)Sched<D, PROBE>::kCut * gridDim.x;
+      const bool whole = TREE ? (rows * longest - Sched<D, PROBE, STREAMS>::kCut) * gridDim.x <= w
+                              : (rows * gridDim.x - nt) * least <= (long long)Sched<D, PROBE, STREAMS>::kCut * gridDim.x;
       if (whole) {
         if (tid == 0) whole_s = most;
         if (lane == 0) bounds[warp] = {p.B, 0, 0, 0};
       } else {
-        const long long share = max((w + gridDim.x - 1) / gridDim.x, (long long)(Sched<D, PROBE>::kPiece));
-        const Place x = locate<D, PROBE, TREE>(p, cost, (blockIdx.x + warp) * share, tokens);
+        const long long share = max((w + gridDim.x - 1) / gridDim.x, (long long)(Sched<D, PROBE, STREAMS>::kPiece));
+        const Place x = locate<D, PROBE, TREE, STREAMS>(p, cost, (blockIdx.x + warp) * share, tokens);
         if (lane == 0) bounds[warp] = x;
         if (tid == 0) whole_s = 0;
       }
@@ -418,7 +427,7 @@ attend_tc_kernel(Params p, const __grid_constant__ CUtensorMap kmap, const __gri
     // S_o = operand o x K^T for operands o0 .. o0 + count - 1 at step gi; the last of a step frees its
     // stage, the last of a piece its operands
     auto scores = [&](auto o0, auto count, int gi, bool last) {
-      const uint32_t st = stage(2 * gi);
+      const uint32_t st = stage(STREAMS ? 4 * gi + 2 * o0 : 2 * gi);
       const uint64_t k = kd + (uint64_t)(st * tile16);
       tc_fence_after();
       if (elect_one()) {
@@ -426,20 +435,18 @@ attend_tc_kernel(Params p, const __grid_constant__ CUtensorMap kmap, const __gri
         for (int o = o0; o < o0 + count; ++o) {
 #pragma unroll
           for (int s = 0; s < D / 16; ++s)
-            mma_ss(tbase + o * KT, xd + (uint64_t)(o * (C::op_bytes >> 4) + (s >> 2) * 1024 + (s & 3) * 2),
+            mma_ss(tbase + o * KT, xd + (uint64_t)((STREAMS ? 0 : o) * (C::op_bytes >> 4) + (s >> 2) * 1024 + (s & 3) * 2),
                    k + (uint64_t)((s >> 2) * (C::half >> 4) + (s & 3) * 2), id_s, s > 0);
           mma_commit(&bar.sfull[o]);
         }
-        if (o0 + count == C::ops) {
-          mma_commit(&bar.empty[st]);
-          if (last) mma_commit(&bar.opempty);
-        }
+        if (STREAMS || o0 + count == C::ops) mma_commit(&bar.empty[st]);
+        if (o0 + count == C::ops && last) mma_commit(&bar.opempty);
       }
       __syncwarp();
     };
     // O_o += P_o V over one half of the step's keys
     auto values = [&](auto o0, auto count, int gi, bool first, auto half) {
-      const uint32_t st = stage(2 * gi + 1);
+      const uint32_t st = stage(STREAMS ? 4 * gi + 2 * o0 + 1 : 2 * gi + 1);
       const uint64_t v = vd + (uint64_t)(st * tile16);
       tc_fence_after();
       if (elect_one()) {
@@ -456,7 +463,7 @@ attend_tc_kernel(Params p, const __grid_constant__ CUtensorMap kmap, const __gri
           }
           if (half) mma_commit(&bar.pvdone[o]);
         }
-        if (half && o0 + count == C::ops) mma_commit(&bar.empty[st]);
+        if (half && (STREAMS || o0 + count == C::ops)) mma_commit(&bar.empty[st]);
       }
       __syncwarp();
     };
@@ -464,13 +471,13 @@ attend_tc_kernel(Params p, const __grid_constant__ CUtensorMap kmap, const __gri
     using I1 = std::integral_constant<int, 1>;
     using Per = std::integral_constant<int, PROBE ? 2 : 1>;  // operands of a row block
     using All = std::integral_constant<int, C::ops>;
-    using Second = std::integral_constant<int, C::blocks - 1>;
+    using Second = std::integral_constant<int, C::halves - 1>;
     bool ok = true;
     int pieces = 0;
     for (int k = 0; ok; ++k) {
       const volatile Work* w = take(k);
       if (!w) break;
-      const int n = uni(w->n);
+      const int n = STREAMS ? (uni(w->n) + 1) / 2 : uni(w->n);
       give_back(k);
       if (n == 0) continue;
       // A row block's value products, half a step's weights at a time (the first product runs while
@@ -481,12 +488,24 @@ attend_tc_kernel(Params p, const __grid_constant__ CUtensorMap kmap, const __gri
         if (d) values(o, Per{}, gi, i == 0, I0{});
         d = d && wait(&bar.pfull[h][1], gi & 1);
         if (d) values(o, Per{}, gi, i == 0, I1{});
+        if (STREAMS && d && i + 1 < n) d = wait(&bar.full[stage(4 * gi + 4 + 2 * h)], parity(4 * gi + 4 + 2 * h));
         if (d && i + 1 < n) scores(o, Per{}, gi + 1, i + 2 == n);
         return d;
       };
-      ok = wait(&bar.opfull, pieces++ & 1) && wait(&bar.full[stage(2 * base)], parity(2 * base));
-      if (ok) scores(I0{}, All{}, base, n == 1);
-      for (int i = 0; i < n && ok; ++i) {
+      ok = wait(&bar.opfull, pieces++ & 1) && wait(&bar.full[stage(C::items * base)], parity(C::items * base));
+      if (STREAMS) {
+        if (ok) scores(I0{}, I1{}, base, false);
+        ok = ok && wait(&bar.full[stage(4 * base + 2)], parity(4 * base + 2));
+        if (ok) scores(Second{}, I1{}, base, n == 1);
+      } else if (ok) {
+        scores(I0{}, All{}, base, n == 1);
+      }
+      for (int i = 0; STREAMS && i < n && ok; ++i) {
+        const int x = 4 * (base + i);
+        ok = wait(&bar.full[stage(x + 1)], parity(x + 1)) && block(I0{}, I0{}, i);
+        ok = ok && wait(&bar.full[stage(x + 3)], parity(x + 3)) && block(Second{}, Second{}, i);
+      }
+      for (int i = 0; !STREAMS && i < n && ok; ++i) {
         const int x = 2 * (base + i);
         if (i + 1 < n) ok = wait(&bar.full[stage(x + 2)], parity(x + 2));
         ok = ok && wait(&bar.full[stage(x + 1)], parity(x + 1));
@@ -569,14 +588,15 @@ attend_tc_kernel(Params p, const __grid_constant__ CUtensorMap kmap, const __gri
       if (!ok) break;
       ++pieces;
       if (lane == 0) {  // boxes of [per tokens][g heads][64 features]
-        mbar_arrive_expect_tx(&bar.opfull, C::ops * width * D * 2);
-        for (int o = 0; o < C::ops; ++o)
+        mbar_arrive_expect_tx(&bar.opfull, C::operands * width * D * 2);
+        for (int o = 0; o < C::operands; ++o)
           for (int c = 0; c < D / 64; ++c)
             tma_load_3d(smem + o * C::op_bytes + c * 16384, PROBE && o ? &rmap : &qmap, c * 64, w.hk * p.g,
                         w.t0 + w.tile * tokens + (PROBE ? 0 : o * per), &bar.opfull);
       }
       __syncwarp();
-      for (int i = 0; i < w.n && ok; ++i) {
+      const int tiles = STREAMS ? (w.n + 1) / 2 * 2 : w.n;  // (the last step's second may be none: zeros)
+      for (int i = 0; i < tiles && ok; ++i) {
         const int k0 = first_key(i), j = k0 + lane * frag, c2 = c2_next;
         c2_next = page_row(i + 1);
         int info = k0 | (k0 + KT > w.len ? 4 : 0);
@@ -587,12 +607,13 @@ attend_tc_kernel(Params p, const __grid_constant__ CUtensorMap kmap, const __gri
                    : !all_visible(p, q0, min(q0 + per - 1, x.p1), k0, k0 + KT))
             info |= 1 << h;
         }
+        if (STREAMS && i >= w.n) info = 1 | 8;
         for (int kv = 0; kv < 2 && ok; ++kv) {
-          const int y = 2 * (base + i) + kv, st = y % C::stages;
+          const int y = 2 * (C::items / 2 * base + i) + kv, st = y % C::stages;
           if (y >= C::stages) ok = wait(&bar.empty[st], ((y / C::stages) - 1) & 1);
           if (!ok) break;
           if (lane == 0) {
-            if (kv == 0) step_s[(base + i) & 7] = info;
+            if (kv == 0) step_s[(C::items / 2 * base + i) % (4 * C::items)] = info;
             mbar_arrive_expect_tx(&bar.full[st], C::tile);
           }
           __syncwarp();
@@ -605,7 +626,7 @@ attend_tc_kernel(Params p, const __grid_constant__ CUtensorMap kmap, const __gri
           issued = y + 1;
         }
       }
-      base += w.n;
+      base += STREAMS ? tiles / 2 : w.n;
     }
     // Nothing may land in this CTA's shared memory after it exits (the last copies; after an abort
     // nobody else has waited for them).
@@ -629,21 +650,27 @@ attend_tc_kernel(Params p, const __grid_constant__ CUtensorMap kmap, const __gri
     // Exchange among the groups of a row: x[buffer][group][row], buffers 0 to 2 for the maxima of steps in
     // turn, 3 to 5 for a piece's sums; between warps of the same rows.
     float* const xm = reinterpret_cast<float*>(smem + C::sm_x);
-    auto slot = [&](int buf, int g) -> float& { return xm[((buf * C::blocks + h) * NG + g) * BM + r]; };
+    auto slot = [&](int buf, int g) -> float& {
+      return STREAMS ? xm[(buf * 2 + g) * BM + r] : xm[((buf * C::blocks + h) * NG + g) * BM + r];
+    };
     int xphase = 0;  // phases of rowx used so far
     auto exchange = [&]() {
-      if (NG == 1) return true;
+      if (NG == 1 && !STREAMS) return true;
       __syncwarp();
-      if (lane == 0) mbar_arrive(&bar.rowx[h][warp & 3]);
-      return wait(&bar.rowx[h][warp & 3], (xphase++) & 1);
+      const int of = STREAMS ? 0 : h;
+      if (lane == 0) mbar_arrive(&bar.rowx[of][warp & 3]);
+      return wait(&bar.rowx[of][warp & 3], (xphase++) & 1);
     };
-    const int r_tok = r < width ? h * per + r / p.g : 1 << 30, r_head = r % p.g;  // this row: token of the tile, grouped head
+    // The groups that share a piece's output, of a row block or the streams, and this one's place among them.
+    constexpr int NS = STREAMS ? 2 : NG;
+    const int share = STREAMS ? h : sub;
+    const int r_tok = r < width ? (STREAMS ? 0 : h * per) + r / p.g : 1 << 30, r_head = r % p.g;  // this row: token of the tile, grouped head
     int base = 0;
     bool ok = true;
     for (int k = 0; ok; ++k) {
     const volatile Work* w = take(k);  // read again where it is needed: registers are what is short here
     if (!w) break;
-    const int n = uni(w->n);
+    const int n = STREAMS ? (uni(w->n) + 1) / 2 : uni(w->n);
     auto tile_of = [&]() {
       Seq sq;
       sq.n = w->seq_n;
@@ -666,8 +693,9 @@ attend_tc_kernel(Params p, const __grid_constant__ CUtensorMap kmap, const __gri
       for (int c = 0; c < NC / 32; ++c) tmem_ld32(lanes + h * KT + sub * NC + c * 32, s[c]);
       tmem_ld_wait();
       if constexpr (PROBE) tmem_ld16(lanes + KT + sub * NC, tt[0]);
-      const int info = uni(*(volatile int*)&step_s[gi & 7]), k0 = info & ~63, kb = k0 + sub * NC;
-      const bool masked = (info >> h) & 1;
+      const int info = uni(*(volatile int*)&step_s[(STREAMS ? 2 * gi + h : gi) % (4 * C::items)]);
+      const int k0 = info & ~63, kb = k0 + sub * NC;
+      const bool masked = (info >> (STREAMS ? 0 : h)) & 1;
       if (masked) {
         const Tile tile = tile_of();
         int pos = r_tok < tile.ntok ? tile.p0 + r_tok : tile.p1;  // rows that do not exist are not written
@@ -686,6 +714,7 @@ attend_tc_kernel(Params p, const __grid_constant__ CUtensorMap kmap, const __gri
         for (int c = 0; c < NC / 32; ++c) {
           seen[c] = below(hi - c * 32) & (~below(lo + 1 - c * 32) | below(first - c * 32));
           if (TREE && hi < (c + 1) * 32) seen[c] |= node_bits(p, token, c * 32 - hi);
+          if (STREAMS && info & 8) seen[c] = 0u;
 #pragma unroll
           for (int e = 0; e < 32; ++e) s[c][e] = seen[c] & (1u << e) ? s[c][e] : 0xFF800000u;
         }
@@ -762,7 +791,7 @@ attend_tc_kernel(Params p, const __grid_constant__ CUtensorMap kmap, const __gri
         // the last page's slots past the sequence's end may hold anything: their weight is zero,
         // and so must be the values
         const int len = w->len;
-        const int x = 2 * gi + 1, st = x % C::stages;
+        const int x = STREAMS ? 4 * gi + 2 * h + 1 : 2 * gi + 1, st = x % C::stages;
         ok = wait(&bar.full[st], (x / C::stages) & 1);
         if (!ok) break;
         // every warp zeroes every row: its own arrival below is then enough for the products it lets go
@@ -856,9 +885,25 @@ attend_tc_kernel(Params p, const __grid_constant__ CUtensorMap kmap, const __gri
         d1r += slot(5, g);
       }
     }
+    [[maybe_unused]] float scale[2] = {};  // of the streams' accumulators
+    if constexpr (STREAMS) {  // the streams' sums, taken against the larger reference
+      if (ok) {
+        slot(3, h) = d1;
+        slot(4, h) = m;
+        ok = exchange();
+        m = fmaxf(slot(4, 0), slot(4, 1));
+        d1 = 0.f;
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
+          const float x = slot(3, g);
+          scale[g] = slot(4, g) == -CUDART_INF_F ? 0.f : ex2((slot(4, g) - m) * c2);
+          d1 = isinf(x) || isinf(d1) ? CUDART_INF_F : fmaf(x, scale[g], d1);  // (infinite: see repair_row)
+        }
+      }
+    }
     if (ok && n > 0) {
       ok = wait(&bar.pvdone[h], (base + n - 1) & 1);
-      if (PROBE) ok = ok && wait(&bar.pvdone[1], (base + n - 1) & 1);
+      if (PROBE || STREAMS) ok = ok && wait(&bar.pvdone[STREAMS ? h ^ 1 : 1], (base + n - 1) & 1);
       tc_fence_after();
     }
     if (!ok) break;
@@ -871,16 +916,21 @@ attend_tc_kernel(Params p, const __grid_constant__ CUtensorMap kmap, const __gri
     const long long id = (long long)(t0 + tile.tok0 + r_tok) * p.Hq + hk * p.g + r_head;
     // a piece of a tile: slot 0 when it begins inside the tile, else 1
     const int piece = blockIdx.x * 2 + (w->i0 == 0);
-    const long long pid = (long long)piece * Sched<D, PROBE>::rows + h * BM + r;
+    const long long pid = (long long)piece * Sched<D, PROBE, STREAMS>::rows + (STREAMS ? 0 : h * BM) + r;
     float bad = (d1 + d2) * 0.f;  // NaN when something is not finite
-    constexpr int NO = D / NG;  // output columns per thread
+    constexpr int NO = D / NS;  // output columns per thread
 #pragma unroll 1
-    for (int c0 = sub * NO; c0 < (sub + 1) * NO; c0 += 32) {
-      uint32_t a[32], e[PROBE ? 32 : 1];
+    for (int c0 = share * NO; c0 < (share + 1) * NO; c0 += 32) {
+      uint32_t a[32], e[PROBE || STREAMS ? 32 : 1];
       if (n > 0) {
-        tmem_ld32(lanes + C::t_o + h * D + c0, a);
-        if constexpr (PROBE) tmem_ld32(lanes + C::t_o + D + c0, e);
+        tmem_ld32(lanes + C::t_o + (STREAMS ? 0 : h * D) + c0, a);
+        if constexpr (PROBE || STREAMS) tmem_ld32(lanes + C::t_o + D + c0, e);
         tmem_ld_wait();
+        if constexpr (STREAMS) {
+#pragma unroll
+          for (int u = 0; u < 32; ++u)
+            a[u] = __float_as_uint(fmaf(__uint_as_float(a[u]), scale[0], __uint_as_float(e[u]) * scale[1]));
+        }
       } else {
 #pragma unroll
         for (int u = 0; u < 32; ++u) {
@@ -917,37 +967,37 @@ attend_tc_kernel(Params p, const __grid_constant__ CUtensorMap kmap, const __gri
       }
     }
     tc_fence_before();  // these reads, before the arrivals that let the next piece's products go
-    if (there && sub == 0) {
+    if (there && share == 0) {
       if (!whole) p.part_s[pid] = make_float4(m, d1, d2, d1r);
       else if (p.lse) p.lse[id] = d1 == 0.f ? -CUDART_INF_F : (m * c2 + log2f(d1)) * kLn2;
     }
     if (!whole) {
       if (tid == 0) p.pieces[piece] = make_int4(w->b, w->tile, hk, 1);
       give_back(k);
-      if (NG > 1) ok = exchange();  // the sums have been read
+      if (NS > 1) ok = exchange();  // the sums have been read, and the accumulators
       continue;
     }
     // Rows that are not finite, again by themselves: once every group has written its columns, by the
     // first.
-    if (NG > 1) {
-      ok = exchange();  // the sums have been read
+    if (NS > 1) {
+      ok = exchange();  // the sums have been read, and the accumulators
       if (!ok) break;
-      slot(3, sub) = bad;
+      slot(3, share) = bad;
       ok = exchange();
       bad = 0.f;
 #pragma unroll
-      for (int g = 0; g < NG; ++g) bad += slot(3, g);
+      for (int g = 0; g < NS; ++g) bad += slot(3, g);
     }
-    unsigned again = __ballot_sync(0xffffffffu, ok && there && !(bad == 0.f) && sub == 0);
+    unsigned again = __ballot_sync(0xffffffffu, ok && there && !(bad == 0.f) && share == 0);
     while (again) {
-      const int l = __ffs(again) - 1, row = (warp & 3) * 32 + l, tk = h * per + row / p.g;
+      const int l = __ffs(again) - 1, row = (warp & 3) * 32 + l, tk = (STREAMS ? 0 : h * per) + row / p.g;
       again &= again - 1;
       const Seq sq{t0, w->seq_n, w->len, w->first};
       repair_row<__nv_bfloat16, KT>(p, sq, w->b, tile.p0, tile.p1, t0 + tile.tok0 + tk, hk * p.g + row % p.g,
                                     __shfl_sync(0xffffffffu, d1, l));
     }
     give_back(k);
-    if (NG > 1 && ok) ok = exchange();  // and these
+    if (NS > 1 && ok) ok = exchange();  // and these
     }
   }
 
@@ -960,20 +1010,21 @@ attend_tc_kernel(Params p, const __grid_constant__ CUtensorMap kmap, const __gri
   }
 }
 
-// The pieces of a tile that was cut: block x joins the tile whose first piece CTA x has (slot 1); the
-// next CTAs' slots 0 continue it. One warp per row, blocks y apart.
-template <int D, bool PROBE>
+// The pieces of a tile that was cut: blocks y join the tile whose first piece CTA y has (slot 1); the
+// next CTAs' slots 0 continue it. One warp per row, blocks x apart: neighbouring blocks go to different SMs, and
+// the few tiles that were cut are spread over all of them.
+template <int D, bool PROBE, bool STREAMS>
 __global__ void __launch_bounds__(256, 4) join_tc_kernel(Params p) {
-  using C = Cfg<D, PROBE>;
-  constexpr int ROWS = Sched<D, PROBE>::rows, VC = D / 32;
+  using C = Cfg<D, PROBE, STREAMS>;
+  constexpr int ROWS = Sched<D, PROBE, STREAMS>::rows, VC = D / 32;
   wait_previous();
-  const int4 first = p.pieces[blockIdx.x * 2 + 1];
+  const int4 first = p.pieces[blockIdx.y * 2 + 1];
   if (!first.w) return;
   const int lane = threadIdx.x & 31;
   int n = 1;
   for (;; n += 32) {  // the CTAs that continue it, 32 looked at together
-    const int c = blockIdx.x + n + lane;
-    const int4 x = c < gridDim.x ? p.pieces[c * 2] : make_int4(0, 0, 0, 0);
+    const int c = blockIdx.y + n + lane;
+    const int4 x = c < gridDim.y ? p.pieces[c * 2] : make_int4(0, 0, 0, 0);
     const unsigned on = __ballot_sync(0xffffffffu, x.w && x.x == first.x && x.y == first.y && x.z == first.z);
     if (on != 0xffffffffu) {
       n += __ffs(~on) - 1;
@@ -984,8 +1035,8 @@ __global__ void __launch_bounds__(256, 4) join_tc_kernel(Params p) {
   const Seq sq = load_seq(p, b);
   const Tile tile(sq, first.y, tokens, p.parents != nullptr);
   const float c2 = p.inv_h * kLog2e;
-  auto at = [&](int i, int row) { return (long long)((blockIdx.x + i) * 2 + (i == 0)) * ROWS + row; };
-  for (int row = blockIdx.y * 8 + (threadIdx.x >> 5); row < ROWS; row += gridDim.y * 8) {
+  auto at = [&](int i, int row) { return (long long)((blockIdx.y + i) * 2 + (i == 0)) * ROWS + row; };
+  for (int row = blockIdx.x * 8 + (threadIdx.x >> 5); row < ROWS; row += gridDim.x * 8) {
     const int r = row % BM, t = row / BM * per + r / p.g;
     if (r >= per * p.g || t >= tile.ntok) continue;
     float top = -CUDART_INF_F;
@@ -1030,23 +1081,23 @@ __global__ void __launch_bounds__(256, 4) join_tc_kernel(Params p) {
   }
 }
 
-template <int D, bool PROBE, bool TREE>
+template <int D, bool PROBE, bool TREE, bool STREAMS = false>
 cudaError_t launch_tc_t(const Params& p, cudaStream_t s) {
-  using C = Cfg<D, PROBE>;
+  using C = Cfg<D, PROBE, STREAMS>;
   CUtensorMap kmap, vmap, qmap, rmap;
   cudaError_t err = encode_page_map(p, p.k, p.d, C::kt, &kmap);
   if (err == cudaSuccess) err = encode_page_map(p, p.v, p.dv, C::kt, &vmap);
   if (err == cudaSuccess) err = encode_query_map(p, p.q, &qmap);
   if (err == cudaSuccess) err = encode_query_map(p, PROBE ? p.r : p.q, &rmap);
   if (err != cudaSuccess) return err;
-  return launch(attend_tc_kernel<D, PROBE, TREE>, dim3((unsigned)p.split), C::threads, C::bytes, 1, TREE, s, p, kmap,
+  return launch(attend_tc_kernel<D, PROBE, TREE, STREAMS>, dim3((unsigned)p.split), C::threads, C::bytes, 1, TREE, s, p, kmap,
                 vmap, qmap, rmap);
 }
 
-template <int D, bool PROBE>
+template <int D, bool PROBE, bool STREAMS = false>
 TcPlan plan_t(long long tokens, int B, int Hkv, int g, long long keys) {
-  using C = Cfg<D, PROBE>;
-  using S = Sched<D, PROBE>;
+  using C = Cfg<D, PROBE, STREAMS>;
+  using S = Sched<D, PROBE, STREAMS>;
   // No more CTAs than pieces there can be.
   const long long tiles = (tokens / (BM / g * C::blocks) + B) * Hkv;
   const long long steps = (keys + C::kt - 1) / C::kt + 3;  // first tokens and window may begin and end inside tiles
@@ -1093,8 +1144,9 @@ cudaError_t encode_query_map(const Params& p, const void* q, CUtensorMap* map) {
              : cudaErrorInvalidValue;
 }
 
-TcPlan plan_tc(int D, bool probe, long long tokens, int B, int Hkv, int g, long long keys) {
+TcPlan plan_tc(int D, bool probe, bool streams, long long tokens, int B, int Hkv, int g, long long keys) {
   if (B > kMaxSeqs || g > BM) return {};
+  if (streams) return plan_t<128, false, true>(tokens, B, Hkv, g, keys);
   if (probe) return D == 128 ? plan_t<128, true>(tokens, B, Hkv, g, keys) : plan_t<64, true>(tokens, B, Hkv, g, keys);
   return D == 128 ? plan_t<128, false>(tokens, B, Hkv, g, keys) : plan_t<64, false>(tokens, B, Hkv, g, keys);
 }
@@ -1105,15 +1157,15 @@ static cudaError_t pick(const Params& p, int D, cudaStream_t s) {
   return D == 128 ? launch_tc_t<128, false, TREE>(p, s) : launch_tc_t<64, false, TREE>(p, s);
 }
 cudaError_t launch_attend_tc(const Params& p, int D, cudaStream_t s) {
+  if (p.streams) return launch_tc_t<128, false, true, true>(p, s);
   return p.parents ? pick<true>(p, D, s) : pick<false>(p, D, s);
 }
 
 cudaError_t launch_join_tc(const Params& p, int D, cudaStream_t s) {
-  auto kern = p.r ? (D == 128 ? join_tc_kernel<128, true> : join_tc_kernel<64, true>)
-                  : (D == 128 ? join_tc_kernel<128, false> : join_tc_kernel<64, false>);
-  // Blocks to a cut tile: with few rows to a warp its loads' latencies do not add up (256 nodes at 32768, 8
-  // heads, ends from a cold L2: 18 us with 8 blocks, 14 with 32).
-  return launch(kern, dim3((unsigned)p.split, 32), 256, 0, 1, true, s, p);
+  auto kern = p.r ? (D == 128 ? join_tc_kernel<128, true, false> : join_tc_kernel<64, true, false>)
+                  : (D == 128 ? join_tc_kernel<128, false, false> : join_tc_kernel<64, false, false>);
+  if (p.streams) kern = join_tc_kernel<128, false, true>;
+  return launch(kern, dim3(16, (unsigned)p.split), 256, 0, 1, true, s, p);
 }
 
 }  // namespace paged
