@@ -128,11 +128,12 @@ struct Plan {
 // with 2, 30 with 4; 62 of 12k to 18k, 2 heads, 1.00 ms as it takes, 1.21 with 2, 1.29 with 64; 7 of 16k to
 // 24k, 96 us with 64, 184 with 16. It is not always the best: 34 of 10k, one tile each, with weights, 178 us,
 // 146 with 20; 10 of 11k to 23k with weights 224, 190 with 20.
-int f32_splits(long long tiles, long long keys, long long rows, int D, bool probe) {
+int f32_splits(long long tiles, long long keys, long long rows, int D, bool probe, bool tree) {
   if (tiles <= 0) return 1;
   const double rate = 8.0 * 16 / (rows < 4 ? 4 : rows > 16 ? 16 : rows) * 128 / D * (probe ? 1 : 1.6);  // keys a us
   const double start = 8 * rate, join = 4 * rate;
-  long long most = keys / 128 < 64 ? keys / 128 : 64;
+  const long long rounds_of_all = tree ? (keys + 127) / 128 : keys / 128;
+  long long most = rounds_of_all < 64 ? rounds_of_all : 64;
   if (most > 16 * 304 / tiles) most = 16 * 304 / tiles;
   int best = 1;
   double least = 0;
@@ -183,7 +184,7 @@ Plan make_plan(const lla_paged_cache* c, const lla_paged_query* a, bool tree) {
     if (n > keys / least) n = keys / least;
     return n < 1 ? 1 : n > 512 ? 512 : (int)n;
   };
-  pl.tree = tree && (c->dtype == LLA_F32 || pl.tiles);
+  pl.tree = tree && (c->dtype == LLA_F32 ? max_new > kRowsNodes : pl.tiles);
   if (pl.tree) {
     pl.words = (int)((max_new + 31) / 32);
     pl.bits = take((size_t)a->tokens * pl.words * sizeof(uint32_t));
@@ -193,7 +194,7 @@ Plan make_plan(const lla_paged_cache* c, const lla_paged_query* a, bool tree) {
     pl.f32 = f32_tiles(a->tokens, max_new, c->num_seqs, g);
     // (the bound counts a part tile for every sequence: as likely as not there is one)
     const long long likely = pl.f32 - (pl.f32 > 2 * c->num_seqs ? c->num_seqs / 2 : 0);
-    pl.tiles_split = f32_splits(likely * c->kv_heads, keys, rows, pl.D, a->r != nullptr);
+    pl.tiles_split = f32_splits(likely * c->kv_heads, keys, rows, pl.D, a->r != nullptr, tree);
     if (pl.tiles_split > kRowsCluster) {
       const size_t all = (size_t)a->tokens * a->q_heads * pl.tiles_split;
       pl.tiles_s = take(all * sizeof(float4));

@@ -23,6 +23,8 @@
 // 3.8k, 4 heads of 128, 0.71 ms (1.13, tiles of 64 rows); 3 sequences of up to 37 new tokens and 2047
 // positions, 6 heads over 2, d 64, dv 32, with a probe and weights, 22 us (47) in two launches. Eight warps
 // an SM (registers and shared memory) wait for their own instructions' results most of the time.
+#include <type_traits>
+
 #include "lla_paged_rows.cuh"
 
 namespace lla {
@@ -55,11 +57,15 @@ __device__ __forceinline__ void load2(const void* at, uint64_t& a, uint64_t& b) 
   b = x.y;
 }
 
+struct Nodes {  // of a small tree
+  uint64_t bits[kRowsNodes];
+  int pos[kRowsNodes];
+};
 // A tile of nrows <= RT rows over this block's part of its keys: leaves the warps' sums for the join. TREE: the
-// new tokens are a tree's nodes, whose bits and depths the launch before this one writes.
+// new tokens are a tree's nodes; of more than kRowsNodes the launch before this one writes bits and depths.
 template <int D, int RT, bool PROBE, bool TREE>
 __device__ __forceinline__ void attend_tile(const Params& p, const Seq& sq, const Rows& rows, int nrows, int b, int hk,
-                                            int part, uint8_t* smem, float4 (&stats)[NW][16]) {
+                                            int part, uint8_t* smem, float4 (&stats)[NW][16], Nodes* nodes) {
   using C = Cfg<D, RT, PROBE>;
   constexpr int RG = RT / 4, KL = 32 / RG;  // row groups; lanes of one
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, p0 = rows.p0, p1 = rows.p1;
@@ -145,20 +151,22 @@ __device__ __forceinline__ void attend_tile(const Params& p, const Seq& sq, cons
       x = *reinterpret_cast<const float4*>(src + ((long long)(rows.t0 + r / rows.width) * p.Hq + rows.h0 + r % rows.width) * p.d + c);
     *reinterpret_cast<float4*>(qs + (br * RT + r) * C::qp + c) = x;
   }
+  const bool small = TREE && sq.n <= kRowsNodes;
+  if (TREE && small && warp == NW - 1) small_tree(p, sq, nodes->bits, nodes->pos);
   __syncthreads();
 
   // Rows i * RG + rg of this lane, keys kl + KL kk of a step. The weights of a key lie as
   // [rg][i], so slot rg * 4 + i of the second product is row i * RG + rg.
   const int rg = lane / KL, kl = lane % KL;
   int pos[4], token[4];
-  if (TREE) wait_previous();
+  if (TREE && !small) wait_previous();
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const int r = i * RG + rg;
     pos[i] = r < nrows ? p0 + r / rows.width : p1;  // rows past the end are not written
     if constexpr (TREE) {
       token[i] = rows.t0 + min(r, nrows - 1) / rows.width;
-      pos[i] = p0 + p.depth[token[i]];
+      pos[i] = small ? nodes->pos[token[i] - sq.t0] : p0 + p.depth[token[i]];
     }
   }
   const float c2 = p.inv_h * kLog2e, slack = fminf(8.f / c2, 1e38f);
@@ -243,7 +251,13 @@ __device__ __forceinline__ void attend_tile(const Params& p, const Seq& sq, cons
         unpair(s2[i][k], lo, hi);
         x[i][k] = lo + hi;
         const int key = kl + KL * k, j = (key < KT ? cur.j[0] : cur.j[1]) + (key & (KT - 1));
-        if (!full && !(TREE ? node_sees(p, p0, token[i], pos[i], j) : visible(p, pos[i], j))) x[i][k] = -CUDART_INF_F;
+        if (!full) {
+          bool see;
+          if (!TREE) see = visible(p, pos[i], j);
+          else if (small && j >= p0) see = j - p0 < kRowsNodes && (nodes->bits[token[i] - sq.t0] >> (j - p0) & 1u);
+          else see = node_sees(p, p0, token[i], pos[i], j);
+          if (!see) x[i][k] = -CUDART_INF_F;
+        }
         top = fmaxf(top, x[i][k]);
       }
       grew |= top > m[i] + slack;
@@ -383,13 +397,16 @@ __global__ void __launch_bounds__(NW * 32, 2) attend_f32_kernel(Params p) {
   extern __shared__ __align__(1024) uint8_t smem[];
   __shared__ float4 stats[NW][16];
   __shared__ float4 fin_stats[16];
+  __shared__ std::conditional_t<TREE, Nodes, int> nodes_s;
+  Nodes* nodes = nullptr;
+  if constexpr (TREE) nodes = &nodes_s;
   // The parts of a tile follow one another: clusters are made of neighbours.
   const int index = blockIdx.x / p.split, part = blockIdx.x % p.split, hk = index % p.Hkv;
   const int per = max(1, kF32Rows / p.g), slices = (p.g + kF32Rows - 1) / kF32Rows;  // tokens a tile; tiles a token
   let_next();
   // Sequences of more rows than p.hi (beyond max_new) have no tiles here, since the grid was not sized for
   // them: they are reported.
-  if (TREE && blockIdx.x == 0) wait_previous();  // the end of this grid is the end of both, whatever the others do
+  if (TREE && p.bits && blockIdx.x == 0) wait_previous();  // the end of this grid is the end of both, whatever the others do
   if (blockIdx.x == 0)
     for (int i = threadIdx.x; i < p.B; i += NW * 32) {
       const int n = load_seq(p, i).n;
@@ -403,9 +420,9 @@ __global__ void __launch_bounds__(NW * 32, 2) attend_f32_kernel(Params p) {
   const int p0 = sq.first + tok0;
   const Rows rows{sq.t0 + tok0, TREE ? sq.first : p0, p0 + ntok - 1, min(p.g - u0, kF32Rows), hk * p.g + u0};
   const int nrows = ntok * rows.width;
-  if (nrows <= 4) attend_tile<D, 4, PROBE, TREE>(p, sq, rows, nrows, b, hk, part, smem, stats);
-  else if (nrows <= 8) attend_tile<D, 8, PROBE, TREE>(p, sq, rows, nrows, b, hk, part, smem, stats);
-  else attend_tile<D, 16, PROBE, TREE>(p, sq, rows, nrows, b, hk, part, smem, stats);
+  if (nrows <= 4) attend_tile<D, 4, PROBE, TREE>(p, sq, rows, nrows, b, hk, part, smem, stats, nodes);
+  else if (nrows <= 8) attend_tile<D, 8, PROBE, TREE>(p, sq, rows, nrows, b, hk, part, smem, stats, nodes);
+  else attend_tile<D, 16, PROBE, TREE>(p, sq, rows, nrows, b, hk, part, smem, stats, nodes);
   __syncthreads();
   using C = Cfg<D, kF32Rows, PROBE>;
   const float* os = reinterpret_cast<const float*>(smem);
@@ -479,7 +496,7 @@ cudaError_t launch_t(const Params& p, long long tiles, cudaStream_t s) {
   if (blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
   const bool cluster = p.split > 1 && p.split <= kRowsCluster;
   return launch(attend_f32_kernel<D, PROBE, TREE>, dim3((unsigned)blocks), NW * 32, Cfg<D, kF32Rows, PROBE>::bytes,
-                cluster ? p.split : 1, TREE, s, p);
+                cluster ? p.split : 1, TREE && p.bits, s, p);
 }
 
 }  // namespace

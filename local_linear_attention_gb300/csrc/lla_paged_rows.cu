@@ -54,45 +54,6 @@ struct Cfg {
   static_assert(fin + 16 * D * 4 <= bytes, "join regions");
 };
 
-// The nodes of a sequence of at most 64: of each the nodes that it sees (its parent, its parent's, .. and itself,
-// less those that fell out of the window) as bits, and its position. One warp, lane l has nodes l and l + 32;
-// parents come from the other lanes, so a tree costs one load and no launch before this one's.
-__device__ __forceinline__ void small_tree(const Params& p, const Seq& sq, uint64_t* bits_of, int* pos_of) {
-  const int lane = threadIdx.x & 31, n = min(sq.n, 64);
-  int parent[2];
-  bool bad = false;
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const int i = lane + 32 * h, a = i < n ? __ldg(p.parents + sq.t0 + i) : -1;
-    bad |= a < -1 || a >= i;
-    parent[h] = a < i ? max(a, -1) : -1;
-  }
-  if (bad) atomicOr(p.status, kStatusBadIndex);
-  auto up = [&](int a) {  // whole warps call
-    const int x = __shfl_sync(0xffffffffu, parent[0], a & 31), y = __shfl_sync(0xffffffffu, parent[1], a & 31);
-    return a < 0 ? -1 : a < 32 ? x : y;
-  };
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const int i = lane + 32 * h;
-    uint64_t bits = 1ull << i;
-    int d = 0;
-    for (int a = parent[h]; __any_sync(0xffffffffu, a >= 0); a = up(a)) {
-      if (a >= 0) {
-        bits |= 1ull << a;
-        ++d;
-      }
-    }
-    if (p.window < n) {
-      int steps = 1;
-      for (int a = parent[h]; __any_sync(0xffffffffu, a >= 0); a = up(a), ++steps)
-        if (a >= 0 && steps >= p.window && sq.first + d - steps >= p.sinks) bits &= ~(1ull << a);
-    }
-    bits_of[i] = bits;
-    pos_of[i] = sq.first + d;
-  }
-}
-
 // CLUSTER: the blocks of a pair (and tile) are one cluster and join there.
 // TREE: the new tokens are a tree's nodes (64 at most), their rows in tiles of a block's, which find the keys again in L2.
 template <int D, bool PROBE, bool LOGITS, bool CLUSTER, bool TREE>
