@@ -162,14 +162,15 @@ Plan make_plan(const lla_paged_cache* c, const lla_paged_query* a, bool tree) {
   const bool tc = c->dtype == LLA_BF16 && a->path != LLA_PATH_CUDA_CORE;
   pl.D = padded(c->d > c->dv ? c->d : c->dv);
   int limit = c->dtype == LLA_F32 ? kF32Rows : rows_limit(a->r != nullptr);
-  const long long pairs_keys = pairs * keys;
   if (tree && tc) {
     // The few-rows kernel goes over the keys again for every 16 rows (8 with a probe) and the tiled one once for
-    // 128, but starts up in 7 to 10 us against 20 to 35. 8 heads, rows: few-rows / tiled us. 64, 24: 7.5 / 21 at
-    // 1000 positions, 18 / 25 at 16000, 88 / 77 at 16 x 8000; 64 rows: 8 / 21, 31 / 27, 138 / 82. Probe, 24: 8 / 32,
-    // 25 / 40, 119 / 126. 128, 24: 10 / 24, 25 / 33, 123 / 115; 64 rows: 11 / 24, 48 / 34, 230 / 116.
-    limit *= pairs_keys <= 1 << 16 ? 8 : a->r ? 3 : 2;
-    if (limit > kRowsNodes) limit = kRowsNodes;
+    // 128, but starts up in 7 to 10 us against 20 to 30. 8 heads, few-rows / tiled us at 1000 positions, at 16000 and
+    // at 16 x 8000. D = 64, 24 rows: 7.5 / 21, 18 / 25, 88 / 77; 64 rows: 8 / 21, 31 / 27, 138 / 82; 128 rows at 1000:
+    // 14 / 22. With a probe 24 rows: 8 / 32, 25 / 40, 119 / 126; 128 rows at 1000: 15 / 33. D = 128, 24 rows: 10 / 24,
+    // 25 / 33, 123 / 115; 64 rows: 11 / 21, 48 / 29, 230 / 100.
+    if (pairs * keys * (pl.D / 64) * (a->r ? 2 : 1) <= 1 << 16) limit = 128;
+    else limit *= a->r ? 3 : 2;
+    if (limit > kRowsNodes * g) limit = kRowsNodes * g;
   }
   const int branches = a->r ? 2 : 1;
   // The few-rows kernel, unless the counts leave no sequence for it: a sequence of at most limit / g

@@ -1011,73 +1011,120 @@ attend_tc_kernel(Params p, const __grid_constant__ CUtensorMap kmap, const __gri
 }
 
 // The pieces of a tile that was cut: blocks y join the tile whose first piece CTA y has (slot 1); the
-// next CTAs' slots 0 continue it. One warp per row, blocks x apart: neighbouring blocks go to different SMs, and
-// the few tiles that were cut are spread over all of them.
+// next CTAs' slots 0 continue it. A thread has kJoinCols columns of a row, so that what a row costs whatever its
+// size (its place, the pieces' factors) is paid by few threads, and blocks x apart of a tile go to different SMs. (16 trees
+// at 4k to 16k, nearly every tile cut: 14.4 us with a warp to a row, JOIN_US so.)
+constexpr int kJoinCols = 16;
 template <int D, bool PROBE, bool STREAMS>
-__global__ void __launch_bounds__(256, 4) join_tc_kernel(Params p) {
+__global__ void __launch_bounds__(256) join_tc_kernel(Params p) {
   using C = Cfg<D, PROBE, STREAMS>;
-  constexpr int ROWS = Sched<D, PROBE, STREAMS>::rows, VC = D / 32;
+  constexpr int ROWS = Sched<D, PROBE, STREAMS>::rows, TR = D / kJoinCols;  // threads of a row
   wait_previous();
-  const int4 first = p.pieces[blockIdx.y * 2 + 1];
-  if (!first.w) return;
   const int lane = threadIdx.x & 31;
+  auto piece = [&](int c) { return c < gridDim.y ? p.pieces[c * 2] : make_int4(0, 0, 0, 0); };
+  const int4 first = p.pieces[blockIdx.y * 2 + 1];
+  int4 next = piece(blockIdx.y + 1 + lane);  // with the first: one latency
+  if (!first.w) return;
   int n = 1;
-  for (;; n += 32) {  // the CTAs that continue it, 32 looked at together
-    const int c = blockIdx.y + n + lane;
-    const int4 x = c < gridDim.y ? p.pieces[c * 2] : make_int4(0, 0, 0, 0);
-    const unsigned on = __ballot_sync(0xffffffffu, x.w && x.x == first.x && x.y == first.y && x.z == first.z);
+  for (;;) {  // the CTAs that continue it, 32 looked at together
+    const unsigned on =
+        __ballot_sync(0xffffffffu, next.w && next.x == first.x && next.y == first.y && next.z == first.z);
     if (on != 0xffffffffu) {
       n += __ffs(~on) - 1;
       break;
     }
+    n += 32;
+    next = piece(blockIdx.y + n + lane);
   }
+  // The pieces' results of this row, the next ones on their way beside the sequence's lengths.
+  const int row = blockIdx.x * (256 / TR) + threadIdx.x / TR, col = threadIdx.x % TR * kJoinCols;
+  auto at = [&](int i) { return (long long)((blockIdx.y + i) * 2 + (i == 0)) * ROWS + row; };
+  constexpr int CH = PROBE ? 2 : 4;  // pieces at once
+  const bool cols = col < p.dv;
+  float4 st[CH], o[CH][kJoinCols / 4], e[PROBE ? CH : 1][kJoinCols / 4];
+  auto load = [&](int c) {
+#pragma unroll
+    for (int i = 0; i < CH; ++i) {
+      if (c + i >= n) break;
+      st[i] = p.part_s[at(c + i)];
+      if (!cols) continue;
+      const float4* src = reinterpret_cast<const float4*>(p.part_o + at(c + i) * (PROBE ? 2 : 1) * D + col);
+#pragma unroll
+      for (int u = 0; u < kJoinCols / 4; ++u) {
+        o[i][u] = src[u];
+        if constexpr (PROBE) e[i][u] = src[D / 4 + u];
+      }
+    }
+  };
+  load(0);
+  float top = -CUDART_INF_F;
+  for (int i = threadIdx.x % TR; i < n; i += TR) top = fmaxf(top, p.part_s[at(i)].x);
+#pragma unroll
+  for (int i = 1; i < TR; i <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, i));
   const int per = BM / p.g, tokens = C::blocks * per, b = first.x, hk = first.z;
   const Seq sq = load_seq(p, b);
   const Tile tile(sq, first.y, tokens, p.parents != nullptr);
   const float c2 = p.inv_h * kLog2e;
-  auto at = [&](int i, int row) { return (long long)((blockIdx.y + i) * 2 + (i == 0)) * ROWS + row; };
-  for (int row = blockIdx.x * 8 + (threadIdx.x >> 5); row < ROWS; row += gridDim.x * 8) {
-    const int r = row % BM, t = row / BM * per + r / p.g;
-    if (r >= per * p.g || t >= tile.ntok) continue;
-    float top = -CUDART_INF_F;
-    for (int i = lane; i < n; i += 32) top = fmaxf(top, p.part_s[at(i, row)].x);
-#pragma unroll
-    for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+  const int r = row % BM, t = row / BM * per + r / p.g;
+  const bool there = r < per * p.g && t < tile.ntok;  // the other rows hold anything
+  float s1 = 0.f, s2 = 0.f, s1r = 0.f, bad = 0.f;
+  const int token = sq.t0 + tile.tok0 + t, head = hk * p.g + r % p.g;
+  if (there) {
     const float ref = top == -CUDART_INF_F ? 0.f : top * c2;
-    float s1 = 0.f, s2 = 0.f, s1r = 0.f, o1[VC] = {}, o2[VC] = {};
-#pragma unroll 4
-    for (int i = 0; i < n; ++i) {
-      const float4 st = p.part_s[at(i, row)];
-      const float f = ex2(fmaf(st.x, c2, -ref));
-      s1 = isinf(st.y) ? st.y : fmaf(st.y, f, s1);  // (infinite: see repair_row; times f it might be NaN)
-      s2 = fmaf(st.z, f, s2);
-      s1r = fmaf(st.w, f, s1r);
-      const float* src = p.part_o + at(i, row) * (PROBE ? 2 : 1) * D + lane * VC;
-      if (lane * VC < p.dv) {
+    float o1[kJoinCols] = {}, o2[PROBE ? kJoinCols : 1] = {};
+    for (int c = 0; c < n; c += CH) {
+      if (c) load(c);
 #pragma unroll
-        for (int c = 0; c < VC; ++c) {
-          o1[c] = fmaf(src[c], f, o1[c]);
-          if (PROBE) o2[c] = fmaf(src[D + c], f, o2[c]);
+      for (int i = 0; i < CH; ++i) {
+        if (c + i >= n) break;
+        const float f = ex2(fmaf(st[i].x, c2, -ref));
+        s1 = isinf(st[i].y) ? st[i].y : fmaf(st[i].y, f, s1);  // (infinite: see repair_row; times f it might be NaN)
+        s2 = fmaf(st[i].z, f, s2);
+        s1r = fmaf(st[i].w, f, s1r);
+        if (!cols) continue;
+#pragma unroll
+        for (int u = 0; u < kJoinCols; u += 4) {
+          const float4 x = o[i][u / 4];
+          o1[u] = fmaf(x.x, f, o1[u]);
+          o1[u + 1] = fmaf(x.y, f, o1[u + 1]);
+          o1[u + 2] = fmaf(x.z, f, o1[u + 2]);
+          o1[u + 3] = fmaf(x.w, f, o1[u + 3]);
+          if constexpr (PROBE) {
+            const float4 y = e[i][u / 4];
+            o2[u] = fmaf(y.x, f, o2[u]);
+            o2[u + 1] = fmaf(y.y, f, o2[u + 1]);
+            o2[u + 2] = fmaf(y.z, f, o2[u + 2]);
+            o2[u + 3] = fmaf(y.w, f, o2[u + 3]);
+          }
         }
       }
     }
-    const int token = sq.t0 + tile.tok0 + t, head = hk * p.g + r % p.g;
     const float norm = PROBE ? s1r : s1;
     const float inv = norm == 0.f ? 0.f : 1.f / norm, f1 = (1.f + s2 * inv) * inv;
-    __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.out) + ((long long)token * p.Hq + head) * p.dv + lane * VC;
-    float bad = (s1 + s2) * 0.f;
+    bad = (s1 + s2) * 0.f;
+    uint32_t w[kJoinCols / 2];
 #pragma unroll
-    for (int c = 0; c < VC; c += 2) {
-      const float y0 = PROBE ? fmaf(o1[c], f1, -o2[c] * inv) : o1[c] * inv;
-      const float y1 = PROBE ? fmaf(o1[c + 1], f1, -o2[c + 1] * inv) : o1[c + 1] * inv;
+    for (int c = 0; c < kJoinCols; c += 2) {
+      const float y0 = PROBE ? fmaf(o1[c], f1, -o2[PROBE ? c : 0] * inv) : o1[c] * inv;
+      const float y1 = PROBE ? fmaf(o1[c + 1], f1, -o2[PROBE ? c + 1 : 0] * inv) : o1[c + 1] * inv;
       bad += (y0 + y1) * 0.f;
-      if (lane * VC < p.dv) *reinterpret_cast<uint32_t*>(dst + c) = pack_bf16(y0, y1);
+      w[c / 2] = pack_bf16(y0, y1);
     }
-    if (p.lse && lane == 0)
+    if (cols) {
+      uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out) + ((long long)token * p.Hq + head) * p.dv + col);
+#pragma unroll
+      for (int u = 0; u < kJoinCols / 8; ++u) dst[u] = make_uint4(w[4 * u], w[4 * u + 1], w[4 * u + 2], w[4 * u + 3]);
+    }
+    if (p.lse && col == 0)
       p.lse[(long long)token * p.Hq + head] = s1 == 0.f ? -CUDART_INF_F : (top * c2 + log2f(s1)) * kLn2;
-    if (__any_sync(0xffffffffu, !(bad == 0.f))) {
-      repair_row<__nv_bfloat16, C::kt>(p, sq, b, tile.p0, tile.p1, token, head, s1);
-    }
+  }
+  // Rows that are not finite, again by themselves, once the warp has written all of their columns.
+  unsigned again = __ballot_sync(0xffffffffu, there && !(bad == 0.f));
+  while (again) {
+    const int l = (__ffs(again) - 1) / TR * TR;  // a row's first lane
+    again &= ~(((1u << TR) - 1u) << l);
+    repair_row<__nv_bfloat16, C::kt>(p, sq, b, tile.p0, tile.p1, __shfl_sync(0xffffffffu, token, l),
+                                     __shfl_sync(0xffffffffu, head, l), __shfl_sync(0xffffffffu, s1, l));
   }
 }
 
@@ -1165,7 +1212,8 @@ cudaError_t launch_join_tc(const Params& p, int D, cudaStream_t s) {
   auto kern = p.r ? (D == 128 ? join_tc_kernel<128, true, false> : join_tc_kernel<64, true, false>)
                   : (D == 128 ? join_tc_kernel<128, false, false> : join_tc_kernel<64, false, false>);
   if (p.streams) kern = join_tc_kernel<128, false, true>;
-  return launch(kern, dim3(16, (unsigned)p.split), 256, 0, 1, true, s, p);
+  const int rows = p.streams || p.r || D == 64 ? BM : 2 * BM;
+  return launch(kern, dim3(rows * (D / kJoinCols) / 256, (unsigned)p.split), 256, 0, 1, true, s, p);
 }
 
 }  // namespace paged
