@@ -479,36 +479,40 @@ class PagedCache:
                  "dtype", "device", "_packed", "_index")
 
     def __init__(self, k_pages, v_pages, page_table, lens, mass=None):
-        k_shape, v_shape, device, dtype = k_pages.shape, v_pages.shape, k_pages.device, k_pages.dtype
-        tensors = (k_pages, v_pages, page_table, lens) if mass is None else (k_pages, v_pages, page_table, lens, mass)
-        if len(k_shape) != 4 or v_shape[:3] != k_shape[:3] or len(v_shape) != 4:
+        device, dtype, index = k_pages.device, k_pages.dtype, k_pages.get_device()  # -1: not on a CUDA device
+        code = DTYPE_CODES.get(dtype)
+        try:
+            num_pages, kv_heads, page, d = k_pages.shape
+            v_heads = v_pages.shape
+            dv = v_heads[3]
+        except (ValueError, IndexError):
+            num_pages = v_heads = None
+        if num_pages is None or v_heads != (num_pages, kv_heads, page, dv):
             raise ValueError("expected k_pages [num_pages, kv_heads, page_size, d] and v_pages "
                              "[num_pages, kv_heads, page_size, dv]")
-        code = DTYPE_CODES.get(dtype)
         if code is None or v_pages.dtype != dtype:
             raise ValueError("k_pages and v_pages must share one dtype: float32 or bfloat16")
         t_shape = page_table.shape
         if len(t_shape) != 2 or page_table.dtype != torch.int32:
             raise ValueError("page_table must be int32 [num_seqs, max_pages]")
-        if lens.dtype != torch.int32 or lens.shape != t_shape[:1]:
+        num_seqs, max_pages = t_shape
+        if lens.dtype != torch.int32 or lens.shape != (num_seqs,):
             raise ValueError("lens must be int32 [num_seqs]")
-        if mass is not None and (mass.shape != k_shape[:3] or mass.dtype != torch.float32):
+        if mass is not None and (mass.shape != (num_pages, kv_heads, page) or mass.dtype != torch.float32):
             raise ValueError("mass must be float32 [num_pages, kv_heads, page_size]")
-        index = k_pages.get_device()  # -1: not on a CUDA device
         if index < 0:
             raise ValueError("liblla runs on CUDA tensors only")
-        for t in tensors:
-            if t.get_device() != index or not t.is_contiguous():
-                raise ValueError("the cache's tensors must be contiguous, on one device")
-        num_pages, self.kv_heads, page, self.d = k_shape
-        self.num_seqs, max_pages = t_shape
-        self.dv = v_shape[3]
+        if not (k_pages.is_contiguous() and v_pages.is_contiguous() and page_table.is_contiguous() and
+                lens.is_contiguous() and v_pages.get_device() == index and page_table.get_device() == index and
+                lens.get_device() == index and (mass is None or mass.is_contiguous() and mass.get_device() == index)):
+            raise ValueError("the cache's tensors must be contiguous, on one device")
+        self.num_seqs, self.kv_heads, self.d, self.dv = num_seqs, kv_heads, d, dv
         self.k_pages, self.v_pages, self.mass = k_pages, v_pages, mass
         self.page_table, self.lens, self.dtype, self.device, self._index = page_table, lens, dtype, device, index
         self._packed = _CACHE.pack(
             k_pages.data_ptr(), v_pages.data_ptr(), 0 if mass is None else mass.data_ptr(),
-            page_table.data_ptr(), lens.data_ptr(), self.num_seqs, self.kv_heads, page, max_pages,
-            num_pages, self.d, self.dv, code, 0, 0)
+            page_table.data_ptr(), lens.data_ptr(), num_seqs, kv_heads, page, max_pages,
+            num_pages, d, dv, code, 0, 0)
 
 
 def _paged_rows(name, x, cache, shape):
