@@ -32,6 +32,11 @@
 // over 8: 1.4 PFLOP/s in a row of calls); at D = 64 the N = 64 products (about 59 cycles for 32 of work) and
 // the same chain, which is longer with a probe (prompts B4 T4096, 8 heads of 64: 99 us, with a probe 186); at
 // D = 128 with a probe the chain of the one block a CTA has (8 heads of 128: 361 us, tensor pipe 42 % active).
+// Trees of drafted tokens (TREE) run here too: a masked step looks a row's nodes up as bits that the launch before
+// this one finds. With at most 128 rows to a sequence a CTA takes two key tiles at a time (STREAMS): 19 trees of
+// 32 nodes at 10240, 32 heads over 8 of 128: 134 us, 89 % of the copy bandwidth (152 with an empty second row
+// block); 16 of 4k to 16k 141 us in three launches, of which the cut tiles' join is the last 13; 256 nodes at 32768, where
+// the same chain as a chunk's bounds it, 122 us.
 // All mbarrier waits are bounded.
 #include <type_traits>
 
@@ -374,7 +379,7 @@ attend_tc_kernel(Params p, const __grid_constant__ CUtensorMap kmap, const __gri
       // Whole tiles: the CTAs that the last row leaves out wait for about the shortest tile.
       const long long rows = (nt + gridDim.x - 1) / gridDim.x;
       // (Trees: a sequence's tiles all see its whole prefix, so few sequences of unlike lengths leave CTAs idle
-      // behind the longest. 16 of 4k to 16k, 8 heads of 128, a tile each: 201 us whole, 163 cut.)
+      // behind the longest. 16 of 4k to 16k, 8 heads of 128, a tile each: 201 us whole, 141 cut.)
       const bool whole = TREE ? (rows * longest - Sched<D, PROBE, STREAMS>::kCut) * gridDim.x <= w
                               : (rows * gridDim.x - nt) * least <= (long long)Sched<D, PROBE, STREAMS>::kCut * gridDim.x;
       if (whole) {
@@ -1013,7 +1018,7 @@ attend_tc_kernel(Params p, const __grid_constant__ CUtensorMap kmap, const __gri
 // The pieces of a tile that was cut: blocks y join the tile whose first piece CTA y has (slot 1); the
 // next CTAs' slots 0 continue it. A thread has kJoinCols columns of a row, so that what a row costs whatever its
 // size (its place, the pieces' factors) is paid by few threads, and blocks x apart of a tile go to different SMs. (16 trees
-// at 4k to 16k, nearly every tile cut: 14.4 us with a warp to a row, JOIN_US so.)
+// at 4k to 16k, nearly every tile cut: 14.4 us with a warp to a row, 9.3 so.)
 constexpr int kJoinCols = 16;
 template <int D, bool PROBE, bool STREAMS>
 __global__ void __launch_bounds__(256) join_tc_kernel(Params p) {
