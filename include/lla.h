@@ -569,7 +569,7 @@ int lla_paged_grow(const lla_paged_cache* cache, const int* starts, int* refs, i
  * Copies whole pages, keys, values and (where both caches have it) mass: page pairs[i][0] of `from` to page
  * pairs[i][1] of `to`, count pairs in device memory, 8-byte aligned; a pair with a negative number is skipped. The caches (which may be
  * one) agree in kv_heads, page_size, d, dv and type; tables and lens are not used. No page may be written
- * twice, or written and read, in one call.
+ * twice, or written and read, in one call. Fewer than 2^31 pieces of 32 KB (LLA_ERR_UNSUPPORTED).
  */
 int lla_paged_copy(const lla_paged_cache* from, const lla_paged_cache* to, const int* pairs, int count, void* stream);
 
@@ -580,7 +580,7 @@ int lla_paged_copy(const lla_paged_cache* from, const lla_paged_cache* to, const
  * first + their number is what lla_paged_free is then given, once all layers are done: lens and table stay as
  * they are here. A path that does not rise or leaves the new tokens is reported and nothing of it kept. The
  * moved positions' pages must be the sequence's own (as after lla_paged_grow). tokens: of the batch, as in
- * lla_paged_append.
+ * lla_paged_append. keep is not the cache's lens.
  */
 int lla_paged_compact(const lla_paged_cache* cache, const int* starts, int tokens, const int* path, int max_path, int* keep,
                       void* stream);

@@ -586,8 +586,8 @@ int lla_paged_copy(const lla_paged_cache* from, const lla_paged_cache* to, const
     return LLA_ERR_INVALID_ARG;
   Params p = cache_params(from), t = cache_params(to);
   if (device_status(&p.status) != cudaSuccess) return LLA_ERR_CUDA;
-  return launch_copy(p, t, pairs, count, from->dtype, static_cast<cudaStream_t>(stream)) == cudaSuccess ? LLA_OK
-                                                                                                       : LLA_ERR_CUDA;
+  const cudaError_t err = launch_copy(p, t, pairs, count, from->dtype, static_cast<cudaStream_t>(stream));
+  return err == cudaSuccess ? LLA_OK : err == cudaErrorInvalidConfiguration ? LLA_ERR_UNSUPPORTED : LLA_ERR_CUDA;
 }
 
 int lla_paged_compact(const lla_paged_cache* cache, const int* starts, int tokens, const int* path, int max_path, int* keep,
@@ -599,7 +599,8 @@ int lla_paged_compact(const lla_paged_cache* cache, const int* starts, int token
   if (cache->num_seqs == 0) return LLA_OK;
   st = check_cache_pointers(cache, false);
   if (st != LLA_OK) return st;
-  if (!aligned16(cache->mass) || !starts || !keep || (max_path > 0 && !path)) return LLA_ERR_INVALID_ARG;
+  if (!aligned16(cache->mass) || !starts || !keep || keep == cache->lens || (max_path > 0 && !path))
+    return LLA_ERR_INVALID_ARG;
   Params p = cache_params(cache);
   if (device_status(&p.status) != cudaSuccess) return LLA_ERR_CUDA;
   p.starts = starts;

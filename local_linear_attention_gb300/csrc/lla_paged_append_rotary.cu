@@ -142,10 +142,11 @@ cudaError_t launch_t(const Params& p, const rotary::Turn& turn, int layout, Rows
     // heads of 128: 8.4 us with a thousand, 6.1 so).
     const long long threads = (long long)p.tokens * a.items, per = threads * a.units / (152 * 512);
     a.per = per < 1 ? 1 : per > 8 ? 8 : (int)per;
+    if (a.per < (a.units + p.Hkv + 65532) / 65533) a.per = (a.units + p.Hkv + 65532) / 65533;  // (the grid's limit)
     const long long blocks = (threads + 255) / 256;
     a.groups = (a.units + a.per - 1) / a.per;
     const long long groups = a.groups + (p.Hkv + a.per - 1) / a.per;
-    if (blocks > 0x7fffffffLL || groups > 65535) return;
+    if (blocks > 0x7fffffffLL) return;
     append_rotary_kernel<I, T><<<dim3((unsigned)blocks, (unsigned)groups), 256, 0, s>>>(turn, p, a);
     count_launch();
     err = cudaGetLastError();

@@ -85,12 +85,14 @@ struct Grow {
   int last[kMaxGrow];     // the page that b copies because others hold it too; -1: none
   int sums[kGrowWarps];   // free pages of the warps before
   int free;               // and of this block
+  long long need;         // of all sequences; `off` holds where it does not pass what is free
 };
 
-__device__ __forceinline__ int warp_incl(int x) {
+template <typename T>
+__device__ __forceinline__ T warp_incl(T x) {
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int y = __shfl_up_sync(0xffffffffu, x, o);
+    const T y = __shfl_up_sync(0xffffffffu, x, o);
     if ((threadIdx.x & 31) >= o) x += y;
   }
   return x;
@@ -151,17 +153,21 @@ __global__ void __launch_bounds__(kGrowThreads) grow_kernel(Params p, int* table
     if (keeps >> i & 1u) g.last[b] = -1;
   __syncthreads();
   if (warp == 0) {
-    int before = 0;
+    // (in 64 bits: starts that go up and down may ask for more than there can be)
+    long long before = 0;
     for (int base = 0; base < p.B; base += 32) {
       const int b = base + lane;
-      int x = 0;
+      long long x = 0;
       if (b < p.B && g.more[b] > 0)
         x = (g.last[b] >= 0) + pages_of(p, lens[b] + g.more[b]) - g.held[b];
-      const int incl = warp_incl(x);
-      if (b < p.B) g.off[b] = before + incl - x;
+      const long long incl = warp_incl(x);
+      if (b < p.B) g.off[b] = (int)(before + incl - x);
       before += __shfl_sync(0xffffffffu, incl, 31);
     }
-    if (lane == 0) g.off[p.B] = before;
+    if (lane == 0) {
+      g.off[p.B] = (int)before;
+      g.need = before;
+    }
   } else if (warp == 1) {
     const int x = g.sums[lane], incl = warp_incl(x);
     __syncwarp();
@@ -175,11 +181,11 @@ __global__ void __launch_bounds__(kGrowThreads) grow_kernel(Params p, int* table
     if (i < rank) first += x;
     all += x;
   }
-  const int need = g.off[p.B];
-  const bool enough = need <= all;
+  const bool enough = g.need <= all;
+  const int need = enough ? (int)g.need : 0;
   cluster.sync();  // no block leaves before its sum has been read
   if (rank == 0) {
-    if (tid == 0) *left = all - need;
+    if (tid == 0) *left = (int)max(all - g.need, -2147483647LL);
     for (int b = tid; b < p.B; b += kGrowThreads) {
       if (!enough || g.last[b] < 0) copies[b] = make_int2(-1, -1);
       if (!enough) continue;

@@ -94,8 +94,9 @@ cudaError_t launch(const Turn& turn, int layout, Tensors a, cudaStream_t s) {
     const long long threads = a.rows * a.items, all = threads * a.heads;
     const long long per = all / (152 * 512);
     a.per = per < 1 ? 1 : per > 8 ? 8 : (int)per;
+    if (a.per < (a.heads + 65534) / 65535) a.per = (a.heads + 65534) / 65535;  // (the grid's limit)
     const long long blocks = (threads + 255) / 256, groups = (a.heads + a.per - 1) / a.per;
-    if (blocks > 0x7fffffffLL || groups > 65535) return;
+    if (blocks > 0x7fffffffLL) return;
     rotary_kernel<I, T><<<dim3((unsigned)blocks, (unsigned)groups), 256, 0, s>>>(turn, a);
     count_launch();
     err = cudaGetLastError();

@@ -122,3 +122,14 @@ def test_tensors_of_another_kind_or_place_are_refused(calls):  # noqa: F811
         with pytest.raises(ValueError):
             call()
     assert not calls
+
+
+def test_compact_does_not_write_the_lengths_it_reads(lla):  # noqa: F811
+    assert lla._load().lla_paged_compact(byref(lla, {}), 256, 4, 512, 2, 1280, None) == INVALID
+
+
+@pytest.mark.gpu
+def test_copy_beyond_the_grid(lla):  # noqa: F811
+    """2^30 pairs of pages of 512 KB: refused before a launch, with the device asked for its status word alone."""
+    big = byref(lla, dict(page_size=1024, kv_heads=2, d=64, dv=64))
+    assert lla._load().lla_paged_copy(big, big, 256, 1 << 30, None) == UNSUPPORTED

@@ -284,3 +284,17 @@ def test_no_sequences(lla):  # noqa: F811
     lla.lla_paged_fork(empty, some.device, ints([-1]), refs)
     lla.lla_paged_copy(empty, empty, ints([]).reshape(0, 2))
     assert some.device.lens.tolist() == [0] and refs.tolist() == [0, 1] * 5 and lla.lla_stream_status() == 0
+
+
+def test_grow_beyond_all_numbers(lla):  # noqa: F811
+    """Starts that go up and down (reported) ask for 2^31 pages and more in all: nothing changes."""
+    B, max_pages, page = 80, (1 << 26) - 1, 16
+    pool = pools(4, Hkv=1, page=page, d=16, dv=16, mass=False)
+    wide = torch.empty(B, max_pages, dtype=torch.int32, device="cuda")
+    cache = lla.PagedCache(pool[0], pool[1], wide, torch.zeros(B, dtype=torch.int32, device="cuda"))
+    refs = ints([0, 1, 0, 0])
+    most = max_pages * page
+    copies, left = lla.lla_paged_grow(cache, ints([0 if b % 2 == 0 else most for b in range(B + 1)]), refs)
+    assert lla.lla_stream_status() == 1
+    assert left.tolist() == [max(3 - 40 * max_pages, -2 ** 31 + 1)]
+    assert (copies == -1).all() and (cache.lens == 0).all() and refs.tolist() == [0, 1, 0, 0]

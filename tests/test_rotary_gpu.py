@@ -232,3 +232,17 @@ def test_binding_refusals(lla):  # noqa: F811
         lla.lla_rotary(x[..., :32].contiguous(), spec)
     with pytest.raises(lla.LlaError):
         lla.lla_rotary([x, x.clone()], spec, out=[x, x])
+
+
+def test_more_heads_than_a_grid_has_rows(lla):  # noqa: F811
+    g = torch.Generator().manual_seed(1)
+    x = torch.randn(1, 600000, 1, 16, generator=g).to(BF)
+    spec = lla.RotarySpec(16)
+    pos = torch.tensor([[7]], dtype=torch.int32)
+    check("y", lla.lla_rotary(x.cuda(), spec, positions=pos.cuda()), *turned(x, spec, pos[:, None]))
+    P = Problem([20], [1], 600000, 1, 16, 16, 16, BF, False, seed=1)
+    cache, q, _, starts = P.cuda(lla)
+    k = torch.zeros(1, 1, 16, dtype=BF, device="cuda")
+    got, _ = lla.lla_paged_append_rotary(k, k, cache, starts, spec, q)
+    check("q", got, *turned(P.q, spec, torch.tensor([[19]])))
+    assert lla.lla_stream_status() == 0
