@@ -1016,14 +1016,14 @@ attend_tc_kernel(Params p, const __grid_constant__ CUtensorMap kmap, const __gri
 }
 
 // The pieces of a tile that was cut: blocks y join the tile whose first piece CTA y has (slot 1); the
-// next CTAs' slots 0 continue it. A thread has kJoinCols columns of a row, so that what a row costs whatever its
+// next CTAs' slots 0 continue it. A thread has COLS columns of a row, so that what a row costs whatever its
 // size (its place, the pieces' factors) is paid by few threads, and blocks x apart of a tile go to different SMs. (16 trees
 // at 4k to 16k, nearly every tile cut: 14.4 us with a warp to a row, 9.3 so.)
-constexpr int kJoinCols = 16;
-template <int D, bool PROBE, bool STREAMS>
+// COLS is 16, or 4 where the tiles are few and each has many pieces: then the pieces' loads in flight count.
+template <int D, bool PROBE, bool STREAMS, int COLS>
 __global__ void __launch_bounds__(256) join_tc_kernel(Params p) {
   using C = Cfg<D, PROBE, STREAMS>;
-  constexpr int ROWS = Sched<D, PROBE, STREAMS>::rows, TR = D / kJoinCols;  // threads of a row
+  constexpr int ROWS = Sched<D, PROBE, STREAMS>::rows, TR = D / COLS;  // threads of a row
   wait_previous();
   const int lane = threadIdx.x & 31;
   auto piece = [&](int c) { return c < gridDim.y ? p.pieces[c * 2] : make_int4(0, 0, 0, 0); };
@@ -1042,11 +1042,11 @@ __global__ void __launch_bounds__(256) join_tc_kernel(Params p) {
     next = piece(blockIdx.y + n + lane);
   }
   // The pieces' results of this row, the next ones on their way beside the sequence's lengths.
-  const int row = blockIdx.x * (256 / TR) + threadIdx.x / TR, col = threadIdx.x % TR * kJoinCols;
+  const int row = blockIdx.x * (256 / TR) + threadIdx.x / TR, col = threadIdx.x % TR * COLS;
   auto at = [&](int i) { return (long long)((blockIdx.y + i) * 2 + (i == 0)) * ROWS + row; };
-  constexpr int CH = PROBE ? 2 : 4;  // pieces at once
+  constexpr int CH = (COLS == 4 ? 8 : 4) / (PROBE ? 2 : 1);  // pieces at once
   const bool cols = col < p.dv;
-  float4 st[CH], o[CH][kJoinCols / 4], e[PROBE ? CH : 1][kJoinCols / 4];
+  float4 st[CH], o[CH][COLS / 4], e[PROBE ? CH : 1][COLS / 4];
   auto load = [&](int c) {
 #pragma unroll
     for (int i = 0; i < CH; ++i) {
@@ -1055,7 +1055,7 @@ __global__ void __launch_bounds__(256) join_tc_kernel(Params p) {
       if (!cols) continue;
       const float4* src = reinterpret_cast<const float4*>(p.part_o + at(c + i) * (PROBE ? 2 : 1) * D + col);
 #pragma unroll
-      for (int u = 0; u < kJoinCols / 4; ++u) {
+      for (int u = 0; u < COLS / 4; ++u) {
         o[i][u] = src[u];
         if constexpr (PROBE) e[i][u] = src[D / 4 + u];
       }
@@ -1076,7 +1076,7 @@ __global__ void __launch_bounds__(256) join_tc_kernel(Params p) {
   const int token = sq.t0 + tile.tok0 + t, head = hk * p.g + r % p.g;
   if (there) {
     const float ref = top == -CUDART_INF_F ? 0.f : top * c2;
-    float o1[kJoinCols] = {}, o2[PROBE ? kJoinCols : 1] = {};
+    float o1[COLS] = {}, o2[PROBE ? COLS : 1] = {};
     for (int c = 0; c < n; c += CH) {
       if (c) load(c);
 #pragma unroll
@@ -1088,7 +1088,7 @@ __global__ void __launch_bounds__(256) join_tc_kernel(Params p) {
         s1r = fmaf(st[i].w, f, s1r);
         if (!cols) continue;
 #pragma unroll
-        for (int u = 0; u < kJoinCols; u += 4) {
+        for (int u = 0; u < COLS; u += 4) {
           const float4 x = o[i][u / 4];
           o1[u] = fmaf(x.x, f, o1[u]);
           o1[u + 1] = fmaf(x.y, f, o1[u + 1]);
@@ -1107,18 +1107,23 @@ __global__ void __launch_bounds__(256) join_tc_kernel(Params p) {
     const float norm = PROBE ? s1r : s1;
     const float inv = norm == 0.f ? 0.f : 1.f / norm, f1 = (1.f + s2 * inv) * inv;
     bad = (s1 + s2) * 0.f;
-    uint32_t w[kJoinCols / 2];
+    uint32_t w[COLS / 2];
 #pragma unroll
-    for (int c = 0; c < kJoinCols; c += 2) {
+    for (int c = 0; c < COLS; c += 2) {
       const float y0 = PROBE ? fmaf(o1[c], f1, -o2[PROBE ? c : 0] * inv) : o1[c] * inv;
       const float y1 = PROBE ? fmaf(o1[c + 1], f1, -o2[PROBE ? c + 1 : 0] * inv) : o1[c + 1] * inv;
       bad += (y0 + y1) * 0.f;
       w[c / 2] = pack_bf16(y0, y1);
     }
     if (cols) {
-      uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out) + ((long long)token * p.Hq + head) * p.dv + col);
+      __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.out) + ((long long)token * p.Hq + head) * p.dv + col;
+      if constexpr (COLS == 4) {
+        *reinterpret_cast<uint2*>(dst) = make_uint2(w[0], w[1]);
+      } else {
 #pragma unroll
-      for (int u = 0; u < kJoinCols / 8; ++u) dst[u] = make_uint4(w[4 * u], w[4 * u + 1], w[4 * u + 2], w[4 * u + 3]);
+        for (int u = 0; u < COLS / 2; u += 4)
+          reinterpret_cast<uint4*>(dst)[u / 4] = make_uint4(w[u], w[u + 1], w[u + 2], w[u + 3]);
+      }
     }
     if (p.lse && col == 0)
       p.lse[(long long)token * p.Hq + head] = s1 == 0.f ? -CUDART_INF_F : (top * c2 + log2f(s1)) * kLn2;
@@ -1127,7 +1132,7 @@ __global__ void __launch_bounds__(256) join_tc_kernel(Params p) {
   unsigned again = __ballot_sync(0xffffffffu, there && !(bad == 0.f));
   while (again) {
     const int l = (__ffs(again) - 1) / TR * TR;  // a row's first lane
-    again &= ~(((1u << TR) - 1u) << l);
+    again &= ~((TR == 32 ? 0xffffffffu : (1u << (TR & 31)) - 1u) << l);
     repair_row<__nv_bfloat16, C::kt>(p, sq, b, tile.p0, tile.p1, __shfl_sync(0xffffffffu, token, l),
                                      __shfl_sync(0xffffffffu, head, l), __shfl_sync(0xffffffffu, s1, l));
   }
@@ -1213,12 +1218,21 @@ cudaError_t launch_attend_tc(const Params& p, int D, cudaStream_t s) {
   return p.parents ? pick<true>(p, D, s) : pick<false>(p, D, s);
 }
 
-cudaError_t launch_join_tc(const Params& p, int D, cudaStream_t s) {
-  auto kern = p.r ? (D == 128 ? join_tc_kernel<128, true, false> : join_tc_kernel<64, true, false>)
-                  : (D == 128 ? join_tc_kernel<128, false, false> : join_tc_kernel<64, false, false>);
-  if (p.streams) kern = join_tc_kernel<128, false, true>;
+template <int COLS>
+static cudaError_t join(const Params& p, int D, cudaStream_t s) {
+  auto kern = p.r ? (D == 128 ? join_tc_kernel<128, true, false, COLS> : join_tc_kernel<64, true, false, COLS>)
+                  : (D == 128 ? join_tc_kernel<128, false, false, COLS> : join_tc_kernel<64, false, false, COLS>);
+  if (p.streams) kern = join_tc_kernel<128, false, true, COLS>;
   const int rows = p.streams || p.r || D == 64 ? BM : 2 * BM;
-  return launch(kern, dim3(rows * (D / kJoinCols) / 256, (unsigned)p.split), 256, 0, 1, true, s, p);
+  return launch(kern, dim3(rows * (D / COLS) / 256, (unsigned)p.split), 256, 0, 1, true, s, p);
+}
+cudaError_t launch_join_tc(const Params& p, int D, cudaStream_t s) {
+  // Few tiles: fewer than a quarter of the CTAs, so that most have more pieces than a thread of 16 columns loads
+  // at once (32 nodes at 16000, 32 heads over 8 of 64 with a
+  // probe, 38 pieces to a tile: 73 us in all with 16 columns, 44 with 4; of 128 without: 37 and 31).
+  const int tokens = BM / p.g * (D == 128 && !p.r && !p.streams ? 2 : 1);
+  const long long tiles = ((long long)p.tokens / tokens + p.B) * p.Hkv;
+  return tiles * 4 <= p.split ? join<4>(p, D, s) : join<16>(p, D, s);
 }
 
 }  // namespace paged
