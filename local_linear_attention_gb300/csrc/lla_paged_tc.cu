@@ -1228,8 +1228,8 @@ static cudaError_t join(const Params& p, int D, cudaStream_t s) {
 }
 cudaError_t launch_join_tc(const Params& p, int D, cudaStream_t s) {
   // Few tiles: fewer than a quarter of the CTAs, so that most have more pieces than a thread of 16 columns loads
-  // at once (32 nodes at 16000, 32 heads over 8 of 64 with a
-  // probe, 38 pieces to a tile: 73 us in all with 16 columns, 44 with 4; of 128 without: 37 and 31).
+  // at once (32 nodes at 16000, 32 heads over 8 of 64 with a probe, 38 pieces to a tile: 73 us in all with 16
+  // columns, 44 with 4; of 128 without: 37 and 31).
   const int tokens = BM / p.g * (D == 128 && !p.r && !p.streams ? 2 : 1);
   const long long tiles = ((long long)p.tokens / tokens + p.B) * p.Hkv;
   return tiles * 4 <= p.split ? join<4>(p, D, s) : join<16>(p, D, s);
