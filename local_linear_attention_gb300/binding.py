@@ -390,22 +390,31 @@ class RotarySpec:
     base^(-2i/rot), stretched for contexts `factor` times longer as lla_rotary_frequencies describes
     (STRETCH_*; `context`, `slow` and `fast` belong to STRETCH_WAVELENGTHS), or given, rot/2 numbers."""
 
-    __slots__ = ("rot", "layout", "scale", "freq", "_packed")
+    __slots__ = ("rot", "layout", "_packed")
 
     def __init__(self, rot, layout=ROTARY_HALVES, base=10000.0, stretch=STRETCH_NONE, factor=1.0, context=0, slow=1.0,
                  fast=32.0, scale=None, freq=None):
+        self.rot, self.layout = rot, layout
         if freq is None:
             buf = ctypes.create_string_buffer(_SPEC.size)
             _check(_load().lla_rotary_frequencies(buf, rot, layout, base, stretch, factor, context, slow, fast),
                    "lla_rotary_frequencies")
-            values = _SPEC.unpack(buf.raw)
-            freq, scale = values[:rot // 2], values[64] if scale is None else scale
-        else:
-            freq, scale = tuple(float(x) for x in freq), 1.0 if scale is None else scale
-            if len(freq) != rot // 2 or len(freq) > 64:
-                raise ValueError("freq must have rot/2 numbers, at most 64")
-        self.rot, self.layout, self.freq, self.scale = rot, layout, tuple(freq), float(scale)
-        self._packed = _SPEC.pack(*freq, *[0.0] * (64 - len(freq)), scale, rot, layout, 0, 0, 0)
+            self._packed = buf.raw
+            if scale is None:
+                return
+            freq = self.freq
+        freq = tuple(float(x) for x in freq)
+        if len(freq) != rot // 2 or len(freq) > 64:
+            raise ValueError("freq must have rot/2 numbers, at most 64")
+        self._packed = _SPEC.pack(*freq, *[0.0] * (64 - len(freq)), 1.0 if scale is None else scale, rot, layout, 0, 0, 0)
+
+    @property
+    def freq(self):
+        return _SPEC.unpack(self._packed)[:self.rot // 2]
+
+    @property
+    def scale(self):
+        return _SPEC.unpack(self._packed)[64]
 
 
 def lla_rotary(x, spec: RotarySpec, positions=None, backward=False, out=None, stream=None):
