@@ -75,3 +75,51 @@ def test_the_same_bits_whatever_the_run(lla):  # noqa: F811
     for _ in range(5):
         again = lla.lla_paged_tree_attention(q, cache, starts, flat(forest), P.h, max_new=64)
         assert all(torch.equal(x, y) for x, y in zip(first, again))
+
+
+@pytest.mark.parametrize("d,t", [(128, 50), (64, 70), (128, 200)])
+def test_two_streams_and_a_graph_with_one_workspace(lla, d, t):  # noqa: F811
+    P = Problem([9000, 4100], [t, t], 8, 4, d, d, 32, BF, False, seed=6, max_pages=400)
+    cache, q, _, starts = P.cuda(lla, mass=False)
+    parents = [flat(trees(P.news_l, branch, 1)) for branch in (2, 0)]
+    call = lambda i, **kw: lla.lla_paged_tree_attention(q, cache, starts, parents[i], P.h, max_new=t, **kw)  # noqa: E731
+    want = [call(i) for i in range(2)]
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    got = [(call(0), call(1, stream=side)) for _ in range(20)]
+    torch.cuda.synchronize()
+    for pair in got:
+        for i in range(2):
+            assert torch.equal(pair[i][0], want[i][0]) and torch.equal(pair[i][1], want[i][1])
+    size = lla.lla_paged_tree_workspace_size(q, cache, starts, P.h, max_new=t)
+    workspace = torch.full((size,), 255, dtype=torch.uint8, device="cuda")
+    outs = [(torch.empty_like(o), torch.empty_like(x)) for o, x in want]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        for i, (o, x) in enumerate(outs):
+            call(i, out=o, lse=x, workspace=workspace)
+    q.mul_(0.5)
+    for _ in range(3):
+        graph.replay()
+    want = [call(i) for i in range(2)]
+    torch.cuda.synchronize()
+    for (o, x), (a, b) in zip(outs, want):
+        assert torch.equal(o, a) and torch.equal(x, b)
+    assert lla.lla_stream_status() == 0
+
+
+def test_a_node_without_anything_to_see(lla):  # noqa: F811
+    """Roots with no context before them whose own logit is -infinity: nothing comes out of them, their children
+    see themselves."""
+    for dtype, d in ((BF, 128), (BF, 64), (torch.float32, 32)):
+        P = Problem([40], [40], 2, 1, d, d, 16, dtype, False, seed=2)
+        forest = [[-1] * 20 + list(range(20))]
+        pg, off = P.slots(0)
+        P.q[:] = P.q.abs()
+        P.k[pg[:20], :, off[:20]] = -math.inf
+        cache, q, _, starts = P.cuda(lla, mass=False)
+        out, lse = lla.lla_paged_tree_attention(q, cache, starts, flat(forest), P.h, max_new=40)
+        assert lla.lla_stream_status() == 0
+        assert (out[:20] == 0).all() and (lse[:20] == -math.inf).all()
+        own = P.v[pg[20:], 0, off[20:]].to(torch.float64)[:, None].expand(-1, 2, -1)
+        check("out", out[20:], own, own.abs() * (2.0 ** -8 if dtype == BF else 2.0 ** -22))
