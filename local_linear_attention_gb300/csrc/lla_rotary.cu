@@ -44,7 +44,7 @@ struct Tensors {
   const void* x[3];
   void* y[3];
   int upto[3];  // heads of this tensor and those before it
-  int count, heads, T, d, items, per;
+  int heads, T, d, items, per;
   long long rows;  // B * T
   const int* positions;
 };
@@ -171,7 +171,6 @@ int lla_rotary(const lla_rotary_spec* spec, const void* const* x, void* const* y
   for (int i = 0; i < count; ++i)  // what is written is nobody else's
     for (int j = 0; j < count; ++j)
       if (i != j && heads[i] > 0 && heads[j] > 0 && (y[i] == y[j] || y[i] == x[j])) return LLA_ERR_INVALID_ARG;
-  a.count = count;
   a.heads = (int)all;
   a.T = T;
   a.d = d;
