@@ -569,7 +569,8 @@ int lla_paged_grow(const lla_paged_cache* cache, const int* starts, int* refs, i
  * Copies whole pages, keys, values and (where both caches have it) mass: page pairs[i][0] of `from` to page
  * pairs[i][1] of `to`, count pairs in device memory, 8-byte aligned; a pair with a negative number is skipped. The caches (which may be
  * one) agree in kv_heads, page_size, d, dv and type; tables and lens are not used. No page may be written
- * twice, or written and read, in one call. Fewer than 2^31 pieces of 32 KB (LLA_ERR_UNSUPPORTED).
+ * twice, or written and read, in one call. A page's keys, values and mass: at most 32 GB less 32 KB; all pairs: fewer than
+ * 2^31 pieces of 32 KB (LLA_ERR_UNSUPPORTED).
  */
 int lla_paged_copy(const lla_paged_cache* from, const lla_paged_cache* to, const int* pairs, int count, void* stream);
 

@@ -471,6 +471,9 @@ cudaError_t launch_fork(const Params& p, const int* parents, int* table, int* le
 cudaError_t launch_free(const Params& p, const int* keep, int* lens, int* refs, cudaStream_t s);
 constexpr int kMaxGrow = 4096;  // sequences that grow in one call
 cudaError_t launch_grow(const Params& p, int* table, int* lens, int* refs, int* copies, int* left, cudaStream_t s);
+// Whether `count` pairs of pages of that many bytes (keys, values, mass) fit a launch.
+constexpr int kCopyBytes = 32 * 1024;
+bool copy_fits(long long page_bytes, int count);
 cudaError_t launch_copy(const Params& from, const Params& to, const int* pairs, int count, int dtype, cudaStream_t s);
 cudaError_t launch_compact(const Params& p, const int* path, int max_path, int* keep, int dtype, cudaStream_t s);
 // `p` is the source cache; the other arguments the destination and the choice.

@@ -584,10 +584,12 @@ int lla_paged_copy(const lla_paged_cache* from, const lla_paged_cache* to, const
       !aligned16(from->v_pages) || !aligned16(to->k_pages) || !aligned16(to->v_pages) || !aligned16(from->mass) ||
       !aligned16(to->mass) || !pairs || (reinterpret_cast<uintptr_t>(pairs) & 7u))
     return LLA_ERR_INVALID_ARG;
+  const int slot_bytes = (from->d + from->dv) * (from->dtype == LLA_F32 ? 4 : 2) + (from->mass && to->mass ? 4 : 0);
+  if (!copy_fits((long long)from->kv_heads * from->page_size * slot_bytes, count)) return LLA_ERR_UNSUPPORTED;
   Params p = cache_params(from), t = cache_params(to);
   if (device_status(&p.status) != cudaSuccess) return LLA_ERR_CUDA;
-  const cudaError_t err = launch_copy(p, t, pairs, count, from->dtype, static_cast<cudaStream_t>(stream));
-  return err == cudaSuccess ? LLA_OK : err == cudaErrorInvalidConfiguration ? LLA_ERR_UNSUPPORTED : LLA_ERR_CUDA;
+  return launch_copy(p, t, pairs, count, from->dtype, static_cast<cudaStream_t>(stream)) == cudaSuccess ? LLA_OK
+                                                                                                        : LLA_ERR_CUDA;
 }
 
 int lla_paged_compact(const lla_paged_cache* cache, const int* starts, int tokens, const int* path, int max_path, int* keep,

@@ -224,8 +224,8 @@ __global__ void __launch_bounds__(kGrowThreads) grow_kernel(Params p, int* table
 }
 
 // ------------------------------------------------------------------------------------ copy
-// A block moves kCopyBytes of one pair's pages, taken as one stretch: keys, values, mass.
-constexpr int kCopyBytes = 32 * 1024;
+// A block moves kCopyBytes of one pair's pages, taken as one stretch: keys, values, mass. Its words are counted in
+// 32 bits (copy_fits).
 struct Pools {
   const uint4* from[3];
   uint4* to[3];
@@ -349,6 +349,11 @@ cudaError_t launch_grow(const Params& p, int* table, int* lens, int* refs, int* 
                 reinterpret_cast<int2*>(copies), left);
 }
 
+bool copy_fits(long long page_bytes, int count) {
+  const long long chunks = (page_bytes + kCopyBytes - 1) / kCopyBytes;
+  return page_bytes <= (1LL << 35) - kCopyBytes && count * chunks <= 0x7fffffffLL;
+}
+
 cudaError_t launch_copy(const Params& from, const Params& to, const int* pairs, int count, int dtype, cudaStream_t s) {
   const int eb = dtype == LLA_F32 ? 4 : 2;
   Pools a = {};
@@ -360,15 +365,12 @@ cudaError_t launch_copy(const Params& from, const Params& to, const int* pairs, 
   for (int i = 0; i < 3; ++i) {
     a.from[i] = static_cast<const uint4*>(f[i]);
     a.to[i] = static_cast<uint4*>(t[i]);
-    const long long w = (long long)from.Hkv * from.page * bytes[i] / 16;
-    if (w >= (1LL << 30)) return cudaErrorInvalidConfiguration;
-    a.words[i] = (int)w;
-    words += w;
+    a.words[i] = (int)((long long)from.Hkv * from.page * bytes[i] / 16);
+    words += a.words[i];
   }
   a.from_pages = from.num_pages;
   a.to_pages = to.num_pages;
   a.chunks = (int)((words * 16 + kCopyBytes - 1) / kCopyBytes);
-  if ((long long)count * a.chunks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
   copy_kernel<<<(unsigned)(count * (long long)a.chunks), 256, 0, s>>>(a, reinterpret_cast<const int2*>(pairs), from.status);
   count_launch();
   return cudaGetLastError();
