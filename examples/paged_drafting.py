@@ -70,7 +70,7 @@ class Pages:
         for cache in caches:
             lla.lla_paged_copy(cache, cache, copies)
         if int(left) < 0:
-            raise RuntimeError(f"{-int(left)} pages too few")
+            raise RuntimeError(f"{-int(left)} pages or entries of the table too few")
         return starts
 
 

@@ -559,8 +559,12 @@ int lla_paged_free(const lla_paged_cache* cache, const int* keep, int* refs, voi
  * takes that page's place in the table before any other, and copies[b] = (old page, new page) is to be made by
  * lla_paged_copy for each layer; elsewhere copies[b] = (-1, -1). Among sequences that share such a page and
  * all grow, the last keeps it if nobody else holds it. copies: [num_seqs][2], 8-byte aligned.
- * *left (device memory): free pages afterwards. Negative: so many were missing, and nothing has changed but
- * copies, which is all -1; lens then does not count the new tokens, so they may not be appended.
+ * *left (device memory): free pages afterwards. Negative: nothing has changed but copies, which is all -1. So many
+ * free pages were missing, or entries in the rows of sequences that would outgrow the table (the sum of both); lens
+ * then does not count the new tokens, so they may not be appended: lla_paged_append would take them for the
+ * last positions that are there. The same holds for the tokens of a sequence with copies[b] = (-2, -2), which an
+ * impossible length, descending starts or starts for more positions than a row holds leave out, reported, while the others
+ * grow. A last page out of range is reported and stays in the table.
  * At most 4096 sequences (LLA_ERR_UNSUPPORTED).
  */
 int lla_paged_grow(const lla_paged_cache* cache, const int* starts, int* refs, int* copies, int* left, void* stream);

@@ -771,7 +771,8 @@ def lla_paged_grow(cache: PagedCache, starts, refs, copies=None, left=None, stre
     """Room for the new tokens of `starts`: cache.lens grows by them and the table gets the lowest free pages.
     Returns (copies [num_seqs, 2], left [1]), int32: the pages (old, new) that lla_paged_copy has to copy in
     each layer because others hold the old one too (-1: none), and how many pages are free afterwards. left
-    below zero: so many were missing and nothing has changed."""
+    below zero: so many pages were missing, or table entries of sequences that would outgrow their rows, and nothing
+    has changed; a sequence with copies of -2 was left out (see lla.h). Neither's new tokens may be appended."""
     _paged_starts(starts, cache)
     _paged_ints("refs", refs, cache, cache.k_pages.shape[:1])
     if copies is not None:

@@ -80,12 +80,13 @@ constexpr int kGrowBlocks = 8, kGrowThreads = 1024, kGrowWarps = kGrowThreads / 
 
 struct Grow {
   int off[kMaxGrow + 1];  // pages that sequences 0 .. b-1 take
-  int more[kMaxGrow];     // new positions; 0: b stays as it is
+  int more[kMaxGrow];     // new positions; 0: b stays as it is; -1: and is left out
   int held[kMaxGrow];     // pages that b has
   int last[kMaxGrow];     // the page that b copies because others hold it too; -1: none
   int sums[kGrowWarps];   // free pages of the warps before
   int free;               // and of this block
   long long need;         // of all sequences; `off` holds where it does not pass what is free
+  unsigned long long over;  // table entries that full rows lack
 };
 
 template <typename T>
@@ -122,12 +123,18 @@ __global__ void __launch_bounds__(kGrowThreads) grow_kernel(Params p, int* table
 #pragma unroll 4
   for (int s = s0; s < s1; ++s) mine += zeros(load(s));
 
-  // What the sequences need.
+  // What the sequences need: of pages up to the end of their row of the table, and beyond it of entries.
+  if (tid == 0) g.over = 0;
+  unsigned long long over = 0;
   for (int b = tid; b < p.B; b += kGrowThreads) {
     const int n = load_len(p, b), t0 = p.starts[b], t1 = p.starts[b + 1], cap = p.max_pages << p.page_shift;
-    const bool bad = t0 < 0 || t1 < t0 || (n >= 0 && t1 - t0 > cap - n);
+    const bool bad = t0 < 0 || t1 < t0 || t1 - t0 > cap;
     if (bad) atomicOr(p.status, kStatusBadIndex);
-    const int more = n < 0 || bad ? 0 : t1 - t0;
+    int more = n < 0 || bad ? -1 : t1 - t0;
+    if (more > cap - n) {
+      over += (((long long)n + more + p.page - 1) >> p.page_shift) - p.max_pages;
+      more = cap - n;
+    }
     int last = -1;
     if (more > 0 && n & (p.page - 1)) last = load_page(p, b, n >> p.page_shift);
     if (last >= 0 && refs[last] <= 1) last = -1;
@@ -136,6 +143,7 @@ __global__ void __launch_bounds__(kGrowThreads) grow_kernel(Params p, int* table
     g.last[b] = last;
   }
   __syncthreads();
+  if (over) atomicAdd(&g.over, over);
   // Of the sequences that share a last page and grow, the last keeps it if nobody else holds it.
   unsigned keeps = 0;  // bit i: this thread's i-th sequence
   static_assert(kMaxGrow <= 32 * kGrowThreads, "bits");
@@ -181,13 +189,14 @@ __global__ void __launch_bounds__(kGrowThreads) grow_kernel(Params p, int* table
     if (i < rank) first += x;
     all += x;
   }
-  const bool enough = g.need <= all;
+  const bool enough = g.need <= all && g.over == 0;
   const int need = enough ? (int)g.need : 0;
   cluster.sync();  // no block leaves before its sum has been read
   if (rank == 0) {
-    if (tid == 0) *left = (int)max(all - g.need, -2147483647LL);
+    if (tid == 0)
+      *left = (int)max(enough ? all - g.need : -(max(g.need - all, 0LL) + (long long)g.over), -2147483647LL);
     for (int b = tid; b < p.B; b += kGrowThreads) {
-      if (!enough || g.last[b] < 0) copies[b] = make_int2(-1, -1);
+      if (!enough || g.last[b] < 0) copies[b] = enough && g.more[b] < 0 ? make_int2(-2, -2) : make_int2(-1, -1);
       if (!enough) continue;
       if (g.last[b] >= 0) atomicSub(refs + g.last[b], 1);
       if (g.more[b] > 0) lens[b] += g.more[b];
