@@ -541,8 +541,8 @@ int lla_paged_evict(const lla_paged_cache* from, const lla_paged_cache* to, int 
  *
  * lla_paged_fork: sequence c of `to` becomes a copy of sequence parents[c] of `from` (-1: an empty one): its table
  * entries and length, the pages' refs one more each. `to` is another table and lens over the same pages (what
- * it held before is not released), with room for the lengths. A parent out of range, or one that does not
- * fit, gives an empty sequence.
+ * it held before is not released), with room for the lengths. A parent out of range, one that does not
+ * fit, or one with a page number out of range, gives an empty sequence.
  */
 int lla_paged_fork(const lla_paged_cache* from, const lla_paged_cache* to, const int* parents, int* refs, void* stream);
 

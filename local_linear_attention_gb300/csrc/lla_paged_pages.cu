@@ -45,11 +45,13 @@ __global__ void __launch_bounds__(256) fork_kernel(Params p, const int* parents,
     }
     n = max(n, 0);
   }
+  bool bad = false;
+  for (int i = threadIdx.x; i < pages_of(p, n); i += 256) bad |= load_page(p, from, i) < 0;
+  if (__syncthreads_or(bad)) n = 0;
   for (int i = threadIdx.x; i < pages_of(p, n); i += 256) {
     const int pg = p.table[(long long)from * p.max_pages + i];
     table[(long long)c * max_pages + i] = pg;
-    if ((unsigned)pg < (unsigned)p.num_pages) atomicAdd(refs + pg, 1);
-    else atomicOr(p.status, kStatusBadIndex);
+    atomicAdd(refs + pg, 1);
   }
   if (threadIdx.x == 0) lens[c] = n;
 }
