@@ -537,7 +537,7 @@ int lla_paged_evict(const lla_paged_cache* from, const lla_paged_cache* to, int 
  * grow touch tables, lens and refs alone, which the caches of a model's layers share: they are called once,
  * lla_paged_copy and lla_paged_compact once per layer. None of them allocates or synchronises, and all give
  * the same pages whatever the scheduling. Impossible lengths, page numbers, parents and paths are reported in the
- * status word (LLA_ERR_INVALID_ARG); that sequence or pair is left as it is.
+ * status word (LLA_ERR_INVALID_ARG); unless it says otherwise below, that sequence or pair is left as it is.
  *
  * lla_paged_fork: sequence c of `to` becomes a copy of sequence parents[c] of `from` (-1: an empty one): its table
  * entries and length, the pages' refs one more each. `to` is another table and lens over the same pages (what
@@ -548,7 +548,8 @@ int lla_paged_fork(const lla_paged_cache* from, const lla_paged_cache* to, const
 
 /*
  * Shortens each sequence to its first keep[b] positions (keep NULL or negative: to none; more than it has: as
- * it is) and gives up the pages behind them: refs one less each. A page that nobody held is reported.
+ * it is) and gives up the pages behind them: refs one less each. A page that nobody held, or a number out of range,
+ * is reported and passed over.
  */
 int lla_paged_free(const lla_paged_cache* cache, const int* keep, int* refs, void* stream);
 
@@ -583,7 +584,8 @@ int lla_paged_copy(const lla_paged_cache* from, const lla_paged_cache* to, const
  * kept ones among sequence b's new tokens, ended by -1 where there are fewer than max_path. Their keys,
  * values and mass move to the slots first, first + 1, .. (first = lens[b] - number of new tokens), and keep[b] =
  * first + their number is what lla_paged_free is then given, once all layers are done: lens and table stay as
- * they are here. A path that does not rise or leaves the new tokens is reported and nothing of it kept. The
+ * they are here. A path that does not rise, leaves the new tokens or moves one from or to a page out of range is
+ * reported and nothing of it kept. The
  * moved positions' pages must be the sequence's own (as after lla_paged_grow). tokens: of the batch, as in
  * lla_paged_append. keep is not the cache's lens.
  */

@@ -280,7 +280,8 @@ __global__ void __launch_bounds__(kCompactThreads) compact_kernel(Params p, cons
   const int b = blockIdx.x / p.Hkv, hk = blockIdx.x % p.Hkv, tid = threadIdx.x;
   const Seq sq = load_seq(p, b);
   const int* mine = path + (long long)b * max_path;
-  // The path: entries before the first that is negative, rising, below the number of nodes.
+  // The path: entries before the first that is negative, rising, below the number of nodes; it moves between pages of
+  // the pool.
   int count = max_path;
   for (int i = tid; i < max_path; i += kCompactThreads)
     if (mine[i] < 0) count = min(count, i);
@@ -291,7 +292,12 @@ __global__ void __launch_bounds__(kCompactThreads) compact_kernel(Params p, cons
   __syncthreads();
   count = shared_count;
   bool bad = sq.first < 0;
-  for (int i = tid; i < count; i += kCompactThreads) bad |= mine[i] >= sq.n || (i > 0 && mine[i] <= mine[i - 1]);
+  for (int i = tid; i < count; i += kCompactThreads) {
+    const int a = mine[i];
+    bad |= a >= sq.n || a < i || (i > 0 && a <= mine[i - 1]);  // (what rises from 0 on stays at or above its index)
+    if (!bad && a != i)  // both slots are the sequence's: are their pages the pool's
+      bad = load_page(p, b, (sq.first + a) >> p.page_shift) < 0 || load_page(p, b, (sq.first + i) >> p.page_shift) < 0;
+  }
   bad = __syncthreads_or(bad);
   if (tid == 0 && hk == 0) {
     if (bad) atomicOr(p.status, kStatusBadIndex);
