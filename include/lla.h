@@ -301,7 +301,8 @@ int lla_rotary_frequencies(lla_rotary_spec* spec, int rot, int layout, double ba
  * [B, heads[i], T, d], y[i] the same (x[i] == y[i]: in place; otherwise none may overlap another), x, y and
  * heads host arrays. positions [B, T] (device) or NULL: 0 .. T-1. backward nonzero: the gradient with respect
  * to the input from that with respect to the output, which is the transposed rotation times scale. d in {16, 32, 64,
- * 128}; fewer than 2^31 rows in all. One launch, asynchronous, allocates nothing; fp32 arithmetic, one rounding.
+ * 128}; fewer than 2^31 rows, and at most 2^31 - 2^17 heads, in all (LLA_ERR_UNSUPPORTED). One launch, asynchronous,
+ * allocates nothing; fp32 arithmetic, one rounding.
  */
 int lla_rotary(const lla_rotary_spec* spec, const void* const* x, void* const* y, const int* heads, int count,
                const int* positions, int B, int T, int d, int backward, int dtype, void* stream);
@@ -450,7 +451,8 @@ int lla_paged_append(const lla_paged_cache* cache, const void* k_new, const void
  * ([tokens, q_heads, d] or NULL; r needs q) come out rotated in q_out and r_out (which may be q and r; no other overlap). The
  * token's position is that of its sequence's first new token's slot plus offsets[token] (device memory,
  * [tokens]; NULL: its index among the sequence's new tokens, so its own slot's): the depth of a drafted
- * node, and, where eviction has dropped positions, their number besides. Rows of q_out and r_out that no sequence covers are not written.
+ * node, and, where eviction has dropped positions, their number besides. Rows of q_out and r_out that no sequence covers
+ * are not written. At most 2^31 - 2^17 heads of k, q and r in all (LLA_ERR_UNSUPPORTED).
  */
 int lla_paged_append_rotary(const lla_paged_cache* cache, const lla_rotary_spec* spec, const void* k_new,
                             const void* v_new, const void* q, const void* r, void* q_out, void* r_out, int q_heads,

@@ -450,7 +450,8 @@ int lla_paged_append_rotary(const lla_paged_cache* cache, const lla_rotary_spec*
   if (st != LLA_OK) return st;
   if (tokens < 0 || (r && !q) || (q && q_heads <= 0)) return LLA_ERR_INVALID_ARG;
   if ((long long)tokens * cache->kv_heads >= (1LL << 31) || tokens >= kNoWindow ||
-      (q && (long long)tokens * q_heads >= (1LL << 31)))
+      (q && (long long)tokens * q_heads >= (1LL << 31)) ||
+      cache->kv_heads + (q ? (long long)q_heads : 0) + (r ? (long long)q_heads : 0) > rotary::kMostHeads)
     return LLA_ERR_UNSUPPORTED;
   if (tokens == 0 || cache->num_seqs == 0) return LLA_OK;
   st = check_cache_pointers(cache, false);

@@ -158,7 +158,7 @@ int lla_rotary(const lla_rotary_spec* spec, const void* const* x, void* const* y
     if (heads[i] < 0) return LLA_ERR_INVALID_ARG;
     all += heads[i];
   }
-  if (all * B >= (1LL << 31) || all * B * T >= (1LL << 31)) return LLA_ERR_UNSUPPORTED;
+  if (all > rotary::kMostHeads || all * B >= (1LL << 31) || all * B * T >= (1LL << 31)) return LLA_ERR_UNSUPPORTED;
   if (all * B * T == 0) return LLA_OK;
   for (int i = 0; i < 3; ++i) {
     a.upto[i] = (i ? a.upto[i - 1] : 0) + (i < count ? heads[i] : 0);

@@ -16,6 +16,8 @@ namespace lla {
 namespace rotary {
 
 constexpr int kMaxPairs = 64;
+// Heads that a position's threads go over: their indices, and those of a last group of them, stay within 31 bits.
+constexpr long long kMostHeads = (1LL << 31) - (1 << 17);
 
 // Passed to kernels by value.
 struct Turn {
