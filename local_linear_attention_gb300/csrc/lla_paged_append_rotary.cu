@@ -112,7 +112,7 @@ __global__ void __launch_bounds__(256, 3) append_rotary_kernel(const __grid_cons
   };
   load(u0);
   if (!find_place(p, token, u0 < p.Hkv, starts_s, &at)) return;
-  item.angles(turn, at.first + (a.offsets ? __ldg(a.offsets + token) : at.index));
+  item.angles(turn, (long long)at.first + (a.offsets ? __ldg(a.offsets + token) : at.index));
   for (int v0 = u0; v0 < u1; v0 += U) {
     if (v0 > u0) load(v0);
 #pragma unroll

@@ -31,8 +31,8 @@ __device__ __forceinline__ float2 fast_cos_sin(float x) { return make_float2(__c
 // scale * (cos, sin) of a pair's angle. FAST (bf16): the hardware's sine and cosine, off by 2^-21 at most
 // where a feature is rounded to 2^-9 of its value; else CUDA's sincospif.
 template <bool FAST>
-__device__ __forceinline__ void cos_sin(const Turn& t, int pair, int pos, float& c, float& s) {
-  const unsigned long long at = (unsigned long long)(long long)pos * t.turns[pair];
+__device__ __forceinline__ void cos_sin(const Turn& t, int pair, long long pos, float& c, float& s) {
+  const unsigned long long at = (unsigned long long)pos * t.turns[pair];
   const unsigned q = (unsigned)((at + (1ull << 61)) >> 62);
   const float f = (float)(int)((long long)(at - ((unsigned long long)q << 62)) >> 32) * 0x1p-31f;  // half turns
   float s0, c0;
@@ -99,7 +99,7 @@ struct Item {
     }
   }
   // The cosines and sines of the item's pairs; before the first store.
-  __device__ __forceinline__ void angles(const Turn& t, int pos) {
+  __device__ __forceinline__ void angles(const Turn& t, long long pos) {
 #pragma unroll
     for (int i = 0; i < P; ++i)
       if (first + i < t.half) cos_sin<kFast>(t, first + i, pos, c[i], s[i]);
