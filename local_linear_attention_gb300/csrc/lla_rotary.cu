@@ -11,6 +11,7 @@
 #include <type_traits>
 
 #include "lla_rotary.cuh"
+#include "lla_turns.h"
 
 namespace lla {
 namespace rotary {
@@ -26,14 +27,8 @@ int make_turn(const lla_rotary_spec* spec, int d, bool back, Turn* out) {
   out->half = spec->rot / 2;
   out->back = back;
   for (int i = 0; i < out->half; ++i) {
-    const double f = std::fabs(spec->freq[i]);
-    if (!(f <= 0x1p20)) return LLA_ERR_INVALID_ARG;
-    // |f| / (2 pi) as a sum of two doubles (1 / (2 pi) = hi + lo), its whole turns dropped
-    const double hi = 0x1.45f306dc9c883p-3, lo = -0x1.6b01ec5417056p-57;
-    const double p = f * hi, e = std::fma(f, hi, -p) + f * lo;
-    const unsigned long long turns =
-        (unsigned long long)((p - std::floor(p)) * 0x1p64) + (unsigned long long)std::llround(e * 0x1p64);
-    out->turns[i] = spec->freq[i] < 0 ? 0ull - turns : turns;
+    if (!(std::fabs(spec->freq[i]) <= 0x1p20)) return LLA_ERR_INVALID_ARG;
+    out->turns[i] = turns_of(spec->freq[i]);
   }
   return LLA_OK;
 }

@@ -7,7 +7,7 @@
 // product is off by 0.03 rad), and fp64 is slow here. So a frequency is held in turns as a 64-bit fraction,
 // pos times it wraps around modulo a turn by itself, exactly, in integers: off by pos * 2^-65 turns. The two
 // highest bits of the sum with an eighth are the quadrant; what is left, within an eighth of a turn, goes to
-// fp32 (2^-33 turns) and to sine and cosine.
+// fp32 (off by little more than 2^-28 turns at its ends) and to sine and cosine.
 #pragma once
 
 #include "lla_internal.cuh"
