@@ -388,13 +388,13 @@ class RotarySpec:
     """How positions rotate the first `rot` features of a head (lla_rotary_spec): pairs (i, i + rot/2)
     (ROTARY_HALVES) or (2i, 2i + 1) (ROTARY_INTERLEAVED) by pos * freq[i] radians, times scale. freq is
     base^(-2i/rot), stretched for contexts `factor` times longer as lla_rotary_frequencies describes
-    (STRETCH_*; `context`, `slow` and `fast` belong to STRETCH_WAVELENGTHS), or given, rot/2 numbers."""
+    (STRETCH_*; `context`, `slow` and `fast` belong to STRETCH_WAVELENGTHS), or given, rot/2 numbers. A spec does not
+    change: calls read the packed struct that is made here."""
 
-    __slots__ = ("rot", "layout", "_packed")
+    __slots__ = ("_packed",)
 
     def __init__(self, rot, layout=ROTARY_HALVES, base=10000.0, stretch=STRETCH_NONE, factor=1.0, context=0, slow=1.0,
                  fast=32.0, scale=None, freq=None):
-        self.rot, self.layout = rot, layout
         if freq is None:
             buf = ctypes.create_string_buffer(_SPEC.size)
             _check(_load().lla_rotary_frequencies(buf, rot, layout, base, stretch, factor, context, slow, fast),
@@ -415,6 +415,14 @@ class RotarySpec:
     @property
     def scale(self):
         return _SPEC.unpack(self._packed)[64]
+
+    @property
+    def rot(self):
+        return _SPEC.unpack(self._packed)[65]
+
+    @property
+    def layout(self):
+        return _SPEC.unpack(self._packed)[66]
 
 
 def lla_rotary(x, spec: RotarySpec, positions=None, backward=False, out=None, stream=None):
