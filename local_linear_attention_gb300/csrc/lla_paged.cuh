@@ -36,6 +36,9 @@ struct Params {
   const int* starts;  // [B + 1]
   const int* table;   // [B, max_pages]
   const int* lens;    // [B]
+  // Trees of drafted tokens (lla_paged_tree.cu): the new tokens of a sequence are nodes. Here, beside what load_seq reads,
+  // since a further line of a launch's parameters takes every kernel 0.1 to 0.2 us.
+  const int* parents;    // [tokens]: a node's parent, an index among its sequence's new tokens or -1; nullptr: no trees
   int* status;
   int B, tokens, Hq, Hkv, g, d, dv;
   int page, page_shift, max_pages, num_pages;
@@ -55,8 +58,7 @@ struct Params {
   float* logits;     // [B * Hkv][row_cap][keys_cap]  raw q.k of the few-rows kernel, by the key's
                      // place among the visible 16-key steps (weight tracking)
   int row_cap, keys_cap;
-  // Trees of drafted tokens (lla_paged_tree.cu): the new tokens of a sequence are nodes.
-  const int* parents;    // [tokens]: a node's parent, an index among its sequence's new tokens or -1; nullptr: no trees
+  // Trees:
   const uint32_t* bits;  // [tokens][words]: which nodes a node sees
   const int* depth;      // [tokens]
   int words;
