@@ -36,9 +36,6 @@ struct Params {
   const int* starts;  // [B + 1]
   const int* table;   // [B, max_pages]
   const int* lens;    // [B]
-  // Trees of drafted tokens (lla_paged_tree.cu): the new tokens of a sequence are nodes. Here, beside what load_seq reads,
-  // since a further line of a launch's parameters takes every kernel 0.1 to 0.2 us.
-  const int* parents;    // [tokens]: a node's parent, an index among its sequence's new tokens or -1; nullptr: no trees
   int* status;
   int B, tokens, Hq, Hkv, g, d, dv;
   int page, page_shift, max_pages, num_pages;
@@ -58,7 +55,8 @@ struct Params {
   float* logits;     // [B * Hkv][row_cap][keys_cap]  raw q.k of the few-rows kernel, by the key's
                      // place among the visible 16-key steps (weight tracking)
   int row_cap, keys_cap;
-  // Trees:
+  // Trees of drafted tokens (lla_paged_tree.cu): the new tokens of a sequence are nodes.
+  const int* parents;    // [tokens]: a node's parent, an index among its sequence's new tokens or -1; nullptr: no trees
   const uint32_t* bits;  // [tokens][words]: which nodes a node sees
   const int* depth;      // [tokens]
   int words;
@@ -74,19 +72,26 @@ struct Seq {
 
 // Sequence b; one with impossible starts or length is treated as having no positions and no new tokens,
 // and reported once per reader. (Cut to the nearest possible length instead, it would write to whatever
-// its row of the table ends in.)
+// its row of the table ends in.) TREE: the new tokens are nodes, whose keys have to be in the cache, so more of them than
+// positions are impossible too. (Known at compile time: a look at p.parents, a line of the launch's parameters apart,
+// took one token of 8 heads at 1000 from 5.35 to 5.55 us.)
+template <bool TREE = false>
 __device__ __forceinline__ Seq load_seq(const Params& p, int b) {
   Seq s;
   const int t0 = p.starts[b], t1 = p.starts[b + 1];
   const int len = p.lens[b], cap = p.max_pages << p.page_shift;
-  // (A node's key has to be in the cache: more nodes than positions are impossible too.)
-  const bool bad = t0 < 0 || t1 < t0 || t1 > p.tokens || len < 0 || len > cap || (p.parents && t1 - t0 > len);
+  const bool bad = t0 < 0 || t1 < t0 || t1 > p.tokens || len < 0 || len > cap || (TREE && t1 - t0 > len);
   s.t0 = bad ? 0 : t0;
   s.n = bad ? 0 : t1 - t0;
   s.len = bad ? 0 : len;
   s.first = s.len - s.n;
   if (bad) atomicOr(p.status, kStatusBadIndex);
   return s;
+}
+
+// The same in kernels that serve both.
+__device__ __forceinline__ Seq load_seq_or_tree(const Params& p, int b) {
+  return p.parents ? load_seq<true>(p, b) : load_seq(p, b);
 }
 
 // Page index of a position's page, or -1 (reported) when the table's entry is out of range.

@@ -95,7 +95,7 @@ __global__ void __launch_bounds__(NT) attend_cc_kernel(Params p) {
   int b, tile;
   const int index = blockIdx.x / p.Hkv;
   if (!find_tile(p, per, index / slices, &b, &tile)) return;
-  const Seq sq = load_seq(p, b);
+  const Seq sq = load_seq_or_tree(p, b);
   if (sq.n == 0) return;                     // an impossible length (find_tile counts by the starts)
   const int u0 = (index % slices) * BM;      // first grouped head of this tile (g > BM)
   const int tok0 = tile * per, ntok = min(per, sq.n - tok0);
@@ -339,7 +339,7 @@ __global__ void __launch_bounds__(128) join_kernel(Params p) {
     if (p.starts[mid] <= token) b = mid;
     else e = mid;
   }
-  const Seq sq = load_seq(p, b);
+  const Seq sq = load_seq_or_tree(p, b);
   if (token < sq.t0 || token >= sq.t0 + sq.n || !mine(p, sq.n)) return;
   float m = -CUDART_INF_F;
   for (int s = lane; s < p.split; s += 32) m = fmaxf(m, p.part_s[s * rows + id].x);

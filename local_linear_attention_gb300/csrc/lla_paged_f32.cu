@@ -409,12 +409,12 @@ __global__ void __launch_bounds__(NW * 32, 2) attend_f32_kernel(Params p) {
   if (TREE && p.bits && blockIdx.x == 0) wait_previous();  // the end of this grid is the end of both, whatever the others do
   if (blockIdx.x == 0)
     for (int i = threadIdx.x; i < p.B; i += NW * 32) {
-      const int n = load_seq(p, i).n;
+      const int n = load_seq<TREE>(p, i).n;
       if (n > 0 && !mine(p, n)) atomicOr(p.status, kStatusBadIndex);
     }
   int b, tile;
   if (!find_tile(p, per, index / p.Hkv / slices, &b, &tile)) return;
-  const Seq sq = load_seq(p, b);
+  const Seq sq = load_seq<TREE>(p, b);
   if (sq.n == 0) return;  // an impossible length (find_tile counts by the starts)
   const int u0 = index / p.Hkv % slices * kF32Rows, tok0 = tile * per, ntok = min(per, sq.n - tok0);
   const int p0 = sq.first + tok0;

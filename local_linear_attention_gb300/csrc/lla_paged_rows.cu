@@ -77,7 +77,7 @@ __global__ void __launch_bounds__(NW * 32) attend_rows_kernel(Params p) {
   // Set up behind the tiled kernel of the same call, this one may run beside its last blocks (they
   // share no output); one thread's wait makes the end of this grid the end of both.
   if (p.beside && blockIdx.x == 0 && threadIdx.x == 0) wait_previous();
-  const Seq sq = load_seq(p, b);
+  const Seq sq = load_seq<TREE>(p, b);
   if (!mine(p, sq.n)) {
     if (sq.n > 0 && sq.n * p.g > p.max_rows) atomicOr(p.status, kStatusBadIndex);  // beyond max_new
     return;
@@ -331,7 +331,7 @@ __global__ void __launch_bounds__(128) join_rows_kernel(Params p) {
   const int pair = (int)(id / p.row_cap), r = (int)(id % p.row_cap);
   if (pair >= pairs) return;
   const int b = pair / p.Hkv, hk = pair % p.Hkv;
-  const Seq sq = load_seq(p, b);
+  const Seq sq = load_seq_or_tree(p, b);
   if (!mine(p, sq.n) || r >= sq.n * p.g) return;
   const float c2 = p.inv_h * kLog2e;
   auto at = [&](int s) { return ((long long)s * pairs + pair) * p.row_cap + r; };

@@ -157,7 +157,7 @@ struct Tile {
 template <int D, bool PROBE, bool TREE, bool STREAMS>
 __device__ __forceinline__ long long seq_cost(const Params& p, int b, int tokens, int* tiles, int* shortest) {
   using S = Sched<D, PROBE, STREAMS>;
-  const Seq sq = load_seq(p, b);
+  const Seq sq = load_seq<TREE>(p, b);
   long long c = 0;
   int least = 0x7fffffff, nt = 0;
   if (mine(p, sq.n)) {
@@ -201,7 +201,7 @@ __device__ __forceinline__ Place locate(const Params& p, const long long* cost, 
     }
     const int l = __ffs(hit) - 1, b = base + l;
     u -= __shfl_sync(0xffffffffu, incl - c, l);
-    const Seq sq = load_seq(p, b);
+    const Seq sq = load_seq<TREE>(p, b);
     const int nt = (sq.n + tokens - 1) / tokens;
     for (int tb = 0; tb < nt; tb += 32) {
       int count = 0;
@@ -275,10 +275,11 @@ struct Work {
   int n1, w0;                 // of the tile's key tiles (TileRange)
 };
 // The first of this launch's sequences from b on (a whole warp calls and agrees).
+template <bool TREE>
 __device__ __forceinline__ int next_seq(const Params& p, int b) {
   for (; b < p.B; b += 32) {
     const int i = b + (threadIdx.x & 31);
-    const unsigned hit = __ballot_sync(0xffffffffu, i < p.B && mine(p, load_seq(p, i).n));
+    const unsigned hit = __ballot_sync(0xffffffffu, i < p.B && mine(p, load_seq<TREE>(p, i).n));
     if (hit) return b + __ffs(hit) - 1;
   }
   return p.B;
@@ -542,14 +543,14 @@ attend_tc_kernel(Params p, const __grid_constant__ CUtensorMap kmap, const __gri
         const long long at = (long long)k * gridDim.x + (k & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
         const Place t = at < ntiles ? by_rank(p, tiles_s, most, (unsigned)at) : Place{p.B, 0, 0, 0};
         if (t.b < p.B) {
-          const Seq sq = load_seq(p, t.b);
+          const Seq sq = load_seq<TREE>(p, t.b);
           const Tile x(sq, t.tile, tokens, TREE);
           const TileRange<KT> range(p, x.p0, x.p1);
           w = {t.b, t.tile, t.hk, 0, range.count, 1, 0, sq.t0, sq.n, sq.len, sq.first, range.n1, range.w0};
         }
       }
       while (most == 0 && !over && cur.b < p.B) {
-        const Seq sq = load_seq(p, cur.b);
+        const Seq sq = load_seq<TREE>(p, cur.b);
         const Tile x(sq, cur.tile, tokens, TREE);
         const TileRange<KT> range(p, x.p0, x.p1);
         const int count = range.count;
@@ -563,7 +564,7 @@ attend_tc_kernel(Params p, const __grid_constant__ CUtensorMap kmap, const __gri
           cur.hk = 0;
           if (++cur.tile >= (sq.n + tokens - 1) / tokens) {
             cur.tile = 0;
-            cur.b = next_seq(p, cur.b + 1);
+            cur.b = next_seq<TREE>(p, cur.b + 1);
           }
         }
         if (!w.none) break;

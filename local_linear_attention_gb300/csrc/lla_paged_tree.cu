@@ -16,7 +16,7 @@ __global__ void __launch_bounds__(256) tree_kernel(Params p, uint32_t* bits, int
   __shared__ int parent[kMaxNodes];
   let_next();  // which waits for this kernel's end itself
   const int b = blockIdx.x;
-  const Seq sq = load_seq(p, b);
+  const Seq sq = load_seq<true>(p, b);
   if (sq.n == 0) return;
   if (!mine(p, sq.n)) {
     if (blockIdx.y == 0 && threadIdx.x == 0) atomicOr(p.status, kStatusBadIndex);  // beyond max_new
