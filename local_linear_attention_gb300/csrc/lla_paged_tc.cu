@@ -1021,8 +1021,12 @@ attend_tc_kernel(Params p, const __grid_constant__ CUtensorMap kmap, const __gri
 // size (its place, the pieces' factors) is paid by few threads, and blocks x apart of a tile go to different SMs. (16 trees
 // at 4k to 16k, nearly every tile cut: 14.4 us with a warp to a row, 9.3 so.)
 // COLS is 16, or 4 where the tiles are few and each has many pieces: then the pieces' loads in flight count.
+// Three blocks an SM, with few loads a thread in flight each: with twice those and one or two blocks, a call without cut
+// tiles waited 1.5 us for waves of blocks that find nothing (24 mixed sequences 110.1 us, 109.1 so; chunk of 64 at 32768
+// 55.6 and 53.9, of 256 at 16000 with heads of 64 58.1 and 56.7; four blocks, with spills, took 256 nodes at 32768 from 122
+// to 125).
 template <int D, bool PROBE, bool STREAMS, int COLS>
-__global__ void __launch_bounds__(256) join_tc_kernel(Params p) {
+__global__ void __launch_bounds__(256, 3) join_tc_kernel(Params p) {
   using C = Cfg<D, PROBE, STREAMS>;
   constexpr int ROWS = Sched<D, PROBE, STREAMS>::rows, TR = D / COLS;  // threads of a row
   wait_previous();
@@ -1045,7 +1049,7 @@ __global__ void __launch_bounds__(256) join_tc_kernel(Params p) {
   // The pieces' results of this row, the next ones on their way beside the sequence's lengths.
   const int row = blockIdx.x * (256 / TR) + threadIdx.x / TR, col = threadIdx.x % TR * COLS;
   auto at = [&](int i) { return (long long)((blockIdx.y + i) * 2 + (i == 0)) * ROWS + row; };
-  constexpr int CH = (COLS == 4 ? 8 : 4) / (PROBE ? 2 : 1);  // pieces at once
+  constexpr int CH = (COLS == 4 ? 4 : 2) / (PROBE ? 2 : 1);  // pieces at once
   const bool cols = col < p.dv;
   float4 st[CH], o[CH][COLS / 4], e[PROBE ? CH : 1][COLS / 4];
   auto load = [&](int c) {
@@ -1228,7 +1232,7 @@ static cudaError_t join(const Params& p, int D, cudaStream_t s) {
   return launch(kern, dim3(rows * (D / COLS) / 256, (unsigned)p.split), 256, 0, 1, true, s, p);
 }
 cudaError_t launch_join_tc(const Params& p, int D, cudaStream_t s) {
-  // Few tiles: fewer than a quarter of the CTAs, so that most have more pieces than a thread of 16 columns loads
+  // Few tiles: fewer than a quarter of the CTAs, so that most have many more pieces than a thread of 16 columns loads
   // at once (32 nodes at 16000, 32 heads over 8 of 64 with a probe, 38 pieces to a tile: 73 us in all with 16
   // columns, 44 with 4; of 128 without: 37 and 31).
   const int tokens = BM / p.g * (D == 128 && !p.r && !p.streams ? 2 : 1);
