@@ -298,8 +298,8 @@ int lla_rotary_frequencies(lla_rotary_spec* spec, int rot, int layout, double ba
 
 /*
  * Rotates `count` (1 .. 3) tensors that share their positions, such as q, k and r of an attention: x[i] is
- * [B, heads[i], T, d], y[i] the same (x[i] == y[i]: in place; otherwise none may overlap another), x, y and
- * heads host arrays. positions [B, T] (device) or NULL: 0 .. T-1. backward nonzero: the gradient with respect
+ * [B, heads[i], T, d], y[i] the same, 16-byte aligned (x[i] == y[i]: in place; otherwise none may overlap another), x,
+ * y and heads host arrays. positions [B, T] (device) or NULL: 0 .. T-1. backward nonzero: the gradient with respect
  * to the input from that with respect to the output, which is the transposed rotation times scale. d in {16, 32, 64,
  * 128}; fewer than 2^31 rows, and at most 2^31 - 2^17 heads, in all (LLA_ERR_UNSUPPORTED). One launch, asynchronous,
  * allocates nothing; fp32 arithmetic, one rounding.
@@ -508,8 +508,9 @@ int lla_paged_attention(const lla_paged_cache* cache, const lla_paged_query* que
  * first = lens - (number of nodes), and is at position first + depth(i), depth 0 being a child of -1. It sees
  * itself, its ancestors, and the positions before the nodes; with a window those of them whose position is
  * within the last `window` up to its own or among the first `sinks`. Otherwise as lla_paged_attention, for
- * the same caches and queries: parents[i] = i - 1 gives its results. A drafted node's weight is not
- * counted: track_mass has to be 0.
+ * the same caches and queries: parents[i] = i - 1 gives its results. Weights are not tracked: track_mass has to be 0,
+ * and the positions that a node sees get nothing from it, not even when it is kept. After drafted steps the mass
+ * that lla_paged_evict goes by holds the weights of the other tokens only.
  *
  * At most 1024 nodes to a sequence (LLA_ERR_UNSUPPORTED where max_new and tokens are both larger). Reported
  * in the status word, the sequence's outputs unspecified: a parent that does not come before its child,
@@ -537,7 +538,8 @@ int lla_paged_evict(const lla_paged_cache* from, const lla_paged_cache* to, int 
  * entries of its row, and a page is free while refs is 0. Sequences that fork share all their pages; one
  * that grows takes its own copy of a last page that it would write to while others hold it. Fork, free and
  * grow touch tables, lens and refs alone, which the caches of a model's layers share: they are called once,
- * lla_paged_copy and lla_paged_compact once per layer. None of them allocates or synchronises, and all give
+ * lla_paged_copy and lla_paged_compact once per layer. lla_paged_evict neither reads nor changes refs: its `to`
+ * gets the pages for the kept positions by lla_paged_grow. None of them allocates or synchronises, and all give
  * the same pages whatever the scheduling. Impossible lengths, page numbers, parents and paths are reported in the
  * status word (LLA_ERR_INVALID_ARG); unless it says otherwise below, that sequence or pair is left as it is.
  *

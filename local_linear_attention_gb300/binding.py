@@ -698,8 +698,8 @@ def lla_paged_tree_attention(q, cache: PagedCache, starts, parents, h: float, r=
     """Attention of trees of drafted tokens over the cache that they were appended to: sequence b's new
     tokens are nodes, parents [tokens] int32 holds of each its parent's index among them (below its
     own) or -1. A node sees the positions before the nodes, its ancestors and itself; its position is
-    that of the first node's slot plus its depth. Otherwise as lla_paged_attention. max_new: a bound of the nodes
-    of one sequence (default: all tokens, at most 1024)."""
+    that of the first node's slot plus its depth. Otherwise as lla_paged_attention, but cache.mass gets no weights.
+    max_new: a bound of the nodes of one sequence (default: all tokens, at most 1024)."""
     tokens = q.shape[0]
     _paged_parents(parents, cache, tokens)
     max_new = min(tokens, MAX_NODES) if max_new is None else max_new

@@ -21,8 +21,10 @@
 // Measured: 62 single tokens at 12k to 18k, 16 heads each over 2 of 128, with a probe, 0.90 ms (35 TFLOP/s;
 // 2.3 ms in the block-wide form of lla_paged_cc.cuh, with tiles of 16 rows); prompts of 7 sequences of
 // 3.8k, 4 heads of 128, 0.71 ms (1.13, tiles of 64 rows); 3 sequences of up to 37 new tokens and 2047
-// positions, 6 heads over 2, d 64, dv 32, with a probe and weights, 22 us (47) in two launches. Eight warps
+// positions, 6 heads over 2, d 64, dv 32, with a probe and weights, 23.5 us (47) in two launches. Eight warps
 // an SM (registers and shared memory) wait for their own instructions' results most of the time.
+// Short calls pay for the way through the code, not for keys: trees of 16 nodes, 6 heads over 2 of 64, take 16.6 us at 32
+// positions and 16.7 at 704 (without a probe 9.5 and 10.5; the bf16 kernel 4.6 and 7.8).
 #include <type_traits>
 
 #include "lla_paged_rows.cuh"

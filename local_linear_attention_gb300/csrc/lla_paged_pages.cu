@@ -7,9 +7,9 @@
 // What bounds them: the bookkeeping its launch and the chain lens - table - refs; copy and compact HBM,
 // each byte read once and written once. Counts are integers and pages are taken lowest first, in the order of
 // sequences, so results do not depend on scheduling.
-// Measured: fork 1.8, free 1.1, grow 4.1 us for 8 sequences (grow: two passes over the counts with a barrier of the cluster
-// between them; 64 sequences of 880 pages the same); 60 pages of 262 KB copied in some 8 us, 4 TB/s; the kept paths of 64
-// drafts of 64, 8 heads of 128, 2 us.
+// Measured, warm caches: fork 1.9, free 1.9, grow 4.6 us for 8 sequences (grow: two passes over the counts with a barrier of
+// the cluster between them; 7.5 for 64); 60 pages of 524 KB (keys and values) copied in 4.8 us, within L2; kept paths of 8 in
+// 64 drafts of 64, 8 heads of 128, 4.0 us.
 #include <cooperative_groups.h>
 
 #include "lla_paged.cuh"

@@ -24,7 +24,7 @@
 // exp(s - lse) once the rows' lse is known. (Done by the attention's own blocks after their join,
 // the same pass took 60 us longer at B32 L16384 d128: 128 threads a block waiting for scratch.)
 // Trees of drafted tokens (TREE, up to 64 nodes): masks come from the tree, which a warp finds between its lanes, and
-// more than 16 rows are several tiles. Measured: 12 nodes at 1000 positions, 8 heads of 64 with a probe, 6.8 us; 32
+// more than 16 rows are several tiles. Measured: 12 nodes at 1000 positions, 8 heads of 64 with a probe, 7.0 us; 32
 // nodes at 4000, 32 heads over 8 of 64, 17 us.
 // Rows: 16 without a probe. With one, rows 0-7 of the MMA are q and rows 8-15 the same rows' r:
 // the accumulator fragment gives a thread s and t of one row, p goes back as row i and p t as row

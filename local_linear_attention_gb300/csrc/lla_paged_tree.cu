@@ -4,8 +4,8 @@
 //
 // A thread per node goes up the tree by parents in shared memory. Indices fall on the way, so the words of a
 // node's bits are met from the last to the first and each is written once, without atomics. What bounds
-// it: the launch and the longest way up (2 us of a call for 16 trees of 32 nodes, mostly behind the attention's first
-// keys); the attention is set up meanwhile and waits only where it meets the first masked keys.
+// it: the launch and the longest way up (6 us by itself with cold caches for 16 trees of 32 nodes; a call without it takes
+// 1.8 us less); the attention is set up meanwhile and waits only where it meets the first masked keys.
 #include "lla_paged.cuh"
 
 namespace lla {

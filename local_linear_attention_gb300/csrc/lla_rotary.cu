@@ -6,7 +6,7 @@
 // angle's sine and cosine (some 30 instructions with the integer product) are found once for `per` heads, while the
 // first of them are on their way;
 // the loads of several heads are in flight together. Measured: q, k and r of B4 H8 T4096 d64,
-// 17.5 us, 5.8 TB/s (85 % of the copy bandwidth); fp32, two of B2 H8 T2047, 6.4 us.
+// 18 us, 5.6 TB/s (82 % of the copy bandwidth); fp32, two of B2 H8 T2047, 6.3 us.
 #include <cmath>
 #include <type_traits>
 
