@@ -100,3 +100,60 @@ def test_no_table_is_too_wide(lla):  # noqa: F811
     copies, left = lla.lla_paged_grow(cache, ints([0, most]), refs)
     assert left.tolist() == [-max_pages] and copies.tolist() == [[-1, -1]]
     assert cache.lens.tolist() == [most - 1] and lla.lla_stream_status() == 0
+
+
+def grown(book, rows, lens, news, width):
+    """The rules: (copies, left), rows and lens changed where there is room for all."""
+    over = sum(max(0, book.pages(n + t) - width) for n, t in zip(lens, news))
+    within = [min(t, width * book.page - n) for n, t in zip(lens, news)]
+    trial = Book(0, book.page)
+    trial.refs = list(book.refs)
+    trial_rows, trial_lens = [list(r) for r in rows], list(lens)
+    copies, left = trial.grow(trial_rows, trial_lens, within)
+    if over:
+        return [[-1, -1]] * len(lens), min(left, 0) - over
+    if left >= 0:
+        book.refs, rows[:], lens[:] = trial.refs, trial_rows, trial_lens
+    return copies, left
+
+
+@pytest.mark.parametrize("page,num_pages,B,width,seed", [(16, 40, 3, 4, 0), (32, 300, 33, 3, 1), (16, 2000, 500, 5, 2), (64, 90, 8, 9, 3),
+                                                         (16, 9000, 4096, 2, 4)])
+def test_any_order_with_narrow_tables(lla, page, num_pages, B, width, seed):  # noqa: F811
+    """Rows that fill up, pools that run out, forks and shorter sequences, step after step."""
+    import random
+    rng = random.Random(seed)
+    pool = pools(num_pages, Hkv=1, page=page, d=16, dv=16, mass=False)
+    book, refs = Book(num_pages, page), torch.zeros(num_pages, dtype=torch.int32, device="cuda")
+    cur, old = (Pair(lla, [[] for _ in range(B)], [0] * B, width, pool) for _ in range(2))
+    seen = set()
+    for step in range(40):
+        kind = rng.choice(["grow", "grow", "grow", "fork", "keep"])
+        if kind == "grow" or step % 10 == 9 and any(cur.lens):  # then one position more than a row has
+            most = rng.choice([1, 2, page, width * page])
+            news = [rng.choice([0, 1, rng.randint(0, most)]) if rng.random() < 8 / B else 0 for _ in range(B)]
+            if rng.random() < 0.6:  # a step that fits its rows
+                news = [min(t, width * page - n) for t, n in zip(news, cur.lens)]
+            if step % 10 == 9 and any(cur.lens):
+                b = next(b for b, n in enumerate(cur.lens) if n)
+                news[b] = width * page - cur.lens[b] + 1
+            full = any(n + t > width * page for n, t in zip(cur.lens, news))
+            copies, left = lla.lla_paged_grow(cur.device, starts_of(news), refs)
+            want, want_left = grown(book, cur.rows, cur.lens, news, width)
+            assert copies.tolist() == want and left.tolist() == [want_left]
+            seen.add((want_left < 0, full))
+        elif kind == "fork":
+            parents = [rng.randrange(-1, B) if rng.random() < 0.5 else rng.randrange(max(1, B // 4)) for _ in range(B)]
+            lla.lla_paged_fork(cur.device, old.device, ints(parents), refs)
+            old.rows, old.lens = book.fork(cur.rows, cur.lens, parents)
+            lla.lla_paged_free(cur.device, refs)
+            book.free(cur.rows, cur.lens)
+            cur, old = old, cur
+        else:
+            keep = [rng.randint(-2, n + 3) if rng.random() < 0.2 else n for n in cur.lens]
+            lla.lla_paged_free(cur.device, refs, ints(keep))
+            book.free(cur.rows, cur.lens, keep)
+        cur.check(book, refs)
+        old.check(book, refs)
+    assert lla.lla_stream_status() == 0
+    assert {(False, False), (True, True)} <= seen
